@@ -573,6 +573,161 @@ typedef struct {
 } biv_attn_bwd_desc;
 biv_status biv_attention_backward(const biv_attn_bwd_desc* desc, biv_stream_t stream);
 
+/* --------------------------------------------------------- policy loss --
+ * The trainer's loss on the recomputed logprobs ("No More Train-Inference
+ * Mismatch", section "方法细节": the trainer's forward and backward around the
+ * imported ops; GRPO without importance correction, "Finish RL Training
+ * Faster", section "两组结果，要连同分母一起读"): a clipped policy loss with a KL
+ * term, and its gradient in the same call.
+ *
+ * Rows t = 0..T-1 are tokens; sequence s holds rows [seq_start[s],
+ * seq_start[s+1]).  A row counts when it lies in a sequence and its mask byte
+ * is not 0.  With A the advantage (of the row or of its sequence), x clamped
+ * to [-20, 20] written clamp(x):
+ *   r  = exp(clamp(lp - old_lp)),  u = -A r,  c = -A min(max(r, 1-clip_lo), 1+clip_hi)
+ *   pg = max(u, c);  dual_clip > 0 and A < 0:  pg = min(pg, -A dual_clip)
+ *   e  = clamp(ref_lp - lp),  kl = exp(e) - e - 1   (the k3 estimator)
+ *   loss = sum_t w_t (pg + kl_coef kl - ent_coef H)
+ *   dlp  = w ((u is taken ? u : 0) + kl_coef (1 - exp(e)))
+ * where u is taken when u >= c, the dual bound does not act and |lp - old_lp|
+ * < 20, and the KL part is 0 at |ref_lp - lp| >= 20 (the clamps' derivative).
+ * w_t by `reduce`: TOKEN_MEAN 1/N, N counted rows; SEQ_MEAN 1/(S n_s), S
+ * sequences that have counted rows, n_s their number; SUM 1/norm.
+ * A row that does not count has weight 0: its lp, logits and target are not
+ * read, and its dlp, lp, entropy and dz are written as zeros; with no counted
+ * row at all loss, statistics and gradients are zeros.
+ *
+ * stats float32 [8]: loss, sum w pg, sum w kl, sum w H, then over counted rows
+ * the share where u is not taken by clipping, mean of exp(d) - 1 - d (d =
+ * clamp(lp - old_lp)), max |lp - old_lp|, and their number.  Blocks of 1024
+ * rows are summed in one fixed order, blocks ascending (32 lanes, then a xor
+ * tree): every call repeats its bits, and a row's gradient depends on that row
+ * and its weight only.
+ * seq_start outside [0, T] or not ascending is reported through
+ * biv_poll_error (results are then unspecified; no access leaves [0, T)).
+ * Workspace: biv_policy_loss_workspace bytes, 16-byte aligned, caller-owned,
+ * no initial value; calls that can overlap on the GPU need separate ones. */
+typedef enum { BIV_LOSS_TOKEN_MEAN = 0, BIV_LOSS_SEQ_MEAN = 1, BIV_LOSS_SUM = 2 } biv_loss_reduce;
+typedef struct {
+  int T, nseq;
+  const int32_t* seq_start;  /* [nseq + 1], ascending, within [0, T] */
+  const uint8_t* mask;       /* [T]; NULL: every row of a sequence counts */
+  const float* old_lp;       /* [T] logprobs of the policy that sampled; NULL: lp itself (r = 1) */
+  const float* ref_lp;       /* [T] reference logprobs; may be NULL when kl_coef is 0 */
+  const float* adv;          /* [T] when adv_per_row, else [nseq] */
+  int adv_per_row;
+  float clip_lo, clip_hi;    /* 0 <= clip_lo <= 1, 0 <= clip_hi */
+  float dual_clip;           /* 0: off; else > 1 */
+  float kl_coef, ent_coef;
+  int reduce;                /* biv_loss_reduce */
+  float norm;                /* SUM only: > 0 */
+  float* stats;              /* [8] */
+  void* workspace;
+  size_t workspace_bytes;
+} biv_policy_desc;
+biv_status biv_policy_loss_workspace(int T, int nseq, size_t* bytes);
+
+/* From per-token logprobs (biv_lm_head_logprob's or biv_logprob's output):
+ * lp float32 [T] -> dlp float32 [T] (NULL: statistics only), ready for
+ * biv_logprob_backward.  ent_coef must be 0 (the entropy needs the logits). */
+biv_status biv_policy_loss(const biv_policy_desc* desc, const float* lp, float* dlp,
+                           biv_stream_t stream);
+
+/* From the logits, in one pass over them: z [T, V] rows at ld (z_dtype
+ * BIV_F32 or BIV_BF16), x = z inv_temp, target int32 [T]:
+ *   lp = x[target] - lse, p = exp(x - lse), H = lse - sum_v p_v x_v
+ *   dz_v = inv_temp (dlp ([v = target] - p_v) + w ent_coef p_v (log p_v + H))
+ * lp, entropy float32 [T]; dz [T, V] rows at ldz (dz_dtype BIV_F32 or
+ * BIV_BF16, one rounding; NULL: no gradient).  dz may be z itself (same
+ * pointer, type and stride), and must not overlap it otherwise.  A logit of
+ * -inf has p = 0 and dz = 0 (a row with no finite logit gives NaN).  A counted
+ * row whose target is outside [0, V) gives lp = NaN and the device error code
+ * 2.  Each row's bits depend on V and the row only: 1024-logit groups are
+ * reduced to (max, sum, entropy sum) by one warp and merged in one order,
+ * however the row is spread over CTAs.  1 <= V <= 262144.  Rows that keep 16
+ * bytes' alignment load and store fastest; any element alignment works. */
+biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, int64_t ld,
+                                  int z_dtype, const int32_t* target, int V, float inv_temp,
+                                  float* lp, float* entropy, void* dz, int64_t ldz, int dz_dtype,
+                                  biv_stream_t stream);
+
+/* ------------------------------------------------------ optimizer step --
+ * AdamW over many tensors in one launch, writing the model's own weights in
+ * place (captured graphs keep their addresses; BF16 weights that the forward
+ * reads, "Finish RL Training Faster", section "让训练前向使用推理的数值").  Per
+ * element, in FP32:
+ *   g = grad * coef;  m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2
+ *   w = w (1 - lr wd) - (lr / (1-b1^t)) m / (sqrt(v) / sqrt(1-b2^t) + eps)
+ * with t the step's number, lr = *lr * lr_scale and wd of the tensor.
+ *
+ * A biv_opt_tensor describes one tensor of numel elements, all arrays dense:
+ *   param  BIV_F32: the weight; BIV_BF16 with master (float32): the master is
+ *          updated and param gets its nearest bf16; BIV_BF16 without master:
+ *          w is the bf16 weight, rounded back to bf16.
+ *   grad   BIV_F32 or BIV_BF16.
+ *   state  BIV_F32: m, v float32.  BIV_E4M3: blocks of 128 consecutive
+ *          elements (the last one shorter); m holds e4m3 codes of m / s with
+ *          s = max(amax|m|, 2^-100) / 448 in m_scale; v holds codes of
+ *          sqrt(v) / s the same way in v_scale (the root halves the exponent
+ *          range that the codes have to cover), and a positive root never gets
+ *          code 0.  m_scale, v_scale float32 [ceil(numel / 128)].
+ * rounding (8-bit states and bf16 weights without a master): NEAREST (ties to
+ * even), or STOCHASTIC: the magnitude goes up with a chance equal to the part
+ * cut off, from 16 bits of a hash of (seed, t, element), so that steps below
+ * half a grid spacing still move the value on average; a rerun repeats it.
+ *
+ * biv_opt_plan (host only, no launch) checks a HOST array of n tensors and
+ * fills first_chunk, rng_base and vec; *chunks receives the launch size.  The
+ * caller then copies the array to the device.  It refuses null pointers,
+ * misaligned elements, unsupported type combinations and tensors whose written
+ * ranges overlap. */
+typedef enum { BIV_ROUND_NEAREST = 0, BIV_ROUND_STOCHASTIC = 1 } biv_rounding;
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+  int64_t first_chunk;       /* filled by biv_opt_plan */
+  int64_t rng_base;          /* filled by biv_opt_plan */
+  float lr_scale, weight_decay;
+  int32_t param_dtype, grad_dtype, state_dtype;
+  int32_t vec;               /* filled by biv_opt_plan */
+} biv_opt_tensor;
+biv_status biv_opt_plan(biv_opt_tensor* host_tensors, int n, int64_t* chunks);
+
+/* Global L2 norm of all gradients: out[0] = norm, out[1] = min(1, max_norm /
+ * (norm + 1e-6)) (1 when max_norm is 0).  FP32 sums in one order fixed by the
+ * tensors' sizes; a norm beyond about 1.8e19 reads as infinity.  tensors:
+ * device copy of the planned array.  Workspace: biv_grad_norm_workspace bytes,
+ * 16-byte aligned, caller-owned, no initial value. */
+biv_status biv_grad_norm_workspace(int64_t chunks, size_t* bytes);
+biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, float max_norm,
+                         float* out, void* workspace, size_t workspace_bytes, biv_stream_t stream);
+
+/* One AdamW step.  lr (float32 [1]), step (int32 [2]) and clip (float32 [2],
+ * biv_grad_norm's out, or NULL for coef = 1) are device memory read by the
+ * kernel, so a captured step replays with new values.  step[0] counts the
+ * steps taken (0 for new states): the call uses t = step[0] + 1 and stores it;
+ * step[1] must be 0 between calls and is 0 again after each.  With clip given
+ * and its norm not finite the whole call changes nothing, step included. */
+typedef struct {
+  const biv_opt_tensor* tensors;   /* device */
+  int n;
+  int64_t chunks;
+  const float* lr;
+  const float* clip;
+  int32_t* step;
+  double beta1, beta2;             /* 0 <= beta < 1 */
+  float eps;                       /* > 0 */
+  int rounding;                    /* biv_rounding */
+  uint64_t seed;
+} biv_adamw_desc;
+biv_status biv_adamw(const biv_adamw_desc* desc, biv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

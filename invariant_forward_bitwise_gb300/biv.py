@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(_PKG, "libbiv.so")
 BIV_OK, BIV_ERR_INVALID, BIV_ERR_UNSUPPORTED, BIV_ERR_WORKSPACE, BIV_ERR_CUDA, BIV_ERR_TIMEOUT = range(6)
 MODE_INVARIANT, MODE_FAST = 0, 1
 BF16, F32, E4M3 = 0, 1, 2
+LOSS_TOKEN_MEAN, LOSS_SEQ_MEAN, LOSS_SUM = 0, 1, 2
+ROUND_NEAREST, ROUND_STOCHASTIC = 0, 1
 
 EXPORTS = [
     "biv_version", "biv_last_error", "biv_device_sm_count", "biv_poll_error",
@@ -30,6 +32,8 @@ EXPORTS = [
     "biv_causal_conv1d", "biv_gated_rmsnorm", "biv_nvfp4_dequant",
     "biv_gemm_nvfp4_workspace", "biv_gemm_nvfp4",
     "biv_rmsnorm_backward", "biv_silu_mul_backward", "biv_logprob_backward", "biv_attention_backward",
+    "biv_policy_loss_workspace", "biv_policy_loss", "biv_policy_loss_logits",
+    "biv_opt_plan", "biv_grad_norm_workspace", "biv_grad_norm", "biv_adamw",
 ]
 
 
@@ -112,6 +116,34 @@ class AttnBwdDesc(C.Structure):
                 ("workspace", C.c_void_p)]
 
 
+class PolicyDesc(C.Structure):
+    _fields_ = [("T", C.c_int), ("nseq", C.c_int),
+                ("seq_start", C.c_void_p), ("mask", C.c_void_p),
+                ("old_lp", C.c_void_p), ("ref_lp", C.c_void_p),
+                ("adv", C.c_void_p), ("adv_per_row", C.c_int),
+                ("clip_lo", C.c_float), ("clip_hi", C.c_float), ("dual_clip", C.c_float),
+                ("kl_coef", C.c_float), ("ent_coef", C.c_float),
+                ("reduce", C.c_int), ("norm", C.c_float),
+                ("stats", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class OptTensor(C.Structure):
+    _fields_ = [("param", C.c_void_p), ("master", C.c_void_p), ("grad", C.c_void_p),
+                ("m", C.c_void_p), ("v", C.c_void_p),
+                ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("numel", C.c_int64), ("first_chunk", C.c_int64), ("rng_base", C.c_int64),
+                ("lr_scale", C.c_float), ("weight_decay", C.c_float),
+                ("param_dtype", C.c_int32), ("grad_dtype", C.c_int32), ("state_dtype", C.c_int32),
+                ("vec", C.c_int32)]
+
+
+class AdamWDesc(C.Structure):
+    _fields_ = [("tensors", C.c_void_p), ("n", C.c_int), ("chunks", C.c_int64),
+                ("lr", C.c_void_p), ("clip", C.c_void_p), ("step", C.c_void_p),
+                ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float),
+                ("rounding", C.c_int), ("seed", C.c_uint64)]
+
+
 _lib: Optional[C.CDLL] = None
 
 
@@ -163,6 +195,10 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "biv_silu_mul_backward": ([P, I64, P, I64, P, I64, I, I, P], I),
         "biv_logprob_backward": ([P, I64, P, P, I, I, P, I64, P], I),
         "biv_attention_backward": ([P, P], I),
+        "biv_policy_loss_workspace": ([I, I, P], I), "biv_policy_loss": ([P, P, P, P], I),
+        "biv_policy_loss_logits": ([P, P, I64, I, P, I, F, P, P, P, I64, I, P], I),
+        "biv_opt_plan": ([P, I, P], I), "biv_grad_norm_workspace": ([I64, P], I),
+        "biv_grad_norm": ([P, I, I64, F, P, P, C.c_size_t, P], I), "biv_adamw": ([P, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name, None)
@@ -524,3 +560,113 @@ def biv_attention_backward(q, k, v, dout, q_pos, k_pos, scale, dq, dk, dv, strea
     d.Tq, d.Tk, d.Hq, d.Hkv, d.D = Tq, k.shape[0], Hq, k.shape[1], D
     d.q_pos, d.k_pos, d.scale, d.workspace = q_pos.data_ptr(), k_pos.data_ptr(), float(scale), ws.data_ptr()
     _check(load().biv_attention_backward(C.byref(d), _stream(stream)), "biv_attention_backward")
+
+
+# ---------------------------------------------------------- policy loss --
+def _rows_ok(what, t, dtype, n):
+    """A contiguous vector of at least n values on the current device (None passes)."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {n} values")
+
+
+def biv_policy_loss_workspace(T: int, nseq: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().biv_policy_loss_workspace(T, nseq, C.byref(n)), "biv_policy_loss_workspace")
+    return n.value
+
+
+def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None, ref_lp=None,
+                clip_lo=0.2, clip_hi=0.2, dual_clip=0.0, kl_coef=0.0, ent_coef=0.0,
+                reduce=LOSS_TOKEN_MEAN, norm=1.0) -> PolicyDesc:
+    """The part that biv_policy_loss and biv_policy_loss_logits share (see
+    include/biv.h).  seq_start int32 [nseq + 1]; adv float32 [nseq] (one per
+    sequence) or [T]; mask uint8 or bool [T]; old_lp, ref_lp float32 [T];
+    stats float32 [8]; workspace uint8 of biv_policy_loss_workspace bytes.
+    With nseq == T an advantage vector counts as one per sequence."""
+    nseq = seq_start.numel() - 1
+    if nseq < 0:
+        raise ValueError("seq_start needs at least one entry")
+    _rows_ok("seq_start", seq_start, torch.int32, 1)
+    if adv.numel() not in (nseq, T):
+        raise ValueError(f"adv must hold {nseq} (sequences) or {T} (rows) values")
+    _rows_ok("adv", adv, torch.float32, 0)
+    if mask is not None:
+        _rows_ok("mask", mask, torch.bool if mask.dtype == torch.bool else torch.uint8, T)
+    _rows_ok("old_lp", old_lp, torch.float32, T)
+    _rows_ok("ref_lp", ref_lp, torch.float32, T)
+    _rows_ok("stats", stats, torch.float32, 8)
+    _rows_ok("workspace", workspace, torch.uint8, 0)
+    d = PolicyDesc()
+    d.T, d.nseq = T, nseq
+    d.seq_start, d.adv, d.stats = seq_start.data_ptr(), adv.data_ptr(), stats.data_ptr()
+    d.mask = None if mask is None else mask.data_ptr()
+    d.old_lp = None if old_lp is None else old_lp.data_ptr()
+    d.ref_lp = None if ref_lp is None else ref_lp.data_ptr()
+    d.adv_per_row = int(adv.numel() != nseq)
+    d.clip_lo, d.clip_hi, d.dual_clip, d.kl_coef, d.ent_coef = clip_lo, clip_hi, dual_clip, kl_coef, ent_coef
+    d.reduce, d.norm = reduce, norm
+    d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return d
+
+
+def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):
+    """lp float32 [T] -> dlp float32 [T] (or None: statistics only) and desc's stats."""
+    _rows_ok("lp", lp, torch.float32, desc.T)
+    _rows_ok("dlp", dlp, torch.float32, desc.T)
+    _check(load().biv_policy_loss(C.byref(desc), _p(lp), _p(dlp), _stream(stream)), "biv_policy_loss")
+
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def biv_policy_loss_logits(desc: PolicyDesc, logits, target, lp, entropy, dz=None, inv_temp=1.0,
+                           stream=None):
+    """logits float32 or bf16 [T, V] (rows of stride 1) -> lp, entropy float32
+    [T] and dz float32 or bf16 [T, V] (None: no gradient; may be logits)."""
+    for what, t in (("logits", logits), ("dz", dz)):
+        if t is None:
+            continue
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what} must be on the current CUDA device")
+        if t.dim() != 2 or t.dtype not in _FLOATS or t.shape[0] < desc.T or t.shape[1] != logits.shape[1] or \
+                (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what} must be a float32 or bf16 [T, V] tensor with rows of stride 1")
+    _rows_ok("target", target, torch.int32, desc.T)
+    _rows_ok("lp", lp, torch.float32, desc.T)
+    _rows_ok("entropy", entropy, torch.float32, desc.T)
+    V = logits.shape[1]
+    # one row: its stride says nothing, and may be below V
+    ld = max(logits.stride(0), V) if desc.T <= 1 else logits.stride(0)
+    ldz = 0 if dz is None else max(dz.stride(0), V) if desc.T <= 1 else dz.stride(0)
+    _check(load().biv_policy_loss_logits(
+        C.byref(desc), _p(logits), ld, _FLOATS[logits.dtype], _p(target), V, float(inv_temp), _p(lp),
+        _p(entropy), _p(dz), ldz, F32 if dz is None else _FLOATS[dz.dtype], _stream(stream)),
+        "biv_policy_loss_logits")
+
+
+# ------------------------------------------------------- optimizer step --
+def biv_opt_plan(tensors) -> int:
+    """Checks and completes a ctypes array of OptTensor; returns its chunks."""
+    n = C.c_int64(0)
+    _check(load().biv_opt_plan(tensors, len(tensors), C.byref(n)), "biv_opt_plan")
+    return n.value
+
+
+def biv_grad_norm_workspace(chunks: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().biv_grad_norm_workspace(chunks, C.byref(n)), "biv_grad_norm_workspace")
+    return n.value
+
+
+def biv_grad_norm(table, n: int, chunks: int, max_norm, out, ws, stream=None):
+    """table: device copy (uint8) of n planned OptTensors; out float32 [2]."""
+    _check(load().biv_grad_norm(_p(table), n, chunks, float(max_norm), _p(out), _p(ws), ws.numel(),
+                                _stream(stream)), "biv_grad_norm")
+
+
+def biv_adamw(desc: AdamWDesc, stream=None):
+    _check(load().biv_adamw(C.byref(desc), _stream(stream)), "biv_adamw")
