@@ -618,7 +618,7 @@ typedef struct {
   int adv_per_row;
   float clip_lo, clip_hi;    /* 0 <= clip_lo <= 1, 0 <= clip_hi */
   float dual_clip;           /* 0: off; else > 1 */
-  float kl_coef, ent_coef;
+  float kl_coef, ent_coef;   /* in [-1000, 1000] */
   int reduce;                /* biv_loss_reduce */
   float norm;                /* SUM only: > 0 */
   float* stats;              /* [8] */
@@ -640,11 +640,13 @@ biv_status biv_policy_loss(const biv_policy_desc* desc, const float* lp, float* 
  * lp, entropy float32 [T]; dz [T, V] rows at ldz (dz_dtype BIV_F32 or
  * BIV_BF16, one rounding; NULL: no gradient).  dz may be z itself (same
  * pointer, type and stride), and must not overlap it otherwise.  A logit of
- * -inf has p = 0 and dz = 0 (a row with no finite logit gives NaN).  A counted
+ * -1e30 or less (-inf, a type's lowest value) is masked: p = 0 and dz = 0; a
+ * row of masked logits alone gives NaN, as a NaN or +inf among them does.  A counted
  * row whose target is outside [0, V) gives lp = NaN and the device error code
- * 2.  Each row's bits depend on V and the row only: 1024-logit groups are
- * reduced to (max, sum, entropy sum) by one warp and merged in one order,
- * however the row is spread over CTAs.  1 <= V <= 262144.  Rows that keep 16
+ * 2.  Each row's bits depend on V and the row only: 4 KB groups of logits
+ * are reduced to (max, sum, entropy sum) by one warp and merged in one order,
+ * however the row is spread over CTAs.  1 <= V <= 262144, 0.01 <= inv_temp <=
+ * 100.  Rows that keep 16
  * bytes' alignment load and store fastest; any element alignment works. */
 biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, int64_t ld,
                                   int z_dtype, const int32_t* target, int V, float inv_temp,

@@ -344,19 +344,22 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------- logits --
-// A cluster of CTAs holds one row of logits in shared memory, 1024 logits
-// (one group) per buffer; each warp owns its groups' buffers and their
-// mbarriers.  Per row: a warp reduces each group to (max, sum, entropy sum)
-// as it arrives and writes the triple to every CTA of the cluster; after one
-// cluster barrier each warp merges all groups, forms the token's gradient and
-// writes its groups' dz straight from shared memory, refilling each buffer
-// with the next row's logits as soon as it is done with it.  So logits are
-// read once, dz is written once, and the next row streams in while this one is
-// written.  A group's arithmetic and the merge order do not depend on the
-// cluster size.
-constexpr int kGroup = 1024;
-constexpr int kMaxWarps = 20;
+// A cluster of CTAs holds one row of logits in shared memory, 4 KB (one group:
+// 1024 FP32 or 2048 bf16 logits) per buffer; each warp owns a ring of buffers
+// for its groups of all rows.  Per row: a warp reduces each group, as it
+// arrives, to (max, sum, entropy sum) and writes the triple to every CTA of the
+// cluster; after one cluster barrier each warp merges all groups, forms the
+// token's gradient and writes its groups' dz from shared memory, handing each
+// buffer to the next group to be loaded.  Logits are read once, dz is written
+// once, and the next rows stream in while this one is reduced and written.  A
+// group's arithmetic and the merge order do not depend on the cluster size.
+constexpr int kGroupBytes = 4096;
+constexpr int kMaxWarps = 16;
 constexpr int kMaxV = 262144;
+constexpr int kMaxMerge = kMaxV * 4 / kGroupBytes / 32;   // groups per lane of the merge
+// Logits of kMasked or less are masked: what a mask of -inf or of the type's
+// lowest value leaves has p = 0.
+constexpr float kMasked = -1e30f;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -369,281 +372,580 @@ struct LogitsArgs {
   const void* z;
   int64_t ld;
   const int32_t* target;
-  int V, G, gpc;            // groups of a row, groups per CTA
+  int V, G, gpc, slots;     // groups of a row, groups per CTA, buffers per warp
   float it, c;              // 1 / temperature, and that times log2(e)
   float* lp;
   float* ent;
   void* dz;
   int64_t ldz;
-  int dz_vec;               // dz rows keep 4 elements' alignment
 };
 
-// one group of a row from shared memory (SHIFT: its elements are aligned to
-// their own size only)
-template <bool ZB, bool SHIFT>
-__device__ __forceinline__ void read_group(const uint8_t* buf, int lane, float (&x)[32]) {
+// two FP32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// two FP32 values rounded to bf16 by one conversion (two single ones go through
+// the unit that also serves the exponentials)
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// max that gives NaN where either is one
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max_keep_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A lane's logits of a group are 8 runs of 16 bytes: run j starts at element
+// (32 j + lane) RUN.  One run as pairs of FP32.
+template <bool ZB>
+struct Run {
+  static constexpr int RUN = ZB ? 8 : 4;
+  uint4 v;
+  __device__ __forceinline__ Run(const uint8_t* buf, int j, int lane)
+      : v(reinterpret_cast<const uint4*>(buf)[j * 32 + lane]) {}
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (ZB) return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+};
+
+// largest logit of the group, over the warp
+template <bool ZB>
+__device__ __forceinline__ float group_max(const uint8_t* buf, int lane) {
+  float m;
+  if constexpr (ZB) {
+    uint32_t a = 0, b = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 v = reinterpret_cast<const uint4*>(buf)[j * 32 + lane];
+      if (j == 0) {
+        a = max_bf16x2_nan(v.x, v.y);
+        b = max_bf16x2_nan(v.z, v.w);
+      } else {
+        a = max_bf16x2_nan(a, max_bf16x2_nan(v.x, v.y));
+        b = max_bf16x2_nan(b, max_bf16x2_nan(v.z, v.w));
+      }
+    }
+    a = max_bf16x2_nan(a, b);
+    m = fmax_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+  } else {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 v = reinterpret_cast<const float4*>(buf)[j * 32 + lane];
+      a = fmax3_nan(a, v.x, v.y);
+      b = fmax3_nan(b, v.z, v.w);
+    }
+    m = fmax_nan(a, b);
+  }
+  return warp_max_keep_nan(m);
+}
+
+// sums over the group's 2^y and 2^y y, y = x c - mc, over the warp
+template <bool ZB>
+__device__ __forceinline__ void group_sums(const uint8_t* buf, int lane, float c, float mc, float& s,
+                                           float& t) {
+  const uint64_t c2 = pack2(c, c), n2 = pack2(-mc, -mc);
+  uint64_t sa = 0, sb = 0, ta = 0, tb = 0;
+#pragma unroll 4
+  for (int j = 0; j < 8; ++j) {
+    const Run<ZB> r(buf, j, lane);
+#pragma unroll
+    for (int i = 0; i < Run<ZB>::RUN / 2; ++i) {
+      const uint64_t y2 = fma2(r.pair(i), c2, n2);
+      float y0, y1;
+      unpack2(y2, y0, y1);
+      const uint64_t e2 = pack2(ex2f(y0), ex2f(y1));
+      if (i & 1) {
+        sb = add2(sb, e2);
+        tb = fma2(e2, y2, tb);
+      } else {
+        sa = add2(sa, e2);
+        ta = fma2(e2, y2, ta);
+      }
+    }
+  }
+  float s0, s1, t0, t1;
+  unpack2(add2(sa, sb), s0, s1);
+  unpack2(add2(ta, tb), t0, t1);
+  s = warp_sum_x(s0 + s1);
+  t = warp_sum_x(t0 + t1);
+}
+
+// every logit of the group at least kMasked (a NaN stays)
+template <bool ZB>
+__device__ __forceinline__ void clamp_group(uint8_t* buf, int lane) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int e = j * 128 + lane * 4;
-    if constexpr (ZB) {
-      uint32_t w0, w1;
-      if constexpr (SHIFT) {
-        const uint16_t* p = reinterpret_cast<const uint16_t*>(buf) + e;
-        w0 = p[0] | (uint32_t(p[1]) << 16);
-        w1 = p[2] | (uint32_t(p[3]) << 16);
-      } else {
-        const uint2 r = *reinterpret_cast<const uint2*>(buf + e * 2);
-        w0 = r.x; w1 = r.y;
-      }
-      x[4 * j] = __uint_as_float(w0 << 16);
-      x[4 * j + 1] = __uint_as_float(w0 & 0xFFFF0000u);
-      x[4 * j + 2] = __uint_as_float(w1 << 16);
-      x[4 * j + 3] = __uint_as_float(w1 & 0xFFFF0000u);
-    } else if constexpr (SHIFT) {
-      const float* p = reinterpret_cast<const float*>(buf) + e;
+    uint4* p = reinterpret_cast<uint4*>(buf) + j * 32 + lane;
+    uint4 v = *p;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[4 * j + i] = p[i];
-    } else {
-      const float4 r = *reinterpret_cast<const float4*>(buf + e * 4);
-      x[4 * j] = r.x; x[4 * j + 1] = r.y; x[4 * j + 2] = r.z; x[4 * j + 3] = r.w;
+    for (int i = 0; i < 4; ++i)   // (for bf16 the next value below kMasked, twice)
+      w[i] = ZB ? max_bf16x2_nan(w[i], 0xF14AF14Au)
+                : __float_as_uint(fmax_nan(__uint_as_float(w[i]), kMasked));
+    *p = v;
+  }
+}
+
+// 16 bytes from WS words (and, where `half`, another half word) behind the
+// start of a 16-byte unit on
+template <int WS>
+__device__ __forceinline__ uint4 unaligned_unit(const uint4* p, bool half) {
+  const uint4 a = p[0], b = p[1];
+  const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = half ? __funnelshift_r(v[i + WS], v[i + WS + 1], 16) : v[i + WS];
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// Bring a group that starts `off` bytes into its buffer (a row that is not
+// 16-byte aligned) to the buffer's start, and mask what lies behind `left`
+// logits.
+template <int WS, bool ZB>
+__device__ __forceinline__ void settle(uint8_t* buf, int lane, bool half, int left) {
+  uint4 r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r[j] = unaligned_unit<WS>(reinterpret_cast<const uint4*>(buf) + j * 32 + lane, ZB && half);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(buf)[j * 32 + lane] = r[j];
+}
+template <bool ZB, bool SHIFT>
+__device__ __forceinline__ void settle_group(uint8_t* buf, int lane, int off, int left) {
+  __syncwarp();
+  if (SHIFT && off) {
+    const bool half = (off & 2) != 0;
+    switch (off >> 2) {
+      case 0: settle<0, ZB>(buf, lane, half, left); break;
+      case 1: settle<1, ZB>(buf, lane, half, left); break;
+      case 2: settle<2, ZB>(buf, lane, half, left); break;
+      default: settle<3, ZB>(buf, lane, half, left);
     }
+    __syncwarp();
+  }
+  for (int e = left + lane; e < kGroupBytes / (ZB ? 2 : 4); e += 32) {
+    if (ZB) reinterpret_cast<uint16_t*>(buf)[e] = 0xF14A;
+    else reinterpret_cast<float*>(buf)[e] = kMasked;
+  }
+  __syncwarp();
+}
+
+// Copy a group's results (`left` of DS bytes, from the start of its buffer) to a
+// row of any alignment: whole 16-byte units of the destination, put together
+// from two of the buffer's; the first and last elements, which share their unit
+// with a neighbour, one by one.
+template <int DS>
+__device__ __forceinline__ void store_unaligned(uint8_t* dst, const uint8_t* buf, int lane, int left) {
+  const int off = int(reinterpret_cast<uintptr_t>(dst) & 15);
+  uint4* unit = reinterpret_cast<uint4*>(dst - off);
+  const uint4* src = reinterpret_cast<const uint4*>(buf);
+  const int u0 = off ? 1 : 0, u1 = (off + left * DS) >> 4;
+  const bool half = DS == 2 && (off & 2) != 0;
+  switch ((16 - off) >> 2) {
+    case 0: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<0>(src + u - 1, half); break;
+    case 1: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<1>(src + u - 1, half); break;
+    case 2: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<2>(src + u - 1, half); break;
+    case 3: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<3>(src + u - 1, half); break;
+    default: for (int u = lane; u < u1; u += 32) unit[u] = src[u];
+  }
+  const int head = off ? min(left, (16 - off) / DS) : 0;    // elements before unit u0
+  const int tail0 = max(head, (u1 * 16 - off) / DS);
+  const int e = lane < 16 ? lane : tail0 + lane - 16;
+  if (lane < 16 ? e < head : e < left) {
+    if (DS == 2) reinterpret_cast<uint16_t*>(dst)[e] = reinterpret_cast<const uint16_t*>(buf)[e];
+    else reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(buf)[e];
+  }
+}
+
+// `bytes` zeros (elements of `ds` bytes) from d on, by a warp
+__device__ __forceinline__ void zero_fill(uint8_t* d, int bytes, int ds, int lane) {
+  const int head = min(bytes, int(-reinterpret_cast<uintptr_t>(d) & 15));
+  const int units = (bytes - head) >> 4;
+  uint4* u = reinterpret_cast<uint4*>(d + head);
+#pragma unroll 4
+  for (int i = lane; i < units; i += 32) u[i] = make_uint4(0, 0, 0, 0);
+  // the first and last elements, which share their 16 bytes with others
+  for (int i = lane * ds; i < head; i += 32 * ds) {
+    if (ds == 2) *reinterpret_cast<uint16_t*>(d + i) = 0;
+    else *reinterpret_cast<float*>(d + i) = 0.f;
+  }
+  for (int i = head + units * 16 + lane * ds; i < bytes; i += 32 * ds) {
+    if (ds == 2) *reinterpret_cast<uint16_t*>(d + i) = 0;
+    else *reinterpret_cast<float*>(d + i) = 0.f;
   }
 }
 
 template <bool ZB, bool DB, bool SHIFT>
-__global__ void __launch_bounds__(kMaxWarps * 32) policy_logits_kernel(
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     const __grid_constant__ LogitsArgs a) {
-  constexpr int ES = ZB ? 2 : 4;
-  constexpr int GB = kGroup * ES;
-  constexpr int BUF = GB + (SHIFT ? 16 : 0);
+  constexpr int ES = ZB ? 2 : 4, DS = DB ? 2 : 4, RUN = Run<ZB>::RUN;
+  constexpr int kGroup = kGroupBytes / ES;
+  constexpr int BUF = kGroupBytes + (SHIFT ? 16 : 0);
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* bufs = smem;
-  float4* stats = reinterpret_cast<float4*>(smem + size_t(a.gpc) * BUF);   // [2][G]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * a.G);           // [gpc]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+  uint8_t* bufs = smem + size_t(warp) * a.slots * BUF;                          // this warp's ring
+  float4* stats = reinterpret_cast<float4*>(smem + size_t(nw) * a.slots * BUF); // [2][G]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + 2 * a.G) + warp * a.slots;
   uint32_t ncta;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ncta));
   const int rank = int(cluster_rank());
   const int clusters = int(gridDim.x / ncta), me = int(blockIdx.x / ncta);
-  const int g0 = rank * a.gpc, mine = max(0, min(a.gpc, a.G - g0));
+  const int g0 = rank * a.gpc, mine = max(0, min(a.gpc, a.G - g0));   // this CTA's groups
+  const int per = warp < mine ? (mine - warp - 1) / nw + 1 : 0;       // of these, this warp's
 
-  if (tid == 0) {
-    for (int i = 0; i < a.gpc; ++i) mbar_init(smem_u32(bars + i), 1);
+  if (lane == 0) {
+    for (int i = 0; i < a.slots; ++i) mbar_init(smem_u32(bars + i), 1);
     fence_barrier_init();
   }
   pdl_wait();
   pdl_trigger();
   cluster_sync();
 
-  auto counted = [&](int r) { return a.p.ws.row[r].x > 0.f; };
-  auto next_row = [&](int r) {
-    while (r < a.p.T && !counted(r)) r += clusters;
-    return r;
+  // The cluster's rows are me + q clusters, q < rows.  Lane l holds what the
+  // token's gradient needs of row 32 win + l (and its target's logit); a bit
+  // per row says whether it counts.
+  const int rows = me < a.p.T ? (a.p.T - 1 - me) / clusters + 1 : 0;
+  auto row_of = [&](int q) { return me + q * clusters; };
+  auto row_ptr = [&](int q) {
+    return static_cast<const uint8_t*>(a.z) + int64_t(row_of(q)) * a.ld * ES;
   };
-  auto row_ptr = [&](int r) { return static_cast<const uint8_t*>(a.z) + int64_t(r) * a.ld * ES; };
-  // start the copy of this CTA's group i of row r: the 16-byte units that lie
-  // in the row; what is left of the row's first and last unit is read later
-  auto load_group = [&](int r, int i) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(row_ptr(r)), e = b + size_t(a.V) * ES;
-    const uintptr_t gb = b + size_t(g0 + i) * GB;
-    const uintptr_t ge = min(gb + GB, e);
-    uintptr_t lo = gb & ~uintptr_t(15), hi = (ge + 15) & ~uintptr_t(15);
-    if (lo < b) lo += 16;
-    if (hi > e) hi -= 16;
-    uint8_t* dst = bufs + size_t(i) * BUF + (lo - (gb & ~uintptr_t(15)));
-    const uint32_t bar = smem_u32(bars + i);
-    const uint32_t bytes = hi > lo ? uint32_t(hi - lo) : 0u;
-    mbar_expect_tx(bar, bytes);
-    if (bytes) bulk_load(smem_u32(dst), reinterpret_cast<const void*>(lo), bytes, bar);
+  auto counted = [&](int w) {
+    const int q = w * 32 + lane;
+    return __ballot_sync(0xffffffffu, q < rows && a.p.ws.row[row_of(q)].x > 0.f);
+  };
+  int win = 0;
+  uint32_t on0 = counted(0), on1 = counted(1);      // windows win and win + 1
+  float2 m_wa;
+  int m_tg;
+  float m_old, m_ref, m_zt;
+  auto load_window = [&]() {
+    const int q = win * 32 + lane;
+    m_wa = make_float2(0.f, 0.f);
+    m_tg = -1;
+    m_old = m_ref = m_zt = 0.f;
+    if ((on0 >> lane) & 1u) {
+      const int r = row_of(q);
+      m_wa = a.p.ws.row[r];
+      m_tg = a.target[r];
+      if (a.p.old_lp) m_old = a.p.old_lp[r];
+      if (a.p.ref_lp) m_ref = a.p.ref_lp[r];
+      if (m_tg >= 0 && m_tg < a.V) {
+        if (ZB) m_zt = bf2f(reinterpret_cast<const uint16_t*>(row_ptr(q))[m_tg]);
+        else m_zt = reinterpret_cast<const float*>(row_ptr(q))[m_tg];
+      }
+    }
+  };
+  load_window();
+  // the first row from q on that counts (rows: none)
+  auto next_counted = [&](int q) {
+    while (q < rows) {
+      const int w = q >> 5;
+      const uint32_t bits = (w == win ? on0 : w == win + 1 ? on1 : counted(w)) >> (q & 31);
+      if (bits) return q + __ffs(int(bits)) - 1;
+      q = (w + 1) << 5;
+    }
+    return rows;
   };
 
-  int row = me;
-  int ahead = next_row(me);      // the counted row whose loads are in flight
-  if (ahead < a.p.T && lane == 0)
-    for (int i = warp; i < mine; i += nw) load_group(ahead, i);
+  // A warp's groups of all its rows form one sequence, n = 0, 1, ...; group n
+  // sits in slot n % slots, and is loaded when group n - slots is done with
+  // (at most two rows ahead).
+  const uint32_t slots = uint32_t(min(a.slots, 2 * per));
+  // q0: the row whose dz is written; q1: the one that is reduced
+  int q0 = -1, q1 = next_counted(0), q2 = next_counted(q1 + 1), q3 = next_counted(q2 + 1);
+  int ahead = 1, ai = 0;           // next group to load: the ai-th of row q<ahead>
+  // starts the copy of that group: the 16-byte units that lie in the row; what
+  // is left of the row's first and last unit is read later
+  auto load_next = [&](uint32_t slot) {
+    const int q = ahead == 1 ? q1 : ahead == 2 ? q2 : q3;
+    if (q < rows && lane == 0) {
+      const uint32_t bar = smem_u32(bars + slot), dst = smem_u32(bufs + slot * BUF);
+      const int g = g0 + warp + ai * nw;
+      const uint8_t* gp = row_ptr(q) + size_t(g) * kGroupBytes;
+      if (!SHIFT) {
+        const uint32_t bytes = uint32_t(min(kGroup, a.V - g * kGroup) * ES) & ~15u;
+        mbar_expect_tx(bar, bytes);
+        if (bytes) bulk_load(dst, gp, bytes, bar);
+      } else {
+        const uintptr_t gb = reinterpret_cast<uintptr_t>(gp), b = gb - size_t(g) * kGroupBytes;
+        const uintptr_t e = b + size_t(a.V) * ES, ge = min(gb + kGroupBytes, e);
+        uintptr_t lo = gb & ~uintptr_t(15), hi = (ge + 15) & ~uintptr_t(15);
+        if (lo < b) lo += 16;
+        if (hi > e) hi -= 16;
+        const uint32_t bytes = hi > lo ? uint32_t(hi - lo) : 0u;
+        mbar_expect_tx(bar, bytes);
+        if (bytes)
+          bulk_load(dst + uint32_t(lo - (gb & ~uintptr_t(15))), reinterpret_cast<const void*>(lo), bytes, bar);
+      }
+    }
+    if (++ai == per) {
+      ai = 0;
+      ++ahead;
+    }
+  };
+  for (uint32_t i = 0; i < slots; ++i) load_next(i);
   __syncwarp();
-  uint32_t phase = 0;
-  for (; row < a.p.T; row += clusters) {
-    if (row != ahead) {          // a row that does not count: zeros
-      if (a.dz) {
-        for (int i = warp; i < mine; i += nw)
-          for (int j = lane; j < kGroup && (g0 + i) * kGroup + j < a.V; j += 32) {
-            const int64_t at = int64_t(row) * a.ldz + (g0 + i) * kGroup + j;
-            if (DB) static_cast<uint16_t*>(a.dz)[at] = 0;
-            else static_cast<float*>(a.dz)[at] = 0.f;
+  uint32_t slot0 = 0;              // of row q0's next group
+  uint32_t slot1 = 0, phase1 = 0;  // of row q1's next group
+  uint32_t dirty = 0;              // slots (mod 32) this warp has written to
+  uint32_t flip = 0;
+  // of row q0, where there is one
+  float M = 0.f, a0 = 0.f, a1 = 0.f, at_target = 0.f, zt = 0.f;
+  int tg0 = -1;
+  while (true) {
+    // ---- row q0: dz = p (a0 + a1 y) (+ at_target), y = log2 of p S
+    if (q0 >= 0) {
+      uint8_t* row = static_cast<uint8_t*>(a.dz) + int64_t(row_of(q0)) * a.ldz * DS;
+      for (int i = 0; i < per; ++i) {
+        const int g = g0 + warp + i * nw;
+        if (a.dz) {
+          const int left = min(kGroup, a.V - g * kGroup);
+          uint8_t* buf = bufs + slot0 * BUF;
+          uint8_t* dst = row + int64_t(g) * kGroup * DS;
+          const uint64_t c2 = pack2(a.c, a.c), n2 = pack2(-M, -M);
+          const uint64_t p0 = pack2(a0, a0), p1 = pack2(a1, a1);
+          const bool ent = a1 != 0.f;
+          float at = 0.f;              // dz at the target
+          const int tl = tg0 - g * kGroup;
+          if (tl >= 0 && tl < kGroup) {
+            const float y = fmaf(zt, a.c, -M), e = ex2f(y);
+            at = fmaf(e, a0, ent ? e * fmaxf(y, kMasked) * a1 : 0.f) + at_target;
           }
+#pragma unroll 4
+          for (int j = 0; j < 8; ++j) {
+            const Run<ZB> r(buf, j, lane);
+            float x[RUN];
+#pragma unroll
+            for (int k = 0; k < RUN / 2; ++k) {
+              const uint64_t y2 = fma2(r.pair(k), c2, n2);
+              float y0, y1;
+              unpack2(y2, y0, y1);
+              const uint64_t e2 = pack2(ex2f(y0), ex2f(y1));
+              // (e y first: with e = 0 and y far below, y a1 may overflow)
+              const uint64_t ea = mul2(e2, p0);
+              unpack2(ent ? fma2(mul2(e2, y2), p1, ea) : ea, x[2 * k], x[2 * k + 1]);
+            }
+            const int el = (j * 32 + lane) * RUN;
+            if (SHIFT && DS <= ES) {
+              // results take their logits' place in the buffer
+              if (DS < ES) __syncwarp();
+              if constexpr (DB) {
+                uint32_t h[RUN / 2];
+#pragma unroll
+                for (int k = 0; k < RUN / 2; ++k) h[k] = cvt_bf16x2(x[2 * k], x[2 * k + 1]);
+                if constexpr (RUN == 8) *reinterpret_cast<uint4*>(buf + el * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+                else *reinterpret_cast<uint2*>(buf + el * 2) = make_uint2(h[0], h[1]);
+              } else {
+                *reinterpret_cast<float4*>(buf + el * 4) = make_float4(x[0], x[1], x[2], x[3]);
+              }
+            } else if (!SHIFT && el + RUN <= left) {
+              if constexpr (DB) {
+                uint32_t h[RUN / 2];
+#pragma unroll
+                for (int k = 0; k < RUN / 2; ++k) h[k] = cvt_bf16x2(x[2 * k], x[2 * k + 1]);
+                if constexpr (RUN == 8) *reinterpret_cast<uint4*>(dst + el * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+                else *reinterpret_cast<uint2*>(dst + el * 2) = make_uint2(h[0], h[1]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < RUN; k += 4)
+                  *reinterpret_cast<float4*>(dst + (el + k) * 4) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < RUN; ++k)
+                if (el + k < left) {
+                  if (DB) reinterpret_cast<uint16_t*>(dst)[el + k] = f2bf(x[k]);
+                  else reinterpret_cast<float*>(dst)[el + k] = x[k];
+                }
+            }
+          }
+          // the target's element again, by the lane that wrote it
+          if (tl >= 0 && tl < kGroup && ((tl / RUN) & 31) == lane) {
+            uint8_t* d = (SHIFT && DS <= ES ? buf : dst) + tl * DS;
+            if (DB) *reinterpret_cast<uint16_t*>(d) = f2bf(at);
+            else *reinterpret_cast<float*>(d) = at;
+          }
+          if (SHIFT && DS <= ES) {
+            __syncwarp();
+            store_unaligned<DS>(dst, buf, lane, left);
+            dirty |= 1u << (slot0 & 31);
+          }
+        }
+        // the warp's reads of the buffer are done (their values were used);
+        // what it wrote there is ordered before the copy that comes next
+        if ((dirty >> (slot0 & 31)) & 1u) fence_proxy_async();
+        dirty &= ~(1u << (slot0 & 31));
+        __syncwarp();
+        load_next(slot0);
+        if (++slot0 == slots) slot0 = 0;
+      }
+    }
+    // rows that do not count, up to q1 (all that are left: q1 = rows): zeros
+    for (int q = q0 + 1; q < q1; ++q) {
+      if (a.dz) {
+        uint8_t* row = static_cast<uint8_t*>(a.dz) + int64_t(row_of(q)) * a.ldz * DS;
+        for (int i = 0; i < per; ++i) {
+          const int g = g0 + warp + i * nw;
+          zero_fill(row + int64_t(g) * kGroup * DS, min(kGroup, a.V - g * kGroup) * DS, DS, lane);
+        }
       }
       if (rank == 0 && tid == 0) {
-        a.lp[row] = 0.f;
-        a.ent[row] = 0.f;
+        a.lp[row_of(q)] = 0.f;
+        a.ent[row_of(q)] = 0.f;
       }
-      continue;
     }
-    const int nxt = next_row(row + clusters);
-    const float2 wa = a.p.ws.row[row];
-    const int tg = a.target[row];
-    const float old = a.p.old_lp ? a.p.old_lp[row] : 0.f, ref = a.p.ref_lp ? a.p.ref_lp[row] : 0.f;
-    const bool tg_ok = tg >= 0 && tg < a.V;
-    float zt = 0.f;
-    if (tg_ok) {
-      if (ZB) zt = bf2f(reinterpret_cast<const uint16_t*>(row_ptr(row))[tg]);
-      else zt = reinterpret_cast<const float*>(row_ptr(row))[tg];
+    if (q1 >= rows) break;
+    __syncwarp();
+    while ((q1 >> 5) != win) {     // the next window of rows
+      ++win;
+      on0 = on1;
+      on1 = counted(win + 1);
+      if ((q1 >> 5) == win) load_window();
     }
-    const int off = SHIFT ? int(reinterpret_cast<uintptr_t>(row_ptr(row)) & 15) : 0;
-    float4* st = stats + (phase & 1) * a.G;
-
-    // ---- each group: (max, sum, entropy sum) relative to its own max
-    for (int i = warp; i < mine; i += nw) {
-      const int g = g0 + i;
-      uint8_t* buf = bufs + size_t(i) * BUF + off;
-      mbar_wait(smem_u32(bars + i), phase & 1, a.p.err);
+    // ---- row q1: each group's (max, sum, entropy sum), relative to its own max
+    const uint8_t* src = row_ptr(q1);
+    const int off = SHIFT ? int(reinterpret_cast<uintptr_t>(src) & 15) : 0;
+    float4* st = stats + flip * a.G;
+    for (int i = 0; i < per; ++i) {
+      const int g = g0 + warp + i * nw;
       const int left = min(kGroup, a.V - g * kGroup);
-      if (g * kGroup + left + 16 / ES > a.V || (SHIFT && g == 0)) {
+      uint8_t* buf = bufs + slot1 * BUF;
+      mbar_wait(smem_u32(bars + slot1), phase1, a.p.err);
+      if ((SHIFT && off) || left < kGroup) {
         // elements of the row's first and last 16-byte unit, where it holds
         // bytes outside the row: not part of any copy
-        const uint8_t* src = row_ptr(row);
-        const uintptr_t b = reinterpret_cast<uintptr_t>(src), e = b + size_t(a.V) * ES;
-        auto fetch = [&](int idx) {
-          uint8_t* d = buf + (idx - g * kGroup) * ES;
-          if (ZB) *reinterpret_cast<uint16_t*>(d) = reinterpret_cast<const uint16_t*>(src)[idx];
-          else *reinterpret_cast<float*>(d) = reinterpret_cast<const float*>(src)[idx];
-        };
-        if (lane < 16 / ES) {
-          const int tail = a.V - 1 - lane;
-          if (tail >= g * kGroup && tail < g * kGroup + left && b + size_t(tail) * ES >= (e & ~uintptr_t(15)))
-            fetch(tail);
-          if (SHIFT && g == 0 && lane < left && (b & 15) && (b & 15) + lane * ES < 16) fetch(lane);
+        if (g * kGroup + left + 16 / ES > a.V || (SHIFT && g == 0)) {
+          const uintptr_t b = reinterpret_cast<uintptr_t>(src), e = b + size_t(a.V) * ES;
+          auto fetch = [&](int idx) {
+            uint8_t* d = buf + off + (idx - g * kGroup) * ES;
+            if (ZB) *reinterpret_cast<uint16_t*>(d) = reinterpret_cast<const uint16_t*>(src)[idx];
+            else *reinterpret_cast<float*>(d) = reinterpret_cast<const float*>(src)[idx];
+          };
+          if (lane < 16 / ES) {
+            const int tail = a.V - 1 - lane;
+            if (tail >= g * kGroup && tail < g * kGroup + left &&
+                b + size_t(tail) * ES >= (e & ~uintptr_t(15)))
+              fetch(tail);
+            if (SHIFT && g == 0 && lane < left && (b & 15) && (b & 15) + lane * ES < 16) fetch(lane);
+          }
         }
+        settle_group<ZB, SHIFT>(buf, lane, off, left);
+        dirty |= 1u << (slot1 & 31);
+      }
+      const float m = group_max<ZB>(buf, lane);
+      float mc = -INFINITY, s = 0.f, t = 0.f;
+      if (!(m <= kMasked)) {         // (a NaN comes through)
+        mc = m * a.c;
+        group_sums<ZB>(buf, lane, a.c, mc, s, t);
+      }
+      // masked logits among the others (0 times an exponent of -inf), or alone:
+      // clamped once, for these sums and for dz
+      if (t != t || m <= kMasked) {
         __syncwarp();
-      }
-      float x[32];
-      read_group<ZB, SHIFT>(buf, lane, x);
-      if (left < kGroup) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if ((j >> 2) * 128 + lane * 4 + (j & 3) >= left) x[j] = -INFINITY;
-      }
-      float m = x[0];
-#pragma unroll
-      for (int j = 1; j < 32; ++j) m = fmaxf(m, x[j]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float mc = m * a.c;
-      float s = 0.f, t = 0.f;
-      if (m > -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float y = fmaf(x[j], a.c, -mc);
-          const float e = ex2f(y);
-          s += e;
-          t = fmaf(e, y < -1000.f ? 0.f : y, t);
-        }
-        s = warp_sum_x(s);
-        t = warp_sum_x(t);
-      } else {
-        bool bad = false;          // only -inf, or NaN among it
-#pragma unroll
-        for (int j = 0; j < 32; ++j) bad |= x[j] != x[j];
-        if (__any_sync(0xffffffffu, bad)) s = t = NAN;
+        clamp_group<ZB>(buf, lane);
+        __syncwarp();
+        dirty |= 1u << (slot1 & 31);
+        if (t != t) group_sums<ZB>(buf, lane, a.c, mc, s, t);
       }
       if (lane < ncta) st_cluster_v4(smem_u32(st + g), lane, mc, s, t, 0.f);
+      if (++slot1 == slots) {
+        slot1 = 0;
+        phase1 ^= 1;
+      }
     }
     cluster_sync();
 
-    // ---- merge: lane l takes groups l, l + 32, ... in order
-    float M = -INFINITY;
-    for (int g = lane; g < a.G; g += 32) M = fmaxf(M, st[g].x);
-    __syncwarp();
+    // ---- merge row q1's groups: lane l takes groups l, l + 32, ... in order
+    float4 q[kMaxMerge];
+    M = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float S = 0.f, U = 0.f;
-    for (int g = lane; g < a.G; g += 32) {
-      const float4 q = st[g];
-      if (q.x == -INFINITY) {
-        S += q.y;                  // 0, or the NaN of a group without a number
-      } else {
-        const float d = q.x - M, f = ex2f(d);
-        S = fmaf(q.y, f, S);
-        U = fmaf(f, fmaf(q.y, fmaxf(d, -1000.f), q.z), U);
-      }
+    for (int k = 0; k < kMaxMerge; ++k) {
+      const int g = k * 32 + lane;
+      q[k] = g < a.G ? st[g] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      M = fmax_nan(M, q[k].x);
     }
-    __syncwarp();
+    M = warp_max_keep_nan(M);
+    float S = 0.f, U = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxMerge; ++k) {
+      // a group of masked logits alone (M may be -inf too) adds nothing
+      const bool has = q[k].x != -INFINITY;
+      const float d = q[k].x - M, f = ex2f(d);
+      S = has ? fmaf(q[k].y, f, S) : S;
+      U = has ? fmaf(f, fmaf(q[k].y, d, q[k].z), U) : U;
+    }
     S = warp_sum_x(S);
     U = warp_sum_x(U);
-    if (M == -INFINITY) S = NAN;   // no finite logit
+    if (M == -INFINITY) S = NAN;   // nothing but masked logits
     constexpr float kLn2 = 0.6931471805599453f;
     const float lnS = logf(S);
     const float H = lnS - kLn2 * (U / S);
+    const int from = q1 & 31;
+    tg0 = __shfl_sync(0xffffffffu, m_tg, from);
+    zt = __shfl_sync(0xffffffffu, m_zt, from);
+    const bool tg_ok = tg0 >= 0 && tg0 < a.V;
     const float lp = tg_ok ? fmaf(zt, a.c, -M) * kLn2 - lnS : NAN;
     if (rank == 0 && tid == 0) {
-      a.lp[row] = lp;
-      a.ent[row] = H;
+      a.lp[row_of(q1)] = lp;
+      a.ent[row_of(q1)] = H;
       if (!tg_ok) raise_error(a.p.err, kErrBadIndex);
     }
-
-    // ---- dz = p (a0 + a1 y) (+ it dlp at the target), y = log2 of p S
-    float a0 = 0.f, a1 = 0.f, at_target = 0.f;
     if (a.dz) {
-      const Token o = policy_token(a.p, lp, wa.y, old, ref);
-      const float dlp = wa.x * o.dlp, wg = wa.x * a.p.gamma, is = a.it / S;
+      const float wt = __shfl_sync(0xffffffffu, m_wa.x, from), A = __shfl_sync(0xffffffffu, m_wa.y, from);
+      const float old = __shfl_sync(0xffffffffu, m_old, from), ref = __shfl_sync(0xffffffffu, m_ref, from);
+      const Token o = policy_token(a.p, lp, A, old, ref);
+      const float dlp = wt * o.dlp, wg = wt * a.p.gamma, is = a.it / S;
       a0 = is * (wg * (H - lnS) - dlp);
       a1 = is * wg * kLn2;
       at_target = a.it * dlp;
     }
-    for (int i = warp; i < mine; i += nw) {
-      const int g = g0 + i;
-      if (a.dz) {
-        uint8_t* buf = bufs + size_t(i) * BUF + off;
-        const int left = min(kGroup, a.V - g * kGroup);
-        float x[32];
-        read_group<ZB, SHIFT>(buf, lane, x);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float y = fmaf(x[j], a.c, -M);
-          const float e = ex2f(y);
-          x[j] = e * fmaf(a1, y < -1000.f ? 0.f : y, a0);
-        }
-        const int tl = tg - g * kGroup;     // the target inside this group
-        if (tl >= 0 && tl < kGroup && ((tl >> 2) & 31) == lane) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if ((j >> 2) * 128 + lane * 4 + (j & 3) == tl) x[j] += at_target;
-        }
-        const int64_t base = int64_t(row) * a.ldz + g * kGroup;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = j * 128 + lane * 4;
-          if (DB) {
-            uint16_t* d = static_cast<uint16_t*>(a.dz) + base + e;
-            if (a.dz_vec && e + 4 <= left) {
-              *reinterpret_cast<uint2*>(d) =
-                  make_uint2(pack_bf2(x[4 * j], x[4 * j + 1]), pack_bf2(x[4 * j + 2], x[4 * j + 3]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (e + k < left) d[k] = f2bf(x[4 * j + k]);
-            }
-          } else {
-            float* d = static_cast<float*>(a.dz) + base + e;
-            if (a.dz_vec && e + 4 <= left) {
-              *reinterpret_cast<float4*>(d) = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (e + k < left) d[k] = x[4 * j + k];
-            }
-          }
-        }
-      }
-      if (nxt < a.p.T) {
-        fence_proxy_async();       // this warp's accesses to the buffer come first
-        __syncwarp();
-        if (lane == 0) load_group(nxt, i);
-        __syncwarp();
-      }
-    }
-    ahead = nxt;
-    ++phase;
+    flip ^= 1;
+    --ahead;
+    q0 = q1;
+    q1 = q2;
+    q2 = q3;
+    q3 = next_counted(q3 + 1);
   }
   cluster_sync();   // no CTA leaves while another may still write its statistics
 }
@@ -657,7 +959,8 @@ biv_status check_policy(const biv_policy_desc* d, const char* who) {
   BIV_REQUIRE(d->clip_lo >= 0.f && d->clip_lo <= 1.f && d->clip_hi >= 0.f,
               "%s: clip_lo must lie in [0, 1] and clip_hi must not be negative", who);
   BIV_REQUIRE(d->dual_clip == 0.f || d->dual_clip > 1.f, "%s: dual_clip must be 0 or above 1", who);
-  BIV_REQUIRE(d->kl_coef == d->kl_coef && d->ent_coef == d->ent_coef, "%s: a coefficient is NaN", who);
+  BIV_REQUIRE(d->kl_coef >= -1e3f && d->kl_coef <= 1e3f && d->ent_coef >= -1e3f && d->ent_coef <= 1e3f,
+              "%s: kl_coef and ent_coef must lie in [-1000, 1000]", who);
   BIV_REQUIRE(d->kl_coef == 0.f || d->ref_lp, "%s: a KL term needs ref_lp", who);
   BIV_REQUIRE(d->reduce >= BIV_LOSS_TOKEN_MEAN && d->reduce <= BIV_LOSS_SUM, "%s: unknown reduce", who);
   BIV_REQUIRE(d->reduce != BIV_LOSS_SUM || (d->norm > 0.f && d->norm < 3e38f),
@@ -766,20 +1069,33 @@ biv_status max_clusters(K kern, unsigned cluster, unsigned threads, size_t smem,
   return BIV_OK;
 }
 
+
+// Shape of the logits kernel (GB300, GPU time of the whole call).  A row is
+// spread over as few CTAs as hold it in 160 KB each, one CTA per SM: 4096 rows
+// x 151936 FP32 take 726 us on clusters of 4, 1069 us on clusters of 8 with two
+// CTAs per SM; 2037 x 131072 bf16 188 us on clusters of 2, 201 us on 4.  Up to
+// 16 warps (128 registers each): 24 take 786 us on the first case, 189 us on the
+// second.  What is left of 216 KB prefetches the next row: without it the first
+// case takes 786 us.
 constexpr size_t kRowBytesPerCta = 160 << 10;
+constexpr size_t kRingBytes = 216 << 10;
 
 template <bool ZB, bool DB, bool SHIFT>
 biv_status launch_logits(LogitsArgs& a, cudaStream_t s) {
-  constexpr int GB = kGroup * (ZB ? 2 : 4);
+  constexpr int BUF = kGroupBytes + (SHIFT ? 16 : 0);
   const int sms = sm_count() > 0 ? sm_count() : 148;
+  a.G = (a.V + kGroupBytes / (ZB ? 2 : 4) - 1) / (kGroupBytes / (ZB ? 2 : 4));
   unsigned cl = 1;
-  while (cl < 8 && size_t((a.G + cl - 1) / cl) * GB > kRowBytesPerCta) cl *= 2;
+  while (cl < 8 && size_t((a.G + cl - 1) / cl) * kGroupBytes > kRowBytesPerCta) cl *= 2;
   // few rows: spread each over more SMs (no bit depends on it)
   while (cl < 8 && int(cl) * 2 <= a.G && int64_t(a.p.T) * cl * 2 <= sms) cl *= 2;
   a.gpc = int((a.G + cl - 1) / cl);
   const int per = (a.gpc + kMaxWarps - 1) / kMaxWarps;
-  const unsigned threads = unsigned((a.gpc + per - 1) / per) * 32;
-  const size_t smem = size_t(a.gpc) * (GB + (SHIFT ? 16 : 0)) + size_t(a.G) * 32 + size_t(a.gpc) * 8;
+  const unsigned warps = unsigned((a.gpc + per - 1) / per), threads = warps * 32;
+  // a warp's ring: its groups of a row, and of the next one what the room allows
+  a.slots = per;
+  while (a.slots < 2 * per && size_t(a.slots + 1) * warps * BUF <= kRingBytes) ++a.slots;
+  const size_t smem = size_t(a.slots) * warps * (BUF + 8) + size_t(a.G) * 32;
   int fit = 0;
   biv_status st = max_clusters(policy_logits_kernel<ZB, DB, SHIFT>, cl, threads, smem, &fit);
   if (st != BIV_OK) return st;
@@ -826,7 +1142,8 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
                   (!dz || dz_dtype == BIV_F32 || dz_dtype == BIV_BF16),
               "policy_loss_logits: logits and gradient are f32 or bf16");
   BIV_REQUIRE(ld >= V && (!dz || ldz >= V), "policy_loss_logits: a row stride is below V");
-  BIV_REQUIRE(inv_temp > 0.f && inv_temp < 3e38f, "policy_loss_logits: inv_temp must be positive and finite");
+  BIV_REQUIRE(inv_temp >= 0.01f && inv_temp <= 100.f,
+              "policy_loss_logits: inv_temp must lie in [0.01, 100]");
   const size_t es = z_dtype == BIV_F32 ? 4 : 2, ds = dz_dtype == BIV_F32 ? 4 : 2;
   const uintptr_t zb = reinterpret_cast<uintptr_t>(z), db = reinterpret_cast<uintptr_t>(dz);
   BIV_REQUIRE(zb % es == 0 && db % ds == 0, "policy_loss_logits: a pointer is not aligned to its elements");
@@ -839,13 +1156,13 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
   LogitsArgs a;
   a.p = policy_args(*d);
   a.z = z; a.ld = ld; a.target = target; a.V = V;
-  a.G = (V + kGroup - 1) / kGroup;
-  a.gpc = 0;
+  a.G = a.gpc = a.slots = 0;
   a.it = inv_temp;
   a.c = float(double(inv_temp) * 1.4426950408889634);
   a.lp = lp; a.ent = entropy; a.dz = dz; a.ldz = ldz;
-  a.dz_vec = db % (4 * ds) == 0 && ldz % 4 == 0;
-  const bool shift = zb % 16 != 0 || (size_t(ld) * es) % 16 != 0;
+  // rows of logits and gradient that all keep 16 bytes' alignment
+  const bool shift = zb % 16 != 0 || (size_t(ld) * es) % 16 != 0 ||
+                     (dz && (db % 16 != 0 || (size_t(ldz) * ds) % 16 != 0));
   cudaStream_t s = as_cuda(stream);
   st = launch_prep(a.p, s);
   if (st != BIV_OK) return st;

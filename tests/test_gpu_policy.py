@@ -387,3 +387,53 @@ def test_binding_refuses(B):
         a = dict(logits=z, target=t, lp=x, entropy=y, dz=None) | kw
         with pytest.raises((ValueError, B.BivError)):
             B.biv_policy_loss_logits(d, **a)
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-math.inf, "lowest", -1e31])
+def test_masked_logits(B, zt, low):
+    """Whole groups and single logits masked by -inf or by a low value, in rows
+    of which a few logits are left, down to one: p = 0 there, and the rest as
+    if the masked ones were not in the row."""
+    T, V = 5, 3000
+    c = logits_case(T, V, 0, 0, zt, zt, "one", dict(mask=False, gamma=0.05, beta=0.1))
+    low = torch.finfo(TYPES[zt]).min if low == "lowest" else low
+    z = c["z"]
+    keep = [list(range(V)), list(range(0, V, 7)), list(range(1024, 2048)), [2500, 2999], [17]]
+    for t, k in enumerate(keep):
+        on = torch.zeros(V, dtype=torch.bool, device="cuda")
+        on[torch.tensor(k, device="cuda")] = True
+        z[t] = torch.where(on, torch.nan_to_num(z[t], neginf=-2.0), torch.full_like(z[t], low))
+        c["target"][t] = k[-1]
+    c["tgt"] = dev(c["target"], np.int32)
+    c["zz"] = np.where(f64(z) <= -1e30, -np.inf, f64(z))
+    with np.errstate(all="ignore"):
+        c["lp"], c["H"], c["p"], c["logp"] = tr.token_logprobs(c["zz"], c["target"])
+    c["old"], c["ref"] = (c["lp"] - 0.05).astype(np.float32), (c["lp"] + 0.2).astype(np.float32)
+    o = run_logits(B, c)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    want, dlp = oracle_loss(c, c["H"])
+    with np.errstate(all="ignore"):
+        dz = tr.policy_dz(c["zz"], c["target"], dlp, c["w"], 0.05)
+    got = f64(o["dz"])
+    half = 2.0 ** -8 if zt == "bf16" else 2.0 ** -24
+    assert np.all(np.abs(got - dz) <= (REL + half) * dz_size(c) + 1e-37)
+    assert np.all(got[f64(z) <= -1e30] == 0)
+    assert np.all(np.abs(f64(o["lp"]) - c["lp"]) <= REL * (1 + np.abs(c["lp"])))
+    assert np.all(np.abs(f64(o["ent"]) - c["H"]) <= REL * (1 + c["H"]))
+    check_stats(f64(o["stats"]), want, sizes(c, c["H"])[0])
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_logit_spoils_its_row_only(B, zt, bad):
+    c = logits_case(4, 2500, 0, 0, zt, zt, "one", dict(mask=False, gamma=0.05))
+    clean = run_logits(B, c)
+    c["z"][2, :] = -math.inf
+    c["z"][2, 1700] = bad                          # the rest of its group masked
+    o = run_logits(B, c)
+    torch.cuda.synchronize()
+    rows = [0, 1, 3]
+    assert math.isnan(o["lp"][2].item()) and math.isnan(o["stats"][0].item())
+    assert all(same(o[k][rows], clean[k][rows]) for k in ("lp", "ent", "dz"))

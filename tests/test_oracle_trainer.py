@@ -131,7 +131,8 @@ def _policy(B, **kw):
     (dict(T=-1), b"sizes"), (dict(nseq=-1), b"sizes"), (dict(seq_start=None), b"null"),
     (dict(adv=None), b"null"), (dict(stats=None), b"null"), (dict(clip_lo=1.5), b"clip"),
     (dict(clip_hi=-0.1), b"clip"), (dict(clip_lo=float("nan")), b"clip"), (dict(dual_clip=0.5), b"dual"),
-    (dict(kl_coef=0.1, ref_lp=None), b"ref_lp"), (dict(kl_coef=float("nan")), b"NaN"),
+    (dict(kl_coef=0.1, ref_lp=None), b"ref_lp"), (dict(kl_coef=float("nan")), b"kl_coef"),
+    (dict(ent_coef=2000.0), b"ent_coef"),
     (dict(reduce=3), b"reduce"), (dict(reduce=2, norm=0.0), b"norm"),
     (dict(reduce=2, norm=float("inf")), b"norm"), (dict(workspace=0x10008), b"aligned")])
 def test_policy_loss_refuses(B, kw, word):
