@@ -593,8 +593,8 @@ biv_status biv_attention_backward(const biv_attn_bwd_desc* desc, biv_stream_t st
  * < 20, and the KL part is 0 at |ref_lp - lp| >= 20 (the clamps' derivative).
  * w_t by `reduce`: TOKEN_MEAN 1/N, N counted rows; SEQ_MEAN 1/(S n_s), S
  * sequences that have counted rows, n_s their number; SUM 1/norm.
- * A row that does not count has weight 0: its lp, logits and target are not
- * read, and its dlp, lp, entropy and dz are written as zeros; with no counted
+ * A row that does not count has weight 0: what its lp, logits and target hold
+ * does not matter, and its dlp, lp, entropy and dz are written as zeros; with no counted
  * row at all loss, statistics and gradients are zeros.
  *
  * stats float32 [8]: loss, sum w pg, sum w kl, sum w H, then over counted rows
@@ -658,8 +658,10 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * place (captured graphs keep their addresses; BF16 weights that the forward
  * reads, "Finish RL Training Faster", section "让训练前向使用推理的数值").  Per
  * element, in FP32:
- *   g = grad * coef;  m = b1 m + (1-b1) g;  v = b2 v + (1-b2) g^2
+ *   g = grad * coef;  m = b1 m + (1-b1) g;  v = b2 v + ((1-b2) g) g
  *   w = w (1 - lr wd) - (lr / (1-b1^t)) m / (sqrt(v) / sqrt(1-b2^t) + eps)
+ * (m and v are the bits of these operations, each rounded once in the order
+ * written; w is within a few 2^-24 of its step)
  * with t the step's number, lr = *lr * lr_scale and wd of the tensor.
  *
  * A biv_opt_tensor describes one tensor of numel elements, all arrays dense:
@@ -702,8 +704,9 @@ typedef struct {
 biv_status biv_opt_plan(biv_opt_tensor* host_tensors, int n, int64_t* chunks);
 
 /* Global L2 norm of all gradients: out[0] = norm, out[1] = min(1, max_norm /
- * (norm + 1e-6)) (1 when max_norm is 0).  FP32 sums in one order fixed by the
- * tensors' sizes; a norm beyond about 1.8e19 reads as infinity.  tensors:
+ * (norm + 1e-6)) (1 when max_norm is 0).  FP32 sums that carry their rounding
+ * errors along, in one order fixed by the tensors' sizes; a norm beyond about
+ * 1.8e19 is not finite.  tensors:
  * device copy of the planned array.  Workspace: biv_grad_norm_workspace bytes,
  * 16-byte aligned, caller-owned, no initial value. */
 biv_status biv_grad_norm_workspace(int64_t chunks, size_t* bytes);

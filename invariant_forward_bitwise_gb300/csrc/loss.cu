@@ -7,10 +7,11 @@
 // From logits (x = z / temperature, p = softmax x):
 //   dz_v = (dlp ([v = target] - p_v) + w gamma p_v (log p_v + H)) / temperature
 //
-// Launches: policy_prep_kernel (one cluster) counts the rows of each sequence
-// and turns them into a weight and an advantage per row; the logits kernel
-// writes lp, H and dz row by row; policy_token_kernel sums the loss (and, when
-// it starts from logprobs, writes dlp), its last block adding the blocks up.
+// Launches.  Weights need the counted rows of each sequence first.  Up to 4096
+// rows, one CTA does all of it (policy_small_kernel: from logprobs one launch;
+// from logits one before and one after the logits kernel, which writes lp, H
+// and dz row by row).  Above that a launch each zeroes the counts, counts, and
+// sums the loss (policy_token_kernel, whose last block adds the blocks up).
 #include <algorithm>
 #include <mutex>
 
@@ -19,8 +20,7 @@
 namespace biv {
 namespace {
 
-constexpr int kPrepThreads = 1024;
-constexpr int kPrepCtas = 8;       // one cluster
+constexpr int kSmallRows = 4096, kSmallSeqs = 1024;   // what one CTA takes
 constexpr int kTB = 256;           // threads per block of tokens
 constexpr int kTok = 1024;         // tokens per partial sum
 constexpr int kStat = 8;           // floats per partial sum
@@ -39,6 +39,10 @@ __device__ __forceinline__ float warp_max_nan(float v) {
   return v;
 }
 __device__ __forceinline__ float clamp_far(float x) { return x < -kFar ? -kFar : x > kFar ? kFar : x; }
+
+__device__ __forceinline__ bool aligned16_dev(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -108,7 +112,7 @@ struct PolicyArgs {
   int* err;
 };
 
-// ------------------------------------------------------------------ prep --
+// ------------------------------------------------------------------ rows --
 // the sequence that row t may belong to: the last s < nseq with seq_start[s] <=
 // t (-1: none); it does when also t < seq_start[s + 1]
 __device__ __forceinline__ int find_seq(const int32_t* start, int nseq, int t) {
@@ -120,105 +124,36 @@ __device__ __forceinline__ int find_seq(const int32_t* start, int nseq, int t) {
   return lo;
 }
 
-// 16 mask bytes from row t on as bits (rows past T: 0)
-__device__ __forceinline__ uint32_t mask16(const PolicyArgs& a, int t) {
-  const int left = a.T - t;
-  if (left <= 0) return 0;
-  const uint32_t in = left >= 16 ? 0xFFFFu : (1u << left) - 1u;
-  if (!a.mask) return in;
-  uint32_t bits = 0;
-  if (left >= 16 && (reinterpret_cast<uintptr_t>(a.mask + t) & 15) == 0) {
-    const uint4 v = *reinterpret_cast<const uint4*>(a.mask + t);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// a thread's four consecutive rows t0..t0+3: the sequence of each that counts
+// (-1: it does not)
+__device__ __forceinline__ void four_seqs(const PolicyArgs& a, const int32_t* start, int64_t t0,
+                                          int (&seq)[4]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if ((w[i >> 2] >> (8 * (i & 3))) & 0xFFu) bits |= 1u << i;
-  } else {
-    for (int i = 0; i < 16 && i < left; ++i)
-      if (a.mask[t + i]) bits |= 1u << i;
+  for (int i = 0; i < 4; ++i) seq[i] = -1;
+  if (t0 >= a.T) return;
+  int s = find_seq(start, a.nseq, int(t0));
+  int end = s >= 0 ? start[s + 1] : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = int(t0) + i;
+    if (t < a.T) {
+      while (s + 1 < a.nseq && start[s + 1] <= t) {
+        ++s;
+        end = start[s + 1];
+      }
+      if (s >= 0 && t < end && (!a.mask || a.mask[t])) seq[i] = s;
+    }
   }
-  return bits & in;
 }
 
-// One cluster: counts per sequence (integer adds: any order gives the same),
-// totals, then every row's weight and advantage.
-__global__ void __launch_bounds__(kPrepThreads) policy_prep_kernel(const __grid_constant__ PolicyArgs a) {
-  __shared__ int s_red[2][kPrepThreads / 32];
-  pdl_wait();
-  pdl_trigger();
-  const int gt = blockIdx.x * kPrepThreads + threadIdx.x, nt = gridDim.x * kPrepThreads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int s = gt; s < a.nseq; s += nt) {
-    a.ws.counts[s] = 0;
-    const int b = a.seq_start[s], e = a.seq_start[s + 1];
-    if (b < 0 || e < b || e > a.T) raise_error(a.err, kErrBadIndex);
-  }
-  cluster_sync();
-  // 16 rows per lane; the loop's condition is the same for a whole warp
-  for (int64_t t0 = int64_t(gt) * 16; t0 - int64_t(lane) * 16 < a.T; t0 += int64_t(nt) * 16) {
-    const int t = int(t0 < a.T ? t0 : a.T);
-    const uint32_t bits = mask16(a, t);
-    int s = find_seq(a.seq_start, a.nseq, t);
-    int end = s >= 0 ? a.seq_start[s + 1] : (a.nseq > 0 ? a.seq_start[0] : a.T);
-    // a warp inside one sequence adds once
-    const bool whole = s >= 0 && (t >= a.T || end >= min(t + 16, a.T));
-    const int s0 = __shfl_sync(0xffffffffu, s, 0);
-    if (__all_sync(0xffffffffu, t >= a.T || (whole && s == s0)) && s0 >= 0) {
-      const int c = __reduce_add_sync(0xffffffffu, t < a.T ? __popc(bits) : 0);
-      if (lane == 0 && c) atomicAdd(a.ws.counts + s0, c);
-    } else if (t < a.T) {
-      int c = 0;
-      for (int i = 0; i < 16 && t + i < a.T; ++i) {
-        while (t + i >= end && s < a.nseq) {   // the next sequence that reaches past this row
-          if (s >= 0 && c) atomicAdd(a.ws.counts + s, c);
-          c = 0;
-          ++s;
-          end = s < a.nseq ? a.seq_start[s + 1] : a.T;
-        }
-        if (s >= 0 && s < a.nseq && ((bits >> i) & 1u)) ++c;
-      }
-      if (s >= 0 && s < a.nseq && c) atomicAdd(a.ws.counts + s, c);
-    }
-    __syncwarp();
-  }
-  cluster_sync();
-  int n = 0, k = 0;
-  for (int s = threadIdx.x; s < a.nseq; s += kPrepThreads) {
-    const int c = __ldcg(a.ws.counts + s);
-    n += c;
-    k += c > 0;
-  }
-  __syncwarp();
-  n = __reduce_add_sync(0xffffffffu, n);
-  k = __reduce_add_sync(0xffffffffu, k);
-  if (lane == 0) {
-    s_red[0][warp] = n;
-    s_red[1][warp] = k;
-  }
-  __syncthreads();
-  n = __reduce_add_sync(0xffffffffu, s_red[0][lane]);
-  k = __reduce_add_sync(0xffffffffu, s_red[1][lane]);
-  if (gt == 0) {
-    a.ws.totals->rows = n;
-    a.ws.totals->seqs = k;
-    a.ws.totals->ticket = 0;
-  }
-  const float wt = a.reduce == BIV_LOSS_SUM ? 1.0f / a.norm : 1.0f / float(max(n, 1));
-  for (int64_t t0 = int64_t(gt) * 4; t0 < a.T; t0 += int64_t(nt) * 4) {
-    int s = find_seq(a.seq_start, a.nseq, int(t0));
-    for (int i = 0; i < 4 && t0 + i < a.T; ++i) {
-      const int t = int(t0) + i;
-      while (s + 1 < a.nseq && a.seq_start[s + 1] <= t) ++s;
-      float2 o = make_float2(0.f, 0.f);
-      if (s >= 0 && t < a.seq_start[s + 1] && (!a.mask || a.mask[t])) {
-        o.x = a.reduce == BIV_LOSS_SEQ_MEAN
-                  ? 1.0f / (float(k) * float(max(__ldcg(a.ws.counts + s), 1)))
-                  : wt;
-        o.y = a.adv[a.adv_per_row ? t : s];
-      }
-      a.ws.row[t] = o;
-    }
-  }
+__device__ __forceinline__ float row_weight(const PolicyArgs& a, int rows, int seqs, int count) {
+  if (a.reduce == BIV_LOSS_SUM) return 1.0f / a.norm;
+  return 1.0f / (a.reduce == BIV_LOSS_SEQ_MEAN ? float(seqs) * float(max(count, 1)) : float(max(rows, 1)));
+}
+
+__device__ __forceinline__ void check_start(const PolicyArgs& a, int s) {
+  const int b = a.seq_start[s], e = a.seq_start[s + 1];
+  if (b < 0 || e < b || e > a.T) raise_error(a.err, kErrBadIndex);
 }
 
 // ------------------------------------------------------------- one token --
@@ -255,73 +190,262 @@ __device__ __forceinline__ Token policy_token(const PolicyArgs& a, float lp, flo
   return o;
 }
 
-// Tokens [1024 blk, 1024 blk + 1024): dlp (when asked for) and the block's
-// partial sums; thread i takes tokens 4i..4i+3 in order, then a warp xor tree
-// and the warps in order.
-__device__ __forceinline__ void policy_block(const PolicyArgs& a, const float* lp, const float* ent,
-                                             float* dlp, int64_t blk, int tid, float (*red)[kStat]) {
-  float v[kStat] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+// four consecutive values from t0 on (n: their number, 0 past it)
+__device__ __forceinline__ void load4(const float* p, int64_t t0, int64_t n, float (&f)[4]) {
+  if (t0 + 4 <= n && aligned16_dev(p)) {
+    const float4 v = *reinterpret_cast<const float4*>(p + t0);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = t0 + i < n ? p[t0 + i] : 0.f;
+}
+
+// What a thread has of its four rows: weights (0: not counted), advantages and
+// the inputs.
+struct Four {
+  float w[4], A[4], lp[4], old[4], ref[4], ent[4];
+};
+__device__ __forceinline__ void load_inputs(const PolicyArgs& a, const float* lp, const float* ent,
+                                            int64_t t0, Four& f) {
+  load4(lp, t0, a.T, f.lp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.old[i] = f.ref[i] = f.ent[i] = 0.f;
+  if (a.old_lp) load4(a.old_lp, t0, a.T, f.old);
+  if (a.ref_lp) load4(a.ref_lp, t0, a.T, f.ref);
+  if (ent) load4(ent, t0, a.T, f.ent);
+}
+
+// dlp of the four rows (when asked for) and the sums over a block of 1024 rows:
+// thread i's rows 4i..4i+3 in order, a warp xor tree, then the 8 warps in order.
+// tid: the thread within its block of 256; `sync` joins those threads.
+template <typename Sync>
+__device__ __forceinline__ void policy_block(const PolicyArgs& a, const Four& f, float* dlp, int64_t t0,
+                                             int tid, float (*red)[kStat], float* part, Sync sync) {
+  float v[kStat] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, g[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t t = blk * kTok + tid * 4 + i;
-    if (t < a.T) {
-      const float2 wa = a.ws.row[t];
-      float g = 0.f;
-      if (wa.x > 0.f) {
-        const Token o = policy_token(a, lp[t], wa.y, a.old_lp ? a.old_lp[t] : 0.f,
-                                     a.ref_lp ? a.ref_lp[t] : 0.f);
-        const float h = ent ? ent[t] : 0.f;
-        g = wa.x * o.dlp;
-        v[0] += wa.x * (o.pg + a.beta * o.kl - a.gamma * h);
-        v[1] += wa.x * o.pg;
-        v[2] += wa.x * o.kl;
-        v[3] += wa.x * h;
-        v[4] += o.cut ? 1.f : 0.f;
-        v[5] += o.k3;
-        v[6] = max_nan(v[6], fabsf(o.gap));
-      }
-      if (dlp) dlp[t] = g;
+    g[i] = 0.f;
+    if (f.w[i] > 0.f) {
+      const Token o = policy_token(a, f.lp[i], f.A[i], f.old[i], f.ref[i]);
+      g[i] = f.w[i] * o.dlp;
+      v[0] += f.w[i] * (o.pg + a.beta * o.kl - a.gamma * f.ent[i]);
+      v[1] += f.w[i] * o.pg;
+      v[2] += f.w[i] * o.kl;
+      v[3] += f.w[i] * f.ent[i];
+      v[4] += o.cut ? 1.f : 0.f;
+      v[5] += o.k3;
+      v[6] = max_nan(v[6], fabsf(o.gap));
+    }
+  }
+  if (dlp) {
+    if (t0 + 4 <= a.T && aligned16_dev(dlp)) {
+      *reinterpret_cast<float4*>(dlp + t0) = make_float4(g[0], g[1], g[2], g[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < a.T) dlp[t0 + i] = g[i];
     }
   }
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 6; ++k) v[k] = warp_sum_x(v[k]);
   v[6] = warp_max_nan(v[6]);
-  __syncthreads();
+  sync();
   if ((tid & 31) == 0) {
 #pragma unroll
     for (int k = 0; k < 7; ++k) red[tid >> 5][k] = v[k];
   }
-  __syncthreads();
+  sync();
   if (tid < 7) {
     float s = red[0][tid];
     for (int i = 1; i < kTB / 32; ++i) s = tid == 6 ? max_nan(s, red[i][tid]) : s + red[i][tid];
-    a.ws.part[blk * kStat + tid] = s;
+    part[tid] = s;
   }
 }
 
-// all blocks, by one warp: lane l takes blocks l, l + 32, ... in order
-__device__ __forceinline__ void policy_final(const PolicyArgs& a, int64_t blocks, int lane) {
+// all blocks' sums, by one warp: lane l takes blocks l, l + 32, ... in order
+__device__ __forceinline__ void policy_final(const PolicyArgs& a, const float* part, int64_t blocks,
+                                             int rows, int lane) {
   float v[kStat] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int64_t b = lane; b < blocks; b += 32) {
-    const float4* p = reinterpret_cast<const float4*>(a.ws.part + b * kStat);
-    const float4 x = __ldcg(p), y = __ldcg(p + 1);
-    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-    v[4] += y.x; v[5] += y.y; v[6] = max_nan(v[6], y.z);
+    const volatile float* p = part + b * kStat;
+#pragma unroll
+    for (int k = 0; k < 6; ++k) v[k] += p[k];
+    v[6] = max_nan(v[6], p[6]);
   }
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 6; ++k) v[k] = warp_sum_x(v[k]);
   v[6] = warp_max_nan(v[6]);
   if (lane == 0) {
-    const int n = a.ws.totals->rows;
-    const float inv = 1.0f / float(max(n, 1));
+    const float inv = 1.0f / float(max(rows, 1));
     a.stats[0] = v[0]; a.stats[1] = v[1]; a.stats[2] = v[2]; a.stats[3] = v[3];
     a.stats[4] = v[4] * inv;
     a.stats[5] = v[5] * inv;
     a.stats[6] = v[6];
-    a.stats[7] = float(n);
+    a.stats[7] = float(rows);
   }
+}
+
+// ----------------------------------------------------------- small calls --
+// One CTA, four rows per thread; counts and starts in shared memory, the rows'
+// inputs on their way meanwhile.  kAll: from logprobs, all of it; kRows: weights
+// and advantages for the logits kernel; kStats: the loss after it.
+enum SmallMode { kAll = 0, kRows = 1, kStats = 2 };
+template <int MODE>
+__global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
+    const __grid_constant__ PolicyArgs a, const float* lp, const float* ent, float* dlp) {
+  __shared__ int32_t s_start[kSmallSeqs + 1];
+  __shared__ int s_count[kSmallSeqs], s_red[2][32];
+  __shared__ float red[4][kTB / 32][kStat], part[4 * kStat];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int64_t t0 = int64_t(tid) * 4;
+  Four f;
+  int rows;
+  if (MODE != kRows) load_inputs(a, lp, ent, t0, f);
+  if (MODE == kStats) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 wa = t0 + i < a.T ? a.ws.row[t0 + i] : make_float2(0.f, 0.f);
+      f.w[i] = wa.x;
+      f.A[i] = wa.y;
+    }
+    rows = a.ws.totals->rows;
+  } else {
+    for (int s = tid; s <= a.nseq; s += nt) {
+      s_start[s] = a.seq_start[s];
+      if (s < a.nseq) {
+        s_count[s] = 0;
+        check_start(a, s);
+      }
+    }
+    __syncthreads();
+    int seq[4];
+    four_seqs(a, s_start, t0, seq);
+    const bool one = seq[0] >= 0 && seq[0] == seq[1] && seq[0] == seq[2] && seq[0] == seq[3];
+    const int first = __shfl_sync(0xffffffffu, seq[0], 0);
+    if (__all_sync(0xffffffffu, one && seq[0] == first)) {
+      if (lane == 0) atomicAdd(s_count + first, 128);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (seq[i] >= 0) atomicAdd(s_count + seq[i], 1);
+    }
+    float adv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) adv[i] = seq[i] >= 0 ? a.adv[a.adv_per_row ? t0 + i : seq[i]] : 0.f;
+    __syncthreads();
+    int n = 0, k = 0;
+    for (int s = tid; s < a.nseq; s += nt) {
+      n += s_count[s];
+      k += s_count[s] > 0;
+    }
+    __syncwarp();
+    n = __reduce_add_sync(0xffffffffu, n);
+    k = __reduce_add_sync(0xffffffffu, k);
+    if (lane == 0) {
+      s_red[0][warp] = n;
+      s_red[1][warp] = k;
+    }
+    __syncthreads();
+    rows = __reduce_add_sync(0xffffffffu, lane < nt / 32 ? s_red[0][lane] : 0);
+    k = __reduce_add_sync(0xffffffffu, lane < nt / 32 ? s_red[1][lane] : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.w[i] = seq[i] >= 0 ? row_weight(a, rows, k, s_count[seq[i]]) : 0.f;
+      f.A[i] = adv[i];
+    }
+    if (MODE == kRows) {
+      if (tid == 0) a.ws.totals->rows = rows;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t0 + i < a.T) a.ws.row[t0 + i] = make_float2(f.w[i], f.A[i]);
+      return;
+    }
+  }
+  const int grp = tid / kTB;           // blocks of 1024 rows: groups of 256 threads
+  policy_block(a, f, dlp, t0, tid % kTB, red[grp], part + grp * kStat, [] { __syncthreads(); });
+  __syncthreads();
+  if (warp == 0) policy_final(a, part, nt / kTB, rows, lane);
+}
+
+// ----------------------------------------------------------- large calls --
+__global__ void policy_zero_kernel(const __grid_constant__ PolicyArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x * blockDim.x + threadIdx.x;
+  if (s == 0) *a.ws.totals = Totals{0, 0, 0u, 0};
+  if (s < a.nseq) {
+    a.ws.counts[s] = 0;
+    check_start(a, s);
+  }
+}
+
+// Counts per sequence and their totals (integer adds: any order gives the same)
+__global__ void __launch_bounds__(kTB) policy_count_kernel(const __grid_constant__ PolicyArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t t0 = (int64_t(blockIdx.x) * kTB + threadIdx.x) * 4;
+  int seq[4];
+  four_seqs(a, a.seq_start, t0, seq);
+  auto add = [&](int s, int c) {
+    if (atomicAdd(a.ws.counts + s, c) == 0) atomicAdd(&a.ws.totals->seqs, 1);
+  };
+  __syncwarp();
+  int any = max(max(seq[0], seq[1]), max(seq[2], seq[3]));
+  any = __reduce_max_sync(0xffffffffu, any);      // a sequence that counts here
+  if (any < 0) return;
+  bool other = false;
+  int c = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    other |= seq[i] >= 0 && seq[i] != any;
+    c += seq[i] >= 0;
+  }
+  const int n = __reduce_add_sync(0xffffffffu, c);
+  if (lane == 0) atomicAdd(&a.ws.totals->rows, n);
+  if (!__any_sync(0xffffffffu, other)) {          // the warp's only one: add once
+    if (lane == 0) add(any, n);
+    return;
+  }
+  for (int i = 0; i < 4; ++i) {                   // runs of one sequence
+    if (seq[i] < 0) continue;
+    int m = 1;
+    while (i + 1 < 4 && seq[i + 1] == seq[i]) {
+      ++m;
+      ++i;
+    }
+    add(seq[i], m);
+  }
+}
+
+__device__ __forceinline__ void four_rows(const PolicyArgs& a, int64_t t0, Four& f) {
+  int seq[4];
+  four_seqs(a, a.seq_start, t0, seq);
+  const int rows = a.ws.totals->rows, seqs = a.ws.totals->seqs;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.w[i] = f.A[i] = 0.f;
+    if (seq[i] >= 0) {
+      f.w[i] = row_weight(a, rows, seqs, a.ws.counts[seq[i]]);
+      f.A[i] = a.adv[a.adv_per_row ? t0 + i : seq[i]];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kTB) policy_rows_kernel(const __grid_constant__ PolicyArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t t0 = (int64_t(blockIdx.x) * kTB + threadIdx.x) * 4;
+  Four f;
+  four_rows(a, t0, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (t0 + i < a.T) a.ws.row[t0 + i] = make_float2(f.w[i], f.A[i]);
 }
 
 __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant__ PolicyArgs a,
@@ -331,15 +455,20 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
   __shared__ bool s_last;
   pdl_wait();
   pdl_trigger();
-  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x)
-    policy_block(a, lp, ent, dlp, b, threadIdx.x, red);
+  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+    const int64_t t0 = b * kTok + threadIdx.x * 4;
+    Four f;
+    load_inputs(a, lp, ent, t0, f);
+    four_rows(a, t0, f);
+    policy_block(a, f, dlp, t0, threadIdx.x, red, a.ws.part + b * kStat, [] { __syncthreads(); });
+  }
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) s_last = atomicAdd(&a.ws.totals->ticket, 1u) == gridDim.x - 1;
   __syncthreads();
   if (s_last && threadIdx.x < 32) {
     __threadfence();
-    policy_final(a, blocks, threadIdx.x);
+    policy_final(a, a.ws.part, blocks, a.ws.totals->rows, threadIdx.x);
   }
 }
 
@@ -1003,15 +1132,32 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-biv_status launch_prep(const PolicyArgs& a, cudaStream_t s) {
-  // a CTA per 4096 rows or 1024 sequences, at most one cluster
-  const int64_t want = (std::max<int64_t>(a.T, int64_t(a.nseq) * 4) + 4095) / 4096;
-  unsigned ctas = 1;
-  while (ctas < unsigned(kPrepCtas) && int64_t(ctas) < want) ctas *= 2;
-  launch_cluster(policy_prep_kernel, ctas, kPrepThreads, 0, ctas, s, a);
-  return check_launch("policy_prep");
+bool small_call(const PolicyArgs& a) { return a.T <= kSmallRows && a.nseq <= kSmallSeqs; }
+unsigned small_threads(const PolicyArgs& a) { return unsigned(token_blocks(a.T)) * kTB; }
+
+// counts per sequence (large calls)
+biv_status launch_counts(const PolicyArgs& a, cudaStream_t s) {
+  launch_pdl(policy_zero_kernel, unsigned(std::max(1, (a.nseq + kTB - 1) / kTB)), kTB, 0, s, a);
+  biv_status st = check_launch("policy_zero");
+  if (st != BIV_OK) return st;
+  launch_pdl(policy_count_kernel, unsigned(token_blocks(a.T)), kTB, 0, s, a);
+  return check_launch("policy_count");
 }
 
+// weight and advantage of every row, for the logits kernel
+biv_status launch_rows(const PolicyArgs& a, cudaStream_t s) {
+  if (small_call(a)) {
+    launch_pdl(policy_small_kernel<kRows>, 1, small_threads(a), 0, s, a, static_cast<const float*>(nullptr),
+               static_cast<const float*>(nullptr), static_cast<float*>(nullptr));
+    return check_launch("policy_rows");
+  }
+  biv_status st = launch_counts(a, s);
+  if (st != BIV_OK) return st;
+  launch_pdl(policy_rows_kernel, unsigned(token_blocks(a.T)), kTB, 0, s, a);
+  return check_launch("policy_rows");
+}
+
+// the sums over all rows (and dlp): after launch_counts or the small rows kernel
 biv_status launch_tokens(const PolicyArgs& a, const float* lp, const float* ent, float* dlp,
                          cudaStream_t s) {
   const int64_t blocks = token_blocks(a.T);
@@ -1125,7 +1271,11 @@ biv_status biv_policy_loss(const biv_policy_desc* d, const float* lp, float* dlp
   BIV_REQUIRE(d->ent_coef == 0.f, "policy_loss: an entropy term needs the logits");
   const PolicyArgs a = policy_args(*d);
   cudaStream_t s = as_cuda(stream);
-  st = launch_prep(a, s);
+  if (small_call(a)) {
+    launch_pdl(policy_small_kernel<kAll>, 1, small_threads(a), 0, s, a, lp, static_cast<const float*>(nullptr), dlp);
+    return check_launch("policy_loss");
+  }
+  st = launch_counts(a, s);
   if (st != BIV_OK) return st;
   return launch_tokens(a, lp, nullptr, dlp, s);
 }
@@ -1164,7 +1314,7 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
   const bool shift = zb % 16 != 0 || (size_t(ld) * es) % 16 != 0 ||
                      (dz && (db % 16 != 0 || (size_t(ldz) * ds) % 16 != 0));
   cudaStream_t s = as_cuda(stream);
-  st = launch_prep(a.p, s);
+  st = launch_rows(a.p, s);
   if (st != BIV_OK) return st;
   const bool zbf = z_dtype == BIV_BF16, dbf = dz && dz_dtype == BIV_BF16;
   if (zbf) {
@@ -1175,6 +1325,11 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
              : (shift ? launch_logits<false, false, true>(a, s) : launch_logits<false, false, false>(a, s));
   }
   if (st != BIV_OK) return st;
+  if (small_call(a.p)) {
+    launch_pdl(policy_small_kernel<kStats>, 1, small_threads(a.p), 0, s, a.p, static_cast<const float*>(lp),
+               static_cast<const float*>(entropy), static_cast<float*>(nullptr));
+    return check_launch("policy_stats");
+  }
   return launch_tokens(a.p, lp, entropy, nullptr, s);
 }
 

@@ -37,77 +37,109 @@ __device__ __forceinline__ int find_tensor(const biv_opt_tensor* t, int n, int64
   return lo;
 }
 
-// 8 consecutive values from element e on; those past n read as 0
-template <bool BF>
-__device__ __forceinline__ void load8(const void* p, int64_t e, int64_t n, bool vec, float (&f)[8]) {
-  if (vec && e + 8 <= n) {
-    if constexpr (BF) {
-      const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// two FP32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// a + b, by single additions: a product before them keeps its own rounding (an
+// addition of pairs is merged with it into one)
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  return pack2(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 8 consecutive elements of an array, as its bytes: raw words of F32 (8), BF16
+// (4) or e4m3 (2)
+template <int W>
+struct Raw {
+  uint32_t w[W];
+};
+template <int W>
+__device__ __forceinline__ void load_raw(const void* p, int64_t e, Raw<W>& r) {
+  const uint8_t* q = static_cast<const uint8_t*>(p) + e * (W / 2);
+  if constexpr (W == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(q);
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
-      const float4 a = q[0], b = q[1];
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q + i * 4);
+      r.w[i] = v.x; r.w[i + 1] = v.y; r.w[i + 2] = v.z; r.w[i + 3] = v.w;
     }
-    return;
   }
+}
+// the same element by element; those past n read as 0
+template <int W>
+__device__ __forceinline__ void load_raw_slow(const void* p, int64_t e, int64_t n, Raw<W>& r) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) r.w[i] = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    f[i] = 0.f;
-    if (e + i < n)
-      f[i] = BF ? bf2f(static_cast<const uint16_t*>(p)[e + i]) : static_cast<const float*>(p)[e + i];
+    if (e + i >= n) continue;
+    if constexpr (W == 8) r.w[i] = static_cast<const uint32_t*>(p)[e + i];
+    else if constexpr (W == 4) r.w[i >> 1] |= uint32_t(static_cast<const uint16_t*>(p)[e + i]) << (16 * (i & 1));
+    else r.w[i >> 2] |= uint32_t(static_cast<const uint8_t*>(p)[e + i]) << (8 * (i & 3));
   }
 }
-__device__ __forceinline__ void store8_f32(float* p, int64_t e, int64_t n, bool vec,
-                                           const float (&f)[8]) {
-  if (vec && e + 8 <= n) {
-    float4* q = reinterpret_cast<float4*>(p + e);
-    q[0] = make_float4(f[0], f[1], f[2], f[3]);
-    q[1] = make_float4(f[4], f[5], f[6], f[7]);
-    return;
-  }
+template <int W>
+__device__ __forceinline__ void store_raw(void* p, int64_t e, const Raw<W>& r) {
+  uint8_t* q = static_cast<uint8_t*>(p) + e * (W / 2);
+  if constexpr (W == 2) {
+    *reinterpret_cast<uint2*>(q) = make_uint2(r.w[0], r.w[1]);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e + i < n) p[e + i] = f[i];
+    for (int i = 0; i < W; i += 4)
+      *reinterpret_cast<uint4*>(q + i * 4) = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+  }
 }
-__device__ __forceinline__ void store8_bf16(uint16_t* p, int64_t e, int64_t n, bool vec,
-                                            const uint32_t (&b)[8]) {
-  if (vec && e + 8 <= n) {
-    *reinterpret_cast<uint4*>(p + e) = make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16),
-                                                  b[4] | (b[5] << 16), b[6] | (b[7] << 16));
-    return;
-  }
+template <int W>
+__device__ __forceinline__ void store_raw_slow(void* p, int64_t e, int64_t n, const Raw<W>& r) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e + i < n) p[e + i] = uint16_t(b[i]);
+  for (int i = 0; i < 8; ++i) {
+    if (e + i >= n) continue;
+    if constexpr (W == 8) static_cast<uint32_t*>(p)[e + i] = r.w[i];
+    else if constexpr (W == 4) static_cast<uint16_t*>(p)[e + i] = uint16_t(r.w[i >> 1] >> (16 * (i & 1)));
+    else static_cast<uint8_t*>(p)[e + i] = uint8_t(r.w[i >> 2] >> (8 * (i & 3)));
+  }
 }
-__device__ __forceinline__ void load8_codes(const uint8_t* p, int64_t e, int64_t n, bool vec,
-                                            uint32_t (&c)[2]) {
-  if (vec && e + 8 <= n) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p + e);
-    c[0] = r.x; c[1] = r.y;
-    return;
-  }
-  c[0] = c[1] = 0;
+// as four pairs of FP32
+template <int W>
+__device__ __forceinline__ void to_pairs(const Raw<W>& r, uint64_t (&f)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e + i < n) c[i >> 2] |= uint32_t(p[e + i]) << (8 * (i & 3));
-}
-__device__ __forceinline__ void store8_codes(uint8_t* p, int64_t e, int64_t n, bool vec,
-                                             const uint32_t (&c)[2]) {
-  if (vec && e + 8 <= n) {
-    *reinterpret_cast<uint2*>(p + e) = make_uint2(c[0], c[1]);
-    return;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (W == 8) {
+      f[i] = pack2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    } else if constexpr (W == 4) {
+      f[i] = pack2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+    } else {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          __nv_fp8x2_storage_t(r.w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+      const float2 v = __half22float2(__half2(h));
+      f[i] = pack2(v.x, v.y);
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (e + i < n) p[e + i] = uint8_t(c[i >> 2] >> (8 * (i & 3)));
 }
 
 // 32-bit hash: xor-shifts and two odd multipliers (a bijection)
@@ -119,27 +151,32 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// y in [0, 448] to the e4m3 grid, up with a chance of the part cut off (16
-// random bits): normal numbers keep 3 fraction bits, so 20 bits of the float
-// fall away; below 2^-6 the grid is 2^-9 apart
-__device__ __forceinline__ float stochastic_e4m3(float y, uint32_t rnd16) {
-  const float big = __uint_as_float((__float_as_uint(y) + (rnd16 << 4)) & 0xFFF00000u);
-  const float small = floorf(fmaf(float(rnd16), 1.0f / 65536.0f, y * 512.0f)) * (1.0f / 512.0f);
-  return y < 0.015625f ? small : big;
+// |y| <= 448 to the e4m3 grid, up with a chance of the part cut off (16 random
+// bits): normal numbers keep 3 fraction bits, so 20 bits of the float fall
+// away; below 2^-6 the grid is 2^-9 apart
+constexpr float kE4m3Normal = 0.015625f;   // 2^-6
+__device__ __forceinline__ float stochastic_normal(float y, uint32_t rnd16_shl4) {
+  return __uint_as_float((__float_as_uint(y) + rnd16_shl4) & 0xFFF00000u);
+}
+__device__ __forceinline__ float stochastic_any(float y, uint32_t rnd16_shl4) {
+  const float a = fabsf(y);
+  const float small = floorf(fmaf(float(rnd16_shl4), 1.0f / 1048576.0f, a * 512.0f)) * (1.0f / 512.0f);
+  return a < kE4m3Normal ? copysignf(small, y) : stochastic_normal(y, rnd16_shl4);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
-__device__ __forceinline__ void decode8(const uint32_t (&c)[2], float s, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        __nv_fp8x2_storage_t(c[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
-    const float2 v = __half22float2(__half2(h));
-    f[2 * i] = v.x * s;
-    f[2 * i + 1] = v.y * s;
-  }
+// square root and reciprocal to about 2 ulp (a step's own rounding)
+__device__ __forceinline__ float sqrt_near(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float recip_near(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // max over the 16 lanes that hold a block of 128
 __device__ __forceinline__ float block_amax(const float (&x)[8]) {
@@ -149,6 +186,37 @@ __device__ __forceinline__ float block_amax(const float (&x)[8]) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   return fmaxf(a, kMinAmax);
+}
+
+// 8 values as e4m3 codes of x / s, s = amax / 448 given as its inverse.  ROOT: x
+// are roots of second moments: a positive one that would round to 0 takes the
+// smallest code, since a later m / (0 + eps) would throw the weight far off.
+template <bool SR, bool ROOT>
+__device__ __forceinline__ Raw<2> encode8(const float (&x)[8], float inv, const uint32_t (&h)[8]) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) unpack2(mul2(pack2(x[i], x[i + 1]), pack2(inv, inv)), y[i], y[i + 1]);
+  float low = fmin3(fabsf(y[0]), fabsf(y[1]), fabsf(y[2]));
+  low = fmin3(low, fabsf(y[3]), fabsf(y[4]));
+  low = fminf(fmin3(low, fabsf(y[5]), fabsf(y[6])), fabsf(y[7]));
+  auto rnd = [&](int i) { return ROOT ? (h[i] >> 12) & 0xFFFF0u : (h[i] << 4) & 0xFFFF0u; };
+  if (low >= kE4m3Normal) {            // nearly always: no value on the grid's subnormal part
+    if constexpr (SR) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = stochastic_normal(y[i], rnd(i));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (SR) y[i] = stochastic_any(y[i], rnd(i));
+      if (ROOT && x[i] > 0.f) y[i] = fmaxf(y[i], 0.001953125f);
+    }
+  }
+  Raw<2> r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.w[i] = e4m3x2(y[4 * i], y[4 * i + 1]) | (e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16);
+  return r;
 }
 
 struct AdamArgs {
@@ -178,106 +246,140 @@ __device__ __forceinline__ double pow_int(double b, uint32_t t) {
   return r;
 }
 
+// `count` consecutive chunks of one tensor, from this thread's element e on
 template <int PK, bool GB, bool E8, bool SR>
-__device__ __forceinline__ void adam_chunk(const biv_opt_tensor& t, int64_t e, const AdamArgs& a,
-                                           const StepScalars& s) {
+__device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t e, int64_t count,
+                                         const AdamArgs& a, const StepScalars& s) {
+  constexpr int GW = GB ? 4 : 8, PW = PK == kParamBf16 ? 4 : 8, SW = E8 ? 2 : 8;
   const int64_t n = t.numel;
+  const void* grad = t.grad;
+  void* weight = PK == kParamMaster ? static_cast<void*>(t.master) : t.param;
+  void *mp = t.m, *vp = t.v;
+  float *ms = t.m_scale, *vs = t.v_scale;
+  void* copy = t.param;                // the master's bf16 copy
   const bool vec = t.vec != 0;
-  float g[8], w[8], m[8], v[8];
-  load8<GB>(t.grad, e, n, vec, g);
-  load8<PK == kParamBf16>(PK == kParamMaster ? t.master : t.param, e, n, vec, w);
-  const int64_t blk = e / kBlk;
-  if constexpr (E8) {
-    uint32_t cm[2], cv[2];
-    load8_codes(static_cast<const uint8_t*>(t.m), e, n, vec, cm);
-    load8_codes(static_cast<const uint8_t*>(t.v), e, n, vec, cv);
-    const float sm = e < n ? t.m_scale[blk] : 0.f, sv = e < n ? t.v_scale[blk] : 0.f;
-    decode8(cm, sm, m);
-    decode8(cv, sv, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= v[i];
-  } else {
-    load8<false>(t.m, e, n, vec, m);
-    load8<false>(t.v, e, n, vec, v);
-  }
-  const float keep = 1.0f - s.lr * t.lr_scale * t.weight_decay;
-  const float rate = s.lr_bc1 * t.lr_scale;
-  float r[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float gi = g[i] * s.coef;
-    m[i] = fmaf(a.b1, m[i], a.c1 * gi);
-    v[i] = fmaf(a.b2, v[i], a.c2 * gi * gi);
-    r[i] = sqrtf(v[i]);
-    w[i] = w[i] * keep - rate * (m[i] / fmaf(r[i], s.rbc2, a.eps));
-  }
-  uint32_t h[8];
-  if constexpr (SR && (E8 || PK == kParamBf16)) {
-    const uint64_t i0 = uint64_t(t.rng_base + e);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t id = i0 + i;
-      h[i] = mix32((uint32_t(id) ^ s.key) + uint32_t(id >> 32) * 0x85EBCA6Bu);
+  const float lr = __fmul_rn(s.lr, t.lr_scale), rate = __fmul_rn(s.lr_bc1, t.lr_scale);
+  const float keep = __fsub_rn(1.0f, __fmul_rn(lr, t.weight_decay));
+  const uint64_t base = uint64_t(t.rng_base);
+  for (int64_t k = 0; k < count; ++k, e += kChunk) {
+    const bool fast = vec && e + 8 <= n;
+    Raw<GW> gr;
+    Raw<PW> wr;
+    Raw<SW> mr, vr;
+    float sm = 0.f, sv = 0.f;
+    const int64_t blk = e / kBlk;
+    if (fast) {
+      load_raw(grad, e, gr);
+      load_raw(weight, e, wr);
+      load_raw(mp, e, mr);
+      load_raw(vp, e, vr);
+    } else {
+      load_raw_slow(grad, e, n, gr);
+      load_raw_slow(weight, e, n, wr);
+      load_raw_slow(mp, e, n, mr);
+      load_raw_slow(vp, e, n, vr);
     }
-  }
-  if constexpr (PK == kParamF32) {
-    store8_f32(static_cast<float*>(t.param), e, n, vec, w);
-  } else {
-    uint32_t b[8];
-    if constexpr (PK == kParamMaster) store8_f32(t.master, e, n, vec, w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (SR && PK == kParamBf16)
-        b[i] = (__float_as_uint(w[i]) + (mix32(h[i] ^ 0x9E3779B9u) & 0xFFFFu)) >> 16;
-      else
-        b[i] = f2bf(w[i]);
+    if (E8 && e < n) {
+      sm = ms[blk];
+      sv = vs[blk];
     }
-    store8_bf16(static_cast<uint16_t*>(t.param), e, n, vec, b);
-  }
-  if constexpr (E8) {
-    const float am = block_amax(m), ar = block_amax(r);
-    const float im = 448.0f / am, ir = 448.0f / ar;
-    uint32_t cm[2] = {0, 0}, cr[2] = {0, 0};
+    uint64_t g[4], w[4], m[4], v[4];
+    to_pairs(gr, g);
+    to_pairs(wr, w);
+    to_pairs(mr, m);
+    to_pairs(vr, v);
+    float mf[8], rf[8], wf[8];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      float ym[2], yr[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ym[j] = m[i + j] * im;
-        yr[j] = r[i + j] * ir;
-        if constexpr (SR) {
-          ym[j] = copysignf(stochastic_e4m3(fabsf(ym[j]), h[i + j] & 0xFFFFu), ym[j]);
-          yr[j] = stochastic_e4m3(yr[j], h[i + j] >> 16);
-        }
-        // a positive root that would round to 0 takes the smallest code:
-        // a later m / (0 + eps) would throw the weight far off
-        if (r[i + j] > 0.f) yr[j] = fmaxf(yr[j], 0.001953125f);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E8) {
+        m[i] = mul2(m[i], pack2(sm, sm));
+        v[i] = mul2(v[i], pack2(sv, sv));
+        v[i] = mul2(v[i], v[i]);
       }
-      cm[i >> 2] |= e4m3x2(ym[0], ym[1]) << (8 * (i & 3));
-      cr[i >> 2] |= e4m3x2(yr[0], yr[1]) << (8 * (i & 3));
+      const uint64_t gi = mul2(g[i], pack2(s.coef, s.coef));
+      m[i] = add2(mul2(pack2(a.b1, a.b1), m[i]), mul2(pack2(a.c1, a.c1), gi));
+      v[i] = add2(mul2(pack2(a.b2, a.b2), v[i]), mul2(mul2(pack2(a.c2, a.c2), gi), gi));
+      unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
+      float v0, v1;
+      unpack2(v[i], v0, v1);
+      // the root is held in 8 bits: exactly rounded; in a step alone, to 2 ulp
+      rf[2 * i] = E8 ? sqrtf(v0) : sqrt_near(v0);
+      rf[2 * i + 1] = E8 ? sqrtf(v1) : sqrt_near(v1);
+      float d0, d1;
+      unpack2(fma2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2), pack2(a.eps, a.eps)), d0, d1);
+      const uint64_t step = mul2(mul2(pack2(rate, rate), m[i]), pack2(recip_near(d0), recip_near(d1)));
+      const uint64_t neg = pack2(-1.0f, -1.0f);
+      w[i] = fma2(step, neg, mul2(w[i], pack2(keep, keep)));
+      unpack2(w[i], wf[2 * i], wf[2 * i + 1]);
     }
-    store8_codes(static_cast<uint8_t*>(t.m), e, n, vec, cm);
-    store8_codes(static_cast<uint8_t*>(t.v), e, n, vec, cr);
-    if ((threadIdx.x & 15) == 0 && e < n) {
-      t.m_scale[blk] = am / 448.0f;
-      t.v_scale[blk] = ar / 448.0f;
+    uint32_t h[8];
+    if constexpr (SR && (E8 || PK == kParamBf16)) {
+      const uint64_t i0 = base + uint64_t(e);
+      const uint32_t hi = uint32_t(i0 >> 32) * 0x85EBCA6Bu;   // (i0 is a multiple of 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = mix32(((uint32_t(i0) + i) ^ s.key) + hi);
     }
-  } else {
-    store8_f32(static_cast<float*>(t.m), e, n, vec, m);
-    store8_f32(static_cast<float*>(t.v), e, n, vec, v);
+    Raw<8> w32;
+    Raw<4> w16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w32.w[i] = __float_as_uint(wf[i]);
+    if constexpr (PK != kParamF32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (SR && PK == kParamBf16) {
+          const uint32_t lo = w32.w[2 * i] + (mix32(h[2 * i] ^ 0x9E3779B9u) & 0xFFFFu);
+          const uint32_t hi = w32.w[2 * i + 1] + (mix32(h[2 * i + 1] ^ 0x9E3779B9u) & 0xFFFFu);
+          w16.w[i] = __byte_perm(lo, hi, 0x7632);
+        } else {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(wf[2 * i], wf[2 * i + 1]);
+          w16.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+      }
+    }
+    Raw<SW> mo, vo;
+    if constexpr (E8) {
+      const float am = block_amax(mf), ar = block_amax(rf);
+      mo = encode8<SR, false>(mf, 448.0f / am, h);
+      vo = encode8<SR, true>(rf, 448.0f / ar, h);
+      if ((threadIdx.x & 15) == 0 && e < n) {
+        ms[blk] = am / 448.0f;
+        vs[blk] = ar / 448.0f;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mo.w[i] = __float_as_uint(mf[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v0, v1;
+        unpack2(v[i], v0, v1);
+        vo.w[2 * i] = __float_as_uint(v0);
+        vo.w[2 * i + 1] = __float_as_uint(v1);
+      }
+    }
+    if (fast) {
+      if constexpr (PK != kParamBf16) store_raw(weight, e, w32);
+      if constexpr (PK != kParamF32) store_raw(copy, e, w16);
+      store_raw(mp, e, mo);
+      store_raw(vp, e, vo);
+    } else {
+      if constexpr (PK != kParamBf16) store_raw_slow(weight, e, n, w32);
+      if constexpr (PK != kParamF32) store_raw_slow(copy, e, n, w16);
+      store_raw_slow(mp, e, n, mo);
+      store_raw_slow(vp, e, n, vo);
+    }
   }
 }
 
 template <int PK, bool SR>
-__device__ __forceinline__ void adam_chunk_by_type(const biv_opt_tensor& t, int64_t e,
-                                                   const AdamArgs& a, const StepScalars& s) {
+__device__ __forceinline__ void adam_run_by_type(const biv_opt_tensor& t, int64_t e, int64_t count,
+                                                 const AdamArgs& a, const StepScalars& s) {
   const bool gb = t.grad_dtype == BIV_BF16, e8 = t.state_dtype == BIV_E4M3;
   if (gb) {
-    if (e8) adam_chunk<PK, true, true, SR>(t, e, a, s);
-    else adam_chunk<PK, true, false, SR>(t, e, a, s);
+    if (e8) adam_run<PK, true, true, SR>(t, e, count, a, s);
+    else adam_run<PK, true, false, SR>(t, e, count, a, s);
   } else {
-    if (e8) adam_chunk<PK, false, true, SR>(t, e, a, s);
-    else adam_chunk<PK, false, false, SR>(t, e, a, s);
+    if (e8) adam_run<PK, false, true, SR>(t, e, count, a, s);
+    else adam_run<PK, false, false, SR>(t, e, count, a, s);
   }
 }
 
@@ -296,23 +398,23 @@ __global__ void __launch_bounds__(kOT) adamw_kernel(const __grid_constant__ Adam
   }
   if (tid == 0) s_bc[0] = float(1.0 - pow_int(a.b1d, step));
   if (tid == 32) s_bc[1] = float(1.0 / sqrt(1.0 - pow_int(a.b2d, step)));
-  __syncthreads();   // also: every thread of the CTA has read the step
-  s.lr = a.lr[0];
-  s.lr_bc1 = s.lr / s_bc[0];
-  s.rbc2 = s_bc[1];
-  s.key = mix32(a.seed_lo + step * 0x9E3779B9u) ^ (a.seed_hi * 0x9E3779B1u);
   const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
-  if (c0 < c1) {
-    int ti = find_tensor(a.t, a.n, c0);
-    for (int64_t c = c0; c < c1; ++c) {
-      while (ti + 1 < a.n && a.t[ti + 1].first_chunk <= c) ++ti;
-      const biv_opt_tensor& t = a.t[ti];
-      const int64_t e = (c - t.first_chunk) * kChunk + tid * kEPT;
-      if (t.param_dtype == BIV_F32) adam_chunk_by_type<kParamF32, SR>(t, e, a, s);
-      else if (t.master) adam_chunk_by_type<kParamMaster, SR>(t, e, a, s);
-      else adam_chunk_by_type<kParamBf16, SR>(t, e, a, s);
-    }
+  int ti = find_tensor(a.t, a.n, c0);
+  __syncthreads();   // also: every thread of the CTA has read the step
+  s.lr = a.lr[0];
+  s.lr_bc1 = __fdiv_rn(s.lr, s_bc[0]);
+  s.rbc2 = s_bc[1];
+  s.key = mix32(a.seed_lo + step * 0x9E3779B9u) ^ (a.seed_hi * 0x9E3779B1u);
+  for (int64_t c = c0; c < c1;) {
+    while (ti + 1 < a.n && a.t[ti + 1].first_chunk <= c) ++ti;
+    const biv_opt_tensor& t = a.t[ti];
+    const int64_t end = ti + 1 < a.n ? min(c1, a.t[ti + 1].first_chunk) : c1;
+    const int64_t e = (c - t.first_chunk) * kChunk + tid * kEPT;
+    if (t.param_dtype == BIV_F32) adam_run_by_type<kParamF32, SR>(t, e, end - c, a, s);
+    else if (t.master) adam_run_by_type<kParamMaster, SR>(t, e, end - c, a, s);
+    else adam_run_by_type<kParamBf16, SR>(t, e, end - c, a, s);
+    c = end;
   }
   // the last CTA to get here stores the new step: every CTA has read the old one
   if (tid == 0) {
@@ -325,18 +427,45 @@ __global__ void __launch_bounds__(kOT) adamw_kernel(const __grid_constant__ Adam
 }
 
 // ------------------------------------------------------------------ norm --
-__device__ __forceinline__ float warp_sum_x(float v) {
+// sums as (value, what its rounding lost)
+struct Sum2 {
+  float hi, lo;
+};
+__device__ __forceinline__ Sum2 two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+__device__ __forceinline__ Sum2 add_sums(Sum2 a, Sum2 b) {
+  Sum2 r = two_sum(a.hi, b.hi);
+  r.lo = __fadd_rn(r.lo, __fadd_rn(a.lo, b.lo));
+  return r;
+}
+// over the warp, by a xor tree
+__device__ __forceinline__ Sum2 warp_sum2(Sum2 v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+    v = add_sums(v, {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
   return v;
 }
 
-// partial u: the squares of chunks [4u, 4u + 4), per thread in chunk order,
-// then a warp xor tree and the warps in order
+template <int W>
+__device__ __forceinline__ void add_squares(const biv_opt_tensor& t, int64_t e, uint64_t (&q)[4]) {
+  Raw<W> r;
+  if (t.vec && e + 8 <= t.numel) load_raw(t.grad, e, r);
+  else load_raw_slow(t.grad, e, t.numel, r);
+  uint64_t f[4];
+  to_pairs(r, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = fma2(f[i], f[i], q[i]);
+}
+
+// partial u: the squares of chunks [4u, 4u + 4): eight sums per thread, over the
+// chunks in order, then all of them with the rounding errors kept: the thread's
+// in order, a warp xor tree, the warps in order
 __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __restrict__ tens,
                                                         int n, int64_t chunks, int64_t units,
-                                                        float* __restrict__ part) {
-  __shared__ float red[kOT / 32];
+                                                        float2* __restrict__ part) {
+  __shared__ Sum2 red[2][kOT / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -344,7 +473,7 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
   if (u0 >= u1) return;
   int ti = find_tensor(tens, n, u0 * kNormChunks);
   for (int64_t u = u0; u < u1; ++u) {
-    float f[kNormChunks][8];
+    uint64_t q[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < kNormChunks; ++k) {
       const int64_t c = u * kNormChunks + k;
@@ -352,57 +481,56 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
         while (ti + 1 < n && tens[ti + 1].first_chunk <= c) ++ti;
         const biv_opt_tensor& t = tens[ti];
         const int64_t e = (c - t.first_chunk) * kChunk + tid * kEPT;
-        if (t.grad_dtype == BIV_BF16) load8<true>(t.grad, e, t.numel, t.vec != 0, f[k]);
-        else load8<false>(t.grad, e, t.numel, t.vec != 0, f[k]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[k][i] = 0.f;
+        if (t.grad_dtype == BIV_BF16) add_squares<4>(t, e, q);
+        else add_squares<8>(t, e, q);
       }
     }
-    float q = 0.f;
+    Sum2 v = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < kNormChunks; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q = fmaf(f[k][i], f[k][i], q);
-    q = warp_sum_x(q);
-    __syncthreads();   // red is free again
-    if ((tid & 31) == 0) red[tid >> 5] = q;
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      unpack2(q[i], a, b);
+      v = add_sums(v, two_sum(a, b));
+    }
+    v = warp_sum2(v);
+    // two rows of partials in turn: one barrier per unit
+    Sum2* row = red[u & 1];
+    if ((tid & 31) == 0) row[tid >> 5] = v;
     __syncthreads();
     if (tid == 0) {
-      float tot = 0.f;
+      Sum2 tot = row[0];
 #pragma unroll
-      for (int i = 0; i < kOT / 32; ++i) tot += red[i];
-      part[u] = tot;
+      for (int i = 1; i < kOT / 32; ++i) tot = add_sums(tot, row[i]);
+      part[u] = make_float2(tot.hi, tot.lo);
     }
   }
 }
 
-// all partials: thread i takes i, i + 1024, ... ascending with the rounding
-// errors carried along, then a warp xor tree and the warps in order
-__global__ void __launch_bounds__(kNT) grad_norm_final_kernel(const float* __restrict__ part,
+// all partials: thread i takes i, i + 1024, ... in order, then a warp xor tree
+// and the warps in order
+__global__ void __launch_bounds__(kNT) grad_norm_final_kernel(const float2* __restrict__ part,
                                                               int64_t units, float max_norm,
                                                               float* __restrict__ out) {
-  __shared__ float red[kNT / 32];
+  __shared__ Sum2 red[kNT / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  float s = 0.f, lost = 0.f;
+  Sum2 v = {0.f, 0.f};
 #pragma unroll 8
   for (int64_t i = tid; i < units; i += kNT) {
-    const float x = part[i], y = s + x, b = y - s;
-    lost += (s - (y - b)) + (x - b);
-    s = y;
+    const float2 p = part[i];
+    v = add_sums(v, {p.x, p.y});
   }
-  if (isfinite(s)) s += lost;
-  s = warp_sum_x(s);
-  if ((tid & 31) == 0) red[tid >> 5] = s;
+  __syncwarp();
+  v = warp_sum2(v);
+  if ((tid & 31) == 0) red[tid >> 5] = v;
   __syncthreads();
   if (tid == 0) {
-    float tot = 0.f;
-    for (int i = 0; i < kNT / 32; ++i) tot += red[i];
-    const float norm = sqrtf(tot);
+    Sum2 tot = red[0];
+    for (int i = 1; i < kNT / 32; ++i) tot = add_sums(tot, red[i]);
+    const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
     out[0] = norm;
-    out[1] = max_norm > 0.f ? fminf(1.0f, max_norm / (norm + 1e-6f)) : 1.0f;
+    out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
   }
 }
 
@@ -492,7 +620,7 @@ biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks) {
 
 biv_status biv_grad_norm_workspace(int64_t chunks, size_t* bytes) {
   BIV_REQUIRE(chunks >= 0 && bytes, "grad_norm_workspace: bad arguments");
-  *bytes = size_t(std::max<int64_t>(1, norm_units(chunks))) * sizeof(float);
+  *bytes = size_t(std::max<int64_t>(1, norm_units(chunks))) * sizeof(float2);
   return BIV_OK;
 }
 
@@ -502,12 +630,12 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
   BIV_REQUIRE(max_norm >= 0.f, "grad_norm: max_norm must not be negative");
   BIV_REQUIRE(out && (tensors || chunks == 0), "grad_norm: null pointer");
   const int64_t units = norm_units(chunks);
-  const size_t need = size_t(std::max<int64_t>(1, units)) * sizeof(float);
+  const size_t need = size_t(std::max<int64_t>(1, units)) * sizeof(float2);
   if (!workspace || workspace_bytes < need)
     return set_error(BIV_ERR_WORKSPACE, "grad_norm: workspace of %zu bytes needed", need);
   BIV_REQUIRE(aligned16(workspace), "grad_norm: workspace must be 16-byte aligned");
   cudaStream_t s = as_cuda(stream);
-  float* part = static_cast<float*>(workspace);
+  float2* part = static_cast<float2*>(workspace);
   if (units > 0) {
     const int sms = sm_count() > 0 ? sm_count() : 148;
     const unsigned grid = unsigned(std::min<int64_t>(units, int64_t(sms) * 8));
@@ -515,7 +643,7 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
     biv_status st = check_launch("grad_norm");
     if (st != BIV_OK) return st;
   }
-  launch_pdl(grad_norm_final_kernel, 1, kNT, 0, s, static_cast<const float*>(part), units, max_norm, out);
+  launch_pdl(grad_norm_final_kernel, 1, kNT, 0, s, static_cast<const float2*>(part), units, max_norm, out);
   return check_launch("grad_norm_final");
 }
 
