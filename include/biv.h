@@ -654,7 +654,7 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
                                   biv_stream_t stream);
 
 /* ------------------------------------------------------ optimizer step --
- * AdamW over many tensors in one launch, writing the model's own weights in
+ * AdamW over many tensors at once, writing the model's own weights in
  * place (captured graphs keep their addresses; BF16 weights that the forward
  * reads, "Finish RL Training Faster", section "让训练前向使用推理的数值").  Per
  * element, in FP32:
@@ -681,7 +681,8 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * half a grid spacing still move the value on average; a rerun repeats it.
  *
  * biv_opt_plan (host only, no launch) checks a HOST array of n tensors and
- * fills first_chunk, rng_base and vec; *chunks receives the launch size.  The
+ * fills first_chunk, rng_base and vec; *chunks receives the launch size and
+ * *kinds which combinations of types occur (each is a launch of its own).  The
  * caller then copies the array to the device.  It refuses null pointers,
  * misaligned elements, unsupported type combinations and tensors whose written
  * ranges overlap. */
@@ -701,10 +702,11 @@ typedef struct {
   int32_t param_dtype, grad_dtype, state_dtype;
   int32_t vec;               /* filled by biv_opt_plan */
 } biv_opt_tensor;
-biv_status biv_opt_plan(biv_opt_tensor* host_tensors, int n, int64_t* chunks);
+biv_status biv_opt_plan(biv_opt_tensor* host_tensors, int n, int64_t* chunks, int* kinds);
 
-/* Global L2 norm of all gradients: out[0] = norm, out[1] = min(1, max_norm /
- * (norm + 1e-6)) (1 when max_norm is 0).  FP32 sums that carry their rounding
+/* Global L2 norm of all gradients: out (float32 [4]) [0] = norm, [1] = min(1,
+ * max_norm / (norm + 1e-6)) (1 when max_norm is 0); [2] must be 0 before the
+ * first call and is 0 again after each, [3] is not used.  FP32 sums that carry their rounding
  * errors along, in one order fixed by the tensors' sizes; a norm beyond about
  * 1.8e19 is not finite.  tensors:
  * device copy of the planned array.  Workspace: biv_grad_norm_workspace bytes,
@@ -713,7 +715,7 @@ biv_status biv_grad_norm_workspace(int64_t chunks, size_t* bytes);
 biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, float max_norm,
                          float* out, void* workspace, size_t workspace_bytes, biv_stream_t stream);
 
-/* One AdamW step.  lr (float32 [1]), step (int32 [2]) and clip (float32 [2],
+/* One AdamW step.  lr (float32 [1]), step (int32 [2]) and clip (float32 [4],
  * biv_grad_norm's out, or NULL for coef = 1) are device memory read by the
  * kernel, so a captured step replays with new values.  step[0] counts the
  * steps taken (0 for new states): the call uses t = step[0] + 1 and stores it;
@@ -722,6 +724,7 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
 typedef struct {
   const biv_opt_tensor* tensors;   /* device */
   int n;
+  int kinds;                       /* biv_opt_plan's */
   int64_t chunks;
   const float* lr;
   const float* clip;

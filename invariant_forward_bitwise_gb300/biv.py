@@ -138,7 +138,7 @@ class OptTensor(C.Structure):
 
 
 class AdamWDesc(C.Structure):
-    _fields_ = [("tensors", C.c_void_p), ("n", C.c_int), ("chunks", C.c_int64),
+    _fields_ = [("tensors", C.c_void_p), ("n", C.c_int), ("kinds", C.c_int), ("chunks", C.c_int64),
                 ("lr", C.c_void_p), ("clip", C.c_void_p), ("step", C.c_void_p),
                 ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_float),
                 ("rounding", C.c_int), ("seed", C.c_uint64)]
@@ -197,7 +197,7 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "biv_attention_backward": ([P, P], I),
         "biv_policy_loss_workspace": ([I, I, P], I), "biv_policy_loss": ([P, P, P, P], I),
         "biv_policy_loss_logits": ([P, P, I64, I, P, I, F, P, P, P, I64, I, P], I),
-        "biv_opt_plan": ([P, I, P], I), "biv_grad_norm_workspace": ([I64, P], I),
+        "biv_opt_plan": ([P, I, P, P], I), "biv_grad_norm_workspace": ([I64, P], I),
         "biv_grad_norm": ([P, I, I64, F, P, P, C.c_size_t, P], I), "biv_adamw": ([P, P], I),
     }
     for name, (args, res) in sig.items():
@@ -220,10 +220,16 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else C.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> C.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return C.c_void_p(stream.cuda_stream)
+    if _raw_stream is not None:
+        return C.c_void_p(_raw_stream(torch.cuda.current_device()))
+    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
 def _check(st: int, what: str):
@@ -563,14 +569,13 @@ def biv_attention_backward(q, k, v, dout, q_pos, k_pos, scale, dq, dk, dv, strea
 
 
 # ---------------------------------------------------------- policy loss --
-def _rows_ok(what, t, dtype, n):
-    """A contiguous vector of at least n values on the current device (None passes)."""
-    if t is None:
+def _rows_ok(what, t, dtype, n, dev):
+    """A contiguous vector of at least n values on device dev."""
+    if t.get_device() == dev and t.dtype is dtype and t.numel() >= n and t.is_contiguous():
         return
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device")
-    if t.dtype != dtype or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {n} values")
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor of at least {n} values")
 
 
 def biv_policy_loss_workspace(T: int, nseq: int) -> int:
@@ -587,37 +592,38 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
     sequence) or [T]; mask uint8 or bool [T]; old_lp, ref_lp float32 [T];
     stats float32 [8]; workspace uint8 of biv_policy_loss_workspace bytes.
     With nseq == T an advantage vector counts as one per sequence."""
-    nseq = seq_start.numel() - 1
+    dev, f32 = torch.cuda.current_device(), torch.float32
+    nseq, nadv = seq_start.numel() - 1, adv.numel()
     if nseq < 0:
         raise ValueError("seq_start needs at least one entry")
-    _rows_ok("seq_start", seq_start, torch.int32, 1)
-    if adv.numel() not in (nseq, T):
+    if nadv != nseq and nadv != T:
         raise ValueError(f"adv must hold {nseq} (sequences) or {T} (rows) values")
-    _rows_ok("adv", adv, torch.float32, 0)
+    _rows_ok("seq_start", seq_start, torch.int32, 1, dev)
+    _rows_ok("adv", adv, f32, 0, dev)
+    _rows_ok("stats", stats, f32, 8, dev)
+    _rows_ok("workspace", workspace, torch.uint8, 0, dev)
     if mask is not None:
-        _rows_ok("mask", mask, torch.bool if mask.dtype == torch.bool else torch.uint8, T)
-    _rows_ok("old_lp", old_lp, torch.float32, T)
-    _rows_ok("ref_lp", ref_lp, torch.float32, T)
-    _rows_ok("stats", stats, torch.float32, 8)
-    _rows_ok("workspace", workspace, torch.uint8, 0)
-    d = PolicyDesc()
-    d.T, d.nseq = T, nseq
-    d.seq_start, d.adv, d.stats = seq_start.data_ptr(), adv.data_ptr(), stats.data_ptr()
-    d.mask = None if mask is None else mask.data_ptr()
-    d.old_lp = None if old_lp is None else old_lp.data_ptr()
-    d.ref_lp = None if ref_lp is None else ref_lp.data_ptr()
-    d.adv_per_row = int(adv.numel() != nseq)
-    d.clip_lo, d.clip_hi, d.dual_clip, d.kl_coef, d.ent_coef = clip_lo, clip_hi, dual_clip, kl_coef, ent_coef
-    d.reduce, d.norm = reduce, norm
-    d.workspace, d.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    return d
+        _rows_ok("mask", mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T, dev)
+        mask = mask.data_ptr()
+    if old_lp is not None:
+        _rows_ok("old_lp", old_lp, f32, T, dev)
+        old_lp = old_lp.data_ptr()
+    if ref_lp is not None:
+        _rows_ok("ref_lp", ref_lp, f32, T, dev)
+        ref_lp = ref_lp.data_ptr()
+    return PolicyDesc(T, nseq, seq_start.data_ptr(), mask, old_lp, ref_lp, adv.data_ptr(), int(nadv != nseq),
+                      clip_lo, clip_hi, dual_clip, kl_coef, ent_coef, reduce, norm, stats.data_ptr(),
+                      workspace.data_ptr(), workspace.numel())
 
 
 def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):
     """lp float32 [T] -> dlp float32 [T] (or None: statistics only) and desc's stats."""
-    _rows_ok("lp", lp, torch.float32, desc.T)
-    _rows_ok("dlp", dlp, torch.float32, desc.T)
-    _check(load().biv_policy_loss(C.byref(desc), _p(lp), _p(dlp), _stream(stream)), "biv_policy_loss")
+    dev = torch.cuda.current_device()
+    _rows_ok("lp", lp, torch.float32, desc.T, dev)
+    if dlp is not None:
+        _rows_ok("dlp", dlp, torch.float32, desc.T, dev)
+        dlp = dlp.data_ptr()
+    _check(load().biv_policy_loss(C.byref(desc), lp.data_ptr(), dlp, _stream(stream)), "biv_policy_loss")
 
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
@@ -627,33 +633,35 @@ def biv_policy_loss_logits(desc: PolicyDesc, logits, target, lp, entropy, dz=Non
                            stream=None):
     """logits float32 or bf16 [T, V] (rows of stride 1) -> lp, entropy float32
     [T] and dz float32 or bf16 [T, V] (None: no gradient; may be logits)."""
+    dev, T = torch.cuda.current_device(), desc.T
+    V = logits.shape[1] if logits.dim() == 2 else -1
     for what, t in (("logits", logits), ("dz", dz)):
         if t is None:
             continue
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        if t.get_device() != dev:
             raise ValueError(f"{what} must be on the current CUDA device")
-        if t.dim() != 2 or t.dtype not in _FLOATS or t.shape[0] < desc.T or t.shape[1] != logits.shape[1] or \
-                (t.shape[1] > 1 and t.stride(1) != 1):
+        if t.dim() != 2 or t.dtype not in _FLOATS or t.shape[0] < T or t.shape[1] != V or \
+                (V > 1 and t.stride(1) != 1):
             raise ValueError(f"{what} must be a float32 or bf16 [T, V] tensor with rows of stride 1")
-    _rows_ok("target", target, torch.int32, desc.T)
-    _rows_ok("lp", lp, torch.float32, desc.T)
-    _rows_ok("entropy", entropy, torch.float32, desc.T)
-    V = logits.shape[1]
+    _rows_ok("target", target, torch.int32, T, dev)
+    _rows_ok("lp", lp, torch.float32, T, dev)
+    _rows_ok("entropy", entropy, torch.float32, T, dev)
     # one row: its stride says nothing, and may be below V
-    ld = max(logits.stride(0), V) if desc.T <= 1 else logits.stride(0)
-    ldz = 0 if dz is None else max(dz.stride(0), V) if desc.T <= 1 else dz.stride(0)
+    ld, zt = logits.stride(0), _FLOATS[logits.dtype]
+    pz, ldz, dt = (None, 0, F32) if dz is None else (dz.data_ptr(), dz.stride(0), _FLOATS[dz.dtype])
+    if T <= 1:
+        ld, ldz = max(ld, V), max(ldz, V)
     _check(load().biv_policy_loss_logits(
-        C.byref(desc), _p(logits), ld, _FLOATS[logits.dtype], _p(target), V, float(inv_temp), _p(lp),
-        _p(entropy), _p(dz), ldz, F32 if dz is None else _FLOATS[dz.dtype], _stream(stream)),
-        "biv_policy_loss_logits")
+        C.byref(desc), logits.data_ptr(), ld, zt, target.data_ptr(), V, inv_temp, lp.data_ptr(),
+        entropy.data_ptr(), pz, ldz, dt, _stream(stream)), "biv_policy_loss_logits")
 
 
 # ------------------------------------------------------- optimizer step --
-def biv_opt_plan(tensors) -> int:
-    """Checks and completes a ctypes array of OptTensor; returns its chunks."""
-    n = C.c_int64(0)
-    _check(load().biv_opt_plan(tensors, len(tensors), C.byref(n)), "biv_opt_plan")
-    return n.value
+def biv_opt_plan(tensors):
+    """Checks and completes a ctypes array of OptTensor; returns (chunks, kinds)."""
+    n, k = C.c_int64(0), C.c_int(0)
+    _check(load().biv_opt_plan(tensors, len(tensors), C.byref(n), C.byref(k)), "biv_opt_plan")
+    return n.value, k.value
 
 
 def biv_grad_norm_workspace(chunks: int) -> int:
@@ -663,7 +671,7 @@ def biv_grad_norm_workspace(chunks: int) -> int:
 
 
 def biv_grad_norm(table, n: int, chunks: int, max_norm, out, ws, stream=None):
-    """table: device copy (uint8) of n planned OptTensors; out float32 [2]."""
+    """table: device copy (uint8) of n planned OptTensors; out float32 [4], zeros before the first call."""
     _check(load().biv_grad_norm(_p(table), n, chunks, float(max_norm), _p(out), _p(ws), ws.numel(),
                                 _stream(stream)), "biv_grad_norm")
 

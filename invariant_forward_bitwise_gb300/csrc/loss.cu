@@ -113,36 +113,66 @@ struct PolicyArgs {
 };
 
 // ------------------------------------------------------------------ rows --
-// the sequence that row t may belong to: the last s < nseq with seq_start[s] <=
-// t (-1: none); it does when also t < seq_start[s + 1]
-__device__ __forceinline__ int find_seq(const int32_t* start, int nseq, int t) {
-  int lo = -1, hi = nseq;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= t) lo = mid; else hi = mid;
+// The sequence that row t may belong to: the last s < nseq with seq_start[s] <=
+// t (-1: none); it does when also t < seq_start[s + 1].
+// Looked for in [lo, hi]:
+__device__ __forceinline__ int find_seq_between(const int32_t* start, int lo, int hi, int t) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= t) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
+// for rows ta <= tb, by a warp that looks at 32 starts at once
+__device__ __forceinline__ void find_seqs_warp(const int32_t* start, int nseq, int ta, int tb, int& sa,
+                                               int& sb) {
+  const int lane = threadIdx.x & 31;
+  int la = -1, ha = nseq, lb = -1, hb = nseq;     // start[la] <= ta < start[ha]
+  while (ha - la > 1 || hb - lb > 1) {
+    const int pa = (ha - la + 31) >> 5, pb = (hb - lb + 31) >> 5;
+    const int ia = la + (lane + 1) * pa, ib = lb + (lane + 1) * pb;
+    const int na = __popc(__ballot_sync(0xffffffffu, ia < ha && start[ia] <= ta));
+    const int nb = __popc(__ballot_sync(0xffffffffu, ib < hb && start[ib] <= tb));
+    la += na * pa;
+    ha = min(ha, la + pa);
+    lb += nb * pb;
+    hb = min(hb, lb + pb);
+  }
+  sa = la;
+  sb = lb;
+}
 
 // a thread's four consecutive rows t0..t0+3: the sequence of each that counts
-// (-1: it does not)
+// (-1: it does not).  Called by whole warps.
 __device__ __forceinline__ void four_seqs(const PolicyArgs& a, const int32_t* start, int64_t t0,
                                           int (&seq)[4]) {
+  const int64_t first = t0 - (threadIdx.x & 31) * 4;   // the warp's rows
+  int sa, sb;
+  find_seqs_warp(start, a.nseq, int(min(first, int64_t(a.T))), int(min(first + 127, int64_t(a.T))), sa, sb);
 #pragma unroll
   for (int i = 0; i < 4; ++i) seq[i] = -1;
   if (t0 >= a.T) return;
-  int s = find_seq(start, a.nseq, int(t0));
+  bool on[4];
+  if (a.mask && t0 + 4 <= a.T && (reinterpret_cast<uintptr_t>(a.mask + t0) & 3) == 0) {
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(a.mask + t0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) on[i] = (m >> (8 * i)) & 0xFFu;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) on[i] = t0 + i < a.T && (!a.mask || a.mask[t0 + i]);
+  }
+  int s = find_seq_between(start, sa, max(sa, sb), int(t0));
   int end = s >= 0 ? start[s + 1] : 0;
+  int next = s + 1 < a.nseq ? start[s + 1] : a.T;      // where the next sequence begins
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = int(t0) + i;
-    if (t < a.T) {
-      while (s + 1 < a.nseq && start[s + 1] <= t) {
-        ++s;
-        end = start[s + 1];
-      }
-      if (s >= 0 && t < end && (!a.mask || a.mask[t])) seq[i] = s;
+    while (t >= next && s + 1 < a.nseq) {
+      ++s;
+      end = start[s + 1];
+      next = s + 1 < a.nseq ? end : a.T;
     }
+    if (on[i] && s >= 0 && t < end) seq[i] = s;
   }
 }
 

@@ -22,17 +22,21 @@ constexpr int kEPT = 8;             // consecutive elements per thread
 constexpr int kChunk = kOT * kEPT;  // elements per chunk
 constexpr int kBlk = 128;           // elements per scale of an 8-bit state
 constexpr int kNormChunks = 4;      // chunks per partial sum of the norm
-constexpr int kNT = 1024;           // threads of the norm's second kernel
+constexpr int kNT = 1024;           // threads that add the norm's partials up
+constexpr int64_t kUnitsHere = 8192;  // partials that the norm's last CTA adds up itself
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 
 enum ParamKind { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
 
-// the tensor that holds chunk c: the last one with first_chunk <= c
+// the tensor that holds chunk c: the last one with first_chunk <= c, found by a
+// warp that looks at 32 at once
 __device__ __forceinline__ int find_tensor(const biv_opt_tensor* t, int n, int64_t c) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t[mid].first_chunk <= c) lo = mid; else hi = mid - 1;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, i = lo + int(threadIdx.x & 31) * step;
+    const int below = __popc(__ballot_sync(0xffffffffu, i < hi && t[i].first_chunk <= c));
+    lo += max(below - 1, 0) * step;
+    hi = min(hi, lo + step);
   }
   return lo;
 }
@@ -62,6 +66,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
@@ -155,13 +164,15 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // bits): normal numbers keep 3 fraction bits, so 20 bits of the float fall
 // away; below 2^-6 the grid is 2^-9 apart
 constexpr float kE4m3Normal = 0.015625f;   // 2^-6
-__device__ __forceinline__ float stochastic_normal(float y, uint32_t rnd16_shl4) {
-  return __uint_as_float((__float_as_uint(y) + rnd16_shl4) & 0xFFF00000u);
+__device__ __forceinline__ float stochastic_normal(float y, uint32_t rnd16) {
+  uint32_t u;   // (a multiply-add: the adders are the busier unit)
+  asm("mad.lo.u32 %0, %1, 16, %2;" : "=r"(u) : "r"(rnd16), "r"(__float_as_uint(y)));
+  return __uint_as_float(u & 0xFFF00000u);
 }
-__device__ __forceinline__ float stochastic_any(float y, uint32_t rnd16_shl4) {
+__device__ __forceinline__ float stochastic_any(float y, uint32_t rnd16) {
   const float a = fabsf(y);
-  const float small = floorf(fmaf(float(rnd16_shl4), 1.0f / 1048576.0f, a * 512.0f)) * (1.0f / 512.0f);
-  return a < kE4m3Normal ? copysignf(small, y) : stochastic_normal(y, rnd16_shl4);
+  const float small = floorf(fmaf(float(rnd16), 1.0f / 65536.0f, a * 512.0f)) * (1.0f / 512.0f);
+  return a < kE4m3Normal ? copysignf(small, y) : stochastic_normal(y, rnd16);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -170,19 +181,45 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // square root and reciprocal to about 2 ulp (a step's own rounding)
 __device__ __forceinline__ float sqrt_near(float x) {
   float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Eight square roots, rounded to nearest: from an approximate reciprocal root y
+// one Newton step on x^2 = v, r = v y + (v - (v y)^2) y / 2, its residual exact by
+// FMA (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  Zeros and the smallest values take sqrtf.
+__device__ __forceinline__ void sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+  float lo = fmin3(f[0], f[1], f[2]);
+  lo = fmin3(lo, f[3], f[4]);
+  lo = fminf(fmin3(lo, f[5], f[6]), f[7]);
+  if (lo >= 1e-30f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float y0, y1;
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(f[2 * i]));
+      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(f[2 * i + 1]));
+      const uint64_t y = pack2(y0, y1), x = mul2(v[i], y);
+      const uint64_t e = fma2(mul2(x, pack2(-1.0f, -1.0f)), x, v[i]);
+      unpack2(fma2(e, mul2(y, pack2(0.5f, 0.5f)), x), r[2 * i], r[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = sqrtf(f[i]);
+  }
 }
 __device__ __forceinline__ float recip_near(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // max over the 16 lanes that hold a block of 128
 __device__ __forceinline__ float block_amax(const float (&x)[8]) {
-  float a = 0.f;
+  float a = fmaxf(fabsf(x[0]), fabsf(x[1]));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+  for (int i = 2; i < 8; i += 2) a = fmax3(a, fabsf(x[i]), fabsf(x[i + 1]));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   return fmaxf(a, kMinAmax);
@@ -196,20 +233,22 @@ __device__ __forceinline__ Raw<2> encode8(const float (&x)[8], float inv, const 
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; i += 2) unpack2(mul2(pack2(x[i], x[i + 1]), pack2(inv, inv)), y[i], y[i + 1]);
-  float low = fmin3(fabsf(y[0]), fabsf(y[1]), fabsf(y[2]));
-  low = fmin3(low, fabsf(y[3]), fabsf(y[4]));
-  low = fminf(fmin3(low, fabsf(y[5]), fabsf(y[6])), fabsf(y[7]));
-  auto rnd = [&](int i) { return ROOT ? (h[i] >> 12) & 0xFFFF0u : (h[i] << 4) & 0xFFFF0u; };
-  if (low >= kE4m3Normal) {            // nearly always: no value on the grid's subnormal part
-    if constexpr (SR) {
+  auto rnd = [&](int i) { return ROOT ? h[i] >> 16 : h[i] & 0xFFFFu; };
+  if (SR || ROOT) {
+    float low = fmin3(fabsf(y[0]), fabsf(y[1]), fabsf(y[2]));
+    low = fmin3(low, fabsf(y[3]), fabsf(y[4]));
+    low = fminf(fmin3(low, fabsf(y[5]), fabsf(y[6])), fabsf(y[7]));
+    if (low >= kE4m3Normal) {          // nearly always: no value on the grid's subnormal part
+      if constexpr (SR) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = stochastic_normal(y[i], rnd(i));
-    }
-  } else {
+        for (int i = 0; i < 8; ++i) y[i] = stochastic_normal(y[i], rnd(i));
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (SR) y[i] = stochastic_any(y[i], rnd(i));
-      if (ROOT && x[i] > 0.f) y[i] = fmaxf(y[i], 0.001953125f);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (SR) y[i] = stochastic_any(y[i], rnd(i));
+        if (ROOT && x[i] > 0.f) y[i] = fmaxf(y[i], 0.001953125f);
+      }
     }
   }
   Raw<2> r;
@@ -246,146 +285,284 @@ __device__ __forceinline__ double pow_int(double b, uint32_t t) {
   return r;
 }
 
-// `count` consecutive chunks of one tensor, from this thread's element e on
+// What a chunk is made of: PK the weight's kind, GB bf16 gradients, E8 8-bit
+// states, SR stochastic rounding.
 template <int PK, bool GB, bool E8, bool SR>
-__device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t e, int64_t count,
-                                         const AdamArgs& a, const StepScalars& s) {
-  constexpr int GW = GB ? 4 : 8, PW = PK == kParamBf16 ? 4 : 8, SW = E8 ? 2 : 8;
-  const int64_t n = t.numel;
-  const void* grad = t.grad;
-  void* weight = PK == kParamMaster ? static_cast<void*>(t.master) : t.param;
-  void *mp = t.m, *vp = t.v;
-  float *ms = t.m_scale, *vs = t.v_scale;
-  void* copy = t.param;                // the master's bf16 copy
-  const bool vec = t.vec != 0;
-  const float lr = __fmul_rn(s.lr, t.lr_scale), rate = __fmul_rn(s.lr_bc1, t.lr_scale);
-  const float keep = __fsub_rn(1.0f, __fmul_rn(lr, t.weight_decay));
-  const uint64_t base = uint64_t(t.rng_base);
-  for (int64_t k = 0; k < count; ++k, e += kChunk) {
-    const bool fast = vec && e + 8 <= n;
-    Raw<GW> gr;
-    Raw<PW> wr;
-    Raw<SW> mr, vr;
-    float sm = 0.f, sv = 0.f;
-    const int64_t blk = e / kBlk;
-    if (fast) {
-      load_raw(grad, e, gr);
-      load_raw(weight, e, wr);
-      load_raw(mp, e, mr);
-      load_raw(vp, e, vr);
-    } else {
-      load_raw_slow(grad, e, n, gr);
-      load_raw_slow(weight, e, n, wr);
-      load_raw_slow(mp, e, n, mr);
-      load_raw_slow(vp, e, n, vr);
+struct Kind {
+  static constexpr int GW = GB ? 4 : 8, PW = PK == kParamBf16 ? 4 : 8, SW = E8 ? 2 : 8;
+  Raw<GW> g;
+  Raw<PW> w;
+  Raw<SW> m, v;
+  float sm, sv;           // scales of m, v (8-bit states)
+  Raw<4> w16;             // a master's bf16 copy
+};
+
+struct TensorScalars {
+  float keep, rate;       // 1 - lr wd; lr / (1 - b1^t)
+};
+
+// The update of a thread's 8 elements, in place; id: the first one's number for
+// the random bits.
+template <int PK, bool GB, bool E8, bool SR>
+__device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArgs& a,
+                                          const StepScalars& s, const TensorScalars& ts, uint64_t id) {
+  uint64_t g[4], w[4], m[4], v[4];
+  to_pairs(d.g, g);
+  to_pairs(d.w, w);
+  to_pairs(d.m, m);
+  to_pairs(d.v, v);
+  float mf[8], rf[8], wf[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (E8) {
+      m[i] = mul2(m[i], pack2(d.sm, d.sm));
+      v[i] = mul2(v[i], pack2(d.sv, d.sv));
+      v[i] = mul2(v[i], v[i]);
     }
-    if (E8 && e < n) {
-      sm = ms[blk];
-      sv = vs[blk];
-    }
-    uint64_t g[4], w[4], m[4], v[4];
-    to_pairs(gr, g);
-    to_pairs(wr, w);
-    to_pairs(mr, m);
-    to_pairs(vr, v);
-    float mf[8], rf[8], wf[8];
+    const uint64_t gi = mul2(g[i], pack2(s.coef, s.coef));
+    m[i] = add2(mul2(pack2(a.b1, a.b1), m[i]), mul2(pack2(a.c1, a.c1), gi));
+    v[i] = add2(mul2(pack2(a.b2, a.b2), v[i]), mul2(mul2(pack2(a.c2, a.c2), gi), gi));
+    unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
+  }
+  // the root is held in 8 bits: rounded to nearest; in a step alone, to 2 ulp
+  if constexpr (E8) {
+    sqrt8(v, rf);
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (E8) {
-        m[i] = mul2(m[i], pack2(sm, sm));
-        v[i] = mul2(v[i], pack2(sv, sv));
-        v[i] = mul2(v[i], v[i]);
-      }
-      const uint64_t gi = mul2(g[i], pack2(s.coef, s.coef));
-      m[i] = add2(mul2(pack2(a.b1, a.b1), m[i]), mul2(pack2(a.c1, a.c1), gi));
-      v[i] = add2(mul2(pack2(a.b2, a.b2), v[i]), mul2(mul2(pack2(a.c2, a.c2), gi), gi));
-      unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
       float v0, v1;
       unpack2(v[i], v0, v1);
-      // the root is held in 8 bits: exactly rounded; in a step alone, to 2 ulp
-      rf[2 * i] = E8 ? sqrtf(v0) : sqrt_near(v0);
-      rf[2 * i + 1] = E8 ? sqrtf(v1) : sqrt_near(v1);
-      float d0, d1;
-      unpack2(fma2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2), pack2(a.eps, a.eps)), d0, d1);
-      const uint64_t step = mul2(mul2(pack2(rate, rate), m[i]), pack2(recip_near(d0), recip_near(d1)));
-      const uint64_t neg = pack2(-1.0f, -1.0f);
-      w[i] = fma2(step, neg, mul2(w[i], pack2(keep, keep)));
-      unpack2(w[i], wf[2 * i], wf[2 * i + 1]);
+      rf[2 * i] = sqrt_near(v0);
+      rf[2 * i + 1] = sqrt_near(v1);
     }
-    uint32_t h[8];
-    if constexpr (SR && (E8 || PK == kParamBf16)) {
-      const uint64_t i0 = base + uint64_t(e);
-      const uint32_t hi = uint32_t(i0 >> 32) * 0x85EBCA6Bu;   // (i0 is a multiple of 8)
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = mix32(((uint32_t(i0) + i) ^ s.key) + hi);
+  for (int i = 0; i < 4; ++i) {
+    float d0, d1;
+    unpack2(fma2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2), pack2(a.eps, a.eps)), d0, d1);
+    const uint64_t back = mul2(mul2(pack2(-ts.rate, -ts.rate), m[i]), pack2(recip_near(d0), recip_near(d1)));
+    w[i] = fma2(w[i], pack2(ts.keep, ts.keep), back);
+    unpack2(w[i], wf[2 * i], wf[2 * i + 1]);
+  }
+  uint32_t h[8];
+  if constexpr (SR && (E8 || PK == kParamBf16)) {
+    const uint32_t hi = uint32_t(id >> 32) * 0x85EBCA6Bu;   // (id is a multiple of 8)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = mix32(((uint32_t(id) + i) ^ s.key) + hi);
+  }
+  if constexpr (PK != kParamBf16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d.w.w[i] = __float_as_uint(wf[i]);
+  }
+  if constexpr (PK != kParamF32) {
+    Raw<4> b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (SR && PK == kParamBf16) {
+        const uint32_t lo = __float_as_uint(wf[2 * i]) + (mix32(h[2 * i] ^ 0x9E3779B9u) & 0xFFFFu);
+        const uint32_t hi = __float_as_uint(wf[2 * i + 1]) + (mix32(h[2 * i + 1] ^ 0x9E3779B9u) & 0xFFFFu);
+        b.w[i] = __byte_perm(lo, hi, 0x7632);
+      } else {
+        const __nv_bfloat162 c = __floats2bfloat162_rn(wf[2 * i], wf[2 * i + 1]);
+        b.w[i] = *reinterpret_cast<const uint32_t*>(&c);
+      }
     }
-    Raw<8> w32;
-    Raw<4> w16;
+    if constexpr (PK == kParamBf16) d.w = b; else d.w16 = b;
+  }
+  if constexpr (E8) {
+    const float am = block_amax(mf), ar = block_amax(rf);
+    // 448 / am, 448 / ar, am / 448, ar / 448: one division, a quarter of the lanes each
+    const int role = threadIdx.x & 3;
+    const float amax = role & 1 ? ar : am;
+    const float q = __fdiv_rn(role < 2 ? 448.0f : amax, role < 2 ? amax : 448.0f);
+    const int first = threadIdx.x & 28;            // (a lane of the same block)
+    d.m = encode8<SR, false>(mf, __shfl_sync(0xffffffffu, q, first), h);
+    d.v = encode8<SR, true>(rf, __shfl_sync(0xffffffffu, q, first + 1), h);
+    d.sm = __shfl_sync(0xffffffffu, q, first + 2);
+    d.sv = __shfl_sync(0xffffffffu, q, first + 3);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w32.w[i] = __float_as_uint(wf[i]);
-    if constexpr (PK != kParamF32) {
+    for (int i = 0; i < 8; ++i) d.m.w[i] = __float_as_uint(mf[i]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (SR && PK == kParamBf16) {
-          const uint32_t lo = w32.w[2 * i] + (mix32(h[2 * i] ^ 0x9E3779B9u) & 0xFFFFu);
-          const uint32_t hi = w32.w[2 * i + 1] + (mix32(h[2 * i + 1] ^ 0x9E3779B9u) & 0xFFFFu);
-          w16.w[i] = __byte_perm(lo, hi, 0x7632);
-        } else {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(wf[2 * i], wf[2 * i + 1]);
-          w16.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < 4; ++i) {
+      float v0, v1;
+      unpack2(v[i], v0, v1);
+      d.v.w[2 * i] = __float_as_uint(v0);
+      d.v.w[2 * i + 1] = __float_as_uint(v1);
+    }
+  }
+}
+
+// Asynchronous copy of a thread's 8 elements into its own place of a staging
+// area in shared memory (only that thread reads them: no barrier), and back.
+// An array's area of a stage holds 16-byte pieces (8-bit codes: 8), one after
+// the other for the 256 threads.
+template <int W>
+__device__ __forceinline__ void stage_async(const uint8_t* q, uint32_t slot) {
+  if constexpr (W == 2) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + threadIdx.x * 8), "l"(q) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + threadIdx.x * 16 + i / 4 * kOT * 16),
+                   "l"(q + i * 4)
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void stage_async4(const float* p, uint32_t slot) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + threadIdx.x * 4), "l"(p) : "memory");
+}
+template <int W>
+__device__ __forceinline__ void from_stage(const uint8_t* slot, Raw<W>& r) {
+  if constexpr (W == 2) {
+    const uint2 v = reinterpret_cast<const uint2*>(slot)[threadIdx.x];
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+      const uint4 v = reinterpret_cast<const uint4*>(slot)[i / 4 * kOT + threadIdx.x];
+      r.w[i] = v.x; r.w[i + 1] = v.y; r.w[i + 2] = v.z; r.w[i + 3] = v.w;
+    }
+  }
+}
+constexpr int kStages = 3;
+template <int GW, int PW>
+struct StageLayout {   // a stage: gradient, weight, codes, scales
+  static constexpr int W = kOT * GW * 4, M = W + kOT * PW * 4, V = M + kOT * 8, MS = V + kOT * 8,
+                       VS = MS + kOT * 4, BYTES = VS + kOT * 4;
+};
+
+// `count` consecutive chunks of one tensor, the first one number `chunk` of it.
+// Full chunks of 16-byte aligned arrays take the fast way.  With 8-bit states a
+// chunk is few bytes and much arithmetic: its arrays are copied to shared memory
+// two chunks ahead, so that loads are in flight while a warp computes, at no
+// register's cost.
+template <int PK, bool GB, bool E8, bool SR>
+__device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk, int64_t count,
+                                         const AdamArgs& a, const StepScalars& s, uint8_t* stages) {
+  using K = Kind<PK, GB, E8, SR>;
+  using L = StageLayout<K::GW, K::PW>;
+  const int64_t n = t.numel, e0 = chunk * kChunk + threadIdx.x * kEPT;
+  TensorScalars ts;
+  ts.rate = __fmul_rn(s.lr_bc1, t.lr_scale);
+  ts.keep = __fsub_rn(1.0f, __fmul_rn(__fmul_rn(s.lr, t.lr_scale), t.weight_decay));
+  void* weight = PK == kParamMaster ? static_cast<void*>(t.master) : t.param;
+  const int64_t full = t.vec ? min(count, max(int64_t(0), n / kChunk - chunk)) : 0;
+  const uint64_t id0 = uint64_t(t.rng_base + e0);
+  {
+    const uint8_t* pg = static_cast<const uint8_t*>(t.grad) + e0 * (K::GW / 2);
+    uint8_t* pw = static_cast<uint8_t*>(weight) + e0 * (K::PW / 2);
+    uint8_t* pc = static_cast<uint8_t*>(t.param) + e0 * 2;
+    uint8_t* pm = static_cast<uint8_t*>(t.m) + e0 * (K::SW / 2);
+    uint8_t* pv = static_cast<uint8_t*>(t.v) + e0 * (K::SW / 2);
+    float* pms = t.m_scale + e0 / kBlk;
+    float* pvs = t.v_scale + e0 / kBlk;
+    constexpr int kGB = kChunk * K::GW / 2, kPB = kChunk * K::PW / 2, kSB = kChunk * K::SW / 2;
+    const uint32_t st0 = smem_u32(stages);
+    int in = 0, out = 0;                 // stage to fill, stage to read
+    int64_t left = full;                 // chunks still to be copied ahead
+    auto ahead = [&]() {                 // (the copies run kStages - 1 chunks before the pointers)
+      constexpr int D = kStages - 1;
+      if (left > 0) {
+        const uint32_t st = st0 + uint32_t(in) * L::BYTES;
+        stage_async<K::GW>(pg + D * kGB, st);
+        stage_async<K::PW>(pw + D * kPB, st + L::W);
+        stage_async<K::SW>(pm + D * kSB, st + L::M);
+        stage_async<K::SW>(pv + D * kSB, st + L::V);
+        stage_async4(pms + D * (kChunk / kBlk), st + L::MS);
+        stage_async4(pvs + D * (kChunk / kBlk), st + L::VS);
+        in = in == kStages - 1 ? 0 : in + 1;
+      }
+      --left;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto advance = [&](int k) {
+      pg += k * kGB; pw += k * kPB; pc += k * kChunk * 2; pm += k * kSB; pv += k * kSB;
+      pms += k * (kChunk / kBlk); pvs += k * (kChunk / kBlk);
+    };
+    if constexpr (E8) {
+      advance(-(kStages - 1));
+#pragma unroll
+      for (int k = 0; k < kStages - 1; ++k) {
+        ahead();
+        advance(1);
+      }
+    }
+    for (int64_t k = 0; k < full; ++k) {
+      K d;
+      if constexpr (E8) {
+        ahead();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        const uint8_t* st = stages + out * L::BYTES;
+        out = out == kStages - 1 ? 0 : out + 1;
+        from_stage(st, d.g);
+        from_stage(st + L::W, d.w);
+        from_stage(st + L::M, d.m);
+        from_stage(st + L::V, d.v);
+        d.sm = reinterpret_cast<const float*>(st + L::MS)[threadIdx.x];
+        d.sv = reinterpret_cast<const float*>(st + L::VS)[threadIdx.x];
+      } else {
+        load_raw(pg, 0, d.g);
+        load_raw(pw, 0, d.w);
+        load_raw(pm, 0, d.m);
+        load_raw(pv, 0, d.v);
+      }
+      adam_math(d, a, s, ts, id0 + uint64_t(k) * kChunk);
+      store_raw(pw, 0, d.w);
+      if constexpr (PK == kParamMaster) store_raw(pc, 0, d.w16);
+      store_raw(pm, 0, d.m);
+      store_raw(pv, 0, d.v);
+      if constexpr (E8) {
+        if ((threadIdx.x & 15) == 0) {
+          *pms = d.sm;
+          *pvs = d.sv;
         }
       }
+      advance(1);
     }
-    Raw<SW> mo, vo;
-    if constexpr (E8) {
-      const float am = block_amax(mf), ar = block_amax(rf);
-      mo = encode8<SR, false>(mf, 448.0f / am, h);
-      vo = encode8<SR, true>(rf, 448.0f / ar, h);
-      if ((threadIdx.x & 15) == 0 && e < n) {
-        ms[blk] = am / 448.0f;
-        vs[blk] = ar / 448.0f;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) mo.w[i] = __float_as_uint(mf[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v0, v1;
-        unpack2(v[i], v0, v1);
-        vo.w[2 * i] = __float_as_uint(v0);
-        vo.w[2 * i + 1] = __float_as_uint(v1);
-      }
+    if constexpr (E8) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  // the tensor's last chunk, and tensors of any alignment
+  for (int64_t k = full; k < count; ++k) {
+    const int64_t x = e0 + k * kChunk, blk = x >> 7;
+    static_assert(kBlk == 128, "x >> 7");
+    K d;
+    load_raw_slow(t.grad, x, n, d.g);
+    load_raw_slow(weight, x, n, d.w);
+    load_raw_slow(t.m, x, n, d.m);
+    load_raw_slow(t.v, x, n, d.v);
+    d.sm = d.sv = 0.f;
+    if (E8 && x < n) {
+      d.sm = t.m_scale[blk];
+      d.sv = t.v_scale[blk];
     }
-    if (fast) {
-      if constexpr (PK != kParamBf16) store_raw(weight, e, w32);
-      if constexpr (PK != kParamF32) store_raw(copy, e, w16);
-      store_raw(mp, e, mo);
-      store_raw(vp, e, vo);
-    } else {
-      if constexpr (PK != kParamBf16) store_raw_slow(weight, e, n, w32);
-      if constexpr (PK != kParamF32) store_raw_slow(copy, e, n, w16);
-      store_raw_slow(mp, e, n, mo);
-      store_raw_slow(vp, e, n, vo);
+    adam_math(d, a, s, ts, id0 + uint64_t(k) * kChunk);
+    store_raw_slow(weight, x, n, d.w);
+    if constexpr (PK == kParamMaster) store_raw_slow(t.param, x, n, d.w16);
+    store_raw_slow(t.m, x, n, d.m);
+    store_raw_slow(t.v, x, n, d.v);
+    if (E8 && (threadIdx.x & 15) == 0 && x < n) {
+      t.m_scale[blk] = d.sm;
+      t.v_scale[blk] = d.sv;
     }
   }
 }
 
-template <int PK, bool SR>
-__device__ __forceinline__ void adam_run_by_type(const biv_opt_tensor& t, int64_t e, int64_t count,
-                                                 const AdamArgs& a, const StepScalars& s) {
-  const bool gb = t.grad_dtype == BIV_BF16, e8 = t.state_dtype == BIV_E4M3;
-  if (gb) {
-    if (e8) adam_run<PK, true, true, SR>(t, e, count, a, s);
-    else adam_run<PK, true, false, SR>(t, e, count, a, s);
-  } else {
-    if (e8) adam_run<PK, false, true, SR>(t, e, count, a, s);
-    else adam_run<PK, false, false, SR>(t, e, count, a, s);
-  }
+__host__ __device__ inline int kind_of(const biv_opt_tensor& t) {
+  const int pk = t.param_dtype == BIV_F32 ? kParamF32 : t.master ? kParamMaster : kParamBf16;
+  return pk * 4 + (t.grad_dtype == BIV_BF16 ? 2 : 0) + (t.state_dtype == BIV_E4M3 ? 1 : 0);
 }
 
-template <bool SR>
-__global__ void __launch_bounds__(kOT) adamw_kernel(const __grid_constant__ AdamArgs a) {
+// The tensors of one kind (others are passed over); `last`: the call's last
+// launch, which counts the step.
+template <int PK, bool GB, bool E8, bool SR>
+__global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamArgs a, int last) {
+  constexpr int kKind = PK * 4 + (GB ? 2 : 0) + (E8 ? 1 : 0);
   __shared__ float s_bc[2];
+  extern __shared__ __align__(16) uint8_t stages[];
+  const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
+  const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
+  int ti = find_tensor(a.t, a.n, c0);   // (the table is the host's: no kernel writes it)
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -398,9 +575,6 @@ __global__ void __launch_bounds__(kOT) adamw_kernel(const __grid_constant__ Adam
   }
   if (tid == 0) s_bc[0] = float(1.0 - pow_int(a.b1d, step));
   if (tid == 32) s_bc[1] = float(1.0 / sqrt(1.0 - pow_int(a.b2d, step)));
-  const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
-  const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
-  int ti = find_tensor(a.t, a.n, c0);
   __syncthreads();   // also: every thread of the CTA has read the step
   s.lr = a.lr[0];
   s.lr_bc1 = __fdiv_rn(s.lr, s_bc[0]);
@@ -410,14 +584,11 @@ __global__ void __launch_bounds__(kOT) adamw_kernel(const __grid_constant__ Adam
     while (ti + 1 < a.n && a.t[ti + 1].first_chunk <= c) ++ti;
     const biv_opt_tensor& t = a.t[ti];
     const int64_t end = ti + 1 < a.n ? min(c1, a.t[ti + 1].first_chunk) : c1;
-    const int64_t e = (c - t.first_chunk) * kChunk + tid * kEPT;
-    if (t.param_dtype == BIV_F32) adam_run_by_type<kParamF32, SR>(t, e, end - c, a, s);
-    else if (t.master) adam_run_by_type<kParamMaster, SR>(t, e, end - c, a, s);
-    else adam_run_by_type<kParamBf16, SR>(t, e, end - c, a, s);
+    if (kind_of(t) == kKind) adam_run<PK, GB, E8, SR>(t, c - t.first_chunk, end - c, a, s, stages);
     c = end;
   }
   // the last CTA to get here stores the new step: every CTA has read the old one
-  if (tid == 0) {
+  if (last && tid == 0) {
     __threadfence();
     if (atomicAdd(a.step + 1, 1) == int(gridDim.x) - 1) {
       a.step[0] = int32_t(step);
@@ -448,41 +619,98 @@ __device__ __forceinline__ Sum2 warp_sum2(Sum2 v) {
   return v;
 }
 
+// the squares of a thread's 8 values of `n` chunks, all loads first
+template <int W, int N>
+__device__ __forceinline__ void add_squares(const uint8_t* p, uint64_t (&q)[4]) {
+  Raw<W> r[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) load_raw(p, int64_t(k) * kChunk, r[k]);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint64_t f[4];
+    to_pairs(r[k], f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = fma2(f[i], f[i], q[i]);
+  }
+}
 template <int W>
-__device__ __forceinline__ void add_squares(const biv_opt_tensor& t, int64_t e, uint64_t (&q)[4]) {
+__device__ __forceinline__ void add_squares_slow(const biv_opt_tensor& t, int64_t e, uint64_t (&q)[4]) {
   Raw<W> r;
-  if (t.vec && e + 8 <= t.numel) load_raw(t.grad, e, r);
-  else load_raw_slow(t.grad, e, t.numel, r);
+  load_raw_slow(t.grad, e, t.numel, r);
   uint64_t f[4];
   to_pairs(r, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) q[i] = fma2(f[i], f[i], q[i]);
 }
 
+// All partials: thread i of 1024 takes i, i + 1024, ... in order, then a warp xor
+// tree and the warps in order.  By NT threads, each in the place of 1024 / NT.
+template <int NT>
+__device__ __forceinline__ void norm_total(const float2* part, int64_t units, float max_norm, float* out,
+                                           Sum2 (&red)[kNT / 32]) {
+  const int tid = threadIdx.x;
+#pragma unroll
+  for (int k = 0; k < kNT / NT; ++k) {
+    Sum2 v = {0.f, 0.f};
+#pragma unroll 8
+    for (int64_t i = k * NT + tid; i < units; i += kNT) {
+      const float2 p = __ldcg(part + i);
+      v = add_sums(v, {p.x, p.y});
+    }
+    __syncwarp();
+    v = warp_sum2(v);
+    if ((tid & 31) == 0) red[(k * NT + tid) >> 5] = v;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    Sum2 tot = red[0];
+    for (int i = 1; i < kNT / 32; ++i) tot = add_sums(tot, red[i]);
+    const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
+    out[0] = norm;
+    out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
+  }
+}
+
 // partial u: the squares of chunks [4u, 4u + 4): eight sums per thread, over the
 // chunks in order, then all of them with the rounding errors kept: the thread's
-// in order, a warp xor tree, the warps in order
+// in order, a warp xor tree, the warps in order.  `here`: the last CTA to be done
+// adds the partials up too (few of them), counted in out[2].
 __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __restrict__ tens,
                                                         int n, int64_t chunks, int64_t units,
-                                                        float2* __restrict__ part) {
-  __shared__ Sum2 red[2][kOT / 32];
+                                                        float2* __restrict__ part, int here,
+                                                        float max_norm, float* out) {
+  __shared__ Sum2 red[2][kOT / 32], total[kNT / 32];
+  __shared__ bool s_last;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (int64_t(blockIdx.x) + 1) / gridDim.x;
+  int ti = find_tensor(tens, n, u0 * kNormChunks);   // (the table is the host's: no kernel writes it)
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (int64_t(blockIdx.x) + 1) / gridDim.x;
-  if (u0 >= u1) return;
-  int ti = find_tensor(tens, n, u0 * kNormChunks);
   for (int64_t u = u0; u < u1; ++u) {
     uint64_t q[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < kNormChunks; ++k) {
-      const int64_t c = u * kNormChunks + k;
-      if (c < chunks) {
+    const int64_t c0 = u * kNormChunks;
+    while (ti + 1 < n && tens[ti + 1].first_chunk <= c0) ++ti;
+    const biv_opt_tensor& t = tens[ti];
+    const int64_t in = c0 - t.first_chunk;     // chunk of the tensor
+    if (t.vec && (in + kNormChunks) * kChunk <= t.numel) {
+      const int64_t e = in * kChunk + tid * kEPT;
+      const uint8_t* g = static_cast<const uint8_t*>(t.grad);
+      if (t.grad_dtype == BIV_BF16) add_squares<4, kNormChunks>(g + e * 2, q);
+      else add_squares<8, kNormChunks>(g + e * 4, q);
+    } else {
+      for (int64_t c = c0; c < min(c0 + kNormChunks, chunks); ++c) {
         while (ti + 1 < n && tens[ti + 1].first_chunk <= c) ++ti;
-        const biv_opt_tensor& t = tens[ti];
-        const int64_t e = (c - t.first_chunk) * kChunk + tid * kEPT;
-        if (t.grad_dtype == BIV_BF16) add_squares<4>(t, e, q);
-        else add_squares<8>(t, e, q);
+        const biv_opt_tensor& x = tens[ti];
+        const int64_t e = (c - x.first_chunk) * kChunk + tid * kEPT;
+        const uint8_t* g = static_cast<const uint8_t*>(x.grad);
+        const bool bf = x.grad_dtype == BIV_BF16;
+        if (x.vec && (c - x.first_chunk + 1) * kChunk <= x.numel) {
+          if (bf) add_squares<4, 1>(g + e * 2, q);
+          else add_squares<8, 1>(g + e * 4, q);
+        } else {
+          if (bf) add_squares_slow<4>(x, e, q);
+          else add_squares_slow<8>(x, e, q);
+        }
       }
     }
     Sum2 v = {0.f, 0.f};
@@ -504,37 +732,68 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
       part[u] = make_float2(tot.hi, tot.lo);
     }
   }
+  if (!here) return;
+  if (tid == 0) {
+    __threadfence();
+    s_last = atomicAdd(reinterpret_cast<unsigned*>(out) + 2, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (s_last) {
+    __threadfence();
+    norm_total<kOT>(part, units, max_norm, out, total);
+    if (tid == 0) reinterpret_cast<unsigned*>(out)[2] = 0;
+  }
 }
 
-// all partials: thread i takes i, i + 1024, ... in order, then a warp xor tree
-// and the warps in order
 __global__ void __launch_bounds__(kNT) grad_norm_final_kernel(const float2* __restrict__ part,
                                                               int64_t units, float max_norm,
                                                               float* __restrict__ out) {
   __shared__ Sum2 red[kNT / 32];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x;
-  Sum2 v = {0.f, 0.f};
-#pragma unroll 8
-  for (int64_t i = tid; i < units; i += kNT) {
-    const float2 p = part[i];
-    v = add_sums(v, {p.x, p.y});
-  }
-  __syncwarp();
-  v = warp_sum2(v);
-  if ((tid & 31) == 0) red[tid >> 5] = v;
-  __syncthreads();
-  if (tid == 0) {
-    Sum2 tot = red[0];
-    for (int i = 1; i < kNT / 32; ++i) tot = add_sums(tot, red[i]);
-    const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
-    out[0] = norm;
-    out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
-  }
+  norm_total<kNT>(part, units, max_norm, out, red);
 }
 
 int64_t norm_units(int64_t chunks) { return (chunks + kNormChunks - 1) / kNormChunks; }
+
+constexpr int kKinds = 12;
+
+template <int PK, bool GB, bool E8, bool SR>
+biv_status launch_adamw(const AdamArgs& a, bool last, cudaStream_t s) {
+  using L = StageLayout<GB ? 4 : 8, PK == kParamBf16 ? 4 : 8>;
+  constexpr int kSmem = E8 ? kStages * L::BYTES : 0;
+  auto kern = adamw_kernel<PK, GB, E8, SR>;
+  if (kSmem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+    return set_error(BIV_ERR_CUDA, "adamw: cannot set the shared memory size: %s",
+                     cudaGetErrorString(cudaGetLastError()));
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  // six chunks a CTA at least, where there are enough for two CTAs per SM (3.5 M
+  // weights: 25 us against 33 us for one or two chunks), and 16 CTAs per SM at
+  // most, so that the faster SMs take more (714 M weights with 8-bit states: 1510
+  // us against 1807 us for two long CTAs per SM)
+  const int64_t most = std::max<int64_t>(2 * sms, a.chunks / 6);
+  const unsigned grid = unsigned(std::min(a.chunks, std::min<int64_t>(most, int64_t(sms) * 16)));
+  launch_pdl(kern, grid, kOT, kSmem, s, a, int(last));
+  return check_launch("adamw");
+}
+template <bool SR>
+biv_status launch_kind(int kind, const AdamArgs& a, bool last, cudaStream_t s) {
+  switch (kind) {
+    case 0: return launch_adamw<0, false, false, SR>(a, last, s);
+    case 1: return launch_adamw<0, false, true, SR>(a, last, s);
+    case 2: return launch_adamw<0, true, false, SR>(a, last, s);
+    case 3: return launch_adamw<0, true, true, SR>(a, last, s);
+    case 4: return launch_adamw<1, false, false, SR>(a, last, s);
+    case 5: return launch_adamw<1, false, true, SR>(a, last, s);
+    case 6: return launch_adamw<1, true, false, SR>(a, last, s);
+    case 7: return launch_adamw<1, true, true, SR>(a, last, s);
+    case 8: return launch_adamw<2, false, false, SR>(a, last, s);
+    case 9: return launch_adamw<2, false, true, SR>(a, last, s);
+    case 10: return launch_adamw<2, true, false, SR>(a, last, s);
+    default: return launch_adamw<2, true, true, SR>(a, last, s);
+  }
+}
 
 struct Range {
   uintptr_t lo, hi;
@@ -548,9 +807,10 @@ using namespace biv;
 
 extern "C" {
 
-biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks) {
-  BIV_REQUIRE(n >= 0 && chunks && (t || n == 0), "opt_plan: null pointer or negative count");
+biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks, int* kinds) {
+  BIV_REQUIRE(n >= 0 && chunks && kinds && (t || n == 0), "opt_plan: null pointer or negative count");
   int64_t c = 0, base = 0;
+  int seen = 0;
   try {
     std::vector<Range> written;
     written.reserve(size_t(n) * 6);
@@ -584,6 +844,7 @@ biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks) {
       x.vec = at(x.param) % 16 == 0 && at(x.grad) % 16 == 0 && at(x.master) % 16 == 0 &&
               at(x.m) % sa == 0 && at(x.v) % sa == 0;
       c += (x.numel + kChunk - 1) / kChunk;
+      seen |= 1 << kind_of(x);
       const int64_t blocks = (x.numel + kBlk - 1) / kBlk;
       base += blocks * kBlk;
       const size_t ne = size_t(x.numel);
@@ -615,6 +876,7 @@ biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks) {
     return set_error(BIV_ERR_INVALID, "opt_plan: out of host memory");
   }
   *chunks = c;
+  *kinds = seen;
   return BIV_OK;
 }
 
@@ -636,12 +898,13 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
   BIV_REQUIRE(aligned16(workspace), "grad_norm: workspace must be 16-byte aligned");
   cudaStream_t s = as_cuda(stream);
   float2* part = static_cast<float2*>(workspace);
+  const bool here = units > 0 && units <= kUnitsHere;
   if (units > 0) {
     const int sms = sm_count() > 0 ? sm_count() : 148;
     const unsigned grid = unsigned(std::min<int64_t>(units, int64_t(sms) * 8));
-    launch_pdl(grad_norm_kernel, grid, kOT, 0, s, tensors, n, chunks, units, part);
+    launch_pdl(grad_norm_kernel, grid, kOT, 0, s, tensors, n, chunks, units, part, int(here), max_norm, out);
     biv_status st = check_launch("grad_norm");
-    if (st != BIV_OK) return st;
+    if (st != BIV_OK || here) return st;
   }
   launch_pdl(grad_norm_final_kernel, 1, kNT, 0, s, static_cast<const float2*>(part), units, max_norm, out);
   return check_launch("grad_norm_final");
@@ -656,6 +919,7 @@ biv_status biv_adamw(const biv_adamw_desc* d, biv_stream_t stream) {
   BIV_REQUIRE(d->rounding == BIV_ROUND_NEAREST || d->rounding == BIV_ROUND_STOCHASTIC,
               "adamw: unknown rounding");
   if (d->chunks == 0) return BIV_OK;
+  BIV_REQUIRE(d->kinds > 0 && d->kinds < (1 << kKinds), "adamw: kinds is not what biv_opt_plan gave");
   BIV_REQUIRE(d->tensors && d->lr && d->step, "adamw: null pointer");
   AdamArgs a;
   a.t = d->tensors; a.n = d->n; a.chunks = d->chunks;
@@ -665,12 +929,16 @@ biv_status biv_adamw(const biv_adamw_desc* d, biv_stream_t stream) {
   a.b2 = float(d->beta2); a.c2 = float(1.0 - d->beta2);
   a.eps = d->eps;
   a.seed_lo = uint32_t(d->seed); a.seed_hi = uint32_t(d->seed >> 32);
-  const int sms = sm_count() > 0 ? sm_count() : 148;
-  const unsigned grid = unsigned(std::min<int64_t>(d->chunks, int64_t(sms) * 8));
+  int left = d->kinds;
   cudaStream_t s = as_cuda(stream);
-  if (d->rounding == BIV_ROUND_STOCHASTIC) launch_pdl(adamw_kernel<true>, grid, kOT, 0, s, a);
-  else launch_pdl(adamw_kernel<false>, grid, kOT, 0, s, a);
-  return check_launch("adamw");
+  for (int k = 0; k < kKinds; ++k) {
+    if (!((left >> k) & 1)) continue;
+    left &= ~(1 << k);
+    const biv_status st = d->rounding == BIV_ROUND_STOCHASTIC ? launch_kind<true>(k, a, left == 0, s)
+                                                              : launch_kind<false>(k, a, left == 0, s);
+    if (st != BIV_OK) return st;
+  }
+  return BIV_OK;
 }
 
 }  // extern "C"

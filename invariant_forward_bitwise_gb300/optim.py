@@ -1,5 +1,5 @@
-"""AdamW over a model's tensors, as libbiv calls: one launch updates every
-weight in place, with the global gradient-norm clip before it.
+"""AdamW over a model's tensors, as libbiv calls: a launch per combination of
+types (usually one) updates every weight in place, with the global gradient-norm clip before it.
 
 The trainer keeps BF16 weights that the inference forward reads ("Finish RL
 Training Faster", section "让训练前向使用推理的数值"); the step writes them where
@@ -37,8 +37,8 @@ class AdamW:
     or "stochastic" (8-bit states and bf16 weights without a master; the bits
     come from a hash of seed, step and element).
 
-    ``step()`` runs on the current stream.  Attributes: ``norm`` float32 [2]
-    (gradient norm and clip coefficient of the last step), ``steps`` int32 [2]
+    ``step()`` runs on the current stream.  Attributes: ``norm`` float32 [4]
+    (gradient norm and clip coefficient of the last step; the rest is the kernel's), ``steps`` int32 [2]
     (steps taken; the second value is the kernel's own).  A step whose
     gradient norm is not finite changes nothing.
     """
@@ -110,7 +110,7 @@ class AdamW:
             a.v_scale = None if vs is None else vs.data_ptr()
             a.numel, a.lr_scale, a.weight_decay = size, float(ls[i]), float(wd[i])
             a.param_dtype, a.grad_dtype, a.state_dtype = _DT[p.dtype], _DT[g.dtype], _STATE[m.dtype]
-        self.chunks = biv.biv_opt_plan(arr)
+        self.chunks, kinds = biv.biv_opt_plan(arr)
         self.n = n
         self.table = torch.frombuffer(bytearray(bytes(arr)), dtype=torch.uint8).to(self.device)
         self.lr = lr if isinstance(lr, torch.Tensor) else torch.tensor([float(lr)], device=self.device)
@@ -121,10 +121,10 @@ class AdamW:
         if not max_norm >= 0.0:
             raise ValueError("max_norm must not be negative")
         self.max_norm = float(max_norm)
-        self.norm = torch.zeros(2, device=self.device)
+        self.norm = torch.zeros(4, device=self.device)
         self.ws = torch.empty(biv.biv_grad_norm_workspace(self.chunks), dtype=torch.uint8, device=self.device)
         d = biv.AdamWDesc()
-        d.tensors, d.n, d.chunks = self.table.data_ptr(), n, self.chunks
+        d.tensors, d.n, d.chunks, d.kinds = self.table.data_ptr(), n, self.chunks, kinds
         d.lr, d.step = self.lr.data_ptr(), self.steps.data_ptr()
         d.clip = self.norm.data_ptr() if self.max_norm > 0 else None
         d.beta1, d.beta2, d.eps = float(betas[0]), float(betas[1]), float(eps)
@@ -140,7 +140,6 @@ class AdamW:
         """One update of every tensor from its gradient."""
         if torch.cuda.current_device() != self.device.index:
             raise ValueError(f"step() runs on the optimizer's device, {self.device}")
-        stream = torch.cuda.current_stream() if stream is None else stream
         if self.max_norm > 0:
             biv.biv_grad_norm(self.table, self.n, self.chunks, self.max_norm, self.norm, self.ws, stream=stream)
         biv.biv_adamw(self.desc, stream=stream)

@@ -256,15 +256,15 @@ def test_first_step_from_zero_states(O):
 
 
 @pytest.mark.parametrize("grad", ["f32", "bf16"])
-@pytest.mark.parametrize("sizes", [[1], [0, 5, 0], SIZES, [70001, 3, 300000]])
+@pytest.mark.parametrize("sizes", [[1], [0, 5, 0], SIZES, [70001, 3, 300000], [70000000]])
 def test_grad_norm(O, B, grad, sizes):
     ts = tensors(synth.rng(sum(sizes)), sizes, "f32", grad, "f32")
     opt = O.AdamW(**ts, max_norm=0.25)
-    out = torch.zeros(2, device="cuda")
+    out = torch.zeros(4, device="cuda")
     B.biv_grad_norm(opt.table, opt.n, opt.chunks, 0.25, out, opt.ws)
     torch.cuda.synchronize()
     ref = float(np.sqrt(sum(np.sum(f64(x) ** 2) for x in ts["grads"])))
-    norm, coef = f64(out)
+    norm, coef = f64(out)[:2]
     # each square takes at most 4 roundings on the way into its thread's sums, whose
     # own sums keep what they lose; the root halves that, and is rounded once
     assert abs(norm - ref) <= 4 * U * ref
@@ -272,7 +272,7 @@ def test_grad_norm(O, B, grad, sizes):
     first = out.clone()
     B.biv_grad_norm(opt.table, opt.n, opt.chunks, 0.0, out, opt.ws)
     torch.cuda.synchronize()
-    assert out[0] == first[0] and out[1] == 1.0
+    assert out[0] == first[0] and out[1] == 1.0 and int(out[2:].view(torch.int32).abs().sum()) == 0
 
 
 @pytest.mark.parametrize("state", ["f32", "e4m3"])
@@ -386,6 +386,35 @@ def test_captured_steps(O):
         o.step()
     torch.cuda.synchronize()
     assert same(other_ts["params"][0], again["params"][0]) and same(other_ts["exp_avg"][0], again["exp_avg"][0])
+
+
+def test_mixed_kinds_in_one_call(O):
+    """Large matrices with 8-bit states, gains in FP32 beside them, in any order:
+    each as in a call of its own, and one step is counted."""
+    kinds = [("bf16", "bf16", "e4m3"), ("f32", "f32", "f32"), ("master", "f32", "e4m3"), ("bf16", "f32", "f32")]
+    names = ["params", "grads", "master", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"]
+
+    def build():
+        g = synth.rng(17)
+        parts = [tensors(g, [9000, 31], *k) for k in kinds]
+        flat = {k: sum(([p[k][0] if p[k] else None] for p in parts), []) +
+                sum(([p[k][1] if p[k] else None] for p in parts), []) for k in names}
+        return parts, flat
+    parts, flat = build()
+    opt = O.AdamW(**flat, lr=1e-3, max_norm=0.1)
+    opt.step()
+    torch.cuda.synchronize()
+    assert opt.steps.tolist() == [1, 0]
+    alone, _ = build()
+    for p in alone:
+        o = O.AdamW(**p, lr=1e-3, max_norm=0.1)
+        o.norm.copy_(opt.norm)
+        o.max_norm = 0.0                             # the whole call's norm stands in for its own
+        o.step()
+    torch.cuda.synchronize()
+    for p, q in zip(parts, alone):
+        for k in names:
+            assert p[k] is None or all(same(a, b) for a, b in zip(p[k], q[k])), k
 
 
 def test_many_small_tensors_and_lr_scales(O):

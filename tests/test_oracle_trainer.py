@@ -181,8 +181,8 @@ def _tensors(B, n, **kw):
 
 
 def _plan(B, arr):
-    n = C.c_int64(-1)
-    return B.load().biv_opt_plan(arr, len(arr), C.byref(n)), n.value
+    n, k = C.c_int64(-1), C.c_int(-1)
+    return B.load().biv_opt_plan(arr, len(arr), C.byref(n), C.byref(k)), n.value
 
 
 def test_opt_plan_lays_out_chunks(B):
@@ -222,10 +222,10 @@ def test_opt_plan_refuses_shared_memory(B):
 
 @pytest.mark.parametrize("kw", [dict(beta1=1.0), dict(beta2=-0.1), dict(beta1=float("nan")), dict(eps=0.0),
                                 dict(rounding=2), dict(lr=None), dict(step=None), dict(tensors=None),
-                                dict(n=-1), dict(chunks=-1), dict(n=0)])
+                                dict(n=-1), dict(chunks=-1), dict(n=0), dict(kinds=0), dict(kinds=1 << 12)])
 def test_adamw_refuses(B, kw):
     d = B.AdamWDesc()
-    d.tensors, d.n, d.chunks, d.lr, d.step = 0x1000, 1, 1, 0x2000, 0x3000
+    d.tensors, d.n, d.chunks, d.kinds, d.lr, d.step = 0x1000, 1, 1, 1, 0x2000, 0x3000
     d.beta1, d.beta2, d.eps = 0.9, 0.999, 1e-8
     for k, x in kw.items():
         setattr(d, k, x)
