@@ -294,15 +294,18 @@ __device__ __forceinline__ void policy_block(const PolicyArgs& a, const Four& f,
   }
 }
 
-// all blocks' sums, by one warp: lane l takes blocks l, l + 32, ... in order
+// all blocks' sums (in shared or global memory), by one warp: lane l takes blocks
+// l, l + 32, ... in order
+template <bool SHARED>
 __device__ __forceinline__ void policy_final(const PolicyArgs& a, const float* part, int64_t blocks,
                                              int rows, int lane) {
   float v[kStat] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
   for (int64_t b = lane; b < blocks; b += 32) {
-    const volatile float* p = part + b * kStat;
-#pragma unroll
-    for (int k = 0; k < 6; ++k) v[k] += p[k];
-    v[6] = max_nan(v[6], p[6]);
+    const float4* p = reinterpret_cast<const float4*>(part + b * kStat);
+    const float4 x = SHARED ? p[0] : __ldcg(p), y = SHARED ? p[1] : __ldcg(p + 1);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] = max_nan(v[6], y.z);
   }
   __syncwarp();
 #pragma unroll
@@ -328,7 +331,8 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
     const __grid_constant__ PolicyArgs a, const float* lp, const float* ent, float* dlp) {
   __shared__ int32_t s_start[kSmallSeqs + 1];
   __shared__ int s_count[kSmallSeqs], s_red[2][32];
-  __shared__ float red[4][kTB / 32][kStat], part[4 * kStat];
+  __shared__ float red[4][kTB / 32][kStat];
+  __shared__ __align__(16) float part[4 * kStat];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
   const int grp = tid / kTB;           // blocks of 1024 rows: groups of 256 threads
   policy_block(a, f, dlp, t0, tid % kTB, red[grp], part + grp * kStat, [] { __syncthreads(); });
   __syncthreads();
-  if (warp == 0) policy_final(a, part, nt / kTB, rows, lane);
+  if (warp == 0) policy_final<true>(a, part, nt / kTB, rows, lane);
 }
 
 // ----------------------------------------------------------- large calls --
@@ -428,7 +432,6 @@ __global__ void __launch_bounds__(kTB) policy_count_kernel(const __grid_constant
   __syncwarp();
   int any = max(max(seq[0], seq[1]), max(seq[2], seq[3]));
   any = __reduce_max_sync(0xffffffffu, any);      // a sequence that counts here
-  if (any < 0) return;
   bool other = false;
   int c = 0;
 #pragma unroll
@@ -437,7 +440,13 @@ __global__ void __launch_bounds__(kTB) policy_count_kernel(const __grid_constant
     c += seq[i] >= 0;
   }
   const int n = __reduce_add_sync(0xffffffffu, c);
-  if (lane == 0) atomicAdd(&a.ws.totals->rows, n);
+  __shared__ int s_rows;
+  if (threadIdx.x == 0) s_rows = 0;
+  __syncthreads();
+  if (lane == 0 && n) atomicAdd(&s_rows, n);
+  __syncthreads();
+  if (threadIdx.x == 0 && s_rows) atomicAdd(&a.ws.totals->rows, s_rows);
+  if (any < 0) return;
   if (!__any_sync(0xffffffffu, other)) {          // the warp's only one: add once
     if (lane == 0) add(any, n);
     return;
@@ -498,7 +507,7 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
   __syncthreads();
   if (s_last && threadIdx.x < 32) {
     __threadfence();
-    policy_final(a, a.ws.part, blocks, a.ws.totals->rows, threadIdx.x);
+    policy_final<false>(a, a.ws.part, blocks, a.ws.totals->rows, threadIdx.x);
   }
 }
 

@@ -85,10 +85,17 @@ template <int W>
 struct Raw {
   uint32_t w[W];
 };
+// (wide: FP32 arrays keep 32 bytes' alignment, one 256-bit access)
 template <int W>
-__device__ __forceinline__ void load_raw(const void* p, int64_t e, Raw<W>& r) {
-  const uint8_t* q = static_cast<const uint8_t*>(p) + e * (W / 2);
-  if constexpr (W == 2) {
+__device__ __forceinline__ void load_raw(const void* p, bool wide, Raw<W>& r) {
+  const uint8_t* q = static_cast<const uint8_t*>(p);
+  if (W == 8 && wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r.w[0]), "=r"(r.w[1 % W]), "=r"(r.w[2 % W]), "=r"(r.w[3 % W]), "=r"(r.w[4 % W]),
+                   "=r"(r.w[5 % W]), "=r"(r.w[6 % W]), "=r"(r.w[7 % W])
+                 : "l"(q)
+                 : "memory");
+  } else if constexpr (W == 2) {
     const uint2 v = *reinterpret_cast<const uint2*>(q);
     r.w[0] = v.x; r.w[1] = v.y;
   } else {
@@ -113,9 +120,11 @@ __device__ __forceinline__ void load_raw_slow(const void* p, int64_t e, int64_t 
   }
 }
 template <int W>
-__device__ __forceinline__ void store_raw(void* p, int64_t e, const Raw<W>& r) {
-  uint8_t* q = static_cast<uint8_t*>(p) + e * (W / 2);
-  if constexpr (W == 2) {
+__device__ __forceinline__ void store_raw(void* p, bool wide, const Raw<W>& r) {
+  uint8_t* q = static_cast<uint8_t*>(p);
+  if (W == 8 && wide) {
+    st_global_v8(q, r.w);
+  } else if constexpr (W == 2) {
     *reinterpret_cast<uint2*>(q) = make_uint2(r.w[0], r.w[1]);
   } else {
 #pragma unroll
@@ -449,6 +458,7 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
   void* weight = PK == kParamMaster ? static_cast<void*>(t.master) : t.param;
   const int64_t full = t.vec ? min(count, max(int64_t(0), n / kChunk - chunk)) : 0;
   const uint64_t id0 = uint64_t(t.rng_base + e0);
+  const bool wide = t.vec > 1;
   {
     const uint8_t* pg = static_cast<const uint8_t*>(t.grad) + e0 * (K::GW / 2);
     uint8_t* pw = static_cast<uint8_t*>(weight) + e0 * (K::PW / 2);
@@ -502,16 +512,16 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
         d.sm = reinterpret_cast<const float*>(st + L::MS)[threadIdx.x];
         d.sv = reinterpret_cast<const float*>(st + L::VS)[threadIdx.x];
       } else {
-        load_raw(pg, 0, d.g);
-        load_raw(pw, 0, d.w);
-        load_raw(pm, 0, d.m);
-        load_raw(pv, 0, d.v);
+        load_raw(pg, wide, d.g);
+        load_raw(pw, wide, d.w);
+        load_raw(pm, wide, d.m);
+        load_raw(pv, wide, d.v);
       }
       adam_math(d, a, s, ts, id0 + uint64_t(k) * kChunk);
-      store_raw(pw, 0, d.w);
-      if constexpr (PK == kParamMaster) store_raw(pc, 0, d.w16);
-      store_raw(pm, 0, d.m);
-      store_raw(pv, 0, d.v);
+      store_raw(pw, wide, d.w);
+      if constexpr (PK == kParamMaster) store_raw(pc, wide, d.w16);
+      store_raw(pm, wide, d.m);
+      store_raw(pv, wide, d.v);
       if constexpr (E8) {
         if ((threadIdx.x & 15) == 0) {
           *pms = d.sm;
@@ -621,10 +631,10 @@ __device__ __forceinline__ Sum2 warp_sum2(Sum2 v) {
 
 // the squares of a thread's 8 values of `n` chunks, all loads first
 template <int W, int N>
-__device__ __forceinline__ void add_squares(const uint8_t* p, uint64_t (&q)[4]) {
+__device__ __forceinline__ void add_squares(const uint8_t* p, bool wide, uint64_t (&q)[4]) {
   Raw<W> r[N];
 #pragma unroll
-  for (int k = 0; k < N; ++k) load_raw(p, int64_t(k) * kChunk, r[k]);
+  for (int k = 0; k < N; ++k) load_raw(p + int64_t(k) * kChunk * (W / 2), wide, r[k]);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     uint64_t f[4];
@@ -643,31 +653,38 @@ __device__ __forceinline__ void add_squares_slow(const biv_opt_tensor& t, int64_
   for (int i = 0; i < 4; ++i) q[i] = fma2(f[i], f[i], q[i]);
 }
 
-// All partials: thread i of 1024 takes i, i + 1024, ... in order, then a warp xor
-// tree and the warps in order.  By NT threads, each in the place of 1024 / NT.
+// All partials: thread i of 1024 takes i, i + 1024, ... in order, then a xor tree
+// over its warp and one over the 32 warps.  By NT threads, each in the place of 1024 / NT.
 template <int NT>
 __device__ __forceinline__ void norm_total(const float2* part, int64_t units, float max_norm, float* out,
                                            Sum2 (&red)[kNT / 32]) {
+  constexpr int R = kNT / NT;
   const int tid = threadIdx.x;
+  Sum2 v[R];
 #pragma unroll
-  for (int k = 0; k < kNT / NT; ++k) {
-    Sum2 v = {0.f, 0.f};
-#pragma unroll 8
-    for (int64_t i = k * NT + tid; i < units; i += kNT) {
-      const float2 p = __ldcg(part + i);
-      v = add_sums(v, {p.x, p.y});
-    }
-    __syncwarp();
-    v = warp_sum2(v);
-    if ((tid & 31) == 0) red[(k * NT + tid) >> 5] = v;
+  for (int k = 0; k < R; ++k) v[k] = {0.f, 0.f};
+#pragma unroll 2
+  for (int64_t i = tid; i < units; i += kNT) {
+    float2 p[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) p[k] = i + k * NT < units ? __ldcg(part + i + k * NT) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = add_sums(v[k], {p[k].x, p[k].y});
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    v[k] = warp_sum2(v[k]);
+    if ((tid & 31) == 0) red[(k * NT + tid) >> 5] = v[k];
   }
   __syncthreads();
-  if (tid == 0) {
-    Sum2 tot = red[0];
-    for (int i = 1; i < kNT / 32; ++i) tot = add_sums(tot, red[i]);
-    const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
-    out[0] = norm;
-    out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
+  if (tid < 32) {
+    const Sum2 tot = warp_sum2(red[tid]);
+    if (tid == 0) {
+      const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
+      out[0] = norm;
+      out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
+    }
   }
 }
 
@@ -695,8 +712,8 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
     if (t.vec && (in + kNormChunks) * kChunk <= t.numel) {
       const int64_t e = in * kChunk + tid * kEPT;
       const uint8_t* g = static_cast<const uint8_t*>(t.grad);
-      if (t.grad_dtype == BIV_BF16) add_squares<4, kNormChunks>(g + e * 2, q);
-      else add_squares<8, kNormChunks>(g + e * 4, q);
+      if (t.grad_dtype == BIV_BF16) add_squares<4, kNormChunks>(g + e * 2, false, q);
+      else add_squares<8, kNormChunks>(g + e * 4, t.vec > 1, q);
     } else {
       for (int64_t c = c0; c < min(c0 + kNormChunks, chunks); ++c) {
         while (ti + 1 < n && tens[ti + 1].first_chunk <= c) ++ti;
@@ -705,8 +722,8 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
         const uint8_t* g = static_cast<const uint8_t*>(x.grad);
         const bool bf = x.grad_dtype == BIV_BF16;
         if (x.vec && (c - x.first_chunk + 1) * kChunk <= x.numel) {
-          if (bf) add_squares<4, 1>(g + e * 2, q);
-          else add_squares<8, 1>(g + e * 4, q);
+          if (bf) add_squares<4, 1>(g + e * 2, false, q);
+          else add_squares<8, 1>(g + e * 4, x.vec > 1, q);
         } else {
           if (bf) add_squares_slow<4>(x, e, q);
           else add_squares_slow<8>(x, e, q);
@@ -843,6 +860,11 @@ biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks, int* kinds) {
       const size_t sa = e8 ? 8 : 16;
       x.vec = at(x.param) % 16 == 0 && at(x.grad) % 16 == 0 && at(x.master) % 16 == 0 &&
               at(x.m) % sa == 0 && at(x.v) % sa == 0;
+      // 32-byte ones of 8 (f32) elements
+      const bool f32_32 = (x.param_dtype != BIV_F32 || at(x.param) % 32 == 0) && at(x.master) % 32 == 0 &&
+                          (x.grad_dtype != BIV_F32 || at(x.grad) % 32 == 0) &&
+                          (e8 || (at(x.m) % 32 == 0 && at(x.v) % 32 == 0));
+      if (x.vec && f32_32) x.vec = 2;
       c += (x.numel + kChunk - 1) / kChunk;
       seen |= 1 << kind_of(x);
       const int64_t blocks = (x.numel + kBlk - 1) / kBlk;

@@ -224,17 +224,18 @@ def test_states_are_the_bits_of_the_stated_operations(O, state, rounding):
 @pytest.mark.parametrize("param,grad,state", [("f32", "f32", "f32"), ("master", "bf16", "e4m3"),
                                               ("bf16", "f32", "e4m3"), ("bf16", "bf16", "f32")])
 def test_unaligned_tensors_and_neighbours(O, param, grad, state):
-    """Tensors one element off their storage's start give the bits of aligned
-    ones, the element before them is left alone, and tensors beside them change
-    nothing."""
-    a, b, alone = (tensors(synth.rng(3), [3000, 300], param, grad, state, shift) for shift in (0, 1, 0))
-    for ts in (a, b, lists(alone, lambda v: v[:1])):
+    """Tensors one element, or 16 bytes, off their storage's start give the bits of
+    aligned ones, what lies before them is left alone, and tensors beside them
+    change nothing."""
+    a, b, c, d, alone = (tensors(synth.rng(3), [5000, 300], param, grad, state, shift) for shift in (0, 1, 4, 8, 0))
+    for ts in (a, b, c, d, lists(alone, lambda v: v[:1])):
         O.AdamW(**ts, lr=1e-3, weight_decay=0.1).step()
     torch.cuda.synchronize()
     for k, v in a.items():
         for i, t in enumerate(v or []):
-            assert same(t, b[k][i]), (k, i)
-            assert float(b[k][i].as_strided((1,), (1,), 0).float().item()) == 0.0
+            for off, n in ((b, 1), (c, 4), (d, 8)):
+                assert same(t, off[k][i]), (k, i, n)
+                assert not bool(off[k][i].as_strided((n,), (1,), 0).float().any())
         assert v is None or same(v[0], alone[k][0])
 
 
