@@ -26,6 +26,7 @@ constexpr int kNT = 1024;           // threads that add the norm's partials up
 constexpr int64_t kUnitsHere = 8192;  // partials that the norm's last CTA adds up itself
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 
+enum VecBits { kVec16 = 1, kVec32 = 2, kVecBulk = 4 };   // biv_opt_tensor.vec
 enum ParamKind { kParamF32 = 0, kParamBf16 = 1, kParamMaster = 2 };
 
 // the tensor that holds chunk c: the last one with first_chunk <= c, found by a
@@ -277,6 +278,7 @@ struct AdamArgs {
   double b1d, b2d;
   float b1, c1, b2, c2, eps;   // c1 = 1 - b1, c2 = 1 - b2
   uint32_t seed_lo, seed_hi;
+  int* err;
 };
 
 struct StepScalars {
@@ -402,55 +404,50 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
   }
 }
 
-// Asynchronous copy of a thread's 8 elements into its own place of a staging
-// area in shared memory (only that thread reads them: no barrier), and back.
-// An array's area of a stage holds 16-byte pieces (8-bit codes: 8), one after
-// the other for the 256 threads.
-template <int W>
-__device__ __forceinline__ void stage_async(const uint8_t* q, uint32_t slot) {
-  if constexpr (W == 2) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot + threadIdx.x * 8), "l"(q) : "memory");
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; i += 4)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + threadIdx.x * 16 + i / 4 * kOT * 16),
-                   "l"(q + i * 4)
-                   : "memory");
-  }
-}
-__device__ __forceinline__ void stage_async4(const float* p, uint32_t slot) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(slot + threadIdx.x * 4), "l"(p) : "memory");
-}
+// Staging (8-bit states): one thread copies a chunk's arrays to shared memory by
+// bulk copies that complete on the stage's mbarrier, a few chunks ahead; each
+// thread reads its own 8 elements back.  An array's area holds the chunk's bytes
+// in order.
 template <int W>
 __device__ __forceinline__ void from_stage(const uint8_t* slot, Raw<W>& r) {
+  const uint8_t* q = slot + threadIdx.x * (W * 4);
   if constexpr (W == 2) {
-    const uint2 v = reinterpret_cast<const uint2*>(slot)[threadIdx.x];
+    const uint2 v = *reinterpret_cast<const uint2*>(q);
     r.w[0] = v.x; r.w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < W; i += 4) {
-      const uint4 v = reinterpret_cast<const uint4*>(slot)[i / 4 * kOT + threadIdx.x];
+      const uint4 v = *reinterpret_cast<const uint4*>(q + i * 4);
       r.w[i] = v.x; r.w[i + 1] = v.y; r.w[i + 2] = v.z; r.w[i + 3] = v.w;
     }
   }
 }
-constexpr int kStages = 3;
 template <int GW, int PW>
 struct StageLayout {   // a stage: gradient, weight, codes, scales
   static constexpr int W = kOT * GW * 4, M = W + kOT * PW * 4, V = M + kOT * 8, MS = V + kOT * 8,
-                       VS = MS + kOT * 4, BYTES = VS + kOT * 4;
+                       VS = MS + kChunk / kBlk * 4, BYTES = VS + kChunk / kBlk * 4;
+  static constexpr int STAGES = (50 << 10) / BYTES;    // four CTAs per SM
+};
+struct Ring {          // where the next chunk of a CTA is staged, over its tensors
+  uint8_t* bufs;
+  uint64_t* bars;
+  int stage;
+  uint32_t phase;
+  int* err;
 };
 
 // `count` consecutive chunks of one tensor, the first one number `chunk` of it.
-// Full chunks of 16-byte aligned arrays take the fast way.  With 8-bit states a
-// chunk is few bytes and much arithmetic: its arrays are copied to shared memory
-// two chunks ahead, so that loads are in flight while a warp computes, at no
-// register's cost.
+// Full chunks of aligned arrays take the fast way.  With 8-bit states a chunk is
+// few bytes and much arithmetic: its arrays are copied to shared memory ahead, so
+// that loads are in flight while a warp computes, at no register's cost and a
+// few instructions of one thread.
 template <int PK, bool GB, bool E8, bool SR>
 __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk, int64_t count,
-                                         const AdamArgs& a, const StepScalars& s, uint8_t* stages) {
+                                         const AdamArgs& a, const StepScalars& s, Ring& ring) {
   using K = Kind<PK, GB, E8, SR>;
   using L = StageLayout<K::GW, K::PW>;
+  constexpr int kGB = kChunk * K::GW / 2, kPB = kChunk * K::PW / 2, kSB = kChunk * K::SW / 2,
+                kScales = kChunk / kBlk;
   const int64_t n = t.numel, e0 = chunk * kChunk + threadIdx.x * kEPT;
   TensorScalars ts;
   ts.rate = __fmul_rn(s.lr_bc1, t.lr_scale);
@@ -458,64 +455,58 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
   void* weight = PK == kParamMaster ? static_cast<void*>(t.master) : t.param;
   const int64_t full = t.vec ? min(count, max(int64_t(0), n / kChunk - chunk)) : 0;
   const uint64_t id0 = uint64_t(t.rng_base + e0);
-  const bool wide = t.vec > 1;
+  const bool wide = (t.vec & kVec32) != 0, staged = E8 && (t.vec & kVecBulk);
   {
     const uint8_t* pg = static_cast<const uint8_t*>(t.grad) + e0 * (K::GW / 2);
     uint8_t* pw = static_cast<uint8_t*>(weight) + e0 * (K::PW / 2);
     uint8_t* pc = static_cast<uint8_t*>(t.param) + e0 * 2;
     uint8_t* pm = static_cast<uint8_t*>(t.m) + e0 * (K::SW / 2);
     uint8_t* pv = static_cast<uint8_t*>(t.v) + e0 * (K::SW / 2);
-    float* pms = t.m_scale + e0 / kBlk;
-    float* pvs = t.v_scale + e0 / kBlk;
-    constexpr int kGB = kChunk * K::GW / 2, kPB = kChunk * K::PW / 2, kSB = kChunk * K::SW / 2;
-    const uint32_t st0 = smem_u32(stages);
-    int in = 0, out = 0;                 // stage to fill, stage to read
-    int64_t left = full;                 // chunks still to be copied ahead
-    auto ahead = [&]() {                 // (the copies run kStages - 1 chunks before the pointers)
-      constexpr int D = kStages - 1;
-      if (left > 0) {
-        const uint32_t st = st0 + uint32_t(in) * L::BYTES;
-        stage_async<K::GW>(pg + D * kGB, st);
-        stage_async<K::PW>(pw + D * kPB, st + L::W);
-        stage_async<K::SW>(pm + D * kSB, st + L::M);
-        stage_async<K::SW>(pv + D * kSB, st + L::V);
-        stage_async4(pms + D * (kChunk / kBlk), st + L::MS);
-        stage_async4(pvs + D * (kChunk / kBlk), st + L::VS);
-        in = in == kStages - 1 ? 0 : in + 1;
-      }
-      --left;
-      asm volatile("cp.async.commit_group;" ::: "memory");
+    float* pms = t.m_scale + (e0 >> 7);
+    float* pvs = t.v_scale + (e0 >> 7);
+    auto copy_ahead = [&](int64_t k, int stage) {     // chunk k of the run, by one thread
+      const uint32_t bar = smem_u32(ring.bars + stage), st = smem_u32(ring.bufs) + stage * L::BYTES;
+      const int64_t c = chunk + k;
+      mbar_expect_tx(bar, kGB + kPB + 2 * kSB + 2 * kScales * 4);
+      bulk_load(st, static_cast<const uint8_t*>(t.grad) + c * kGB, kGB, bar);
+      bulk_load(st + L::W, static_cast<const uint8_t*>(weight) + c * kPB, kPB, bar);
+      bulk_load(st + L::M, static_cast<const uint8_t*>(t.m) + c * kSB, kSB, bar);
+      bulk_load(st + L::V, static_cast<const uint8_t*>(t.v) + c * kSB, kSB, bar);
+      bulk_load(st + L::MS, t.m_scale + c * kScales, kScales * 4, bar);
+      bulk_load(st + L::VS, t.v_scale + c * kScales, kScales * 4, bar);
     };
-    auto advance = [&](int k) {
-      pg += k * kGB; pw += k * kPB; pc += k * kChunk * 2; pm += k * kSB; pv += k * kSB;
-      pms += k * (kChunk / kBlk); pvs += k * (kChunk / kBlk);
-    };
-    if constexpr (E8) {
-      advance(-(kStages - 1));
-#pragma unroll
-      for (int k = 0; k < kStages - 1; ++k) {
-        ahead();
-        advance(1);
+    if (staged && threadIdx.x == 0) {
+      for (int k = 0; k < L::STAGES && k < full; ++k) {
+        const int st = ring.stage + k;
+        copy_ahead(k, st < L::STAGES ? st : st - L::STAGES);
       }
     }
     for (int64_t k = 0; k < full; ++k) {
       K d;
-      if constexpr (E8) {
-        ahead();
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        const uint8_t* st = stages + out * L::BYTES;
-        out = out == kStages - 1 ? 0 : out + 1;
+      if (staged) {
+        mbar_wait(smem_u32(ring.bars + ring.stage), ring.phase, ring.err);
+        const uint8_t* st = ring.bufs + ring.stage * L::BYTES;
         from_stage(st, d.g);
         from_stage(st + L::W, d.w);
         from_stage(st + L::M, d.m);
         from_stage(st + L::V, d.v);
-        d.sm = reinterpret_cast<const float*>(st + L::MS)[threadIdx.x];
-        d.sv = reinterpret_cast<const float*>(st + L::VS)[threadIdx.x];
+        d.sm = reinterpret_cast<const float*>(st + L::MS)[threadIdx.x >> 4];
+        d.sv = reinterpret_cast<const float*>(st + L::VS)[threadIdx.x >> 4];
+        __syncthreads();                   // the stage is read: it may be filled again
+        if (threadIdx.x == 0 && k + L::STAGES < full) copy_ahead(k + L::STAGES, ring.stage);
+        if (++ring.stage == L::STAGES) {
+          ring.stage = 0;
+          ring.phase ^= 1;
+        }
       } else {
         load_raw(pg, wide, d.g);
         load_raw(pw, wide, d.w);
         load_raw(pm, wide, d.m);
         load_raw(pv, wide, d.v);
+        if (E8) {
+          d.sm = *pms;
+          d.sv = *pvs;
+        }
       }
       adam_math(d, a, s, ts, id0 + uint64_t(k) * kChunk);
       store_raw(pw, wide, d.w);
@@ -527,10 +518,10 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
           *pms = d.sm;
           *pvs = d.sv;
         }
+        pms += kScales; pvs += kScales;
       }
-      advance(1);
+      pg += kGB; pw += kPB; pc += kChunk * 2; pm += kSB; pv += kSB;
     }
-    if constexpr (E8) asm volatile("cp.async.wait_all;" ::: "memory");
   }
   // the tensor's last chunk, and tensors of any alignment
   for (int64_t k = full; k < count; ++k) {
@@ -568,8 +559,15 @@ __host__ __device__ inline int kind_of(const biv_opt_tensor& t) {
 template <int PK, bool GB, bool E8, bool SR>
 __global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamArgs a, int last) {
   constexpr int kKind = PK * 4 + (GB ? 2 : 0) + (E8 ? 1 : 0);
+  using L = StageLayout<GB ? 4 : 8, PK == kParamBf16 ? 4 : 8>;
   __shared__ float s_bc[2];
-  extern __shared__ __align__(16) uint8_t stages[];
+  __shared__ __align__(8) uint64_t s_bars[L::STAGES];
+  extern __shared__ __align__(128) uint8_t stages[];
+  if (E8 && threadIdx.x == 0) {
+    for (int i = 0; i < L::STAGES; ++i) mbar_init(smem_u32(s_bars + i), 1);
+    fence_barrier_init();
+  }
+  Ring ring = {stages, s_bars, 0, 0u, a.err};
   const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
   int ti = find_tensor(a.t, a.n, c0);   // (the table is the host's: no kernel writes it)
@@ -594,7 +592,7 @@ __global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_con
     while (ti + 1 < a.n && a.t[ti + 1].first_chunk <= c) ++ti;
     const biv_opt_tensor& t = a.t[ti];
     const int64_t end = ti + 1 < a.n ? min(c1, a.t[ti + 1].first_chunk) : c1;
-    if (kind_of(t) == kKind) adam_run<PK, GB, E8, SR>(t, c - t.first_chunk, end - c, a, s, stages);
+    if (kind_of(t) == kKind) adam_run<PK, GB, E8, SR>(t, c - t.first_chunk, end - c, a, s, ring);
     c = end;
   }
   // the last CTA to get here stores the new step: every CTA has read the old one
@@ -713,7 +711,7 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
       const int64_t e = in * kChunk + tid * kEPT;
       const uint8_t* g = static_cast<const uint8_t*>(t.grad);
       if (t.grad_dtype == BIV_BF16) add_squares<4, kNormChunks>(g + e * 2, false, q);
-      else add_squares<8, kNormChunks>(g + e * 4, t.vec > 1, q);
+      else add_squares<8, kNormChunks>(g + e * 4, (t.vec & kVec32) != 0, q);
     } else {
       for (int64_t c = c0; c < min(c0 + kNormChunks, chunks); ++c) {
         while (ti + 1 < n && tens[ti + 1].first_chunk <= c) ++ti;
@@ -723,7 +721,7 @@ __global__ void __launch_bounds__(kOT) grad_norm_kernel(const biv_opt_tensor* __
         const bool bf = x.grad_dtype == BIV_BF16;
         if (x.vec && (c - x.first_chunk + 1) * kChunk <= x.numel) {
           if (bf) add_squares<4, 1>(g + e * 2, false, q);
-          else add_squares<8, 1>(g + e * 4, x.vec > 1, q);
+          else add_squares<8, 1>(g + e * 4, (x.vec & kVec32) != 0, q);
         } else {
           if (bf) add_squares_slow<4>(x, e, q);
           else add_squares_slow<8>(x, e, q);
@@ -778,7 +776,7 @@ constexpr int kKinds = 12;
 template <int PK, bool GB, bool E8, bool SR>
 biv_status launch_adamw(const AdamArgs& a, bool last, cudaStream_t s) {
   using L = StageLayout<GB ? 4 : 8, PK == kParamBf16 ? 4 : 8>;
-  constexpr int kSmem = E8 ? kStages * L::BYTES : 0;
+  constexpr int kSmem = E8 ? L::STAGES * L::BYTES : 0;
   auto kern = adamw_kernel<PK, GB, E8, SR>;
   if (kSmem > 48 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
@@ -864,7 +862,10 @@ biv_status biv_opt_plan(biv_opt_tensor* t, int n, int64_t* chunks, int* kinds) {
       const bool f32_32 = (x.param_dtype != BIV_F32 || at(x.param) % 32 == 0) && at(x.master) % 32 == 0 &&
                           (x.grad_dtype != BIV_F32 || at(x.grad) % 32 == 0) &&
                           (e8 || (at(x.m) % 32 == 0 && at(x.v) % 32 == 0));
-      if (x.vec && f32_32) x.vec = 2;
+      // bulk copies of whole chunks (8-bit states)
+      const bool bulk = e8 && at(x.m) % 16 == 0 && at(x.v) % 16 == 0 && at(x.m_scale) % 16 == 0 &&
+                        at(x.v_scale) % 16 == 0;
+      if (x.vec) x.vec = kVec16 | (f32_32 ? kVec32 : 0) | (bulk ? kVecBulk : 0);
       c += (x.numel + kChunk - 1) / kChunk;
       seen |= 1 << kind_of(x);
       const int64_t blocks = (x.numel + kBlk - 1) / kBlk;
@@ -950,6 +951,7 @@ biv_status biv_adamw(const biv_adamw_desc* d, biv_stream_t stream) {
   a.b1 = float(d->beta1); a.c1 = float(1.0 - d->beta1);
   a.b2 = float(d->beta2); a.c2 = float(1.0 - d->beta2);
   a.eps = d->eps;
+  a.err = device_error_word();
   a.seed_lo = uint32_t(d->seed); a.seed_hi = uint32_t(d->seed >> 32);
   int left = d->kinds;
   cudaStream_t s = as_cuda(stream);

@@ -228,12 +228,16 @@ def test_unaligned_tensors_and_neighbours(O, param, grad, state):
     aligned ones, what lies before them is left alone, and tensors beside them
     change nothing."""
     a, b, c, d, alone = (tensors(synth.rng(3), [5000, 300], param, grad, state, shift) for shift in (0, 1, 4, 8, 0))
+    # codes aligned, their scales not
+    if state == "e4m3":
+        for k in ("exp_avg_scale", "exp_avg_sq_scale"):
+            d[k] = tensors(synth.rng(3), [5000, 300], param, grad, state, 1)[k]
     for ts in (a, b, c, d, lists(alone, lambda v: v[:1])):
         O.AdamW(**ts, lr=1e-3, weight_decay=0.1).step()
     torch.cuda.synchronize()
     for k, v in a.items():
         for i, t in enumerate(v or []):
-            for off, n in ((b, 1), (c, 4), (d, 8)):
+            for off, n in ((b, 1), (c, 4), (d, 1 if "scale" in k else 8)):
                 assert same(t, off[k][i]), (k, i, n)
                 assert not bool(off[k][i].as_strided((n,), (1,), 0).float().any())
         assert v is None or same(v[0], alone[k][0])

@@ -193,7 +193,7 @@ def test_opt_plan_lays_out_chunks(B):
     assert st == B.BIV_OK and chunks == 1 + 0 + 3 + 1
     assert [a.first_chunk for a in arr] == [0, 1, 1, 4]
     assert [a.rng_base for a in arr] == [0, 1024, 1024, 1024 + 5120]
-    assert [a.vec for a in arr] == [2, 0, 2, 0]
+    assert [a.vec for a in arr] == [3, 0, 3, 0]
     arr[0].grad += 16
     assert _plan(B, arr)[0] == B.BIV_OK and arr[0].vec == 1
     assert _plan(B, (B.OptTensor * 0)()) == (B.BIV_OK, 0)
