@@ -660,8 +660,7 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * element, in FP32:
  *   g = grad * coef;  m = b1 m + (1-b1) g;  v = b2 v + ((1-b2) g) g
  *   w = w (1 - lr wd) - (lr / (1-b1^t)) m / (sqrt(v) / sqrt(1-b2^t) + eps)
- * (m and v are the bits of these operations, each rounded once in the order
- * written; w is within a few 2^-24 of its step)
+ * (each operation rounded once, in the order written)
  * with t the step's number, lr = *lr * lr_scale and wd of the tensor.
  *
  * A biv_opt_tensor describes one tensor of numel elements, all arrays dense:
@@ -670,11 +669,11 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  *          w is the bf16 weight, rounded back to bf16.
  *   grad   BIV_F32 or BIV_BF16.
  *   state  BIV_F32: m, v float32.  BIV_E4M3: blocks of 128 consecutive
- *          elements (the last one shorter); m holds e4m3 codes of m / s with
- *          s = max(amax|m|, 2^-100) / 448 in m_scale; v holds codes of
- *          sqrt(v) / s the same way in v_scale (the root halves the exponent
- *          range that the codes have to cover), and a positive root never gets
- *          code 0.  m_scale, v_scale float32 [ceil(numel / 128)].
+ *          elements (the last one shorter); with a = max(amax|m|, 2^-100) of
+ *          the block, m holds e4m3 codes of m (448 (1/a)) and m_scale a (1/448),
+ *          each operation rounded once; v and v_scale hold sqrt(v) the same way
+ *          (the root halves the exponent range that the codes have to cover),
+ *          and a positive root never gets code 0.  m_scale, v_scale float32 [ceil(numel / 128)].
  * rounding (8-bit states and bf16 weights without a master): NEAREST (ties to
  * even), or STOCHASTIC: the magnitude goes up with a chance equal to the part
  * cut off, from 16 bits of a hash of (seed, t, element), so that steps below

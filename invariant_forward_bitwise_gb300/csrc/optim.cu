@@ -188,12 +188,6 @@ __device__ __forceinline__ float stochastic_any(float y, uint32_t rnd16) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
-// square root and reciprocal to about 2 ulp (a step's own rounding)
-__device__ __forceinline__ float sqrt_near(float x) {
-  float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Eight square roots, rounded to nearest: from an approximate reciprocal root y
 // one Newton step on x^2 = v, r = v y + (v - (v y)^2) y / 2, its residual exact by
 // FMA (Markstein, "Computation of elementary functions on the IBM RISC System/6000
@@ -220,6 +214,7 @@ __device__ __forceinline__ void sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
     for (int i = 0; i < 8; ++i) r[i] = sqrtf(f[i]);
   }
 }
+// reciprocal to about 1 ulp
 __device__ __forceinline__ float recip_near(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -235,7 +230,7 @@ __device__ __forceinline__ float block_amax(const float (&x)[8]) {
   return fmaxf(a, kMinAmax);
 }
 
-// 8 values as e4m3 codes of x / s, s = amax / 448 given as its inverse.  ROOT: x
+// 8 values as e4m3 codes of x inv, inv = 448 (1 / amax).  ROOT: x
 // are roots of second moments: a positive one that would round to 0 takes the
 // smallest code, since a later m / (0 + eps) would throw the weight far off.
 template <bool SR, bool ROOT>
@@ -335,25 +330,24 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
     v[i] = add2(mul2(pack2(a.b2, a.b2), v[i]), mul2(mul2(pack2(a.c2, a.c2), gi), gi));
     unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
   }
-  // the root is held in 8 bits: rounded to nearest; in a step alone, to 2 ulp
-  if constexpr (E8) {
-    sqrt8(v, rf);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v0, v1;
-      unpack2(v[i], v0, v1);
-      rf[2 * i] = sqrt_near(v0);
-      rf[2 * i + 1] = sqrt_near(v1);
-    }
-  }
+  sqrt8(v, rf);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float d0, d1;
-    unpack2(fma2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2), pack2(a.eps, a.eps)), d0, d1);
-    const uint64_t back = mul2(mul2(pack2(-ts.rate, -ts.rate), m[i]), pack2(recip_near(d0), recip_near(d1)));
-    w[i] = fma2(w[i], pack2(ts.keep, ts.keep), back);
-    unpack2(w[i], wf[2 * i], wf[2 * i + 1]);
+    // (rate m) / (r rbc2 + eps), rounded to nearest by one correction of the
+    // quotient with its exact remainder (Markstein, as above)
+    float d[2], q[2], n[2];
+    unpack2(mul2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2)), d[0], d[1]);
+    const uint64_t num = mul2(pack2(ts.rate, ts.rate), m[i]);
+    unpack2(num, n[0], n[1]);
+    d[0] = __fadd_rn(d[0], a.eps);
+    d[1] = __fadd_rn(d[1], a.eps);
+    const uint64_t rc = pack2(recip_near(d[0]), recip_near(d[1])), q0 = mul2(num, rc);
+    unpack2(q0, q[0], q[1]);
+    unpack2(fma2(pack2(__fmaf_rn(-q[0], d[0], n[0]), __fmaf_rn(-q[1], d[1], n[1])), rc, q0), q[0], q[1]);
+    float w0, w1;
+    unpack2(mul2(w[i], pack2(ts.keep, ts.keep)), w0, w1);
+    wf[2 * i] = __fsub_rn(w0, q[0]);
+    wf[2 * i + 1] = __fsub_rn(w1, q[1]);
   }
   uint32_t h[8];
   if constexpr (SR && (E8 || PK == kParamBf16)) {
@@ -382,15 +376,13 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
   }
   if constexpr (E8) {
     const float am = block_amax(mf), ar = block_amax(rf);
-    // 448 / am, 448 / ar, am / 448, ar / 448: one division, a quarter of the lanes each
-    const int role = threadIdx.x & 3;
-    const float amax = role & 1 ? ar : am;
-    const float q = __fdiv_rn(role < 2 ? 448.0f : amax, role < 2 ? amax : 448.0f);
-    const int first = threadIdx.x & 28;            // (a lane of the same block)
-    d.m = encode8<SR, false>(mf, __shfl_sync(0xffffffffu, q, first), h);
-    d.v = encode8<SR, true>(rf, __shfl_sync(0xffffffffu, q, first + 1), h);
-    d.sm = __shfl_sync(0xffffffffu, q, first + 2);
-    d.sv = __shfl_sync(0xffffffffu, q, first + 3);
+    // both reciprocals by one instruction sequence, half of the lanes each
+    const float inv = __fmul_rn(448.0f, __frcp_rn(threadIdx.x & 1 ? ar : am));
+    const int first = threadIdx.x & 30;            // (a lane of the same block)
+    d.m = encode8<SR, false>(mf, __shfl_sync(0xffffffffu, inv, first), h);
+    d.v = encode8<SR, true>(rf, __shfl_sync(0xffffffffu, inv, first + 1), h);
+    d.sm = __fmul_rn(am, 1.0f / 448.0f);
+    d.sv = __fmul_rn(ar, 1.0f / 448.0f);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) d.m.w[i] = __float_as_uint(mf[i]);
@@ -681,7 +673,7 @@ __device__ __forceinline__ void norm_total(const float2* part, int64_t units, fl
     if (tid == 0) {
       const float norm = float(sqrt(double(tot.hi) + double(tot.lo)));
       out[0] = norm;
-      out[1] = max_norm > 0.f ? fminf(1.0f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : 1.0f;
+      out[1] = max_norm > 0.f ? fminf(1.0f, __fmul_rn(max_norm, __frcp_rn(__fadd_rn(norm, 1e-6f)))) : 1.0f;
     }
   }
 }

@@ -141,7 +141,7 @@ def check(was, now, sizes, t, lr, wd, param, state, rounding="nearest", seed=0, 
             assert np.all(np.abs(got_s - s) <= 2 * U * s + blk_err)
             y, got = x / s, f64(now[k][i])
             step = tr.grid_step(y, 4, -6)
-            tol = 4 * U * np.abs(y) + (err + np.abs(y) * blk_err) / s
+            tol = 6 * U * np.abs(y) + (err + np.abs(y) * blk_err) / s
             if sr:
                 assert np.all(np.abs(got - y) <= step + tol)
                 q = tr.stochastic(y, h, 4, -6)
@@ -194,7 +194,8 @@ def test_states_are_the_bits_of_the_stated_operations(O, state, rounding):
     g, m, v = f(ts["grads"][0]), f(ts["exp_avg"][0]), f(ts["exp_avg_sq"][0])
     if state == "e4m3":
         ms, vs = f(ts["exp_avg_scale"][0]), f(ts["exp_avg_sq_scale"][0])
-    opt = O.AdamW(**ts, lr=1e-3, rounding=rounding, seed=77)
+    opt = O.AdamW(**ts, lr=1e-3, rounding=rounding, seed=77, weight_decay=0.1)
+    w, lr = f(ts["params"][0]), F(1e-3)
     for t in (1, 2, 3):
         opt.step()
         torch.cuda.synchronize()
@@ -202,6 +203,11 @@ def test_states_are_the_bits_of_the_stated_operations(O, state, rounding):
             m, v = m * np.repeat(ms, 128)[:n], v * np.repeat(vs, 128)[:n]
             v = v * v
         m, v = b1 * m + c1 * g, b2 * v + (c2 * g) * g
+        rate, rbc2 = lr / F(1 - 0.9 ** t), F(1 / np.sqrt(1 - 0.999 ** t))
+        w = w * (F(1) - lr * F(0.1)) - (rate * m) / (np.sqrt(v) * rbc2 + F(1e-8))
+        # (root and quotient may miss their rounding where the value all but ties)
+        assert np.mean(f(ts["params"][0]) != w) <= 1e-3
+        w = f(ts["params"][0])
         if state == "f32":
             assert np.array_equal(f(ts["exp_avg"][0]), m) and np.array_equal(f(ts["exp_avg_sq"][0]), v)
             continue
@@ -209,12 +215,12 @@ def test_states_are_the_bits_of_the_stated_operations(O, state, rounding):
         held = []
         for x, h in ((m, hm), (np.sqrt(v), hv)):
             a = np.array([np.max(np.abs(x[j:j + 128])) for j in range(0, n, 128)], F)
-            y = x * np.repeat(F(448) / a, 128)[:n]
+            y = x * np.repeat(F(448) * (F(1) / a), 128)[:n]
             if rounding == "stochastic":     # the sum y 512 + bits / 65536 below 2^-6 is rounded once
                 small = np.floor(np.abs(y) * F(512) + h.astype(F) / F(65536)) / F(512)
                 big = (np.abs(y).view(np.uint32) + (h.astype(np.uint32) << 4) & 0xFFF00000).view(F)
                 y = np.copysign(np.minimum(np.where(np.abs(y) < F(2.0 ** -6), small, big), F(448)), y)
-            held += [tr.e4m3_nearest(y).astype(F), a / F(448)]
+            held += [tr.e4m3_nearest(y).astype(F), a * (F(1) / F(448))]
         m, ms, v, vs = held
         v = np.where((np.sqrt(f64(ts["exp_avg_sq"][0])) > 0) & (v == 0), F(2.0 ** -9), v)
         assert np.array_equal(f(ts["exp_avg"][0]), m) and np.array_equal(f(ts["exp_avg_scale"][0]), ms)
