@@ -605,6 +605,7 @@ biv_status biv_attention_backward(const biv_attn_bwd_desc* desc, biv_stream_t st
  * and its weight only.
  * seq_start outside [0, T] or not ascending is reported through
  * biv_poll_error (results are then unspecified; no access leaves [0, T)).
+ * Outputs must not overlap inputs (dz over the logits excepted, see below).
  * Workspace: biv_policy_loss_workspace bytes, 16-byte aligned, caller-owned,
  * no initial value; calls that can overlap on the GPU need separate ones. */
 typedef enum { BIV_LOSS_TOKEN_MEAN = 0, BIV_LOSS_SEQ_MEAN = 1, BIV_LOSS_SUM = 2 } biv_loss_reduce;
@@ -614,7 +615,7 @@ typedef struct {
   const uint8_t* mask;       /* [T]; NULL: every row of a sequence counts */
   const float* old_lp;       /* [T] logprobs of the policy that sampled; NULL: lp itself (r = 1) */
   const float* ref_lp;       /* [T] reference logprobs; may be NULL when kl_coef is 0 */
-  const float* adv;          /* [T] when adv_per_row, else [nseq] */
+  const float* adv;          /* [T] when adv_per_row, else [nseq] (NULL when nseq is 0) */
   int adv_per_row;
   float clip_lo, clip_hi;    /* 0 <= clip_lo <= 1, 0 <= clip_hi */
   float dual_clip;           /* 0: off; else > 1 */
@@ -682,7 +683,8 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * biv_opt_plan (host only, no launch) checks a HOST array of n tensors and
  * fills first_chunk, rng_base and vec; *chunks receives the launch size and
  * *kinds which combinations of types occur (each is a launch of its own).  The
- * caller then copies the array to the device.  It refuses null pointers,
+ * caller then copies the array to the device (by a memory copy: the kernels
+ * read it before earlier kernels of the stream are done).  It refuses null pointers,
  * misaligned elements, unsupported type combinations and tensors whose written
  * ranges overlap. */
 typedef enum { BIV_ROUND_NEAREST = 0, BIV_ROUND_STOCHASTIC = 1 } biv_rounding;
@@ -718,7 +720,8 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
  * biv_grad_norm's out, or NULL for coef = 1) are device memory read by the
  * kernel, so a captured step replays with new values.  step[0] counts the
  * steps taken (0 for new states): the call uses t = step[0] + 1 and stores it;
- * step[1] must be 0 between calls and is 0 again after each.  With clip given
+ * step[1] must be 0 between calls and is 0 again after each; calls that share
+ * it, or tensors, must not overlap on the GPU.  With clip given
  * and its norm not finite the whole call changes nothing, step included. */
 typedef struct {
   const biv_opt_tensor* tensors;   /* device */

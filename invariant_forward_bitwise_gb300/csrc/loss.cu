@@ -1123,7 +1123,7 @@ biv_status check_policy(const biv_policy_desc* d, const char* who) {
   BIV_REQUIRE(d, "%s: null descriptor", who);
   BIV_REQUIRE(d->T >= 0 && d->nseq >= 0 && d->T <= (1 << 30), "%s: bad sizes", who);
   if (d->T == 0) return BIV_OK;
-  BIV_REQUIRE(d->seq_start && d->adv && d->stats, "%s: null pointer", who);
+  BIV_REQUIRE(d->seq_start && (d->adv || (d->nseq == 0 && !d->adv_per_row)) && d->stats, "%s: null pointer", who);
   BIV_REQUIRE(d->clip_lo >= 0.f && d->clip_lo <= 1.f && d->clip_hi >= 0.f,
               "%s: clip_lo must lie in [0, 1] and clip_hi must not be negative", who);
   BIV_REQUIRE(d->dual_clip == 0.f || d->dual_clip > 1.f, "%s: dual_clip must be 0 or above 1", who);

@@ -428,6 +428,29 @@ def test_mixed_kinds_in_one_call(O):
             assert p[k] is None or all(same(a, b) for a, b in zip(p[k], q[k])), k
 
 
+def test_offsets_beyond_32_bits(O):
+    """A tensor of 2^31 + 5000 weights with 8-bit states: its end as a tensor of
+    its own."""
+    n, tail = (1 << 31) + 5000, 5000
+    ts = tensors(synth.rng(8), [tail], "bf16", "bf16", "e4m3")
+    big = {"params": torch.zeros(n, dtype=torch.bfloat16, device="cuda"),
+           "grads": torch.zeros(n, dtype=torch.bfloat16, device="cuda"),
+           "exp_avg": torch.zeros(n, dtype=torch.uint8, device="cuda"),
+           "exp_avg_sq": torch.zeros(n, dtype=torch.uint8, device="cuda"),
+           "exp_avg_scale": torch.zeros((n + 127) // 128, device="cuda"),
+           "exp_avg_sq_scale": torch.zeros((n + 127) // 128, device="cuda")}
+    for k, t in big.items():
+        m = ts[k][0].numel()
+        t[t.numel() - m:] = ts[k][0]
+    O.AdamW(**{k: [v] for k, v in big.items()}, lr=1e-3, max_norm=0.1).step()
+    O.AdamW(**ts, lr=1e-3, max_norm=0.1).step()
+    torch.cuda.synchronize()
+    for k, t in big.items():
+        m = ts[k][0].numel()
+        assert same(t[t.numel() - m:], ts[k][0]), k
+    assert not bool(big["params"][:1 << 20].any()) and not bool(big["exp_avg"][1 << 30:(1 << 30) + 4096].any())
+
+
 def test_many_small_tensors_and_lr_scales(O):
     g = synth.rng(12)
     sizes = [int(x) for x in g.integers(0, 700, 500)]

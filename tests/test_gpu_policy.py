@@ -126,8 +126,8 @@ def desc(B, c, stats, ws):
     (1, "one", dict(mask=False)), (1, "empty", dict(reduce="seq")), (5, "rows", dict(reduce="seq")),
     (31, "many", dict(reduce="sum", dual=3.0)), (1024, "inner", dict(beta=0.1, per_row=True)),
     (1025, "many", dict(reduce="seq", beta=0.1, dual=1.2)), (4099, "empty", dict(no_old=True)),
-    (9000, "rows", dict(beta=0.02)), (70001, "many", dict(reduce="seq", per_row=True, beta=0.5)),
-    (7, "none", dict(per_row=True))])
+    (2000, "rows", dict(beta=0.02, reduce="seq")), (9000, "rows", dict(beta=0.02)), (70001, "many", dict(reduce="seq", per_row=True, beta=0.5)),
+    (7, "none", dict(per_row=True)), (7, "none", dict())])
 def test_policy_loss(B, T, starts, kw):
     g = synth.rng(T)
     lp = (-g.exponential(1.0, T)).astype(np.float32).astype(np.float64)
@@ -225,6 +225,10 @@ def dz_size(c):
     (11, 32003, 0, 0, "f32", "f32", "many", dict(gamma=0.01, it=1.25)),
     (3, 50257, 3, 0, "bf16", "bf16", "one", dict(beta=0.02)),
     (170, 40963, 5, 0, "f32", "bf16", "many", dict(gamma=0.01, reduce="sum")),  # more rows than fit at once
+    (9, 5000, 1, 1, "f32", "f32", "many", dict(gamma=0.01)),      # every offset from 16 bytes in turn
+    (9, 5000, 1, 1, "f32", "bf16", "many", dict(gamma=0.01)),
+    (9, 9000, 1, 3, "bf16", "bf16", "many", dict(gamma=0.01)),
+    (9, 9000, 1, 1, "bf16", "f32", "many", dict(gamma=0.01)),
     (2, 151936, 0, 0, "f32", "f32", "one", dict(gamma=0.01, beta=0.02)),
     (45, 151936, 0, 0, "f32", "bf16", "many", dict(reduce="seq")),
     (2, 262144, 0, 0, "f32", "f32", "one", dict()),
@@ -361,6 +365,46 @@ def test_captured_policy_loss(B):
     torch.cuda.synchronize()
     assert all(same(a, o2[k]) for a, k in zip(got, ("stats", "lp", "ent", "dz")))
     assert not same(got[1], want[1])
+
+
+def test_first_call_of_a_shape_inside_a_capture(B):
+    c = logits_case(5, 777, 0, 0, "bf16", "f32", "many", dict(gamma=0.01))
+    stats = torch.empty(8, device="cuda")
+    d = desc(B, c, stats, workspace(B, 5, len(c["start"]) - 1))
+    lp, ent, dz = torch.empty(5, device="cuda"), torch.empty(5, device="cuda"), torch.empty(5, 777, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.biv_policy_loss_logits(d, c["z"], c["tgt"], lp, ent, dz)
+    g.replay()
+    o = run_logits(B, c)
+    torch.cuda.synchronize()
+    assert same(dz, o["dz"]) and same(stats, o["stats"]) and same(lp, o["lp"])
+
+
+def test_offsets_beyond_32_bits(B):
+    """33000 rows of 131072 bf16 logits (more than 2^32 of them), gradient in
+    place: the first and last rows as in a small call."""
+    T, V = 33000, 131072
+    c = logits_case(6, V, 0, 0, "bf16", "bf16", "one", dict(mask=False, reduce="sum"))
+    small = run_logits(B, c)
+    big = torch.zeros(T, V, dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, 2, T - 3, T - 2, T - 1]
+    for i, r in enumerate(rows):
+        big[r] = c["z"][i]
+    wide = dict(c, T=T, start=[0, T], V=V)
+    idx = np.zeros(T, np.int64)
+    for i, r in enumerate(rows):
+        idx[r] = i
+    wide["old"], wide["ref"] = c["old"][idx], c["ref"][idx]
+    wide["tgt"] = c["tgt"][torch.from_numpy(idx).cuda()].contiguous()
+    wide["mask"] = np.zeros(T, np.uint8)
+    wide["mask"][rows] = 1
+    o = run_logits(B, wide, dz=big, z=big)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    for i, r in enumerate(rows):
+        assert same(big[r], small["dz"][i]) and same(o["lp"][r:r + 1], small["lp"][i:i + 1]), r
+    assert not bool(big[5000].any()) and not bool(big[T - 4].any())
 
 
 def test_binding_refuses(B):
