@@ -14,6 +14,7 @@
 // sums the loss (policy_token_kernel, whose last block adds the blocks up).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -750,12 +751,20 @@ __device__ __forceinline__ void store_unaligned(uint8_t* dst, const uint8_t* buf
   const uint4* src = reinterpret_cast<const uint4*>(buf);
   const int u0 = off ? 1 : 0, u1 = (off + left * DS) >> 4;
   const bool half = DS == 2 && (off & 2) != 0;
+  auto copy = [&](auto ws) {
+    constexpr int WS = decltype(ws)::value;
+#pragma unroll
+    for (int k = 0; k < kGroupBytes / 512; ++k) {    // (a group has at most 256 units)
+      const int u = u0 + lane + k * 32;
+      if (u < u1) unit[u] = WS < 4 ? unaligned_unit<WS & 3>(src + u - 1, half) : src[u];
+    }
+  };
   switch ((16 - off) >> 2) {
-    case 0: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<0>(src + u - 1, half); break;
-    case 1: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<1>(src + u - 1, half); break;
-    case 2: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<2>(src + u - 1, half); break;
-    case 3: for (int u = u0 + lane; u < u1; u += 32) unit[u] = unaligned_unit<3>(src + u - 1, half); break;
-    default: for (int u = lane; u < u1; u += 32) unit[u] = src[u];
+    case 0: copy(std::integral_constant<int, 0>()); break;
+    case 1: copy(std::integral_constant<int, 1>()); break;
+    case 2: copy(std::integral_constant<int, 2>()); break;
+    case 3: copy(std::integral_constant<int, 3>()); break;
+    default: copy(std::integral_constant<int, 4>());
   }
   const int head = off ? min(left, (16 - off) / DS) : 0;    // elements before unit u0
   const int tail0 = max(head, (u1 * 16 - off) / DS);
