@@ -617,36 +617,34 @@ struct Run {
   }
 };
 
-// largest logit of the group, over the warp
+// largest of a lane's logits, run by run
+template <bool ZB>
+struct LaneMax {
+  uint32_t a = ZB ? 0xFF80FF80u : 0xFF800000u, b = a;   // -inf
+  __device__ __forceinline__ void add(const uint4& v) {
+    if constexpr (ZB) {
+      a = max_bf16x2_nan(a, max_bf16x2_nan(v.x, v.y));
+      b = max_bf16x2_nan(b, max_bf16x2_nan(v.z, v.w));
+    } else {
+      a = __float_as_uint(fmax3_nan(__uint_as_float(a), __uint_as_float(v.x), __uint_as_float(v.y)));
+      b = __float_as_uint(fmax3_nan(__uint_as_float(b), __uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+  }
+  __device__ __forceinline__ float value() const {
+    if constexpr (ZB) {
+      const uint32_t m = max_bf16x2_nan(a, b);
+      return fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+    return fmax_nan(__uint_as_float(a), __uint_as_float(b));
+  }
+};
+// of the group, over the warp
 template <bool ZB>
 __device__ __forceinline__ float group_max(const uint8_t* buf, int lane) {
-  float m;
-  if constexpr (ZB) {
-    uint32_t a = 0, b = 0;
+  LaneMax<ZB> m;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 v = reinterpret_cast<const uint4*>(buf)[j * 32 + lane];
-      if (j == 0) {
-        a = max_bf16x2_nan(v.x, v.y);
-        b = max_bf16x2_nan(v.z, v.w);
-      } else {
-        a = max_bf16x2_nan(a, max_bf16x2_nan(v.x, v.y));
-        b = max_bf16x2_nan(b, max_bf16x2_nan(v.z, v.w));
-      }
-    }
-    a = max_bf16x2_nan(a, b);
-    m = fmax_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
-  } else {
-    float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float4 v = reinterpret_cast<const float4*>(buf)[j * 32 + lane];
-      a = fmax3_nan(a, v.x, v.y);
-      b = fmax3_nan(b, v.z, v.w);
-    }
-    m = fmax_nan(a, b);
-  }
-  return warp_max_keep_nan(m);
+  for (int j = 0; j < 8; ++j) m.add(reinterpret_cast<const uint4*>(buf)[j * 32 + lane]);
+  return warp_max_keep_nan(m.value());
 }
 
 // sums over the group's 2^y and 2^y y, y = x c - mc, over the warp
@@ -712,32 +710,42 @@ __device__ __forceinline__ uint4 unaligned_unit(const uint4* p, bool half) {
 // 16-byte aligned) to the buffer's start, and mask what lies behind `left`
 // logits.
 template <int WS, bool ZB>
-__device__ __forceinline__ void settle(uint8_t* buf, int lane, bool half, int left) {
+__device__ __forceinline__ float settle(uint8_t* buf, int lane, bool half) {
   uint4 r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) r[j] = unaligned_unit<WS>(reinterpret_cast<const uint4*>(buf) + j * 32 + lane, ZB && half);
   __syncwarp();
+  LaneMax<ZB> m;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) reinterpret_cast<uint4*>(buf)[j * 32 + lane] = r[j];
+  for (int j = 0; j < 8; ++j) {
+    reinterpret_cast<uint4*>(buf)[j * 32 + lane] = r[j];
+    m.add(r[j]);
+  }
+  return m.value();
 }
+// Returns the largest logit, over the warp.
 template <bool ZB, bool SHIFT>
-__device__ __forceinline__ void settle_group(uint8_t* buf, int lane, int off, int left) {
+__device__ __forceinline__ float settle_group(uint8_t* buf, int lane, int off, int left) {
+  constexpr int kGroup = kGroupBytes / (ZB ? 2 : 4);
+  float m = 0.f;
   __syncwarp();
   if (SHIFT && off) {
     const bool half = (off & 2) != 0;
     switch (off >> 2) {
-      case 0: settle<0, ZB>(buf, lane, half, left); break;
-      case 1: settle<1, ZB>(buf, lane, half, left); break;
-      case 2: settle<2, ZB>(buf, lane, half, left); break;
-      default: settle<3, ZB>(buf, lane, half, left);
+      case 0: m = settle<0, ZB>(buf, lane, half); break;
+      case 1: m = settle<1, ZB>(buf, lane, half); break;
+      case 2: m = settle<2, ZB>(buf, lane, half); break;
+      default: m = settle<3, ZB>(buf, lane, half);
     }
     __syncwarp();
+    if (left == kGroup) return warp_max_keep_nan(m);
   }
-  for (int e = left + lane; e < kGroupBytes / (ZB ? 2 : 4); e += 32) {
+  for (int e = left + lane; e < kGroup; e += 32) {
     if (ZB) reinterpret_cast<uint16_t*>(buf)[e] = 0xF14A;
     else reinterpret_cast<float*>(buf)[e] = kMasked;
   }
   __syncwarp();
+  return group_max<ZB>(buf, lane);
 }
 
 // Copy a group's results (`left` of DS bytes, from the start of its buffer) to a
@@ -1029,6 +1037,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       const int left = min(kGroup, a.V - g * kGroup);
       uint8_t* buf = bufs + slot1 * BUF;
       mbar_wait(smem_u32(bars + slot1), phase1, a.p.err);
+      float m;
       if ((SHIFT && off) || left < kGroup) {
         // elements of the row's first and last 16-byte unit, where it holds
         // bytes outside the row: not part of any copy
@@ -1047,10 +1056,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
             if (SHIFT && g == 0 && lane < left && (b & 15) && (b & 15) + lane * ES < 16) fetch(lane);
           }
         }
-        settle_group<ZB, SHIFT>(buf, lane, off, left);
+        m = settle_group<ZB, SHIFT>(buf, lane, off, left);
         dirty |= 1u << (slot1 & 31);
+      } else {
+        m = group_max<ZB>(buf, lane);
       }
-      const float m = group_max<ZB>(buf, lane);
       float mc = -INFINITY, s = 0.f, t = 0.f;
       if (!(m <= kMasked)) {         // (a NaN comes through)
         mc = m * a.c;
@@ -1097,7 +1107,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     if (M == -INFINITY) S = NAN;   // nothing but masked logits
     constexpr float kLn2 = 0.6931471805599453f;
     const float lnS = logf(S);
-    const float H = lnS - kLn2 * (U / S);
+    const float rS = __frcp_rn(S);
+    const float H = lnS - kLn2 * (U * rS);
     const int from = q1 & 31;
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
     zt = __shfl_sync(0xffffffffu, m_zt, from);
@@ -1112,7 +1123,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       const float wt = __shfl_sync(0xffffffffu, m_wa.x, from), A = __shfl_sync(0xffffffffu, m_wa.y, from);
       const float old = __shfl_sync(0xffffffffu, m_old, from), ref = __shfl_sync(0xffffffffu, m_ref, from);
       const Token o = policy_token(a.p, lp, A, old, ref);
-      const float dlp = wt * o.dlp, wg = wt * a.p.gamma, is = a.it / S;
+      const float dlp = wt * o.dlp, wg = wt * a.p.gamma, is = a.it * rS;
       a0 = is * (wg * (H - lnS) - dlp);
       a1 = is * wg * kLn2;
       at_target = a.it * dlp;
