@@ -14,7 +14,6 @@
 // sums the loss (policy_token_kernel, whose last block adds the blocks up).
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "common.cuh"
 
@@ -694,49 +693,34 @@ __device__ __forceinline__ void clamp_group(uint8_t* buf, int lane) {
   }
 }
 
-// 16 bytes from WS words (and, where `half`, another half word) behind the
-// start of a 16-byte unit on
-template <int WS>
-__device__ __forceinline__ uint4 unaligned_unit(const uint4* p, bool half) {
-  const uint4 a = p[0], b = p[1];
-  const uint32_t v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = half ? __funnelshift_r(v[i + WS], v[i + WS + 1], 16) : v[i + WS];
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 // Bring a group that starts `off` bytes into its buffer (a row that is not
-// 16-byte aligned) to the buffer's start, and mask what lies behind `left`
-// logits.
-template <int WS, bool ZB>
-__device__ __forceinline__ float settle(uint8_t* buf, int lane, bool half) {
-  uint4 r[8];
+// 16-byte aligned) to the buffer's start.  Lanes take consecutive words, so that
+// neither side has bank conflicts at any offset (16 bytes a lane, put together
+// from two units, took 69 us where this takes 53: 1000 rows of 32003 FP32 logits
+// without padding).  Returns the largest of the lane's logits.
+template <bool ZB, bool HALF>
+__device__ __forceinline__ float settle(uint8_t* buf, int lane, int off) {
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(buf + (off & ~3)) + lane;
+  uint32_t r[32];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = unaligned_unit<WS>(reinterpret_cast<const uint4*>(buf) + j * 32 + lane, ZB && half);
+  for (int k = 0; k < 32; ++k)
+    r[k] = HALF ? __funnelshift_r(src[k * 32], src[k * 32 + 1], 16) : src[k * 32];
   __syncwarp();
   LaneMax<ZB> m;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    reinterpret_cast<uint4*>(buf)[j * 32 + lane] = r[j];
-    m.add(r[j]);
-  }
+  for (int k = 0; k < 32; ++k) reinterpret_cast<uint32_t*>(buf)[k * 32 + lane] = r[k];
+#pragma unroll
+  for (int k = 0; k < 32; k += 4) m.add(make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]));
   return m.value();
 }
-// Returns the largest logit, over the warp.
+// ... and mask what lies behind `left` logits.  Returns the largest logit, over
+// the warp.
 template <bool ZB, bool SHIFT>
 __device__ __forceinline__ float settle_group(uint8_t* buf, int lane, int off, int left) {
   constexpr int kGroup = kGroupBytes / (ZB ? 2 : 4);
-  float m = 0.f;
   __syncwarp();
   if (SHIFT && off) {
-    const bool half = (off & 2) != 0;
-    switch (off >> 2) {
-      case 0: m = settle<0, ZB>(buf, lane, half); break;
-      case 1: m = settle<1, ZB>(buf, lane, half); break;
-      case 2: m = settle<2, ZB>(buf, lane, half); break;
-      default: m = settle<3, ZB>(buf, lane, half);
-    }
+    const float m = ZB && (off & 2) ? settle<ZB, ZB>(buf, lane, off) : settle<ZB, false>(buf, lane, off);
     __syncwarp();
     if (left == kGroup) return warp_max_keep_nan(m);
   }
@@ -748,38 +732,28 @@ __device__ __forceinline__ float settle_group(uint8_t* buf, int lane, int off, i
   return group_max<ZB>(buf, lane);
 }
 
-// Copy a group's results (`left` of DS bytes, from the start of its buffer) to a
-// row of any alignment: whole 16-byte units of the destination, put together
-// from two of the buffer's; the first and last elements, which share their unit
-// with a neighbour, one by one.
-template <int DS>
+// Copy a group's N results (`left` of them, DS bytes each, from the start of its
+// buffer) to a row of any alignment, in words of the destination.
+template <int DS, int N>
 __device__ __forceinline__ void store_unaligned(uint8_t* dst, const uint8_t* buf, int lane, int left) {
-  const int off = int(reinterpret_cast<uintptr_t>(dst) & 15);
-  uint4* unit = reinterpret_cast<uint4*>(dst - off);
-  const uint4* src = reinterpret_cast<const uint4*>(buf);
-  const int u0 = off ? 1 : 0, u1 = (off + left * DS) >> 4;
-  const bool half = DS == 2 && (off & 2) != 0;
-  auto copy = [&](auto ws) {
-    constexpr int WS = decltype(ws)::value;
-#pragma unroll
-    for (int k = 0; k < kGroupBytes / 512; ++k) {    // (a group has at most 256 units)
-      const int u = u0 + lane + k * 32;
-      if (u < u1) unit[u] = WS < 4 ? unaligned_unit<WS & 3>(src + u - 1, half) : src[u];
-    }
-  };
-  switch ((16 - off) >> 2) {
-    case 0: copy(std::integral_constant<int, 0>()); break;
-    case 1: copy(std::integral_constant<int, 1>()); break;
-    case 2: copy(std::integral_constant<int, 2>()); break;
-    case 3: copy(std::integral_constant<int, 3>()); break;
-    default: copy(std::integral_constant<int, 4>());
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(buf) + lane;
+  const bool half = DS == 2 && (reinterpret_cast<uintptr_t>(dst) & 2);
+  const int head = half ? 1 : 0, words = (left - head) * DS / 4;
+  uint32_t* d = reinterpret_cast<uint32_t*>(dst + head * DS) + lane;
+  if (half) {
+#pragma unroll 8
+    for (int k = 0; k < N * DS / 128; ++k)
+      if (k * 32 + lane < words) d[k * 32] = __funnelshift_r(src[k * 32], src[k * 32 + 1], 16);
+  } else {
+#pragma unroll 16
+    for (int k = 0; k < N * DS / 128; ++k)
+      if (k * 32 + lane < words) d[k * 32] = src[k * 32];
   }
-  const int head = off ? min(left, (16 - off) / DS) : 0;    // elements before unit u0
-  const int tail0 = max(head, (u1 * 16 - off) / DS);
-  const int e = lane < 16 ? lane : tail0 + lane - 16;
-  if (lane < 16 ? e < head : e < left) {
-    if (DS == 2) reinterpret_cast<uint16_t*>(dst)[e] = reinterpret_cast<const uint16_t*>(buf)[e];
-    else reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(buf)[e];
+  if (DS == 2) {   // the first and last elements, where they share their word with a neighbour
+    uint16_t* h = reinterpret_cast<uint16_t*>(dst);
+    const uint16_t* b = reinterpret_cast<const uint16_t*>(buf);
+    if (lane == 0 && head) h[0] = b[0];
+    if (lane == 1 && head + words * 2 < left) h[left - 1] = b[left - 1];
   }
 }
 
@@ -993,7 +967,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
           }
           if (SHIFT && DS <= ES) {
             __syncwarp();
-            store_unaligned<DS>(dst, buf, lane, left);
+            store_unaligned<DS, kGroup>(dst, buf, lane, left);
             dirty |= 1u << (slot0 & 31);
           }
         }
