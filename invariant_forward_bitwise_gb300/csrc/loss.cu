@@ -1255,9 +1255,10 @@ biv_status max_clusters(K kern, unsigned cluster, unsigned threads, size_t smem,
 // CTAs per SM; 2037 x 131072 bf16 188 us on clusters of 2, 201 us on 4.  Up to
 // 16 warps (128 registers each): 24 take 786 us on the first case, 189 us on the
 // second.  What is left of 216 KB prefetches the next row: without it the first
-// case takes 786 us.
-constexpr size_t kRowBytesPerCta = 160 << 10;
-constexpr size_t kRingBytes = 216 << 10;
+// case takes 786 us.  Shorter rows run two CTAs per SM, so that one's barrier and
+// merge overlap the other's traffic: 1000 x 16384 FP32 28.1 us against 31.6 us;
+// 2000 x 50257 bf16 (100 KB), which would lose its prefetch, 122 us against 104.
+constexpr size_t kRowBytesPerCta = 160 << 10, kPairBytes = 80 << 10, kRingBytes = 216 << 10;
 
 template <bool ZB, bool DB, bool SHIFT>
 biv_status launch_logits(LogitsArgs& a, cudaStream_t s) {
@@ -1269,11 +1270,13 @@ biv_status launch_logits(LogitsArgs& a, cudaStream_t s) {
   // few rows: spread each over more SMs (no bit depends on it)
   while (cl < 8 && int(cl) * 2 <= a.G && int64_t(a.p.T) * cl * 2 <= sms) cl *= 2;
   a.gpc = int((a.G + cl - 1) / cl);
-  const int per = (a.gpc + kMaxWarps - 1) / kMaxWarps;
+  const bool pair = size_t(a.gpc) * kGroupBytes <= kPairBytes;
+  const int most = pair ? kMaxWarps / 2 : kMaxWarps, per = (a.gpc + most - 1) / most;
+  const size_t ring = pair ? kRingBytes / 2 - 1024 : kRingBytes;
   const unsigned warps = unsigned((a.gpc + per - 1) / per), threads = warps * 32;
   // a warp's ring: its groups of a row, and of the next one what the room allows
   a.slots = per;
-  while (a.slots < 2 * per && size_t(a.slots + 1) * warps * BUF <= kRingBytes) ++a.slots;
+  while (a.slots < 2 * per && size_t(a.slots + 1) * warps * BUF <= ring) ++a.slots;
   const size_t smem = size_t(a.slots) * warps * (BUF + 8) + size_t(a.G) * 32;
   int fit = 0;
   biv_status st = max_clusters(policy_logits_kernel<ZB, DB, SHIFT>, cl, threads, smem, &fit);
