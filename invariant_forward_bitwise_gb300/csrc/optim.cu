@@ -161,13 +161,40 @@ __device__ __forceinline__ void to_pairs(const Raw<W>& r, uint64_t (&f)[4]) {
   }
 }
 
-// 32-bit hash: xor-shifts and two odd multipliers (a bijection)
-__device__ __forceinline__ uint32_t mix32(uint32_t x) {
-  x ^= x >> 16;
+// 32-bit hash, a bijection: xor-shifts and two odd multipliers (Wellons,
+// "Prospecting for hash functions", 2018)
+__device__ __forceinline__ uint32_t mix32_tail(uint32_t x) {   // after the first xor-shift, before the last
   x *= 0x7FEB352Du;
   x ^= x >> 15;
-  x *= 0x846CA68Bu;
+  return x * 0x846CA68Bu;
+}
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x = mix32_tail(x ^ (x >> 16));
   return x ^ (x >> 16);
+}
+// The random bits of elements id .. id + 7 (id a multiple of 8): the hash of
+// (low half ^ key) + a multiple of the high half.  Here without its last
+// xor-shift (x ^= x >> 16), which is undone by the first one of a second hash:
+// element: low and high 16 bits of hashed(x); weight: second_hash(x).
+__device__ __forceinline__ void hash8(uint64_t id, uint32_t key, uint32_t (&x)[8]) {
+  const uint32_t a = uint32_t(id) ^ key, hi = uint32_t(id >> 32) * 0x85EBCA6Bu;
+  if (hi == 0) {          // (a warp's elements differ here at most once in 2^32)
+    const uint32_t b = a ^ (a >> 16);        // a ^ i has the same upper half for all eight
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = mix32_tail(b ^ uint32_t(i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t y = (a ^ uint32_t(i)) + hi;
+      x[i] = mix32_tail(y ^ (y >> 16));
+    }
+  }
+}
+// mix32(h ^ G) for h = x ^ (x >> 16): its first xor-shift gives x ^ G ^ (G >> 16)
+__device__ __forceinline__ uint32_t second_hash(uint32_t x) {
+  constexpr uint32_t G = 0x9E3779B9u;
+  const uint32_t y = mix32_tail(x ^ (G ^ (G >> 16)));
+  return y ^ (y >> 16);
 }
 
 // |y| <= 448 to the e4m3 grid, up with a chance of the part cut off (16 random
@@ -206,7 +233,9 @@ __device__ __forceinline__ void sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
       asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(f[2 * i]));
       asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(f[2 * i + 1]));
       const uint64_t y = pack2(y0, y1), x = mul2(v[i], y);
-      const uint64_t e = fma2(mul2(x, pack2(-1.0f, -1.0f)), x, v[i]);
+      float x0, x1;
+      unpack2(x, x0, x1);
+      const uint64_t e = pack2(__fmaf_rn(-x0, x0, f[2 * i]), __fmaf_rn(-x1, x1, f[2 * i + 1]));
       unpack2(fma2(e, mul2(y, pack2(0.5f, 0.5f)), x), r[2 * i], r[2 * i + 1]);
     }
   } else {
@@ -238,7 +267,7 @@ __device__ __forceinline__ Raw<2> encode8(const float (&x)[8], float inv, const 
   float y[8];
 #pragma unroll
   for (int i = 0; i < 8; i += 2) unpack2(mul2(pack2(x[i], x[i + 1]), pack2(inv, inv)), y[i], y[i + 1]);
-  auto rnd = [&](int i) { return ROOT ? h[i] >> 16 : h[i] & 0xFFFFu; };
+  auto rnd = [&](int i) { return ROOT ? h[i] >> 16 : (h[i] ^ (h[i] >> 16)) & 0xFFFFu; };
   if (SR || ROOT) {
     float low = fmin3(fabsf(y[0]), fabsf(y[1]), fabsf(y[2]));
     low = fmin3(low, fabsf(y[3]), fabsf(y[4]));
@@ -350,11 +379,7 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
     wf[2 * i + 1] = __fsub_rn(w1, q[1]);
   }
   uint32_t h[8];
-  if constexpr (SR && (E8 || PK == kParamBf16)) {
-    const uint32_t hi = uint32_t(id >> 32) * 0x85EBCA6Bu;   // (id is a multiple of 8)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = mix32(((uint32_t(id) + i) ^ s.key) + hi);
-  }
+  if constexpr (SR && (E8 || PK == kParamBf16)) hash8(id, s.key, h);
   if constexpr (PK != kParamBf16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) d.w.w[i] = __float_as_uint(wf[i]);
@@ -364,8 +389,8 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (SR && PK == kParamBf16) {
-        const uint32_t lo = __float_as_uint(wf[2 * i]) + (mix32(h[2 * i] ^ 0x9E3779B9u) & 0xFFFFu);
-        const uint32_t hi = __float_as_uint(wf[2 * i + 1]) + (mix32(h[2 * i + 1] ^ 0x9E3779B9u) & 0xFFFFu);
+        const uint32_t lo = __float_as_uint(wf[2 * i]) + (second_hash(h[2 * i]) & 0xFFFFu);
+        const uint32_t hi = __float_as_uint(wf[2 * i + 1]) + (second_hash(h[2 * i + 1]) & 0xFFFFu);
         b.w[i] = __byte_perm(lo, hi, 0x7632);
       } else {
         const __nv_bfloat162 c = __floats2bfloat162_rn(wf[2 * i], wf[2 * i + 1]);
@@ -423,6 +448,7 @@ struct StageLayout {   // a stage: gradient, weight, codes, scales
 struct Ring {          // where the next chunk of a CTA is staged, over its tensors
   uint8_t* bufs;
   uint64_t* bars;
+  uint32_t* read;      // warps that have read the stage
   int stage;
   uint32_t phase;
   int* err;
@@ -467,6 +493,7 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
       bulk_load(st + L::MS, t.m_scale + c * kScales, kScales * 4, bar);
       bulk_load(st + L::VS, t.v_scale + c * kScales, kScales * 4, bar);
     };
+    if (staged) __syncthreads();           // the tensor before: its last stages are read
     if (staged && threadIdx.x == 0) {
       for (int k = 0; k < L::STAGES && k < full; ++k) {
         const int st = ring.stage + k;
@@ -484,8 +511,13 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
         from_stage(st + L::V, d.v);
         d.sm = reinterpret_cast<const float*>(st + L::MS)[threadIdx.x >> 4];
         d.sv = reinterpret_cast<const float*>(st + L::VS)[threadIdx.x >> 4];
-        __syncthreads();                   // the stage is read: it may be filled again
-        if (threadIdx.x == 0 && k + L::STAGES < full) copy_ahead(k + L::STAGES, ring.stage);
+        // the warp that reads a stage last fills it again: none waits for another
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+          __threadfence_block();
+          if (atomicInc(ring.read + ring.stage, kOT / 32 - 1) == kOT / 32 - 1 && k + L::STAGES < full)
+            copy_ahead(k + L::STAGES, ring.stage);
+        }
         if (++ring.stage == L::STAGES) {
           ring.stage = 0;
           ring.phase ^= 1;
@@ -554,12 +586,16 @@ __global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_con
   using L = StageLayout<GB ? 4 : 8, PK == kParamBf16 ? 4 : 8>;
   __shared__ float s_bc[2];
   __shared__ __align__(8) uint64_t s_bars[L::STAGES];
+  __shared__ uint32_t s_read[L::STAGES];
   extern __shared__ __align__(128) uint8_t stages[];
   if (E8 && threadIdx.x == 0) {
-    for (int i = 0; i < L::STAGES; ++i) mbar_init(smem_u32(s_bars + i), 1);
+    for (int i = 0; i < L::STAGES; ++i) {
+      mbar_init(smem_u32(s_bars + i), 1);
+      s_read[i] = 0;
+    }
     fence_barrier_init();
   }
-  Ring ring = {stages, s_bars, 0, 0u, a.err};
+  Ring ring = {stages, s_bars, s_read, 0, 0u, a.err};
   const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
   int ti = find_tensor(a.t, a.n, c0);   // (the table is the host's: no kernel writes it)
