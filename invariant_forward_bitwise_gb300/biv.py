@@ -222,13 +222,15 @@ def _p(t: Optional[torch.Tensor]):
 
 # the current stream's handle without a Stream object around it, where torch has it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# the current device, without the checks of torch.cuda.current_device()
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> C.c_void_p:
     if stream is not None:
         return C.c_void_p(stream.cuda_stream)
     if _raw_stream is not None:
-        return C.c_void_p(_raw_stream(torch.cuda.current_device()))
+        return C.c_void_p(_raw_stream(_device()))
     return C.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
@@ -592,7 +594,7 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
     sequence) or [T]; mask uint8 or bool [T]; old_lp, ref_lp float32 [T];
     stats float32 [8]; workspace uint8 of biv_policy_loss_workspace bytes.
     With nseq == T an advantage vector counts as one per sequence."""
-    dev, f32 = torch.cuda.current_device(), torch.float32
+    dev, f32 = _device(), torch.float32
     nseq, nadv = seq_start.numel() - 1, adv.numel()
     if nseq < 0:
         raise ValueError("seq_start needs at least one entry")
@@ -618,7 +620,7 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
 
 def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):
     """lp float32 [T] -> dlp float32 [T] (or None: statistics only) and desc's stats."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     _rows_ok("lp", lp, torch.float32, desc.T, dev)
     if dlp is not None:
         _rows_ok("dlp", dlp, torch.float32, desc.T, dev)
@@ -633,7 +635,7 @@ def biv_policy_loss_logits(desc: PolicyDesc, logits, target, lp, entropy, dz=Non
                            stream=None):
     """logits float32 or bf16 [T, V] (rows of stride 1) -> lp, entropy float32
     [T] and dz float32 or bf16 [T, V] (None: no gradient; may be logits)."""
-    dev, T = torch.cuda.current_device(), desc.T
+    dev, T = _device(), desc.T
     V = logits.shape[1] if logits.dim() == 2 else -1
     for what, t in (("logits", logits), ("dz", dz)):
         if t is None:

@@ -138,7 +138,7 @@ class AdamW:
 
     def step(self, stream=None):
         """One update of every tensor from its gradient."""
-        if torch.cuda.current_device() != self.device.index:
+        if biv._device() != self.device.index:
             raise ValueError(f"step() runs on the optimizer's device, {self.device}")
         if self.max_norm > 0:
             biv.biv_grad_norm(self.table, self.n, self.chunks, self.max_norm, self.norm, self.ws, stream=stream)
