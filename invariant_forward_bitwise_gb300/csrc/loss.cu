@@ -550,7 +550,7 @@ struct LogitsArgs {
   int64_t ld;
   const int32_t* target;
   int V, G, gpc, slots;     // groups of a row, groups per CTA, buffers per warp
-  float it, c;              // 1 / temperature, and that times log2(e)
+  float it, c, eta;         // 1 / temperature; that times log2(e), c (1 + eta) before its rounding
   float* lp;
   float* ent;
   void* dz;
@@ -1087,9 +1087,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       } else {
         m = group_max<ZB>(buf, lane);
       }
-      float mc = -INFINITY, s = 0.f, t = 0.f;
+      float mc = 0.f, s = 0.f, t = 0.f;
       if (!(m <= kMasked)) {         // (a NaN comes through)
-        mc = m * a.c;
+        mc = __fmul_rn(m, a.c);
         group_sums<ZB>(buf, lane, a.c, mc, s, t);
       }
       // masked logits among the others (0 times an exponent of -inf), or alone:
@@ -1100,8 +1100,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
         __syncwarp();
         dirty |= 1u << (slot1 & 31);
         if (t != t) group_sums<ZB>(buf, lane, a.c, mc, s, t);
+        if (m <= kMasked) m = -INFINITY;
       }
-      if (lane < ncta) st_cluster_v4(smem_u32(st + g), lane, mc, s, t, 0.f);
+      if (lane < ncta) st_cluster_v4(smem_u32(st + g), lane, m, s, t, 0.f);
       if (++slot1 == slots) {
         slot1 = 0;
         phase1 ^= 1;
@@ -1111,26 +1112,27 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
 
     // ---- merge row q1's groups: lane l takes groups l, l + 32, ... in order
     float4 q[kMaxMerge];
-    M = -INFINITY;
+    float top = -INFINITY;             // the row's largest logit
 #pragma unroll
     for (int k = 0; k < kMaxMerge; ++k) {
       const int g = k * 32 + lane;
       q[k] = g < a.G ? st[g] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      M = fmax_nan(M, q[k].x);
+      top = fmax_nan(top, q[k].x);
     }
-    M = warp_max_keep_nan(M);
+    top = warp_max_keep_nan(top);
+    M = __fmul_rn(top, a.c);
     float S = 0.f, U = 0.f;
 #pragma unroll
     for (int k = 0; k < kMaxMerge; ++k) {
       // a group of masked logits alone (M may be -inf too) adds nothing
       const bool has = q[k].x != -INFINITY;
-      const float d = q[k].x - M, f = ex2f(d);
+      const float d = __fsub_rn(__fmul_rn(q[k].x, a.c), M), f = ex2f(d);
       S = has ? fmaf(q[k].y, f, S) : S;
       U = has ? fmaf(f, fmaf(q[k].y, d, q[k].z), U) : U;
     }
     S = warp_sum_x(S);
     U = warp_sum_x(U);
-    if (M == -INFINITY) S = NAN;   // nothing but masked logits
+    if (top == -INFINITY) S = NAN;   // nothing but masked logits
     constexpr float kLn2 = 0.6931471805599453f;
     const float lnS = logf(S);
     const float rS = __frcp_rn(S);
@@ -1139,7 +1141,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
     zt = __shfl_sync(0xffffffffu, m_zt, from);
     const bool tg_ok = tg0 >= 0 && tg0 < a.V;
-    const float lp = tg_ok ? fmaf(zt, a.c, -M) * kLn2 - lnS : NAN;
+    // lp = (x_t - max x) - log of the sum of exp(x - max x), x = z / temperature, as
+    // these FP32 operations.  That sum is S but for three roundings, which log S has
+    // to first order: of max x, of M, and of c (as ln 2 eta U / S).  (From the base-2
+    // exponent, fma(z_t, c, -M) ln 2 - lnS, lp was off by twice as much.)
+    const float xm = __fmul_rn(top, a.it);
+    const float ln_ratio = fmaf(-kLn2, fmaf(top, a.c, -M), fmaf(top, a.it, -xm));
+    const bool near = fabsf(ln_ratio) < 0x1p-12f;     // (not so for logits of some thousands)
+    const float Sm = S + fmaf(near ? ln_ratio : 0.f, S, kLn2 * a.eta * U);
+    const float ls = logf(Sm) + (near ? 0.f : ln_ratio);
+    const float lp = tg_ok ? __fsub_rn(__fsub_rn(__fmul_rn(zt, a.it), xm), ls) : NAN;
     if (teller) {
       a.lp[row_of(q1)] = lp;
       a.ent[row_of(q1)] = H;
@@ -1410,7 +1421,9 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
   a.z = z; a.ld = ld; a.target = target; a.V = V;
   a.G = a.gpc = a.slots = 0;
   a.it = inv_temp;
-  a.c = float(double(inv_temp) * 1.4426950408889634);
+  const double c = double(inv_temp) * 1.4426950408889634;
+  a.c = float(c);
+  a.eta = float(c / a.c - 1.0);
   a.lp = lp; a.ent = entropy; a.dz = dz; a.ldz = ldz;
   // rows of logits and gradient that all keep 16 bytes' alignment
   const bool shift = zb % 16 != 0 || (size_t(ld) * es) % 16 != 0 ||

@@ -342,6 +342,24 @@ def test_bad_targets_bad_starts_and_nothing_left(B):
         assert B.biv_poll_error() == 2 and B.biv_poll_error() == 0
 
 
+@pytest.mark.parametrize("T,V,starts", [
+    (130, 300, "many"), (300, 300, "empty"), (2000, 9000, "many"), (1500, 5000, "rows"), (4096, 2100, "inner"),
+    (5000, 300, "rows"), (40, 5000, "none")])
+def test_sums_are_those_of_the_logprobs(B, T, V, starts):
+    """However the sums of a call from logits are taken (by its last CTA, by a
+    kernel behind it): the bits that its lp alone give."""
+    c = logits_case(T, V, 0, 0, "f32", "bf16", starts, dict(beta=0.05, reduce="seq"))
+    o = run_logits(B, c)
+    stats = torch.full((8,), float("nan"), device="cuda")
+    d = desc(B, c, stats, workspace(B, T, len(c["start"]) - 1))
+    B.biv_policy_loss(d, o["lp"])
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    keep = [0, 1, 2, 4, 5, 6, 7]
+    assert same(stats[keep], o["stats"][keep])
+    check_stats(f64(o["stats"]), oracle_loss(c, c["H"])[0], sizes(c, c["H"])[0])
+
+
 def test_captured_policy_loss(B):
     """A replay reads new inputs and gives the bits of an eager call."""
     c = logits_case(37, 5000, 0, 0, "f32", "bf16", "many", dict(gamma=0.01, beta=0.02))
@@ -467,6 +485,27 @@ def test_masked_logits(B, zt, low):
     assert np.all(np.abs(f64(o["lp"]) - c["lp"]) <= REL * (1 + np.abs(c["lp"])))
     assert np.all(np.abs(f64(o["ent"]) - c["H"]) <= REL * (1 + c["H"]))
     check_stats(f64(o["stats"]), want, sizes(c, c["H"])[0])
+
+
+@pytest.mark.parametrize("size", [1e3, 1e5, 1e7, -1e7])
+@pytest.mark.parametrize("it", [1.0, 1.25, 0.77])
+def test_large_logits(B, size, it):
+    """Rows of logits far from 0.  The products of such logits and 1 / temperature
+    (and of their largest) are rounded, by |size it| 2^-24 each, and so are
+    exponents to base 2."""
+    g = synth.rng(int(abs(size)))
+    T, V = 9, 5000
+    z = (size + g.standard_normal((T, V)) * 3).astype(np.float32)
+    target = g.integers(0, V, T)
+    c = dict(T=T, start=[0, T], kw=dict(no_old=True), adv=np.ones(1), mask=None, V=V, it=it, z=dev(z),
+             tgt=dev(target, np.int32), col=0, ld=V, dzt="f32", ref=None)
+    o = run_logits(B, c)
+    torch.cuda.synchronize()
+    lp, H, _, _ = tr.token_logprobs(z.astype(np.float64), target, float(np.float32(it)))
+    # x and max x, half a step each; the exponents to base 2, half a step of the
+    # largest times ln 2, in the sum and its entropy
+    off = 2 * abs(size) * it * 2.0 ** -24 + abs(size) * it * 2.0 ** -24
+    assert np.all(np.abs(f64(o["lp"]) - lp) <= off + REL * (1 + np.abs(lp)))
 
 
 @pytest.mark.parametrize("zt", ["f32", "bf16"])
