@@ -332,7 +332,8 @@ __device__ __forceinline__ void policy_final(const PolicyArgs& a, const float* p
 }
 
 // ----------------------------------------------------------- small calls --
-// One CTA, four rows per thread; counts and starts in shared memory, the rows'
+// One CTA, four rows per thread (8 sequences of 150 rows: 4.0 us, a launch and two
+// trips to memory); counts and starts in shared memory, the rows'
 // inputs on their way meanwhile.  From logprobs: all of it; ROWS: weights and
 // advantages for the logits kernel.
 template <bool ROWS>
@@ -405,6 +406,9 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
 }
 
 // ----------------------------------------------------------- large calls --
+// Three launches, each a pass over 4 to 17 bytes a row.  524288 rows in 512
+// sequences take 15 us, of which their bytes are 0.8 us at HBM's rate: the launches
+// and the dependent loads of each (starts, counts, rows) take the time.
 __global__ void policy_zero_kernel(const __grid_constant__ PolicyArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -530,6 +534,15 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
 // buffer to the next group to be loaded.  Logits are read once, dz is written
 // once, and the next rows stream in while this one is reduced and written.  A
 // group's arithmetic and the merge order do not depend on the cluster size.
+//
+// Bound by HBM for long rows: 4096 x 151936 FP32 (every seventh row masked and not
+// read) take 736 us, 4.6 GB at 6.3 TB/s; 2037 x 131072 bf16 181 us, 5.9 TB/s, of
+// which every logit's two exponentials and eight FP32 operations come near the
+// issue rate.  Short and unaligned rows by the cluster barrier and the merge of
+// each row and by moving logits to 16 bytes' alignment in shared memory: 1000 x
+// 32003 FP32 55 us (38 us of HBM time), 32004 48 us.  Few rows by latency: 64 x
+// 151936 FP32 20 us (8.7 us), 13 x 4096 11 us, of which the rows kernel before it
+// and the sums behind it are 3 us each.
 constexpr int kGroupBytes = 4096;
 constexpr int kMaxWarps = 16;
 constexpr int kMaxV = 262144;
@@ -537,6 +550,9 @@ constexpr int kMaxMerge = kMaxV * 4 / kGroupBytes / 32;   // groups per lane of 
 // Logits of kMasked or less are masked: what a mask of -inf or of the type's
 // lowest value leaves has p = 0.
 constexpr float kMasked = -1e30f;
+// After a wait that ran out (reported; results are wrong) the others wait no longer
+// than this: every row still goes through the cluster's barriers.
+constexpr uint64_t kLateNs = 10000000;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -550,7 +566,7 @@ struct LogitsArgs {
   int64_t ld;
   const int32_t* target;
   int V, G, gpc, slots;     // groups of a row, groups per CTA, buffers per warp
-  float it, c, eta;         // 1 / temperature; that times log2(e), c (1 + eta) before its rounding
+  float it, c, eta;         // 1 / temperature; that times log2(e); ln 2 times what c's rounding took, by c
   float* lp;
   float* ent;
   void* dz;
@@ -931,7 +947,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
   uint32_t slot1 = 0, phase1 = 0;  // of row q1's next group
   uint32_t dirty = 0;              // slots (mod 32) this warp has written to
   uint32_t flip = 0;
+  bool late = false;               // a wait has run out
   // of row q0, where there is one
+  constexpr float kLn2 = 0.6931471805599453f;
   float M = 0.f, a0 = 0.f, a1 = 0.f, at_target = 0.f, zt = 0.f;
   int tg0 = -1;
   // The thread that writes a row's lp and entropy (of the warp with the fewest
@@ -1062,7 +1080,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       const int g = g0 + warp + i * nw;
       const int left = min(kGroup, a.V - g * kGroup);
       uint8_t* buf = bufs + slot1 * BUF;
-      mbar_wait(smem_u32(bars + slot1), phase1, a.p.err);
+      if (!mbar_wait(smem_u32(bars + slot1), phase1, a.p.err, late ? kLateNs : kWaitLimitNs)) late = true;
       float m;
       if ((SHIFT && off) || left < kGroup) {
         // elements of the row's first and last 16-byte unit, where it holds
@@ -1087,7 +1105,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       } else {
         m = group_max<ZB>(buf, lane);
       }
-      float mc = 0.f, s = 0.f, t = 0.f;
+      float mc = -INFINITY, s = 0.f, t = 0.f;
       if (!(m <= kMasked)) {         // (a NaN comes through)
         mc = __fmul_rn(m, a.c);
         group_sums<ZB>(buf, lane, a.c, mc, s, t);
@@ -1102,7 +1120,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
         if (t != t) group_sums<ZB>(buf, lane, a.c, mc, s, t);
         if (m <= kMasked) m = -INFINITY;
       }
-      if (lane < ncta) st_cluster_v4(smem_u32(st + g), lane, m, s, t, 0.f);
+      if (lane < ncta) st_cluster_v4(smem_u32(st + g), lane, m, s, t, mc);
       if (++slot1 == slots) {
         slot1 = 0;
         phase1 ^= 1;
@@ -1116,40 +1134,40 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
 #pragma unroll
     for (int k = 0; k < kMaxMerge; ++k) {
       const int g = k * 32 + lane;
-      q[k] = g < a.G ? st[g] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      q[k] = g < a.G ? st[g] : make_float4(-INFINITY, 0.f, 0.f, -INFINITY);
       top = fmax_nan(top, q[k].x);
     }
     top = warp_max_keep_nan(top);
     M = __fmul_rn(top, a.c);
+    const float xm = __fmul_rn(top, a.it);
+    const float ln_ratio = fmaf(-kLn2, fmaf(top, a.c, -M), fmaf(top, a.it, -xm));
+    const bool near = fabsf(ln_ratio) < 0x1p-12f;     // (not so for logits of some thousands)
     float S = 0.f, U = 0.f;
 #pragma unroll
     for (int k = 0; k < kMaxMerge; ++k) {
       // a group of masked logits alone (M may be -inf too) adds nothing
       const bool has = q[k].x != -INFINITY;
-      const float d = __fsub_rn(__fmul_rn(q[k].x, a.c), M), f = ex2f(d);
+      const float d = q[k].w - M, f = ex2f(d);
       S = has ? fmaf(q[k].y, f, S) : S;
       U = has ? fmaf(f, fmaf(q[k].y, d, q[k].z), U) : U;
     }
     S = warp_sum_x(S);
     U = warp_sum_x(U);
     if (top == -INFINITY) S = NAN;   // nothing but masked logits
-    constexpr float kLn2 = 0.6931471805599453f;
-    const float lnS = logf(S);
     const float rS = __frcp_rn(S);
+    // lp = (x_t - max x) - log of the sum of exp(x - max x), x = z / temperature, as
+    // these FP32 operations.  That sum is S but for three roundings, which log S has
+    // to first order: of max x and M (ln_ratio), and of c (eta U / S).  (From the
+    // base-2 exponent, fma(z_t, c, -M) ln 2 - lnS, lp was off by twice as much.)
+    const float l0 = logf(S + fmaf(near ? ln_ratio : 0.f, S, a.eta * U));
+    const float ratio = near ? -fmaf(a.eta, U * rS, ln_ratio) : ln_ratio;
+    const float ls = near ? l0 : l0 + ratio;
+    const float lnS = near ? l0 + ratio : l0;
     const float H = lnS - kLn2 * (U * rS);
     const int from = q1 & 31;
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
     zt = __shfl_sync(0xffffffffu, m_zt, from);
     const bool tg_ok = tg0 >= 0 && tg0 < a.V;
-    // lp = (x_t - max x) - log of the sum of exp(x - max x), x = z / temperature, as
-    // these FP32 operations.  That sum is S but for three roundings, which log S has
-    // to first order: of max x, of M, and of c (as ln 2 eta U / S).  (From the base-2
-    // exponent, fma(z_t, c, -M) ln 2 - lnS, lp was off by twice as much.)
-    const float xm = __fmul_rn(top, a.it);
-    const float ln_ratio = fmaf(-kLn2, fmaf(top, a.c, -M), fmaf(top, a.it, -xm));
-    const bool near = fabsf(ln_ratio) < 0x1p-12f;     // (not so for logits of some thousands)
-    const float Sm = S + fmaf(near ? ln_ratio : 0.f, S, kLn2 * a.eta * U);
-    const float ls = logf(Sm) + (near ? 0.f : ln_ratio);
     const float lp = tg_ok ? __fsub_rn(__fsub_rn(__fmul_rn(zt, a.it), xm), ls) : NAN;
     if (teller) {
       a.lp[row_of(q1)] = lp;
@@ -1322,16 +1340,16 @@ biv_status max_clusters(K kern, unsigned cluster, unsigned threads, size_t smem,
   return BIV_OK;
 }
 
-
-// Shape of the logits kernel (GB300, GPU time of the whole call).  A row is
-// spread over as few CTAs as hold it in 160 KB each, one CTA per SM: 4096 rows
-// x 151936 FP32 take 726 us on clusters of 4, 1069 us on clusters of 8 with two
-// CTAs per SM; 2037 x 131072 bf16 188 us on clusters of 2, 201 us on 4.  Up to
-// 16 warps (128 registers each): 24 take 786 us on the first case, 189 us on the
-// second.  What is left of 216 KB prefetches the next row: without it the first
-// case takes 786 us.  Shorter rows run two CTAs per SM, so that one's barrier and
-// merge overlap the other's traffic: 1000 x 16384 FP32 28.1 us against 31.6 us;
-// 2000 x 50257 bf16 (100 KB), which would lose its prefetch, 122 us against 104.
+// Shape of the logits kernel (GB300, GPU time of the whole call, as measured when
+// each choice was made).  A row is spread over as few CTAs as hold it in 160 KB
+// each, one CTA per SM: 4096 rows x 151936 FP32 take 726 us on clusters of 4, 1069
+// us on clusters of 8 with two CTAs per SM; 2037 x 131072 bf16 188 us on clusters
+// of 2, 201 us on 4.  Up to 16 warps (128 registers each): 24 take 786 us on the
+// first case, 189 us on the second.  What is left of 216 KB prefetches the next
+// row: without it the first case takes 786 us.  Shorter rows run two CTAs per SM,
+// so that one's barrier and merge overlap the other's traffic: 1000 x 16384 FP32
+// 28.8 us against 31.6 us; 2000 x 50257 bf16 (100 KB), which would lose its
+// prefetch, 122 us against 104.
 constexpr size_t kRowBytesPerCta = 160 << 10, kPairBytes = 80 << 10, kRingBytes = 216 << 10;
 
 template <bool ZB, bool DB, bool SHIFT>
@@ -1348,8 +1366,9 @@ biv_status launch_logits(LogitsArgs& a, cudaStream_t s) {
   const int most = pair ? kMaxWarps / 2 : kMaxWarps, per = (a.gpc + most - 1) / most;
   const size_t ring = pair ? kRingBytes / 2 - 1024 : kRingBytes;
   const unsigned warps = unsigned((a.gpc + per - 1) / per), threads = warps * 32;
-  // The loss by the last CTA: where its warps take at most twice 128 rows each (one
-  // warp with eight turns takes 4 us more, a launch saved is 3 us of the host's time)
+  // The loss by the last CTA, where its warps take at most twice 128 rows each: 13 x
+  // 4096 FP32 14.5 us a call, bound by the host's launches, against 20.7 us with a
+  // kernel for it (10.8 us of GPU time against 9.9; with eight turns of one warp 13.9)
   a.tail = a.p.T <= kSmallRows && a.p.T <= int(warps) * 256;
   // a warp's ring: its groups of a row, and of the next one what the room allows
   a.slots = per;
@@ -1423,7 +1442,7 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
   a.it = inv_temp;
   const double c = double(inv_temp) * 1.4426950408889634;
   a.c = float(c);
-  a.eta = float(c / a.c - 1.0);
+  a.eta = float((c / a.c - 1.0) * 0.6931471805599453);
   a.lp = lp; a.ent = entropy; a.dz = dz; a.ldz = ldz;
   // rows of logits and gradient that all keep 16 bytes' alignment
   const bool shift = zb % 16 != 0 || (size_t(ld) * es) % 16 != 0 ||

@@ -6,9 +6,17 @@
 //
 // Work is cut into chunks of 2048 elements of one tensor; a CTA takes a run of
 // consecutive chunks, finds its first tensor by bisection on first_chunk and
-// walks on from there, so hundreds of small tensors cost no launch each.  An
-// element's update depends on that element alone (8-bit states: on its block
-// of 128), whatever the grid.
+// walks on from there, so hundreds of small tensors cost no launch each (a launch
+// per combination of types, mostly one).  An element's update depends on that
+// element alone (8-bit states: on its block of 128), whatever the grid.
+//
+// FP32 states (22 to 30 bytes a weight) are bound by HBM: 714 M weights, bf16 with
+// an FP32 master, 3.56 ms with the norm, 6.8 TB/s of the bytes that it asks for.
+// 8-bit states (8 to 16 bytes) by instructions: 714 M bf16 weights 1.51 ms with
+// stochastic rounding, 4.8 TB/s; about 71 instructions a weight issue at 82% of the
+// rate, of which the two hashes are 14 and the roundings 10.  3.5 M weights 20 us
+// (16 us of HBM time), 300 ragged tensors 24 us: the latency of the norm's partials,
+// their total, and a search and a first load per CTA.
 #include <algorithm>
 #include <vector>
 
@@ -24,6 +32,7 @@ constexpr int kBlk = 128;           // elements per scale of an 8-bit state
 constexpr int kNormChunks = 4;      // chunks per partial sum of the norm
 constexpr int kNT = 1024;           // threads that add the norm's partials up
 constexpr int64_t kUnitsHere = 8192;  // partials that the norm's last CTA adds up itself
+constexpr uint64_t kDrainNs = 100000000;   // what a wait for copies behind a failed one takes at most
 constexpr float kMinAmax = 7.888609052210118e-31f;  // 2^-100
 
 enum VecBits { kVec16 = 1, kVec32 = 2, kVecBulk = 4 };   // biv_opt_tensor.vec
@@ -452,6 +461,7 @@ struct Ring {          // where the next chunk of a CTA is staged, over its tens
   int stage;
   uint32_t phase;
   int* err;
+  bool dead;           // a wait ran out: this warp does no more
 };
 
 // `count` consecutive chunks of one tensor, the first one number `chunk` of it.
@@ -494,6 +504,7 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
       bulk_load(st + L::VS, t.v_scale + c * kScales, kScales * 4, bar);
     };
     if (staged) __syncthreads();           // the tensor before: its last stages are read
+    if (ring.dead) return;
     if (staged && threadIdx.x == 0) {
       for (int k = 0; k < L::STAGES && k < full; ++k) {
         const int st = ring.stage + k;
@@ -503,7 +514,14 @@ __device__ __forceinline__ void adam_run(const biv_opt_tensor& t, int64_t chunk,
     for (int64_t k = 0; k < full; ++k) {
       K d;
       if (staged) {
-        mbar_wait(smem_u32(ring.bars + ring.stage), ring.phase, ring.err);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(ring.bars + ring.stage), ring.phase, ring.err))) {
+          // given up: nothing is written from here on, and copies in flight get some
+          // time to land
+          ring.dead = true;
+          for (int i = 0; i < L::STAGES; ++i)
+            mbar_wait(smem_u32(ring.bars + i), i < ring.stage ? ring.phase ^ 1u : ring.phase, ring.err, kDrainNs);
+          return;
+        }
         const uint8_t* st = ring.bufs + ring.stage * L::BYTES;
         from_stage(st, d.g);
         from_stage(st + L::W, d.w);
@@ -579,7 +597,10 @@ __host__ __device__ inline int kind_of(const biv_opt_tensor& t) {
 }
 
 // The tensors of one kind (others are passed over); `last`: the call's last
-// launch, which counts the step.
+// launch, which counts the step.  8-bit states want many warps: four CTAs per SM
+// (64 registers) 1594 us where three take 1684 and five, which spill, 1866 (714 M
+// weights, before the ring's last change); FP32 states are the same to 1% with two
+// to four.
 template <int PK, bool GB, bool E8, bool SR>
 __global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamArgs a, int last) {
   constexpr int kKind = PK * 4 + (GB ? 2 : 0) + (E8 ? 1 : 0);
@@ -595,7 +616,7 @@ __global__ void __launch_bounds__(kOT, E8 ? 4 : 3) adamw_kernel(const __grid_con
     }
     fence_barrier_init();
   }
-  Ring ring = {stages, s_bars, s_read, 0, 0u, a.err};
+  Ring ring = {stages, s_bars, s_read, 0, 0u, a.err, false};
   const int64_t c0 = a.chunks * blockIdx.x / gridDim.x;
   const int64_t c1 = a.chunks * (int64_t(blockIdx.x) + 1) / gridDim.x;
   int ti = find_tensor(a.t, a.n, c0);   // (the table is the host's: no kernel writes it)
@@ -813,8 +834,8 @@ biv_status launch_adamw(const AdamArgs& a, bool last, cudaStream_t s) {
   const int sms = sm_count() > 0 ? sm_count() : 148;
   // six chunks a CTA at least, where there are enough for two CTAs per SM (3.5 M
   // weights: 25 us against 33 us for one or two chunks), and 16 CTAs per SM at
-  // most, so that the faster SMs take more (714 M weights with 8-bit states: 1510
-  // us against 1807 us for two long CTAs per SM)
+  // most, so that the faster SMs take more (714 M weights with 8-bit states: 1.5 ms
+  // against 1.8 ms for two long CTAs per SM)
   const int64_t most = std::max<int64_t>(2 * sms, a.chunks / 6);
   const unsigned grid = unsigned(std::min(a.chunks, std::min<int64_t>(most, int64_t(sms) * 16)));
   launch_pdl(kern, grid, kOT, kSmem, s, a, int(last));
