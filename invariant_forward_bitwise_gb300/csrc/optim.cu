@@ -88,6 +88,12 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// min that gives NaN where one of them is
+__device__ __forceinline__ float fmin3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 // 8 consecutive elements of an array, as its bytes: raw words of F32 (8), BF16
 // (4) or e4m3 (2)
@@ -227,30 +233,40 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 // Eight square roots, rounded to nearest: from an approximate reciprocal root y
 // one Newton step on x^2 = v, r = v y + (v - (v y)^2) y / 2, its residual exact by
 // FMA (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990).  Zeros and the smallest values take sqrtf.
-__device__ __forceinline__ void sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
-  float f[8];
+// processor", 1990).  Zeros, the smallest values and infinities take sqrtf.
+// Returns whether none is infinite.
+__device__ __forceinline__ bool sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
+  float f[8], x[8];
+  uint64_t y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
-  float lo = fmin3(f[0], f[1], f[2]);
-  lo = fmin3(lo, f[3], f[4]);
-  lo = fminf(fmin3(lo, f[5], f[6]), f[7]);
-  if (lo >= 1e-30f) {
+  for (int i = 0; i < 4; ++i) {
+    float y0, y1;
+    unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(f[2 * i]));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(f[2 * i + 1]));
+    y[i] = pack2(y0, y1);
+    unpack2(mul2(v[i], y[i]), x[2 * i], x[2 * i + 1]);
+  }
+  // (v y is NaN for 0 and infinity)
+  float lo = fmin3_nan(x[0], x[1], x[2]);
+  lo = fmin3_nan(lo, x[3], x[4]);
+  lo = fmin3_nan(fmin3_nan(lo, x[5], x[6]), x[7], x[7]);
+  if (lo >= 1e-15f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float y0, y1;
-      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(f[2 * i]));
-      asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(f[2 * i + 1]));
-      const uint64_t y = pack2(y0, y1), x = mul2(v[i], y);
-      float x0, x1;
-      unpack2(x, x0, x1);
-      const uint64_t e = pack2(__fmaf_rn(-x0, x0, f[2 * i]), __fmaf_rn(-x1, x1, f[2 * i + 1]));
-      unpack2(fma2(e, mul2(y, pack2(0.5f, 0.5f)), x), r[2 * i], r[2 * i + 1]);
+      const uint64_t e = pack2(__fmaf_rn(-x[2 * i], x[2 * i], f[2 * i]),
+                               __fmaf_rn(-x[2 * i + 1], x[2 * i + 1], f[2 * i + 1]));
+      unpack2(fma2(e, mul2(y[i], pack2(0.5f, 0.5f)), pack2(x[2 * i], x[2 * i + 1])), r[2 * i], r[2 * i + 1]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = sqrtf(f[i]);
+    return true;
   }
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[i] = sqrtf(f[i]);
+    finite = finite && f[i] != INFINITY;
+  }
+  return finite;
 }
 // reciprocal to about 1 ulp
 __device__ __forceinline__ float recip_near(float x) {
@@ -368,7 +384,7 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
     v[i] = add2(mul2(pack2(a.b2, a.b2), v[i]), mul2(mul2(pack2(a.c2, a.c2), gi), gi));
     unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
   }
-  sqrt8(v, rf);
+  const bool finite = sqrt8(v, rf);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // (rate m) / (r rbc2 + eps), rounded to nearest by one correction of the
@@ -386,6 +402,16 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
     unpack2(mul2(w[i], pack2(ts.keep, ts.keep)), w0, w1);
     wf[2 * i] = __fsub_rn(w0, q[0]);
     wf[2 * i + 1] = __fsub_rn(w1, q[1]);
+  }
+  if (!finite) {           // an infinite second moment moves its weight no more
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float x[2], y[2];
+      unpack2(w[i >> 1], x[0], x[1]);
+      unpack2(m[i >> 1], y[0], y[1]);
+      const float d = __fadd_rn(__fmul_rn(rf[i], s.rbc2), a.eps);
+      wf[i] = __fsub_rn(__fmul_rn(x[i & 1], ts.keep), __fdiv_rn(__fmul_rn(ts.rate, y[i & 1]), d));
+    }
   }
   uint32_t h[8];
   if constexpr (SR && (E8 || PK == kParamBf16)) hash8(id, s.key, h);
@@ -987,7 +1013,7 @@ biv_status biv_adamw(const biv_adamw_desc* d, biv_stream_t stream) {
   BIV_REQUIRE(d->n >= 0 && d->chunks >= 0 && (d->n > 0 || d->chunks == 0), "adamw: bad sizes");
   BIV_REQUIRE(d->beta1 >= 0.0 && d->beta1 < 1.0 && d->beta2 >= 0.0 && d->beta2 < 1.0,
               "adamw: betas must lie in [0, 1)");
-  BIV_REQUIRE(d->eps > 0.f, "adamw: eps must be positive");
+  BIV_REQUIRE(d->eps >= 1e-30f, "adamw: eps must be at least 1e-30");
   BIV_REQUIRE(d->rounding == BIV_ROUND_NEAREST || d->rounding == BIV_ROUND_STOCHASTIC,
               "adamw: unknown rounding");
   if (d->chunks == 0) return BIV_OK;

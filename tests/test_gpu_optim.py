@@ -487,6 +487,29 @@ def test_extreme_gradients(O):
     assert np.all(np.abs(f64(p) - 1) <= 3 * 4.2e-3)
 
 
+@pytest.mark.parametrize("param", ["f32", "master", "bf16"])
+def test_infinite_second_moments(O, param):
+    """A gradient whose square is beyond FP32 makes v infinite and leaves its weight
+    where it is, by the stated operations; its neighbours step as ever."""
+    n = 4100
+    ts = tensors(synth.rng(5), [n], param, "f32", "f32")
+    ts["exp_avg"][0].zero_()
+    ts["exp_avg_sq"][0].zero_()
+    g = ts["grads"][0]
+    g.fill_(0.01)
+    for i, x in ((3, 1e21), (2047, -1e25), (2048, 1e22), (4099, -1e23)):
+        g[i] = x
+    was = ts["params"][0].clone()
+    opt = O.AdamW(lr=1e-2, **ts)
+    for _ in range(2):
+        opt.step()
+    torch.cuda.synchronize()
+    big = g.abs() > 1.0
+    v, w = opt.exp_avg_sq[0], ts["params"][0]
+    assert torch.all(torch.isinf(v[big])) and torch.all(torch.isfinite(v[~big]))
+    assert same(w[big], was[big]) and torch.all(w[~big] != was[~big]) and torch.all(torch.isfinite(w))
+
+
 def test_optimizer_refuses(O, B):
     p, g = torch.zeros(8, device="cuda"), torch.zeros(8, device="cuda")
     O.AdamW([p], [g])

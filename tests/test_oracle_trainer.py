@@ -151,7 +151,7 @@ def test_policy_loss_refuses_small_workspace_and_entropy(B):
     assert lib.biv_policy_loss(C.byref(_policy(B, ent_coef=0.1)), lp, None, None) == B.BIV_ERR_INVALID
     assert lib.biv_policy_loss(C.byref(_policy(B)), None, None, None) == B.BIV_ERR_INVALID
     assert lib.biv_policy_loss(None, None, None, None) == B.BIV_ERR_INVALID
-    assert lib.biv_policy_loss(C.byref(_policy(B, T=0)), None, None, None) == B.BIV_OK   # no rows: nothing to do
+    assert lib.biv_policy_loss(C.byref(_policy(B, T=0, stats=None)), None, None, None) == B.BIV_ERR_INVALID
 
 
 @pytest.mark.parametrize("kw", [
@@ -222,7 +222,7 @@ def test_opt_plan_refuses_shared_memory(B):
     assert _plan(B, arr)[0] == B.BIV_OK
 
 
-@pytest.mark.parametrize("kw", [dict(beta1=1.0), dict(beta2=-0.1), dict(beta1=float("nan")), dict(eps=0.0),
+@pytest.mark.parametrize("kw", [dict(beta1=1.0), dict(beta2=-0.1), dict(beta1=float("nan")), dict(eps=0.0), dict(eps=1e-40),
                                 dict(rounding=2), dict(lr=None), dict(step=None), dict(tensors=None),
                                 dict(n=-1), dict(chunks=-1), dict(n=0), dict(kinds=0), dict(kinds=1 << 12)])
 def test_adamw_refuses(B, kw):
