@@ -595,7 +595,7 @@ biv_status biv_attention_backward(const biv_attn_bwd_desc* desc, biv_stream_t st
  * sequences that have counted rows, n_s their number; SUM 1/norm.
  * A row that does not count has weight 0: what its lp, logits and target hold
  * does not matter, and its dlp, lp, entropy and dz are written as zeros; with no counted
- * row at all loss, statistics and gradients are zeros.
+ * row at all (T = 0 too) loss, statistics and gradients are zeros.
  *
  * stats float32 [8]: loss, sum w pg, sum w kl, sum w H, then over counted rows
  * the share where u is not taken by clipping, mean of exp(d) - 1 - d (d =
@@ -732,7 +732,7 @@ typedef struct {
   const float* clip;
   int32_t* step;
   double beta1, beta2;             /* 0 <= beta < 1 */
-  float eps;                       /* > 0 */
+  float eps;                       /* >= 1e-30 */
   int rounding;                    /* biv_rounding */
   uint64_t seed;
 } biv_adamw_desc;

@@ -594,7 +594,7 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
     sequence) or [T]; mask uint8 or bool [T]; old_lp, ref_lp float32 [T];
     stats float32 [8]; workspace uint8 of biv_policy_loss_workspace bytes.
     With nseq == T an advantage vector counts as one per sequence."""
-    dev, f32 = _device(), torch.float32
+    dev, f32, keep = _device(), torch.float32, (seq_start, adv, stats, workspace, mask, old_lp, ref_lp)
     nseq, nadv = seq_start.numel() - 1, adv.numel()
     if nseq < 0:
         raise ValueError("seq_start needs at least one entry")
@@ -613,9 +613,11 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
     if ref_lp is not None:
         _rows_ok("ref_lp", ref_lp, f32, T, dev)
         ref_lp = ref_lp.data_ptr()
-    return PolicyDesc(T, nseq, seq_start.data_ptr(), mask, old_lp, ref_lp, adv.data_ptr(), int(nadv != nseq),
-                      clip_lo, clip_hi, dual_clip, kl_coef, ent_coef, reduce, norm, stats.data_ptr(),
-                      workspace.data_ptr(), workspace.numel())
+    d = PolicyDesc(T, nseq, seq_start.data_ptr(), mask, old_lp, ref_lp, adv.data_ptr(), int(nadv != nseq),
+                   clip_lo, clip_hi, dual_clip, kl_coef, ent_coef, reduce, norm, stats.data_ptr(),
+                   workspace.data_ptr(), workspace.numel())
+    d.tensors = keep     # they live as long as the descriptor
+    return d
 
 
 def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):

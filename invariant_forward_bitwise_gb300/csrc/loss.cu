@@ -1208,8 +1208,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
 biv_status check_policy(const biv_policy_desc* d, const char* who) {
   BIV_REQUIRE(d, "%s: null descriptor", who);
   BIV_REQUIRE(d->T >= 0 && d->nseq >= 0 && d->T <= (1 << 30), "%s: bad sizes", who);
+  BIV_REQUIRE(d->stats, "%s: null pointer", who);
   if (d->T == 0) return BIV_OK;
-  BIV_REQUIRE(d->seq_start && (d->adv || (d->nseq == 0 && !d->adv_per_row)) && d->stats, "%s: null pointer", who);
+  BIV_REQUIRE(d->seq_start && (d->adv || (d->nseq == 0 && !d->adv_per_row)), "%s: null pointer", who);
   BIV_REQUIRE(d->clip_lo >= 0.f && d->clip_lo <= 1.f && d->clip_hi >= 0.f,
               "%s: clip_lo must lie in [0, 1] and clip_hi must not be negative", who);
   BIV_REQUIRE(d->dual_clip == 0.f || d->dual_clip > 1.f, "%s: dual_clip must be 0 or above 1", who);
@@ -1223,6 +1224,13 @@ biv_status check_policy(const biv_policy_desc* d, const char* who) {
   if (!d->workspace || d->workspace_bytes < need)
     return set_error(BIV_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", who, need);
   BIV_REQUIRE(aligned16(d->workspace), "%s: workspace must be 16-byte aligned", who);
+  return BIV_OK;
+}
+
+// no row at all: statistics are zeros
+biv_status no_rows(const biv_policy_desc& d, biv_stream_t stream) {
+  if (cudaMemsetAsync(d.stats, 0, kStat * sizeof(float), as_cuda(stream)) != cudaSuccess)
+    return set_error(BIV_ERR_CUDA, "policy_loss: %s", cudaGetErrorString(cudaGetLastError()));
   return BIV_OK;
 }
 
@@ -1398,7 +1406,8 @@ biv_status biv_policy_loss_workspace(int T, int nseq, size_t* bytes) {
 biv_status biv_policy_loss(const biv_policy_desc* d, const float* lp, float* dlp,
                            biv_stream_t stream) {
   biv_status st = check_policy(d, "policy_loss");
-  if (st != BIV_OK || d->T == 0) return st;
+  if (st != BIV_OK) return st;
+  if (d->T == 0) return no_rows(*d, stream);
   BIV_REQUIRE(lp, "policy_loss: null pointer");
   BIV_REQUIRE(d->ent_coef == 0.f, "policy_loss: an entropy term needs the logits");
   const PolicyArgs a = policy_args(*d);
@@ -1417,7 +1426,8 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* d, const void* z, int64
                                   float* entropy, void* dz, int64_t ldz, int dz_dtype,
                                   biv_stream_t stream) {
   biv_status st = check_policy(d, "policy_loss_logits");
-  if (st != BIV_OK || d->T == 0) return st;
+  if (st != BIV_OK) return st;
+  if (d->T == 0) return no_rows(*d, stream);
   BIV_REQUIRE(z && target && lp && entropy, "policy_loss_logits: null pointer");
   BIV_REQUIRE(V >= 1 && V <= kMaxV, "policy_loss_logits: V must lie in [1, %d]", kMaxV);
   BIV_REQUIRE((z_dtype == BIV_F32 || z_dtype == BIV_BF16) &&

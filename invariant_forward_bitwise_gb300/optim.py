@@ -131,6 +131,9 @@ class AdamW:
         d.rounding = biv.ROUND_STOCHASTIC if rounding == "stochastic" else biv.ROUND_NEAREST
         d.seed = int(seed) & 0xFFFFFFFFFFFFFFFF
         self.desc = d
+        # what was made here is ready for a step on any stream
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
 
     def set_lr(self, lr: float):
         """A new learning rate for the steps (and graph replays) issued after this."""

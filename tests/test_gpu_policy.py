@@ -360,6 +360,30 @@ def test_sums_are_those_of_the_logprobs(B, T, V, starts):
     check_stats(f64(o["stats"]), oracle_loss(c, c["H"])[0], sizes(c, c["H"])[0])
 
 
+def test_no_rows_and_temporaries(B):
+    """No row at all: statistics of zeros; a descriptor keeps the tensors that only
+    it was given."""
+    z = lambda *n: torch.zeros(*n, device="cuda")  # noqa: E731
+    ws = workspace(B, 0, 2)
+    for call in ("lp", "logits"):
+        stats = torch.full((8,), float("nan"), device="cuda")
+        d = B.policy_desc(torch.zeros(3, dtype=torch.int32, device="cuda"), z(2), stats, ws, T=0)
+        if call == "lp":
+            B.biv_policy_loss(d, z(0), z(0))
+        else:
+            B.biv_policy_loss_logits(d, z(0, 5), torch.zeros(0, dtype=torch.int32, device="cuda"), z(0), z(0), z(0, 5))
+        torch.cuda.synchronize()
+        assert torch.all(stats == 0)
+    T, stats = 600, torch.empty(8, device="cuda")
+    d = B.policy_desc(torch.tensor([0, T], dtype=torch.int32, device="cuda"), z(1) + 2.0, stats, workspace(B, T, 1),
+                      T=T, mask=(torch.arange(T, device="cuda") % 2 == 0), old_lp=z(T) - 1.0)
+    junk = [torch.full((n,), 7.0, device="cuda") for n in (1, 1, 2, T, T, 4 * T) for _ in range(4)]
+    dlp = torch.empty(T, device="cuda")
+    B.biv_policy_loss(d, z(T) - 1.0, dlp)
+    torch.cuda.synchronize()
+    assert stats[7] == T // 2 and torch.all(dlp[::2] == -2.0 / (T // 2)) and torch.all(dlp[1::2] == 0) and junk
+
+
 def test_captured_policy_loss(B):
     """A replay reads new inputs and gives the bits of an eager call."""
     c = logits_case(37, 5000, 0, 0, "f32", "bf16", "many", dict(gamma=0.01, beta=0.02))
