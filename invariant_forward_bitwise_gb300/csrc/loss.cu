@@ -1140,8 +1140,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     top = warp_max_keep_nan(top);
     M = __fmul_rn(top, a.c);
     const float xm = __fmul_rn(top, a.it);
-    const float ln_ratio = fmaf(-kLn2, fmaf(top, a.c, -M), fmaf(top, a.it, -xm));
-    const bool near = fabsf(ln_ratio) < 0x1p-12f;     // (not so for logits of some thousands)
+    const float r_M = -kLn2 * fmaf(top, a.c, -M), r_x = fmaf(top, a.it, -xm);   // what these roundings took
     float S = 0.f, U = 0.f;
 #pragma unroll
     for (int k = 0; k < kMaxMerge; ++k) {
@@ -1156,13 +1155,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     if (top == -INFINITY) S = NAN;   // nothing but masked logits
     const float rS = __frcp_rn(S);
     // lp = (x_t - max x) - log of the sum of exp(x - max x), x = z / temperature, as
-    // these FP32 operations.  That sum is S but for three roundings, which log S has
-    // to first order: of max x and M (ln_ratio), and of c (eta U / S).  (From the
-    // base-2 exponent, fma(z_t, c, -M) ln 2 - lnS, lp was off by twice as much.)
-    const float l0 = logf(S + fmaf(near ? ln_ratio : 0.f, S, a.eta * U));
-    const float ratio = near ? -fmaf(a.eta, U * rS, ln_ratio) : ln_ratio;
+    // these FP32 operations.  That sum is S + t to first order: M's rounding is in all
+    // of S, that of max x in all but the largest term, c's in U.  (From the base-2
+    // exponent, fma(z_t, c, -M) ln 2 - lnS, lp was off by twice as much.)
+    const float t = fmaf(r_x, S - 1.0f, fmaf(r_M, S, a.eta * U)), ratio = t * rS;
+    const bool near = fabsf(t) < 0x1p-12f * S;        // (not so for logits of some thousands)
+    const float l0 = logf(near ? S + t : S);
     const float ls = near ? l0 : l0 + ratio;
-    const float lnS = near ? l0 + ratio : l0;
+    const float lnS = near ? l0 - ratio : l0;
     const float H = lnS - kLn2 * (U * rS);
     const int from = q1 & 31;
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
