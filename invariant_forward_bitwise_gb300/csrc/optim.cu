@@ -859,10 +859,12 @@ biv_status launch_adamw(const AdamArgs& a, bool last, cudaStream_t s) {
                      cudaGetErrorString(cudaGetLastError()));
   const int sms = sm_count() > 0 ? sm_count() : 148;
   // six chunks a CTA at least, where there are enough for two CTAs per SM (3.5 M
-  // weights: 25 us against 33 us for one or two chunks), and 16 CTAs per SM at
-  // most, so that the faster SMs take more (714 M weights with 8-bit states: 1.5 ms
-  // against 1.8 ms for two long CTAs per SM)
-  const int64_t most = std::max<int64_t>(2 * sms, a.chunks / 6);
+  // weights, FP32 states: 20 us; with one or two chunks a CTA, on up to six per SM,
+  // 25 us) or, with 8-bit states, for the four that run at once (300 ragged tensors:
+  // 21 us against 24.5 us for two and 24 us for six); and 16 CTAs per SM at most, so
+  // that the faster SMs take more (714 M weights with 8-bit states: 1.5 ms against
+  // 1.8 ms for two long CTAs per SM)
+  const int64_t most = std::max<int64_t>((E8 ? 4 : 2) * sms, a.chunks / 6);
   const unsigned grid = unsigned(std::min(a.chunks, std::min<int64_t>(most, int64_t(sms) * 16)));
   launch_pdl(kern, grid, kOT, kSmem, s, a, int(last));
   return check_launch("adamw");
