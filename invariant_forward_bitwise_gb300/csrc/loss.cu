@@ -10,9 +10,8 @@
 // Launches.  Weights need the counted rows of each sequence first.  Up to 4096
 // rows, one CTA does all of it (policy_small_kernel: from logprobs one launch;
 // from logits one before the logits kernel, which writes lp, H and dz row by row
-// and whose last CTA mostly sums the loss).  Above that a launch each zeroes the
-// counts, counts, and sums the loss (policy_token_kernel, whose last block adds
-// the blocks up).
+// and whose last CTA mostly sums the loss).  Above that the counts are launches
+// before, and policy_token_kernel sums the loss, its last block adding the blocks up.
 #include <algorithm>
 #include <mutex>
 
@@ -22,6 +21,7 @@ namespace biv {
 namespace {
 
 constexpr int kSmallRows = 4096, kSmallSeqs = 1024;   // what one CTA takes
+constexpr int kMidRows = 1 << 19, kMidSeqs = 4096;    // counts by a block per sequence
 constexpr int kTB = 256;           // threads per block of tokens
 constexpr int kTok = 1024;         // tokens per partial sum
 constexpr int kStat = 8;           // floats per partial sum
@@ -108,6 +108,7 @@ struct PolicyArgs {
   float lo, hi, dual, beta, gamma;   // lo = 1 - clip_lo, hi = 1 + clip_hi
   int reduce;
   float norm;
+  int mid;                           // a block per sequence counts; totals are not stored
   float* stats;
   PolicyWs ws;
   int* err;
@@ -406,9 +407,12 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
 }
 
 // ----------------------------------------------------------- large calls --
-// Three launches, each a pass over 4 to 17 bytes a row.  524288 rows in 512
-// sequences take 15 us, of which their bytes are 0.8 us at HBM's rate: the launches
-// and the dependent loads of each (starts, counts, rows) take the time.
+// Up to 524288 rows in 4096 sequences two launches: counts by a block per
+// sequence, then the sums, each block adding the counts up for itself.  524288 rows
+// at most in 512 sequences take 10.6 us (15.1 with the general way's three launches
+// and atomics), of which their bytes are 0.8 us at HBM's rate: the launches and the
+// dependent loads of each (starts, counts, rows) take the time.  Beyond that a
+// launch zeroes the counts and rows add to them, however long a sequence is.
 __global__ void policy_zero_kernel(const __grid_constant__ PolicyArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -464,10 +468,78 @@ __global__ void __launch_bounds__(kTB) policy_count_kernel(const __grid_constant
   }
 }
 
-__device__ __forceinline__ void four_rows(const PolicyArgs& a, int64_t t0, Four& f) {
+// The same by a block per sequence, which no other one adds to: no zeroing before,
+// no atomics.
+__global__ void __launch_bounds__(kTB) policy_seq_count_kernel(const __grid_constant__ PolicyArgs a) {
+  __shared__ int red[kTB / 32];
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x, tid = threadIdx.x;
+  if (s == 0 && tid == 0) *a.ws.totals = Totals{0, 0, 0u, 0};
+  if (s >= a.nseq) return;
+  const int b = min(max(a.seq_start[s], 0), a.T), e = min(max(a.seq_start[s + 1], b), a.T), len = e - b;
+  if (tid == 0) check_start(a, s);
+  int n = 0;
+  if (!a.mask) {
+    n = tid == 0 ? len : 0;
+  } else {
+    const uint8_t* p = a.mask + b;
+    const int head = min(len, int(-reinterpret_cast<uintptr_t>(p) & 15)), units = (len - head) >> 4;
+    const uint4* u = reinterpret_cast<const uint4*>(p + head);
+    auto nonzero = [](uint32_t x) {    // bytes of x that are not 0
+      return __popc((((x & 0x7F7F7F7Fu) + 0x7F7F7F7Fu) | x) & 0x80808080u);
+    };
+    if (tid < head) n += p[tid] != 0;
+    if (head + units * 16 + tid < len) n += tid < 16 && p[head + units * 16 + tid] != 0;
+#pragma unroll 4
+    for (int i = tid; i < units; i += kTB) {
+      const uint4 v = u[i];
+      n += nonzero(v.x) + nonzero(v.y) + nonzero(v.z) + nonzero(v.w);
+    }
+  }
+  __syncwarp();
+  n = __reduce_add_sync(0xffffffffu, n);
+  if ((tid & 31) == 0) red[tid >> 5] = n;
+  __syncthreads();
+  if (tid == 0) {
+    for (int i = 1; i < kTB / 32; ++i) n += red[i];
+    a.ws.counts[s] = n;
+  }
+}
+
+// counted rows, and sequences that have some: for whole blocks
+__device__ __forceinline__ void block_totals(const PolicyArgs& a, int& rows, int& seqs) {
+  if (!a.mid) {
+    rows = a.ws.totals->rows;
+    seqs = a.ws.totals->seqs;
+    return;
+  }
+  __shared__ int red[2][kTB / 32];
+  int n = 0, k = 0;
+#pragma unroll 4
+  for (int s = threadIdx.x; s < a.nseq; s += kTB) {
+    const int c = a.ws.counts[s];
+    n += c;
+    k += c > 0;
+  }
+  __syncwarp();
+  n = __reduce_add_sync(0xffffffffu, n);
+  k = __reduce_add_sync(0xffffffffu, k);
+  if ((threadIdx.x & 31) == 0) {
+    red[0][threadIdx.x >> 5] = n;
+    red[1][threadIdx.x >> 5] = k;
+  }
+  __syncthreads();
+  rows = seqs = 0;
+  for (int i = 0; i < kTB / 32; ++i) {
+    rows += red[0][i];
+    seqs += red[1][i];
+  }
+}
+
+__device__ __forceinline__ void four_rows(const PolicyArgs& a, int64_t t0, int rows, int seqs, Four& f) {
   int seq[4];
   four_seqs(a, a.seq_start, t0, seq);
-  const int rows = a.ws.totals->rows, seqs = a.ws.totals->seqs;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     f.w[i] = f.A[i] = 0.f;
@@ -493,7 +565,10 @@ __global__ void __launch_bounds__(kTB) policy_rows_kernel(const __grid_constant_
   pdl_trigger();
   const int64_t t0 = (int64_t(blockIdx.x) * kTB + threadIdx.x) * 4;
   Four f;
-  four_rows(a, t0, f);
+  int rows, seqs;
+  block_totals(a, rows, seqs);
+  if (a.mid && blockIdx.x == 0 && threadIdx.x == 0) a.ws.totals->rows = rows;
+  four_rows(a, t0, rows, seqs, f);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (t0 + i < a.T) a.ws.row[t0 + i] = make_float2(f.w[i], f.A[i]);
@@ -506,12 +581,15 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
   __shared__ bool s_last;
   pdl_wait();
   pdl_trigger();
+  int rows, seqs;
+  if (ent) rows = a.ws.totals->rows, seqs = 0;      // (after the logits kernel: weights are stored)
+  else block_totals(a, rows, seqs);
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
     const int64_t t0 = b * kTok + threadIdx.x * 4;
     Four f;
     load_inputs(a, lp, ent, t0, f);
-    if (ent) stored_rows(a, t0, f);       // (after the logits kernel)
-    else four_rows(a, t0, f);
+    if (ent) stored_rows(a, t0, f);
+    else four_rows(a, t0, rows, seqs, f);
     policy_block(a, f, dlp, t0, threadIdx.x, red, a.ws.part + b * kStat, [] { __syncthreads(); });
   }
   __threadfence();
@@ -520,7 +598,7 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
   __syncthreads();
   if (s_last && threadIdx.x < 32) {
     __threadfence();
-    policy_final<false>(a, a.ws.part, blocks, a.ws.totals->rows, threadIdx.x);
+    policy_final<false>(a, a.ws.part, blocks, rows, threadIdx.x);
   }
 }
 
@@ -1240,6 +1318,7 @@ PolicyArgs policy_args(const biv_policy_desc& d) {
   a.old_lp = d.old_lp; a.ref_lp = d.ref_lp; a.adv = d.adv; a.adv_per_row = d.adv_per_row;
   a.lo = 1.0f - d.clip_lo; a.hi = 1.0f + d.clip_hi; a.dual = d.dual_clip;
   a.beta = d.kl_coef; a.gamma = d.ent_coef; a.reduce = d.reduce; a.norm = d.norm;
+  a.mid = d.T <= kMidRows && d.nseq <= kMidSeqs;
   a.stats = d.stats;
   a.ws = policy_ws(d.workspace, d.T, d.nseq);
   a.err = device_error_word();
@@ -1270,6 +1349,10 @@ unsigned small_threads(const PolicyArgs& a) { return unsigned(token_blocks(a.T))
 
 // counts per sequence (large calls)
 biv_status launch_counts(const PolicyArgs& a, cudaStream_t s) {
+  if (a.mid) {
+    launch_pdl(policy_seq_count_kernel, unsigned(std::max(1, a.nseq)), kTB, 0, s, a);
+    return check_launch("policy_seq_count");
+  }
   launch_pdl(policy_zero_kernel, unsigned(std::max(1, (a.nseq + kTB - 1) / kTB)), kTB, 0, s, a);
   biv_status st = check_launch("policy_zero");
   if (st != BIV_OK) return st;

@@ -127,7 +127,8 @@ def desc(B, c, stats, ws):
     (31, "many", dict(reduce="sum", dual=3.0)), (1024, "inner", dict(beta=0.1, per_row=True)),
     (1025, "many", dict(reduce="seq", beta=0.1, dual=1.2)), (4099, "empty", dict(no_old=True)),
     (2000, "rows", dict(beta=0.02, reduce="seq")), (9000, "rows", dict(beta=0.02)), (70001, "many", dict(reduce="seq", per_row=True, beta=0.5)),
-    (7, "none", dict(per_row=True)), (7, "none", dict())])
+    (7, "none", dict(per_row=True)), (7, "none", dict()), (6000, "many", dict(mask=False, reduce="seq")),
+    (5003, "none", dict(per_row=True))])
 def test_policy_loss(B, T, starts, kw):
     g = synth.rng(T)
     lp = (-g.exponential(1.0, T)).astype(np.float32).astype(np.float64)
@@ -358,6 +359,26 @@ def test_sums_are_those_of_the_logprobs(B, T, V, starts):
     keep = [0, 1, 2, 4, 5, 6, 7]
     assert same(stats[keep], o["stats"][keep])
     check_stats(f64(o["stats"]), oracle_loss(c, c["H"])[0], sizes(c, c["H"])[0])
+
+
+def test_masks_of_any_alignment(B):
+    """Counts of sequences that start and end at any byte, masks of any byte values."""
+    g = synth.rng(77)
+    T = 5000
+    for off in range(0, 20, 3):
+        start = np.sort(np.concatenate([[0, T], g.integers(0, T + 1, 29), 100 + np.arange(20)])).astype(np.int32)
+        mask = (g.random(T) < 0.5) * g.integers(1, 256, T)
+        buf = torch.full((T + 40,), 255, dtype=torch.uint8, device="cuda")
+        buf[off:off + T] = dev(mask, np.uint8)
+        n = len(start) - 1
+        stats, dlp = torch.empty(8, device="cuda"), torch.empty(T, device="cuda")
+        d = B.policy_desc(dev(start, np.int32), torch.ones(n, device="cuda"), stats, workspace(B, T, n), T=T,
+                          mask=buf[off:off + T], reduce=1)
+        B.biv_policy_loss(d, torch.zeros(T, device="cuda"), dlp)
+        torch.cuda.synchronize()
+        w, _ = tr.row_weights(T, start, mask, "seq", 1.0)
+        assert stats[7] == np.count_nonzero(w)
+        assert np.all(np.abs(f64(dlp) + w) <= 3 * 2.0 ** -24 * w)
 
 
 def test_no_rows_and_temporaries(B):
