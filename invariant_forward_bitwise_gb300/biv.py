@@ -633,28 +633,31 @@ def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 
 
+def _matrix(what, t, T, V, dev):
+    """(row stride, type) of a float32 or bf16 matrix of at least T rows of V values."""
+    kind, steps = _FLOATS.get(t.dtype), t.stride()
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current CUDA device")
+    if kind is None or len(steps) != 2 or t.size(0) < T or t.size(1) != V or (V > 1 and steps[1] != 1):
+        raise ValueError(f"{what} must be a float32 or bf16 [T, V] tensor with rows of stride 1")
+    # (one row: its stride says nothing, and may be below V)
+    return (steps[0] if T > 1 else max(steps[0], V)), kind
+
+
 def biv_policy_loss_logits(desc: PolicyDesc, logits, target, lp, entropy, dz=None, inv_temp=1.0,
                            stream=None):
     """logits float32 or bf16 [T, V] (rows of stride 1) -> lp, entropy float32
     [T] and dz float32 or bf16 [T, V] (None: no gradient; may be logits)."""
     dev, T = _device(), desc.T
-    V = logits.shape[1] if logits.dim() == 2 else -1
-    for what, t in (("logits", logits), ("dz", dz)):
-        if t is None:
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"{what} must be on the current CUDA device")
-        if t.dim() != 2 or t.dtype not in _FLOATS or t.shape[0] < T or t.shape[1] != V or \
-                (V > 1 and t.stride(1) != 1):
-            raise ValueError(f"{what} must be a float32 or bf16 [T, V] tensor with rows of stride 1")
+    V = logits.size(1) if logits.dim() == 2 else -1
+    ld, zt = _matrix("logits", logits, T, V, dev)
+    pz, ldz, dt = None, 0, F32
+    if dz is not None:
+        ldz, dt = _matrix("dz", dz, T, V, dev)
+        pz = dz.data_ptr()
     _rows_ok("target", target, torch.int32, T, dev)
     _rows_ok("lp", lp, torch.float32, T, dev)
     _rows_ok("entropy", entropy, torch.float32, T, dev)
-    # one row: its stride says nothing, and may be below V
-    ld, zt = logits.stride(0), _FLOATS[logits.dtype]
-    pz, ldz, dt = (None, 0, F32) if dz is None else (dz.data_ptr(), dz.stride(0), _FLOATS[dz.dtype])
-    if T <= 1:
-        ld, ldz = max(ld, V), max(ldz, V)
     _check(load().biv_policy_loss_logits(
         C.byref(desc), logits.data_ptr(), ld, zt, target.data_ptr(), V, inv_temp, lp.data_ptr(),
         entropy.data_ptr(), pz, ldz, dt, _stream(stream)), "biv_policy_loss_logits")
