@@ -20,7 +20,9 @@ prefill_step (one 16384-row step of the 28-layer model: 16 sequences x 1024
 tokens, every row producing a logprob, as in the trainer recompute; one more
 step runs inside cudaProfilerStart/Stop) and hybrid_decode_step (one decode step of the
 Mamba-2 hybrid unit for 3 sequences, graph-timed, then eagerly inside
-cudaProfilerStart/Stop).
+cudaProfilerStart/Stop), policy_logits (the policy loss from 1216 x 151936 FP32,
+1216 x 131072 bf16 and 1000 x 32003 FP32 logits) and adamw_8bit (67 M bf16
+weights, 8-bit states, stochastic rounding).
 Each case times REPS calls with CUDA events after one warm-up call and
 prints the time and the rate against the case's algorithmic bytes or FLOPs;
 it is also the command that the ncu summaries in profiles/ capture.
@@ -403,6 +405,24 @@ elif case == "gemm_sweep":
                   f"  {2*M*N*K/(ms/1e3)/1e12:6.1f} TFLOP/s  {'partials' if need else 'in-CTA fold'}",
                   flush=True)
         del bs
+elif case == "policy_logits":
+    for T, V, dt in ((1216, 151936, torch.float32), (1216, 131072, torch.bfloat16), (1000, 32003, torch.float32)):
+        z = (torch.randn(T, V, device="cuda") * 2.5).to(dt)
+        dz, lp, ent = torch.empty_like(z), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+        target = torch.randint(0, V, (T,), dtype=torch.int32, device="cuda")
+        ws = torch.empty(biv.biv_policy_loss_workspace(T, 1), dtype=torch.uint8, device="cuda")
+        d = biv.policy_desc(torch.tensor([0, T], dtype=torch.int32, device="cuda"), torch.ones(1, device="cuda"),
+                            torch.empty(8, device="cuda"), ws, T=T)
+        ms = timeit(lambda: biv.biv_policy_loss_logits(d, z, target, lp, ent, dz))
+        print(f"policy_logits T={T} V={V} {dt}: {ms*1e3:.1f} us  {2*z.numel()*z.element_size()/(ms/1e3)/1e9:.0f} GB/s")
+        del z, dz
+elif case == "adamw_8bit":
+    from invariant_forward_bitwise_gb300 import optim
+    n = 1 << 26
+    w, grad = torch.randn(n, device="cuda").bfloat16(), torch.randn(n, device="cuda").bfloat16()
+    opt = optim.AdamW([w], [grad], bits=8, rounding="stochastic", lr=1e-6)
+    ms = timeit(opt.step)
+    print(f"adamw_8bit n={n}: {ms*1e3:.1f} us  {n*(10 + 16/128)/(ms/1e3)/1e9:.0f} GB/s")
 else:
     M, N, K = {"gemm_prefill": (8192, 2048, 6144), "gemm_qkv": (16384, 4096, 2048),
                "gemm_decode": (64, 2048, 6144), "lm_head": (4096, 151936, 2048)}[case]
