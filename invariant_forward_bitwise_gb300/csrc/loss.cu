@@ -21,7 +21,8 @@ namespace biv {
 namespace {
 
 constexpr int kSmallRows = 4096, kSmallSeqs = 1024;   // what one CTA takes
-constexpr int kMidRows = 1 << 19, kMidSeqs = 4096;    // counts by a block per sequence
+constexpr int kMidRows = 1 << 19, kMidSeqs = 1024;    // counts by a block per sequence
+constexpr int64_t kMidMean = 1 << 17;                 // ... of this length on average at most
 constexpr int kTB = 256;           // threads per block of tokens
 constexpr int kTok = 1024;         // tokens per partial sum
 constexpr int kStat = 8;           // floats per partial sum
@@ -407,12 +408,14 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
 }
 
 // ----------------------------------------------------------- large calls --
-// Up to 524288 rows in 4096 sequences two launches: counts by a block per
-// sequence, then the sums, each block adding the counts up for itself.  524288 rows
-// at most in 512 sequences take 10.6 us (15.1 with the general way's three launches
-// and atomics), of which their bytes are 0.8 us at HBM's rate: the launches and the
-// dependent loads of each (starts, counts, rows) take the time.  Beyond that a
-// launch zeroes the counts and rows add to them, however long a sequence is.
+// Up to 524288 rows in 1024 sequences two launches: counts by a block per
+// sequence, then the sums, each block adding the counts up for itself.  300 K rows
+// in 512 ragged sequences take 10.6 us against 15.1 by the general way (a launch
+// that zeroes the counts, rows that add to them, and the sums), 524288 rows in 64
+// even ones 11.7 against 16.2, 131072 in 16 7.8 against 9.4; in 4096 sequences 16.3
+// against 16.0, in one sequence 20 against 17, which the rule leaves to the general
+// way.  Their bytes are under 1.5 us at HBM's rate: the launches and the dependent
+// loads of each (starts, counts, rows) take the time.
 __global__ void policy_zero_kernel(const __grid_constant__ PolicyArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -1318,7 +1321,7 @@ PolicyArgs policy_args(const biv_policy_desc& d) {
   a.old_lp = d.old_lp; a.ref_lp = d.ref_lp; a.adv = d.adv; a.adv_per_row = d.adv_per_row;
   a.lo = 1.0f - d.clip_lo; a.hi = 1.0f + d.clip_hi; a.dual = d.dual_clip;
   a.beta = d.kl_coef; a.gamma = d.ent_coef; a.reduce = d.reduce; a.norm = d.norm;
-  a.mid = d.T <= kMidRows && d.nseq <= kMidSeqs;
+  a.mid = d.T <= kMidRows && d.nseq <= kMidSeqs && d.T <= kMidMean * d.nseq;
   a.stats = d.stats;
   a.ws = policy_ws(d.workspace, d.T, d.nseq);
   a.err = device_error_word();

@@ -128,7 +128,7 @@ def desc(B, c, stats, ws):
     (1025, "many", dict(reduce="seq", beta=0.1, dual=1.2)), (4099, "empty", dict(no_old=True)),
     (2000, "rows", dict(beta=0.02, reduce="seq")), (9000, "rows", dict(beta=0.02)), (70001, "many", dict(reduce="seq", per_row=True, beta=0.5)),
     (7, "none", dict(per_row=True)), (7, "none", dict()), (6000, "many", dict(mask=False, reduce="seq")),
-    (5003, "none", dict(per_row=True))])
+    (5003, "none", dict(per_row=True)), (140000, "one", dict(reduce="seq"))])
 def test_policy_loss(B, T, starts, kw):
     g = synth.rng(T)
     lp = (-g.exponential(1.0, T)).astype(np.float32).astype(np.float64)
