@@ -644,7 +644,7 @@ biv_status biv_policy_loss(const biv_policy_desc* desc, const float* lp, float* 
  * -1e30 or less (-inf, a type's lowest value) is masked: p = 0 and dz = 0; a
  * row of masked logits alone gives NaN, as a NaN or +inf among them does.  A counted
  * row whose target is outside [0, V) gives lp = NaN and the device error code
- * 2.  Each row's bits depend on V and the row only: 4 KB groups of logits
+ * 2; other rows' results and what lies around dz stay as they are.  Each row's bits depend on V and the row only: 4 KB groups of logits
  * are reduced to (max, sum, entropy sum) by one warp and merged in one order,
  * however the row is spread over CTAs.  1 <= V <= 262144, 0.01 <= inv_temp <=
  * 100.  Rows that keep 16

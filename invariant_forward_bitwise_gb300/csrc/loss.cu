@@ -1249,6 +1249,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
     zt = __shfl_sync(0xffffffffu, m_zt, from);
     const bool tg_ok = tg0 >= 0 && tg0 < a.V;
+    if (!tg_ok) tg0 = -1;              // the last group may reach past V: no element there is the target's
     const float lp = tg_ok ? __fsub_rn(__fsub_rn(__fmul_rn(zt, a.it), xm), ls) : NAN;
     if (teller) {
       a.lp[row_of(q1)] = lp;

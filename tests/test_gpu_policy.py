@@ -565,3 +565,35 @@ def test_a_bad_logit_spoils_its_row_only(B, zt, bad):
     rows = [0, 1, 3]
     assert math.isnan(o["lp"][2].item()) and math.isnan(o["stats"][0].item())
     assert all(same(o[k][rows], clean[k][rows]) for k in ("lp", "ent", "dz"))
+
+
+@pytest.mark.parametrize("zt,dzt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("pad,col", [(0, 0), (1, 1), (400, 8)])
+def test_a_bad_target_leaves_everything_else(B, zt, dzt, pad, col):
+    """Targets from V on, up to and past the end of the row's last group of logits
+    (2048 here), and negative ones: the other rows, the padding around dz and what
+    lies behind its last row keep their bits."""
+    T, V = 7, 1104                                  # (rows of whole 16 bytes, of either type)
+    c = logits_case(T, V, pad, col, zt, dzt, "one", dict(mask=False, gamma=0.05, reduce="sum"))
+    clean = run_logits(B, c)
+    same_type = zt == dzt
+    for bad in (V, V + 1, V + col + pad, 2047, 2048, 2 ** 31 - 1, -1, -2 ** 31):
+        for row in (0, 3, T - 1):
+            b = c | dict(tgt=c["tgt"].clone())
+            b["tgt"][row] = bad
+            buf = torch.full((T + 2, c["ld"]), 7.0, dtype=TYPES[dzt], device="cuda")
+            runs = [(run_logits(B, b, dz=buf[:T, col:col + V]), buf)]
+            if same_type:                           # the gradient over the logits
+                over = buf.clone()
+                over[:T] = c["zb"]
+                z = over[:T, col:col + V]
+                runs.append((run_logits(B, b, dz=z, z=z), over))
+            torch.cuda.synchronize()
+            assert B.biv_poll_error() == 2
+            keep = torch.arange(T, device="cuda") != row
+            for i, (o, mem) in enumerate(runs):
+                assert math.isnan(o["lp"][row].item()) and same(o["ent"], clean["ent"])
+                assert same(o["lp"][keep], clean["lp"][keep]) and same(o["dz"][keep], clean["dz"][keep])
+                around = c["zb"] if i else buf[:0].new_full((T, c["ld"]), 7.0)
+                assert same(mem[:T, :col], around[:, :col]) and same(mem[:T, col + V:], around[:, col + V:])
+                assert bool((mem[T:] == 7.0).all())
