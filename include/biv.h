@@ -304,6 +304,13 @@ typedef struct {
   int defer_fold;                   /* 1: when the call leaves chunk partials in the
                                        workspace (biv_gemm_partials says so), skip the
                                        fold: a consumer op reads them; C is not written */
+  int b_early;                      /* bf16.  0: B may be the output of the call just before.
+                                       1: the first tiles of B are loaded while calls ahead in
+                                       the stream may still run.  Only for a B with another call
+                                       of this library that is no GEMM (those let their successor
+                                       start before they have waited themselves) between its
+                                       last writer and this call: the weights of a forward that
+                                       begins with biv_embed, say */
 } biv_gemm_desc;
 
 /* Fills *out with the partials layout of a call (chunks = 0 when the plan

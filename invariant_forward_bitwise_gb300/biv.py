@@ -52,7 +52,7 @@ class GemmDesc(C.Structure):
                 ("sa", C.c_void_p), ("ld_sa", C.c_int64),
                 ("sb", C.c_void_p),
                 ("group_offsets", C.c_void_p), ("groups", C.c_int),
-                ("mode", C.c_int), ("defer_fold", C.c_int)]
+                ("mode", C.c_int), ("defer_fold", C.c_int), ("b_early", C.c_int)]
 
 
 class Partials(C.Structure):
@@ -367,7 +367,9 @@ def biv_attention_noalloc(desc: AttnDesc, stream=None):
 
 
 def gemm_desc(A, B, Cout, mode=MODE_INVARIANT, sa=None, sb=None, group_offsets=None, groups=0,
-              M=None) -> GemmDesc:
+              M=None, b_early=False) -> GemmDesc:
+    """b_early: B is loaded while the calls ahead may still run (see
+    include/biv.h); not for a B that the call just before writes."""
     dt = {torch.bfloat16: BF16, torch.float32: F32, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}
     d = GemmDesc()
     d.M = A.shape[0] if M is None else M
@@ -383,6 +385,7 @@ def gemm_desc(A, B, Cout, mode=MODE_INVARIANT, sa=None, sb=None, group_offsets=N
     d.group_offsets = group_offsets.data_ptr() if group_offsets is not None else None
     d.groups = groups
     d.mode = mode
+    d.b_early = int(b_early)
     return d
 
 

@@ -35,8 +35,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Programmatic dependent launch.  Kernels of the forward chain are launched
 // with programmatic stream serialization: a kernel may be scheduled while its
 // predecessor in the stream still runs, executes griddepcontrol.wait before it
-// touches any memory the predecessor writes or reads (weights excepted), and
-// lets its own successor be scheduled early (griddepcontrol.launch_dependents).
+// touches any memory that work ahead of it writes or reads, and lets its own
+// successor be scheduled early (griddepcontrol.launch_dependents).  Before the wait
+// only these are read: B of a GEMM whose caller set b_early, NVFP4 codes and scales,
+// and the optimizer's table, none of which a kernel of this library writes meanwhile.
 // BIV_PDL=0 turns the attribute off (plain stream order).
 bool pdl_enabled();
 

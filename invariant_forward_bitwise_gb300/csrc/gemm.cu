@@ -161,7 +161,7 @@ struct GemmArgs {
   int64_t ldp;          // partial row pitch (N rounded up to the tile width)
   int vec_ok;           // C rows 16-byte aligned
   int n_fastest;        // fold mode: walk N tiles first
-  int b_after_wait;     // 1: B is written by the previous kernel (no early prefetch)
+  int b_early;          // 1: B is not written by kernels that may still run (prefetch before the wait)
   int kpb;              // K blocks of 64 per pipeline stage (2: 3-D maps, two panels per copy)
   // log-softmax epilogue (LSE instantiation): per row and 128-column group g
   // of the output, (max, sum of exp(z - max)) to lse[row * ngroups + g]; the
@@ -284,10 +284,10 @@ __global__ void __launch_bounds__(kGemmThreads, PARTIAL ? 2 : 1)
         else
           tma_load_2d(smem_u32(dst), map, bar, kb * 64, row0);
       };
-      // The weights (B) of the first stages do not depend on the previous
-      // kernel: fetch them before waiting for it, then A and the rest.
+      // With b_early the weights (B) of the first stages do not depend on the
+      // previous kernels: fetch them before waiting for these, then A and the rest.
       int pre = 0;
-      if (!p.b_after_wait) {
+      if (p.b_early) {
         const int i = blockIdx.x, n0 = tile_n0(item_tile(i));
         for (int c = item_c0(i); c < item_c1(i) && pre < S; ++c) {
           const int kb1 = min(KB, (c + 1) * p.kc_blocks);
@@ -1285,7 +1285,7 @@ Plan plan_bf16(const biv_gemm_desc& d) {
 
 template <int BN, bool F32OUT>
 biv_status launch_bf16(const CUtensorMap& ta, const CUtensorMap& tb, const biv_gemm_desc& d,
-                       const Plan& pl, void* ws, cudaStream_t s, bool b_after_wait) {
+                       const Plan& pl, void* ws, cudaStream_t s) {
   // partial mode writes FP32 partials whatever C's type: one instantiation
   constexpr bool kPartialOk = BN <= 128;
   auto kern = (kPartialOk && pl.partial) ? gemm_bf16_kernel<BN, false, kPartialOk>
@@ -1313,7 +1313,7 @@ biv_status launch_bf16(const CUtensorMap& ta, const CUtensorMap& tb, const biv_g
   a.ldp = pl.ldp;
   a.vec_ok = aligned16(d.C) && (d.ldc * eb) % 16 == 0;
   a.n_fastest = !pl.partial && d.N <= d.M;
-  a.b_after_wait = b_after_wait ? 1 : 0;
+  a.b_early = d.b_early;
   a.kpb = pl.kpb;
   a.err = device_error_word();
   const int64_t items = pl.partial ? pl.tiles * pl.chunks : pl.tiles;
@@ -1332,12 +1332,12 @@ biv_status launch_bf16(const CUtensorMap& ta, const CUtensorMap& tb, const biv_g
 
 template <bool F32OUT>
 biv_status dispatch_bf16(const CUtensorMap& ta, const CUtensorMap& tb, const biv_gemm_desc& d,
-                         const Plan& p, void* ws, cudaStream_t s, bool b_after_wait = false) {
+                         const Plan& p, void* ws, cudaStream_t s) {
   switch (p.bn) {
-    case 256: return launch_bf16<256, F32OUT>(ta, tb, d, p, ws, s, b_after_wait);
-    case 192: return launch_bf16<192, F32OUT>(ta, tb, d, p, ws, s, b_after_wait);
-    case 128: return launch_bf16<128, F32OUT>(ta, tb, d, p, ws, s, b_after_wait);
-    default: return launch_bf16<64, F32OUT>(ta, tb, d, p, ws, s, b_after_wait);
+    case 256: return launch_bf16<256, F32OUT>(ta, tb, d, p, ws, s);
+    case 192: return launch_bf16<192, F32OUT>(ta, tb, d, p, ws, s);
+    case 128: return launch_bf16<128, F32OUT>(ta, tb, d, p, ws, s);
+    default: return launch_bf16<64, F32OUT>(ta, tb, d, p, ws, s);
   }
 }
 
@@ -1503,10 +1503,10 @@ biv_status biv_gemm_nvfp4(const uint16_t* A, int64_t lda, const uint8_t* codes,
     CUtensorMap ta, tb;
     if (!make_bf16_maps(&ta, &tb, A, lda, M, dec, K, N, K, f.p))
       return set_error(BIV_ERR_CUDA, "gemm_nvfp4: tensor map encoding failed");
-    // the decoded weights come from the kernel just before: no early B prefetch
+    // the decoded weights come from the kernel just before: b_early stays 0
     void* pws = static_cast<uint8_t*>(ws) + f.dec_bytes;
-    return c_dtype == BIV_F32 ? dispatch_bf16<true>(ta, tb, d, f.p, pws, s, true)
-                              : dispatch_bf16<false>(ta, tb, d, f.p, pws, s, true);
+    return c_dtype == BIV_F32 ? dispatch_bf16<true>(ta, tb, d, f.p, pws, s)
+                              : dispatch_bf16<false>(ta, tb, d, f.p, pws, s);
   }
   const Plan& p = f.p;
   CUtensorMap ta, tc, ts;

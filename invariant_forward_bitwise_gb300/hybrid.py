@@ -159,7 +159,8 @@ class HybridModel:
                                                                self.mode))
             biv.biv_gemm_nvfp4(A, codes, sc, Cout, M=M, mode=self.mode, ws=ws, stream=st)
         else:
-            d = biv.gemm_desc(A, Bw, Cout, mode=self.mode, M=M)
+            # (weights are complete before a step's first calls, embed and RMSNorm)
+            d = biv.gemm_desc(A, Bw, Cout, mode=self.mode, M=M, b_early=True)
             ws = self._grow("gws", biv.biv_gemm_workspace(d))
             biv.biv_gemm(d, ws, stream=st)
         self.launches += 1

@@ -355,7 +355,7 @@ elif case == "gemm_nvfp4":
             c = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
             n4 = len(ws4) * max(1, 8 // len(ws4))
             t4 = graph_time(lambda: [biv.biv_gemm_nvfp4(a, *ws4[i % len(ws4)], c) for i in range(n4)], 1) / n4
-            ds = [biv.gemm_desc(a, w, c) for w in wbs]
+            ds = [biv.gemm_desc(a, w, c, b_early=True) for w in wbs]
             nb = len(ds) * max(1, 8 // len(ds))
             tb = graph_time(lambda: [biv.biv_gemm(ds[i % len(ds)]) for i in range(nb)], 1) / nb
             print(f"{name:8s} M={M:3d} N={N:6d} K={K}: nvfp4 {t4*1e3:7.1f} us "
@@ -371,7 +371,7 @@ elif case == "gemm_prefill_layer":
         b = (torch.randn(N, K, device="cuda") * 0.02).to(torch.bfloat16)
         c = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
         mode = biv.MODE_FAST if os.environ.get("BIV_BENCH_MODE") == "fast" else biv.MODE_INVARIANT
-        d = biv.gemm_desc(a, b, c, mode=mode)
+        d = biv.gemm_desc(a, b, c, mode=mode, b_early=True)
         ms = graph_time(lambda: biv.biv_gemm(d), reps)
         print(f"{name:8s} M={M} N={N:6d} K={K}: {ms*1e3:8.1f} us  {2*M*N*K/(ms/1e3)/1e12:6.0f} TFLOP/s",
               flush=True)
@@ -394,7 +394,7 @@ elif case == "gemm_sweep":
             a = torch.randn(M, K, device="cuda").to(torch.bfloat16)
             c = torch.empty(M, N, device="cuda",
                             dtype=torch.float32 if name == "lm_head" else torch.bfloat16)
-            ds = [biv.gemm_desc(a, b, c) for b in bs]
+            ds = [biv.gemm_desc(a, b, c, b_early=True) for b in bs]
             need = biv.biv_gemm_workspace(ds[0])
             for d in ds:
                 d.defer_fold = int(defer)
@@ -436,6 +436,6 @@ else:
         ms = timeit(lambda: biv.biv_lm_head_logprob(a, b, tgt, lp, ws))
     else:
         c = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
-        d = biv.gemm_desc(a, b, c)
+        d = biv.gemm_desc(a, b, c, b_early=True)
         ms = timeit(lambda: biv.biv_gemm(d))
     print(f"{case} M={M} N={N} K={K}: {ms*1e3:.1f} us  {2*M*N*K/(ms/1e3)/1e12:.0f} TFLOP/s  weights {N*K*2/(ms/1e3)/1e9:.0f} GB/s")

@@ -151,7 +151,8 @@ class DenseModel:
         """Cout = A . Bw^T.  With defer=True a plan that leaves chunk partials
         skips its fold kernel and returns the partials for the consumer op
         (Cout is then not written); otherwise returns None."""
-        d = biv.gemm_desc(A, Bw, Cout, mode=self.mode, M=M)
+        # (weights are complete before a step's first calls, embed and RMSNorm)
+        d = biv.gemm_desc(A, Bw, Cout, mode=self.mode, M=M, b_early=True)
         need = biv.biv_gemm_workspace(d)
         if need > self.gws.numel():
             raise RuntimeError(f"GEMM workspace too small ({need} > {self.gws.numel()}); call reserve()")

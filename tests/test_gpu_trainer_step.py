@@ -175,3 +175,93 @@ def test_captured_step_equals_eager(B):
         torch.cuda.synchronize()
         ends.append([t.clone() for t in s.params + s.opt.exp_avg + s.opt.exp_avg_sq + [s.opt.steps, s.stats]])
     assert all(same(a, b) for a, b in zip(*ends)) and ends[0][-2].tolist() == [2, 0]
+
+
+def weights_and_step(bits, M, seed=3):
+    """An optimizer over 50 M weights whose last two tensors a GEMM and an LM head read."""
+    from invariant_forward_bitwise_gb300.optim import AdamW
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    N, K = 4096, 2048
+    shapes = [(N, K)] * 6
+    p = [(torch.randn(s, device="cuda", generator=gen) * 0.02).bfloat16() for s in shapes]
+    g = [torch.randn(s, device="cuda", generator=gen).bfloat16() for s in shapes]
+    opt = AdamW(p, g, lr=0.01, bits=bits, rounding="stochastic", seed=1)
+    h = torch.randn(M, K, device="cuda", generator=gen).bfloat16()
+    target = torch.randint(0, N, (M,), device="cuda", generator=gen, dtype=torch.int32)
+    return opt, p, h, target
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("M", [16, 300])
+@pytest.mark.parametrize("between", ["nothing", "gemm", "row op"])
+def test_the_call_after_a_step_reads_the_new_weights(B, bits, M, between):
+    """A GEMM, or the fused LM head, right behind the step in its stream or graph
+    gives the bits of the same calls with a synchronisation after each; with a GEMM
+    of other weights between too, and with b_early behind a row op."""
+    outs = []
+    for how in ("waiting", "eager", "graph"):
+        opt, p, h, target = weights_and_step(bits, M)
+        N = p[0].shape[0]
+        c = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        c0, lp, act = torch.empty_like(c), torch.empty(M, device="cuda"), torch.empty_like(h[:, :1024])
+        ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+        lws = torch.empty(B.biv_lm_head_logprob_workspace(M, N), dtype=torch.uint8, device="cuda")
+
+        def calls(sync):
+            for second in (lambda: B.biv_gemm(B.gemm_desc(h, p[5], c, b_early=between == "row op"), ws),
+                           lambda: B.biv_lm_head_logprob(h, p[5], target, lp, lws)):
+                opt.step()
+                sync()
+                if between == "gemm":
+                    B.biv_gemm(B.gemm_desc(h, p[4], c0), ws)
+                if between == "row op":
+                    B.biv_silu_mul(h, act)
+                sync()
+                second()
+                sync()
+        seen = []
+        graph = None
+        if how == "graph":
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                calls(lambda: None)
+        for _ in range(4):
+            if graph:
+                graph.replay()
+            else:
+                calls(torch.cuda.synchronize if how == "waiting" else lambda: None)
+            seen += [c.clone(), lp.clone()]
+        torch.cuda.synchronize()
+        assert B.biv_poll_error() == 0 and opt.steps.tolist() == [8, 0]
+        outs.append(seen + [x.clone() for x in p])
+    for other in outs[1:]:
+        assert all(same(a, b) for a, b in zip(outs[0], other))
+    assert not same(outs[0][0], outs[0][2]) and not same(outs[0][1], outs[0][3])
+
+
+@pytest.mark.parametrize("M", [16, 300])
+def test_a_gemm_may_read_the_output_of_the_call_before_as_b(B, M):
+    """B straight from a GEMM (folded in the CTA, or from partials) or a row op."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    rnd = lambda *s: (torch.randn(*s, device="cuda", generator=gen) * 0.1).bfloat16()  # noqa: E731
+    h, ws = rnd(M, 1024), torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    ins = [(rnd(2048, 2048), rnd(1024, 2048), rnd(2048, 2048)) for _ in range(6)]
+    for sync in (torch.cuda.synchronize, lambda: None):
+        w, w2 = torch.zeros(2048, 1024, dtype=torch.bfloat16, device="cuda"), rnd(2048, 1024)
+        for a, b, gu in ins:
+            c = torch.empty(M, 2048, dtype=torch.bfloat16, device="cuda")
+            c2 = torch.empty_like(c)
+            B.biv_gemm(B.gemm_desc(a, b, w), ws)
+            sync()
+            B.biv_gemm(B.gemm_desc(h, w, c), ws)
+            sync()
+            B.biv_silu_mul(gu, w2)
+            sync()
+            B.biv_gemm(B.gemm_desc(h, w2, c2), ws)
+            sync()
+            outs += [c, c2]
+    torch.cuda.synchronize()
+    n = len(outs) // 2
+    assert all(same(x, y) for x, y in zip(outs[:n], outs[n:]))
