@@ -686,6 +686,11 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * even), or STOCHASTIC: the magnitude goes up with a chance equal to the part
  * cut off, from 16 bits of a hash of (seed, t, element), so that steps below
  * half a grid spacing still move the value on average; a rerun repeats it.
+ * Without a clip a NaN or infinite gradient is not caught: its weight becomes NaN
+ * in either rounding, m and v NaN or infinite.  With 8-bit states an infinite m
+ * makes its block's scale infinite, and at the next step the block's 128 weights
+ * NaN; an infinite v with a finite m (a square beyond FP32) makes all positive v
+ * of the block infinite, whose weights then only decay, and its zeros NaN.
  *
  * biv_opt_plan (host only, no launch) checks a HOST array of n tensors and
  * fills first_chunk, rng_base and vec; *chunks receives the launch size and

@@ -531,3 +531,90 @@ def test_optimizer_refuses(O, B):
     for kw in (dict(betas=(1.0, 0.9)), dict(eps=0.0)):
         with pytest.raises(B.BivError):
             O.AdamW([p], [g], **kw).step()
+
+
+@pytest.mark.parametrize("param", ["f32", "master", "bf16"])
+@pytest.mark.parametrize("state", ["f32", "e4m3"])
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), "weight"])
+def test_nan_and_infinity_stay_visible(O, param, state, rounding, bad):
+    """Without a clip a NaN or infinite gradient, or a NaN weight, leaves NaN in its
+    weight (no draw of random bits may carry it into a zero) and a moment that is
+    not finite; all else has the bits of a run in which that gradient is 0."""
+    at = [(4, 1000), (5, 2047), (8, 77), (8, 4999), (9, 0)]      # whole chunks, the last of them, a short tensor
+    runs = []
+    for spoil in (False, True):
+        ts = tensors(synth.rng(41), SIZES, param, "f32", state)
+        for i, j in at:
+            for k in ("grads", "exp_avg", "exp_avg_sq"):
+                ts[k][i][j] = 0
+            if spoil and bad == "weight":
+                ts["params"][i][j] = float("nan")
+                if param == "master":
+                    ts["master"][i][j] = float("nan")
+            elif spoil:
+                ts["grads"][i][j] = bad
+        opt = O.AdamW(**ts, lr=1e-3, weight_decay=0.1, rounding=rounding, seed=8)
+        seen = []
+        for _ in range(2):
+            opt.step()
+            torch.cuda.synchronize()
+            seen.append(snapshot(ts))
+        runs.append(seen)
+    e8, inf = state == "e4m3", isinstance(bad, float) and np.isinf(bad)
+    for step, (clean, got) in enumerate(zip(*runs)):
+        for i, n in enumerate(SIZES):
+            hit = np.zeros(n, bool)
+            hit[[j for t, j in at if t == i]] = True
+            # the block of an infinite moment: its scale is infinite, so all that it
+            # holds is lost at the next step
+            lost = hit.copy()
+            if e8 and inf:
+                for j in np.nonzero(hit)[0]:
+                    lost[j // 128 * 128:j // 128 * 128 + 128] = True
+            weights = ["params"] + (["master"] if param == "master" else [])
+            for k in weights:
+                w, ref = f64(got[k][i]), f64(clean[k][i])
+                spoiled = lost if step else hit
+                assert np.all(np.isnan(w[spoiled])), (k, i, step)
+                assert np.array_equal(w[~spoiled], ref[~spoiled])
+            if bad == "weight":
+                assert same(got["exp_avg"][i], clean["exp_avg"][i])
+                assert same(got["exp_avg_sq"][i], clean["exp_avg_sq"][i])
+                continue
+            m, v = f64(got["exp_avg"][i]), f64(got["exp_avg_sq"][i])
+            if e8:
+                m, v = m * np.repeat(f64(got["exp_avg_scale"][i]), 128)[:n], v * np.repeat(
+                    f64(got["exp_avg_sq_scale"][i]), 128)[:n]
+                assert np.all(np.isnan(f64(got["exp_avg"][i])[hit]))
+            assert not np.any(np.isfinite(m[hit])) and not np.any(np.isfinite(v[hit]))
+            for k in ("exp_avg", "exp_avg_sq"):
+                x, ref = f64(got[k][i]), f64(clean[k][i])
+                assert np.array_equal(x[~lost], ref[~lost]), (k, i, step)
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_an_infinite_second_moment_in_an_8_bit_block(O, rounding):
+    """A gradient of 1e22 (its square is beyond FP32): at the next step the positive
+    second moments of its block are infinite and their weights only decay, zero ones
+    are NaN; other blocks are not touched."""
+    n = 5000
+    ts, ref = (tensors(synth.rng(43), [n], "f32", "f32", "e4m3") for _ in range(2))
+    for x in (ts, ref):
+        for k in ("grads", "exp_avg", "exp_avg_sq"):
+            x[k][0][[130, 140]] = 0
+    ts["grads"][0][130] = 1e22
+    opts = [O.AdamW(**x, lr=1e-3, weight_decay=0.1, rounding=rounding, seed=8) for x in (ts, ref)]
+    w = []
+    for _ in range(2):
+        for o in opts:
+            o.step()
+        torch.cuda.synchronize()
+        w.append(f64(ts["params"][0]))
+    keep = np.float32(1) - np.float32(1e-3) * np.float32(0.1)
+    blk = np.arange(128, 256)
+    blk = blk[blk != 140]
+    assert np.array_equal(w[1][blk], (w[0][blk].astype(np.float32) * keep).astype(np.float64))
+    assert np.isnan(w[1][140]) and np.all(np.isinf(f64(ts["exp_avg_sq_scale"][0])[1:2]))
+    out = np.r_[0:128, 256:n]
+    assert np.array_equal(w[1][out], f64(ref["params"][0])[out])
