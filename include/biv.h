@@ -597,7 +597,8 @@ biv_status biv_attention_backward(const biv_attn_bwd_desc* desc, biv_stream_t st
  *   loss = sum_t w_t (pg + kl_coef kl - ent_coef H)
  *   dlp  = w ((u is taken ? u : 0) + kl_coef (1 - exp(e)))
  * where u is taken when u >= c, the dual bound does not act and |lp - old_lp|
- * < 20, and the KL part is 0 at |ref_lp - lp| >= 20 (the clamps' derivative).
+ * < 20, and the KL part is 0 at |ref_lp - lp| >= 20 (the clamps' derivative); u's
+ * part is 0 at lp = -inf too, where no old_lp stands beside it.
  * w_t by `reduce`: TOKEN_MEAN 1/N, N counted rows; SEQ_MEAN 1/(S n_s), S
  * sequences that have counted rows, n_s their number; SUM 1/norm.
  * A row that does not count has weight 0: what its lp, logits and target hold
@@ -649,7 +650,8 @@ biv_status biv_policy_loss(const biv_policy_desc* desc, const float* lp, float* 
  * BIV_BF16, one rounding; NULL: no gradient).  dz may be z itself (same
  * pointer, type and stride), and must not overlap it otherwise.  A logit of
  * -1e30 or less (-inf, a type's lowest value) is masked: p = 0 and dz = 0; a
- * row of masked logits alone gives NaN, as a NaN or +inf among them does.  A counted
+ * row of masked logits alone gives NaN, as a NaN or +inf among them does; where
+ * the target is masked, dlp is 0 (its lp is -inf, or the low value's).  A counted
  * row whose target is outside [0, V) gives lp = NaN and the device error code
  * 2; other rows' results and what lies around dz stay as they are.  Each row's bits depend on V and the row only: 4 KB groups of logits
  * are reduced to (max, sum, entropy sum) by one warp and merged in one order,

@@ -260,7 +260,7 @@ __device__ __forceinline__ void policy_four(const PolicyArgs& a, const Four& f, 
     g[i] = 0.f;
     if (f.w[i] > 0.f) {
       const Token o = policy_token(a, f.lp[i], f.A[i], f.old[i], f.ref[i]);
-      g[i] = f.w[i] * o.dlp;
+      g[i] = f.lp[i] == -INFINITY ? 0.f : f.w[i] * o.dlp;   // (also where no old_lp is far from it)
       v[0] += f.w[i] * (o.pg + a.beta * o.kl - a.gamma * f.ent[i]);
       v[1] += f.w[i] * o.pg;
       v[2] += f.w[i] * o.kl;
@@ -965,12 +965,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     if ((on0 >> lane) & 1u) {
       const int r = row_of(q);
       m_wa = a.p.ws.row[r];
-      m_tg = a.target[r];
+      const int tg = a.target[r];
       if (a.p.old_lp) m_old = a.p.old_lp[r];
       if (a.p.ref_lp) m_ref = a.p.ref_lp[r];
-      if (m_tg >= 0 && m_tg < a.V) {
-        if (ZB) m_zt = bf2f(reinterpret_cast<const uint16_t*>(row_ptr(q))[m_tg]);
-        else m_zt = reinterpret_cast<const float*>(row_ptr(q))[m_tg];
+      // a target outside [0, V) stays -1: the row's last group may reach past V, and
+      // no element there is the target's
+      if (tg >= 0 && tg < a.V) {
+        m_tg = tg;
+        if (ZB) m_zt = bf2f(reinterpret_cast<const uint16_t*>(row_ptr(q))[tg]);
+        else m_zt = reinterpret_cast<const float*>(row_ptr(q))[tg];
       }
     }
   };
@@ -1248,8 +1251,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
     const int from = q1 & 31;
     tg0 = __shfl_sync(0xffffffffu, m_tg, from);
     zt = __shfl_sync(0xffffffffu, m_zt, from);
-    const bool tg_ok = tg0 >= 0 && tg0 < a.V;
-    if (!tg_ok) tg0 = -1;              // the last group may reach past V: no element there is the target's
+    const bool tg_ok = tg0 >= 0;
     const float lp = tg_ok ? __fsub_rn(__fsub_rn(__fmul_rn(zt, a.it), xm), ls) : NAN;
     if (teller) {
       a.lp[row_of(q1)] = lp;
@@ -1261,7 +1263,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) policy_logits_kernel(
       const float wt = __shfl_sync(0xffffffffu, m_wa.x, from), A = __shfl_sync(0xffffffffu, m_wa.y, from);
       const float old = __shfl_sync(0xffffffffu, m_old, from), ref = __shfl_sync(0xffffffffu, m_ref, from);
       const Token o = policy_token(a.p, lp, A, old, ref);
-      const float dlp = wt * o.dlp, wg = wt * a.p.gamma, is = a.it * rS;
+      // (a masked target: no gradient by way of lp)
+      const float dlp = zt <= kMasked ? 0.f : wt * o.dlp, wg = wt * a.p.gamma, is = a.it * rS;
       a0 = is * (wg * (H - lnS) - dlp);
       a1 = is * wg * kLn2;
       at_target = a.it * dlp;

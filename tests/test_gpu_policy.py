@@ -597,3 +597,49 @@ def test_a_bad_target_leaves_everything_else(B, zt, dzt, pad, col):
                 around = c["zb"] if i else buf[:0].new_full((T, c["ld"]), 7.0)
                 assert same(mem[:T, :col], around[:, :col]) and same(mem[:T, col + V:], around[:, col + V:])
                 assert bool((mem[T:] == 7.0).all())
+
+
+@pytest.mark.parametrize("zt", ["f32", "bf16"])
+@pytest.mark.parametrize("low", [-math.inf, "lowest", -1e31])
+@pytest.mark.parametrize("old", ["none", "own", "other"])
+def test_a_masked_target_has_no_gradient(B, zt, low, old):
+    """A target whose logit is masked: dz is 0 there and what the entropy term alone
+    gives elsewhere, whatever the old and reference logprobs are; so is dlp from a
+    logprob of -inf.
+    Other rows keep their bits."""
+    T, V, row = 5, 1200, 2
+    kw = dict(mask=False, gamma=0.05, reduce="sum", no_old=old == "none", beta=0.1 if old == "other" else 0.0)
+    c = logits_case(T, V, 0, 0, zt, "f32", "one", kw)
+    clean = run_logits(B, c)
+    c["ref"][row] = -math.inf                       # (the reference masks it too)
+    t = int(c["target"][row])
+    c["zb"][row, t] = torch.finfo(c["zb"].dtype).min if low == "lowest" else low
+    if old == "own":
+        first = run_logits(B, c)
+        torch.cuda.synchronize()
+        # (an old logprob of -inf has no difference from -inf: the lowest value in its place)
+        c["old"] = np.maximum(first["lp"].cpu().numpy(), -3e38)
+    o = run_logits(B, c)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    zz = f64(c["z"])
+    zz[row, t] = -math.inf
+    _, H, p, logp = tr.token_logprobs(zz, np.where(np.arange(T) == row, t, c["target"]))
+    dlp = np.zeros(T)
+    want = tr.policy_dz(zz, c["target"], dlp, c["w"], 0.05)[row]
+    size = 0.05 * c["w"][row] * p[row] * (np.abs(np.where(p[row] > 0, logp[row], 0)) + H[row] + 1)
+    got = f64(o["dz"])[row]
+    assert float(o["lp"][row]) < -1e28 and got[t] == 0.0
+    assert np.all(np.abs(got - want) <= (REL + 2.0 ** -24) * size + 1e-37)
+    keep = torch.arange(T, device="cuda") != row
+    if old != "own":
+        assert same(o["dz"][keep], clean["dz"][keep]) and same(o["lp"][keep], clean["lp"][keep])
+    # from logprobs
+    lp = o["lp"].clone()
+    if old != "own":
+        lp[row] = -math.inf
+        d = desc(B, c | dict(kw=kw | dict(gamma=0.0)), torch.empty(8, device="cuda"), workspace(B, T, 1))
+        out = torch.empty(T, device="cuda")
+        B.biv_policy_loss(d, lp, out)
+        torch.cuda.synchronize()
+        assert float(out[row]) == 0.0 and bool(torch.isfinite(out).all())
