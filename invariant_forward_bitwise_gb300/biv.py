@@ -591,18 +591,22 @@ def biv_policy_loss_workspace(T: int, nseq: int) -> int:
 
 def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None, ref_lp=None,
                 clip_lo=0.2, clip_hi=0.2, dual_clip=0.0, kl_coef=0.0, ent_coef=0.0,
-                reduce=LOSS_TOKEN_MEAN, norm=1.0) -> PolicyDesc:
+                reduce=LOSS_TOKEN_MEAN, norm=1.0, adv_per_row=None) -> PolicyDesc:
     """The part that biv_policy_loss and biv_policy_loss_logits share (see
     include/biv.h).  seq_start int32 [nseq + 1]; adv float32 [nseq] (one per
     sequence) or [T]; mask uint8 or bool [T]; old_lp, ref_lp float32 [T];
     stats float32 [8]; workspace uint8 of biv_policy_loss_workspace bytes.
-    With nseq == T an advantage vector counts as one per sequence."""
+    adv_per_row says which adv is.  None goes by its length, and by sequence
+    where nseq == T: a caller whose batches may have as many rows as sequences,
+    some of them empty, has to say."""
     dev, f32, keep = _device(), torch.float32, (seq_start, adv, stats, workspace, mask, old_lp, ref_lp)
     nseq, nadv = seq_start.numel() - 1, adv.numel()
     if nseq < 0:
         raise ValueError("seq_start needs at least one entry")
-    if nadv != nseq and nadv != T:
-        raise ValueError(f"adv must hold {nseq} (sequences) or {T} (rows) values")
+    if adv_per_row is None:
+        adv_per_row = nadv != nseq
+    if nadv != (T if adv_per_row else nseq):
+        raise ValueError(f"adv must hold {nseq} (sequences) or {T} (rows) values, as adv_per_row says")
     _rows_ok("seq_start", seq_start, torch.int32, 1, dev)
     _rows_ok("adv", adv, f32, 0, dev)
     _rows_ok("stats", stats, f32, 8, dev)
@@ -616,7 +620,7 @@ def policy_desc(seq_start, adv, stats, workspace, T: int, mask=None, old_lp=None
     if ref_lp is not None:
         _rows_ok("ref_lp", ref_lp, f32, T, dev)
         ref_lp = ref_lp.data_ptr()
-    d = PolicyDesc(T, nseq, seq_start.data_ptr(), mask, old_lp, ref_lp, adv.data_ptr(), int(nadv != nseq),
+    d = PolicyDesc(T, nseq, seq_start.data_ptr(), mask, old_lp, ref_lp, adv.data_ptr(), int(adv_per_row),
                    clip_lo, clip_hi, dual_clip, kl_coef, ent_coef, reduce, norm, stats.data_ptr(),
                    workspace.data_ptr(), workspace.numel())
     d.tensors = keep     # they live as long as the descriptor

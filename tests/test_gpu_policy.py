@@ -643,3 +643,22 @@ def test_a_masked_target_has_no_gradient(B, zt, low, old):
         B.biv_policy_loss(d, lp, out)
         torch.cuda.synchronize()
         assert float(out[row]) == 0.0 and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("per_row", [True, False, None])
+def test_as_many_rows_as_sequences(B, per_row):
+    """Four rows in four sequences, two of them empty: the caller says whether the
+    four advantages are the rows' or the sequences' (None: the sequences')."""
+    T, start = 4, [0, 0, 0, 2, 4]
+    adv = np.array([1.0, 2.0, 3.0, 4.0], np.float32)
+    stats, dlp = torch.empty(8, device="cuda"), torch.empty(T, device="cuda")
+    make = lambda a, n, **kw: B.policy_desc(dev(start, np.int32), dev(a), stats, workspace(B, n, 4), T=n, **kw)  # noqa: E731
+    d = make(adv, T, adv_per_row=per_row)
+    B.biv_policy_loss(d, torch.full((T,), -1.0, device="cuda"), dlp)
+    torch.cuda.synchronize()
+    A = adv if per_row else adv[[2, 2, 3, 3]]
+    assert np.all(np.abs(f64(dlp) + A / 4) <= 2.0 ** -23 * A)
+    for a, n, kw in ((adv, 5, dict(adv_per_row=True)), (np.ones(5), 5, dict(adv_per_row=False)),
+                     (np.ones(3), 5, {})):
+        with pytest.raises(ValueError):
+            make(a, n, **kw)
