@@ -21,7 +21,7 @@ namespace biv {
 namespace {
 
 constexpr int kSmallRows = 4096, kSmallSeqs = 1024;   // what one CTA takes
-constexpr int kMidRows = 1 << 19, kMidSeqs = 1024;    // counts by a block per sequence
+constexpr int kMidSeqs = 1024;                        // counts by a block per sequence
 constexpr int64_t kMidMean = 1 << 17;                 // ... of this length on average at most
 constexpr int kTB = 256;           // threads per block of tokens
 constexpr int kTok = 1024;         // tokens per partial sum
@@ -408,14 +408,20 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
 }
 
 // ----------------------------------------------------------- large calls --
-// Up to 524288 rows in 1024 sequences two launches: counts by a block per
-// sequence, then the sums, each block adding the counts up for itself.  300 K rows
-// in 512 ragged sequences take 10.6 us against 15.1 by the general way (a launch
-// that zeroes the counts, rows that add to them, and the sums), 524288 rows in 64
-// even ones 11.7 against 16.2, 131072 in 16 7.8 against 9.4; in 4096 sequences 16.3
-// against 16.0, in one sequence 20 against 17, which the rule leaves to the general
-// way.  Their bytes are under 1.5 us at HBM's rate: the launches and the dependent
-// loads of each (starts, counts, rows) take the time.
+// Up to 1024 sequences of 131072 rows on average two launches: counts by a block
+// per sequence, then the sums, each block adding the counts up for itself.  300 K
+// rows in 512 ragged sequences take 10.6 us against 15.1 by the general way (a launch
+// that zeroes the counts, rows that add to them, and the sums).  With a mask and an
+// old logprob, this way against the general one (us):
+//   131072 rows in 16 sequences 7.9 / 9.6;   524288 in 64 11.7 / 16.4
+//   2^20 in 16 18.9 / 25.8, in 1024 19.0 / 21.8;   2^22 in 64 55 / 79, in 1024 57 / 67
+//   2^24 in 256 239 / 317, in 1024 246 / 293;   2^26 in 1024 959 / 1239
+// so the number of rows sets no limit.  Few long sequences leave most SMs idle: one
+// of 524288 rows 20.4 / 17.0, one of 2^20 36 / 25, four of 2^22 372 / 319.  Many have
+// each block of the sums add many counts up: 4096 of 32 rows 12.5 / 11.5, 4096 of 256
+// 23.9 / 23.4 (from 2^21 rows on they would gain too: 61 / 66 for 2^22).  A rollout's
+// bytes are a few us at HBM's rate at most: the launches and the dependent loads of
+// each (starts, counts, rows) take the time.
 __global__ void policy_zero_kernel(const __grid_constant__ PolicyArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -1325,7 +1331,7 @@ PolicyArgs policy_args(const biv_policy_desc& d) {
   a.old_lp = d.old_lp; a.ref_lp = d.ref_lp; a.adv = d.adv; a.adv_per_row = d.adv_per_row;
   a.lo = 1.0f - d.clip_lo; a.hi = 1.0f + d.clip_hi; a.dual = d.dual_clip;
   a.beta = d.kl_coef; a.gamma = d.ent_coef; a.reduce = d.reduce; a.norm = d.norm;
-  a.mid = d.T <= kMidRows && d.nseq <= kMidSeqs && d.T <= kMidMean * d.nseq;
+  a.mid = d.nseq <= kMidSeqs && d.T <= kMidMean * d.nseq;
   a.stats = d.stats;
   a.ws = policy_ws(d.workspace, d.T, d.nseq);
   a.err = device_error_word();

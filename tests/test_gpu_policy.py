@@ -662,3 +662,28 @@ def test_as_many_rows_as_sequences(B, per_row):
                      (np.ones(3), 5, {})):
         with pytest.raises(ValueError):
             make(a, n, **kw)
+
+
+@pytest.mark.parametrize("T,nseq", [(600_001, 5), (1_100_003, 1024), (1_100_003, 1025), (1_100_003, 3)])
+def test_large_batches(B, T, nseq):
+    """Beyond 524288 rows, by either way of counting: weights, gradient and sums."""
+    g = synth.rng(nseq)
+    start = np.sort(np.concatenate([[3, T - 7], g.integers(3, T - 7, nseq - 1)]))
+    mask, adv = (g.random(T) < 0.9).astype(np.uint8), g.standard_normal(nseq).astype(np.float32)
+    stats, dlp = torch.empty(8, device="cuda"), torch.full((T,), 7.0, device="cuda")
+    d = B.policy_desc(dev(start, np.int32), dev(adv), stats, workspace(B, T, nseq), T=T, mask=dev(mask, np.uint8),
+                      reduce=B.LOSS_SEQ_MEAN)
+    B.biv_policy_loss(d, torch.full((T,), -1.0, device="cuda"), dlp)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    seq = np.searchsorted(start, np.arange(T), side="right") - 1
+    on = (seq >= 0) & (seq < nseq) & (mask != 0)
+    n = np.bincount(seq[on], minlength=nseq)
+    w = np.where(on, 1.0 / (np.sum(n > 0) * np.maximum(n, 1))[np.clip(seq, 0, nseq - 1)], 0)
+    want = -w * adv.astype(np.float64)[np.clip(seq, 0, nseq - 1)]
+    # the weight's product and reciprocal, and its product with A: three roundings
+    assert np.all(np.abs(f64(dlp) - want) <= 3.1 * 2.0 ** -24 * np.abs(want))
+    got = f64(stats)
+    assert got[7] == on.sum() and got[4] == got[5] == got[6] == 0
+    # (blocks of 1024 rows, then 32 lanes over at most 34 blocks each: 4 + 5 + 8 + 34 + 5 additions)
+    assert abs(got[0] - want.sum()) <= 60 * 2.0 ** -24 * np.abs(want).sum()
