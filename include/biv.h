@@ -653,11 +653,17 @@ biv_status biv_policy_loss(const biv_policy_desc* desc, const float* lp, float* 
  * row of masked logits alone gives NaN, as a NaN or +inf among them does; where
  * the target is masked, dlp is 0 (its lp is -inf, or the low value's).  A counted
  * row whose target is outside [0, V) gives lp = NaN and the device error code
- * 2; other rows' results and what lies around dz stay as they are.  Each row's bits depend on V and the row only: 4 KB groups of logits
- * are reduced to (max, sum, entropy sum) by one warp and merged in one order,
- * however the row is spread over CTAs.  1 <= V <= 262144, 0.01 <= inv_temp <=
- * 100.  Rows that keep 16
- * bytes' alignment load and store fastest; any element alignment works. */
+ * 2; other rows' results and what lies around dz stay as they are.
+ * Each row's bits depend on V and the row only: 4 KB groups of logits are
+ * reduced to (max, sum, entropy sum) by one warp and merged in one order,
+ * however the row is spread over CTAs.  They are not the bits of
+ * biv_lm_head_logprob or biv_logprob, whose sums run in another order: lp
+ * agrees with theirs to rounding, so with a rollout's logprobs as old_lp the
+ * ratio of an unchanged policy is 1 to rounding only and the gap's statistics
+ * are not exactly 0.  Where they have to be, take biv_policy_loss on the recompute's
+ * own lp, then biv_logprob_backward; or old_lp from this call.
+ * 1 <= V <= 262144, 0.01 <= inv_temp <= 100.  Rows that keep 16 bytes'
+ * alignment load and store fastest; any element alignment works. */
 biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, int64_t ld,
                                   int z_dtype, const int32_t* target, int V, float inv_temp,
                                   float* lp, float* entropy, void* dz, int64_t ldz, int dz_dtype,
@@ -670,7 +676,9 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * element, in FP32:
  *   g = grad * coef;  m = b1 m + (1-b1) g;  v = b2 v + ((1-b2) g) g
  *   w = w (1 - lr wd) - (lr / (1-b1^t)) m / (sqrt(v) / sqrt(1-b2^t) + eps)
- * (each operation rounded once, in the order written)
+ * (each operation rounded once, in the order written: m and v, and with 8 bits their
+ * codes and scales, have these bits.  w has but for its root and quotient, each an
+ * approximation corrected once, which may miss the nearest value where two all but tie)
  * with t the step's number, lr = *lr * lr_scale and wd of the tensor.
  *
  * A biv_opt_tensor describes one tensor of numel elements, all arrays dense:
@@ -736,7 +744,9 @@ biv_status biv_grad_norm(const biv_opt_tensor* tensors, int n, int64_t chunks, f
  * steps taken (0 for new states): the call uses t = step[0] + 1 and stores it;
  * step[1] must be 0 between calls and is 0 again after each; calls that share
  * it, or tensors, must not overlap on the GPU.  With clip given
- * and its norm not finite the whole call changes nothing, step included. */
+ * and its norm not finite the whole call changes nothing, step included; so does
+ * a call of no chunk (no tensor has an element).  The next call of the stream may
+ * read the new weights. */
 typedef struct {
   const biv_opt_tensor* tensors;   /* device */
   int n;

@@ -622,14 +622,15 @@ __global__ void __launch_bounds__(kTB) policy_token_kernel(const __grid_constant
 // once, and the next rows stream in while this one is reduced and written.  A
 // group's arithmetic and the merge order do not depend on the cluster size.
 //
-// Bound by HBM for long rows: 4096 x 151936 FP32 (every seventh row masked and not
-// read) take 736 us, 4.6 GB at 6.3 TB/s; 2037 x 131072 bf16 181 us, 5.9 TB/s, of
-// which every logit's two exponentials and eight FP32 operations come near the
-// issue rate.  Short and unaligned rows by the cluster barrier and the merge of
-// each row and by moving logits to 16 bytes' alignment in shared memory: 1000 x
-// 32003 FP32 55 us (38 us of HBM time), 32004 48 us.  Few rows by latency: 64 x
-// 151936 FP32 20 us (8.7 us), 13 x 4096 11 us, of which the rows kernel before it
-// and the sums behind it are 3 us each.
+// Bound by HBM for long rows: 4096 x 151936 FP32 take 790 us, 93% of the copy rate
+// (734 us with a sixth of the rows masked, which are not read: 92%).  With bf16 on
+// either side by HBM and issue, two exponentials and eight FP32 operations a logit: the
+// same rows FP32 to bf16 767 us, bf16 to FP32 780, bf16 480 (71 to 77%).  Short and
+// unaligned rows by the cluster barrier and the merge of each row and by moving
+// logits to 16 bytes' alignment in shared memory: 1000 x 32003 FP32 66 us (38 us of
+// HBM time), bf16 to FP32 140 us, whose stores on such rows are single words.  Few rows
+// by latency: 64 x 151936 FP32 to bf16 20 us (8.5 us), 13 x 4096 10.5 us, of which the
+// rows kernel before it is 3 us; the loss is summed by the last CTA.
 constexpr int kGroupBytes = 4096;
 constexpr int kMaxWarps = 16;
 constexpr int kMaxV = 262144;

@@ -12,10 +12,10 @@
 //
 // FP32 states (22 to 30 bytes a weight) are bound by HBM: 714 M weights, bf16 with
 // an FP32 master, 3.56 ms with the norm, 6.8 TB/s of the bytes that it asks for.
-// 8-bit states (8 to 16 bytes) by instructions: 714 M bf16 weights 1.51 ms with
-// stochastic rounding, 4.8 TB/s; about 71 instructions a weight issue at 82% of the
+// 8-bit states (8 to 16 bytes) by instructions: 714 M bf16 weights 1.53 ms with
+// stochastic rounding, 4.7 TB/s; about 72 instructions a weight issue at 81% of the
 // rate, of which the two hashes are 14 and the roundings 10.  3.5 M weights 20 us
-// (16 us of HBM time), 300 ragged tensors 24 us: the latency of the norm's partials,
+// (16 us of HBM time), 300 ragged tensors 21 us: the latency of the norm's partials,
 // their total, and a search and a first load per CTA.
 #include <algorithm>
 #include <vector>
@@ -235,11 +235,11 @@ __device__ __forceinline__ float stochastic_any(float y, uint32_t rnd16) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
-// Eight square roots, rounded to nearest: from an approximate reciprocal root y
-// one Newton step on x^2 = v, r = v y + (v - (v y)^2) y / 2, its residual exact by
-// FMA (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990).  Zeros, the smallest values and infinities take sqrtf.
-// Returns whether none is infinite.
+// Eight square roots, rounded to nearest but where two floats all but tie: from an
+// approximate reciprocal root y one Newton step on x^2 = v, r = v y + (v - (v y)^2) y / 2,
+// its residual exact by FMA (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990).  Zeros, the smallest values and infinities
+// take sqrtf.  Returns whether none is infinite.
 __device__ __forceinline__ bool sqrt8(const uint64_t (&v)[4], float (&r)[8]) {
   float f[8], x[8];
   uint64_t y[4];
@@ -394,8 +394,8 @@ __device__ __forceinline__ void adam_math(Kind<PK, GB, E8, SR>& d, const AdamArg
   const bool finite = sqrt8(v, rf);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // (rate m) / (r rbc2 + eps), rounded to nearest by one correction of the
-    // quotient with its exact remainder (Markstein, as above)
+    // (rate m) / (r rbc2 + eps), rounded to nearest as the roots are, by one correction
+    // of the quotient with its exact remainder (Markstein, as above)
     float d[2], q[2], n[2];
     unpack2(mul2(pack2(rf[2 * i], rf[2 * i + 1]), pack2(s.rbc2, s.rbc2)), d[0], d[1]);
     const uint64_t num = mul2(pack2(ts.rate, ts.rate), m[i]);

@@ -39,8 +39,16 @@ class AdamW:
 
     ``step()`` runs on the current stream.  Attributes: ``norm`` float32 [4]
     (gradient norm and clip coefficient of the last step; the rest is the kernel's), ``steps`` int32 [2]
-    (steps taken; the second value is the kernel's own).  A step whose
-    gradient norm is not finite changes nothing.
+    (steps taken; the second value is the kernel's own).  With a max_norm, a step
+    whose gradient norm is not finite changes nothing; without one nothing looks for
+    NaN and infinite gradients, and their weights become NaN.
+
+    The norm is that of the gradients given here, on this process.  Where ranks
+    hold different weights besides replicated ones (experts spread over ranks),
+    ``step()`` with a max_norm would scale the replicated ones differently on each:
+    take ``biv.biv_grad_norm`` on ``table``, reduce ``norm`` over the ranks (the root
+    of the sum of squares, a replicated weight's counted once) and its coefficient
+    with it, then ``biv.biv_adamw(desc)``.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], master=None,
