@@ -1372,6 +1372,7 @@ biv_status validate(const biv_gemm_desc* d) {
   BIV_REQUIRE(d->M >= 0 && d->N > 0 && d->K > 0, "gemm: bad sizes M=%d N=%d K=%d", d->M, d->N, d->K);
   BIV_REQUIRE(d->M <= 65535 * 64 && d->N < (1 << 24) && d->K < (1 << 24), "gemm: size too large");
   BIV_REQUIRE(d->mode == BIV_MODE_INVARIANT || d->mode == BIV_MODE_FAST, "gemm: bad mode");
+  BIV_REQUIRE(d->b_early == 0 || d->b_early == 1, "gemm: b_early is 0 or 1");
   const bool bf = d->a_dtype == BIV_BF16 && d->b_dtype == BIV_BF16;
   const bool f8 = d->a_dtype == BIV_E4M3 && d->b_dtype == BIV_E4M3;
   if (!bf && !f8) return set_error(BIV_ERR_UNSUPPORTED, "gemm: A/B dtypes must both be bf16 or both e4m3");

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kSmallRows / 4) policy_small_kernel(
 //   2^20 in 16 18.9 / 25.8, in 1024 19.0 / 21.8;   2^22 in 64 55 / 79, in 1024 57 / 67
 //   2^24 in 256 239 / 317, in 1024 246 / 293;   2^26 in 1024 959 / 1239
 // so the number of rows sets no limit.  Few long sequences leave most SMs idle: one
-// of 524288 rows 20.4 / 17.0, one of 2^20 36 / 25, four of 2^22 372 / 319.  Many have
+// of 524288 rows 20.4 / 17.0, one of 2^20 36 / 25, four of 2^22 372 / 319 (and so
+// does one that holds nearly all rows, which the host cannot see).  Many have
 // each block of the sums add many counts up: 4096 of 32 rows 12.5 / 11.5, 4096 of 256
 // 23.9 / 23.4 (from 2^21 rows on they would gain too: 61 / 66 for 2^22).  A rollout's
 // bytes are a few us at HBM's rate at most: the launches and the dependent loads of

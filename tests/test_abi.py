@@ -110,3 +110,18 @@ def test_partials_consumers_reject_bad_layouts(lib_path):
         assert st == biv.BIV_ERR_INVALID
         st = lib.biv_silu_mul_partials(C.byref(p), C.c_void_p(0x3000), 1024, 4, 1024, None)
         assert st == biv.BIV_ERR_INVALID
+
+
+def test_gemm_b_early_is_a_flag(lib_path):
+    """A descriptor that was not cleared does not turn the early load of B on."""
+    import ctypes as C
+    from invariant_forward_bitwise_gb300 import biv
+    lib = biv.load(lib_path)
+    d, n = biv.GemmDesc(), C.c_size_t(0)
+    d.M, d.N, d.K = 16, 128, 512
+    d.a_dtype = d.b_dtype = d.c_dtype = biv.BF16
+    d.lda, d.ldb, d.ldc = 512, 512, 128
+    d.A, d.B, d.C = 0x100000, 0x200000, 0x300000   # never dereferenced: no launch here
+    for flag, want in ((0, biv.BIV_OK), (1, biv.BIV_OK), (2, biv.BIV_ERR_INVALID), (-1, biv.BIV_ERR_INVALID)):
+        d.b_early = flag
+        assert lib.biv_gemm_workspace(C.byref(d), C.byref(n)) == want
