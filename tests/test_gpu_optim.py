@@ -584,8 +584,9 @@ def test_nan_and_infinity_stay_visible(O, param, state, rounding, bad):
                 continue
             m, v = f64(got["exp_avg"][i]), f64(got["exp_avg_sq"][i])
             if e8:
-                m, v = m * np.repeat(f64(got["exp_avg_scale"][i]), 128)[:n], v * np.repeat(
-                    f64(got["exp_avg_sq_scale"][i]), 128)[:n]
+                with np.errstate(invalid="ignore"):          # 0 times an infinite scale
+                    m = m * np.repeat(f64(got["exp_avg_scale"][i]), 128)[:n]
+                    v = v * np.repeat(f64(got["exp_avg_sq_scale"][i]), 128)[:n]
                 assert np.all(np.isnan(f64(got["exp_avg"][i])[hit]))
             assert not np.any(np.isfinite(m[hit])) and not np.any(np.isfinite(v[hit]))
             for k in ("exp_avg", "exp_avg_sq"):
