@@ -671,6 +671,84 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
                                   float* lp, float* entropy, void* dz, int64_t ldz, int dz_dtype,
                                   biv_stream_t stream);
 
+/* ------------------------------------------- cross entropy of the LM head --
+ * The trainer's loss and gradient at the LM head without the [T, V] logits ("No
+ * More Train-Inference Mismatch", section "方法细节": the trainer's forward and
+ * backward around the imported ops).  h bf16 [T, K] rows at ldh, W bf16 [V, K]
+ * rows at ldw (16-byte aligned rows, K % 8 == 0), target int32 [T], any V >= 1.
+ *
+ * biv_lm_head_loss: z = h . W^T as in biv_lm_head_logprob,
+ *   lse = logsumexp_v z_v,  lp = z[target] - lse     (lp has biv_lm_head_logprob's bits)
+ *   c_t = weight_t / N (TOKEN_MEAN, N the sum of the counted rows' weights) or weight_t / norm (SUM)
+ *   loss = sum_t c_t (-lp_t + z_coef lse_t^2)
+ * A row whose target is ignore_index or whose weight is 0 does not count: its
+ * lp, lse, dlp and dlse are written as zeros, whatever its h holds; weight NULL:
+ * all weights are 1; without a counted row loss and statistics are zeros.  A
+ * counted row with another target outside [0, V) gives lp = NaN and the device
+ * error code 2.  Outputs: lp, lse float32 [T]; dlp = dloss/dlp = -c and dlse =
+ * dloss/dlse = 2 z_coef c lse float32 [T] (each may be NULL), ready for
+ * biv_lm_head_backward; stats float32 [4]: loss, sum c nll, sum c lse^2, N.
+ * A row's bits depend on the row, W and N only; the sums run in one order fixed
+ * by T.  Workspace: biv_lm_head_loss_workspace bytes, 16-byte aligned,
+ * caller-owned, no initial value; calls that can overlap on the GPU need
+ * separate ones. */
+typedef struct {
+  int T, V, K;
+  const uint16_t* h; int64_t ldh;
+  const uint16_t* W; int64_t ldw;
+  const int32_t* target;
+  const float* weight;       /* [T] or NULL */
+  int ignore_index;          /* usually -100 */
+  float z_coef;              /* in [0, 1000] */
+  int reduce;                /* BIV_LOSS_TOKEN_MEAN or BIV_LOSS_SUM */
+  float norm;                /* SUM only: > 0 */
+  float* lp; float* lse;     /* [T] */
+  float* dlp; float* dlse;   /* [T] or NULL */
+  float* stats;              /* [4] */
+  void* workspace;
+  size_t workspace_bytes;
+} biv_lm_loss_desc;
+biv_status biv_lm_head_loss_workspace(int T, int V, size_t* bytes);
+biv_status biv_lm_head_loss(const biv_lm_loss_desc* desc, biv_stream_t stream);
+
+/* Gradient of any loss of lp and lse (biv_lm_head_loss, or biv_policy_loss's dlp):
+ * with p = exp(h . W^T - lse),
+ *   dz = dlp ([v = target] - p) + dlse p,   dh = dz . W,   dW = dz^T . h (or dW += it).
+ * lse as the forward wrote it; dlse may be NULL.  A row with dlp = dlse = 0 has
+ * no gradient: its dh is written as zeros, and what its h, lse and target hold
+ * does not matter; it costs no products.  A row with another target outside
+ * [0, V) is treated the same and raises the device error code 2.
+ * dh [T, K] rows at lddh, dW [V, K] rows at lddw, each BIV_BF16 or BIV_F32, each
+ * may be NULL; they must not overlap the inputs or each other.  accumulate = 1
+ * adds to dW what it holds (in FP32, one rounding).
+ * The logits are formed again in pieces of at most a few chunks of 8192 columns
+ * and never stored.  dz enters the products as bf16 (for a FP32 gradient as
+ * two bf16 parts); at each row's target what this rounding cuts off is added
+ * back in FP32.  dh is the sum of its chunks' FP32 products in ascending order:
+ * a row's dh depends on the row, V and K only.  dW adds the counted rows in
+ * ascending order.  Every call repeats its bits.
+ * T <= 2^20, V < 2^24, K <= 65536.  Workspace: biv_lm_head_backward_workspace
+ * bytes (the sizes and gradient types of the call; about 2 T (K + 8192) bytes for
+ * large T), 256-byte aligned, caller-owned, no initial value; calls that can
+ * overlap on the GPU need separate ones. */
+typedef struct {
+  int T, V, K;
+  const uint16_t* h; int64_t ldh;
+  const uint16_t* W; int64_t ldw;
+  const int32_t* target;
+  const float* lse;
+  const float* dlp;
+  const float* dlse;         /* [T] or NULL */
+  void* dh; int64_t lddh; int dh_dtype;
+  void* dW; int64_t lddw; int dw_dtype;
+  int accumulate;
+  void* workspace;
+  size_t workspace_bytes;
+} biv_lm_grad_desc;
+biv_status biv_lm_head_backward_workspace(int T, int V, int K, int dh_dtype, int dw_dtype,
+                                          size_t* bytes);
+biv_status biv_lm_head_backward(const biv_lm_grad_desc* desc, biv_stream_t stream);
+
 /* ------------------------------------------------------ optimizer step --
  * AdamW over many tensors at once, writing the model's own weights in
  * place (captured graphs keep their addresses; BF16 weights that the forward

@@ -33,6 +33,8 @@ EXPORTS = [
     "biv_gemm_nvfp4_workspace", "biv_gemm_nvfp4",
     "biv_rmsnorm_backward", "biv_silu_mul_backward", "biv_logprob_backward", "biv_attention_backward",
     "biv_policy_loss_workspace", "biv_policy_loss", "biv_policy_loss_logits",
+    "biv_lm_head_loss_workspace", "biv_lm_head_loss",
+    "biv_lm_head_backward_workspace", "biv_lm_head_backward",
     "biv_opt_plan", "biv_grad_norm_workspace", "biv_grad_norm", "biv_adamw",
 ]
 
@@ -127,6 +129,24 @@ class PolicyDesc(C.Structure):
                 ("stats", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
 
 
+class LmLossDesc(C.Structure):
+    _fields_ = [("T", C.c_int), ("V", C.c_int), ("K", C.c_int),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("W", C.c_void_p), ("ldw", C.c_int64),
+                ("target", C.c_void_p), ("weight", C.c_void_p), ("ignore_index", C.c_int),
+                ("z_coef", C.c_float), ("reduce", C.c_int), ("norm", C.c_float),
+                ("lp", C.c_void_p), ("lse", C.c_void_p), ("dlp", C.c_void_p), ("dlse", C.c_void_p),
+                ("stats", C.c_void_p), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
+class LmGradDesc(C.Structure):
+    _fields_ = [("T", C.c_int), ("V", C.c_int), ("K", C.c_int),
+                ("h", C.c_void_p), ("ldh", C.c_int64), ("W", C.c_void_p), ("ldw", C.c_int64),
+                ("target", C.c_void_p), ("lse", C.c_void_p), ("dlp", C.c_void_p), ("dlse", C.c_void_p),
+                ("dh", C.c_void_p), ("lddh", C.c_int64), ("dh_dtype", C.c_int),
+                ("dW", C.c_void_p), ("lddw", C.c_int64), ("dw_dtype", C.c_int),
+                ("accumulate", C.c_int), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
 class OptTensor(C.Structure):
     _fields_ = [("param", C.c_void_p), ("master", C.c_void_p), ("grad", C.c_void_p),
                 ("m", C.c_void_p), ("v", C.c_void_p),
@@ -197,6 +217,8 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "biv_attention_backward": ([P, P], I),
         "biv_policy_loss_workspace": ([I, I, P], I), "biv_policy_loss": ([P, P, P, P], I),
         "biv_policy_loss_logits": ([P, P, I64, I, P, I, F, P, P, P, I64, I, P], I),
+        "biv_lm_head_loss_workspace": ([I, I, P], I), "biv_lm_head_loss": ([P, P], I),
+        "biv_lm_head_backward_workspace": ([I, I, I, I, I, P], I), "biv_lm_head_backward": ([P, P], I),
         "biv_opt_plan": ([P, I, P, P], I), "biv_grad_norm_workspace": ([I64, P], I),
         "biv_grad_norm": ([P, I, I64, F, P, P, C.c_size_t, P], I), "biv_adamw": ([P, P], I),
     }
@@ -668,6 +690,78 @@ def biv_policy_loss_logits(desc: PolicyDesc, logits, target, lp, entropy, dz=Non
     _check(load().biv_policy_loss_logits(
         C.byref(desc), logits.data_ptr(), ld, zt, target.data_ptr(), V, inv_temp, lp.data_ptr(),
         entropy.data_ptr(), pz, ldz, dt, _stream(stream)), "biv_policy_loss_logits")
+
+
+# -------------------------------------------- cross entropy of the LM head --
+def _head(h, W, target, T, dev):
+    """The sizes and row strides of an LM head's h bf16 [>= T, K] and W bf16 [V, K]."""
+    T = h.size(0) if T is None else T
+    for what, t in (("h", h), ("W", W)):
+        if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.get_device() != dev or \
+                (t.size(1) > 1 and t.stride(1) != 1):
+            raise ValueError(f"{what} must be a bf16 matrix with rows of stride 1 on the current CUDA device")
+    if h.size(1) != W.size(1) or not 0 <= T <= h.size(0):
+        raise ValueError("h [T, K] and W [V, K] do not fit")
+    _rows_ok("target", target, torch.int32, T, dev)
+    V, K = W.shape
+    return T, V, K, (h.stride(0) if h.size(0) > 1 else K), (W.stride(0) if V > 1 else K)
+
+
+def _vector(what, t, T, dev):
+    """The address of a float32 vector of at least T values, or None."""
+    if t is None:
+        return None
+    _rows_ok(what, t, torch.float32, T, dev)
+    return t.data_ptr()
+
+
+def biv_lm_head_loss_workspace(T: int, V: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().biv_lm_head_loss_workspace(T, V, C.byref(n)), "biv_lm_head_loss_workspace")
+    return n.value
+
+
+def biv_lm_head_loss(h, W, target, lp, lse, stats, workspace, weight=None, dlp=None, dlse=None, z_coef=0.0,
+                     reduce=LOSS_TOKEN_MEAN, norm=1.0, ignore_index=-100, T=None, stream=None):
+    """Cross entropy of the head's logits h . W^T with its coefficients dlp, dlse
+    for biv_lm_head_backward (see include/biv.h).  stats float32 [4]; workspace
+    uint8 of biv_lm_head_loss_workspace bytes; T: rows of h (all of them)."""
+    dev = _device()
+    T, V, K, ldh, ldw = _head(h, W, target, T, dev)
+    _rows_ok("stats", stats, torch.float32, 4, dev)
+    _rows_ok("workspace", workspace, torch.uint8, 0, dev)
+    d = LmLossDesc(T, V, K, h.data_ptr(), ldh, W.data_ptr(), ldw, target.data_ptr(),
+                   _vector("weight", weight, T, dev), ignore_index, z_coef, reduce, norm,
+                   _vector("lp", lp, T, dev), _vector("lse", lse, T, dev), _vector("dlp", dlp, T, dev),
+                   _vector("dlse", dlse, T, dev), stats.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _check(load().biv_lm_head_loss(C.byref(d), _stream(stream)), "biv_lm_head_loss")
+
+
+def biv_lm_head_backward_workspace(T: int, V: int, K: int, dh_dtype=torch.bfloat16, dw_dtype=torch.bfloat16) -> int:
+    n = C.c_size_t(0)
+    _check(load().biv_lm_head_backward_workspace(T, V, K, _FLOATS[dh_dtype], _FLOATS[dw_dtype], C.byref(n)),
+           "biv_lm_head_backward_workspace")
+    return n.value
+
+
+def biv_lm_head_backward(h, W, target, lse, dlp, dh, dW, workspace, dlse=None, accumulate=False, T=None,
+                         stream=None):
+    """dh [T, K] and dW [V, K] (float32 or bf16; either may be None) from the
+    coefficients dlp, dlse of a loss of lp and lse; accumulate adds to dW."""
+    dev = _device()
+    T, V, K, ldh, ldw = _head(h, W, target, T, dev)
+    (lddh, ht), (lddw, wt) = (K, BF16), (K, BF16)
+    if dh is not None:
+        lddh, ht = _matrix("dh", dh, T, K, dev)
+    if dW is not None:
+        lddw, wt = _matrix("dW", dW, V, K, dev)
+    _rows_ok("workspace", workspace, torch.uint8, 0, dev)
+    d = LmGradDesc(T, V, K, h.data_ptr(), ldh, W.data_ptr(), ldw, target.data_ptr(),
+                   _vector("lse", lse, T, dev), _vector("dlp", dlp, T, dev), _vector("dlse", dlse, T, dev),
+                   None if dh is None else dh.data_ptr(), lddh, ht,
+                   None if dW is None else dW.data_ptr(), lddw, wt,
+                   int(accumulate), workspace.data_ptr(), workspace.numel())
+    _check(load().biv_lm_head_backward(C.byref(d), _stream(stream)), "biv_lm_head_backward")
 
 
 # ------------------------------------------------------- optimizer step --

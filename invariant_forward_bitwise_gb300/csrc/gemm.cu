@@ -1692,39 +1692,41 @@ extern "C" biv_status biv_lm_head_logprob_workspace(int M, int V, size_t* bytes)
   return BIV_OK;
 }
 
-extern "C" biv_status biv_lm_head_logprob(const uint16_t* h, int64_t ldh, const uint16_t* W,
-                                          int64_t ldw, int M, int V, int K,
-                                          const int32_t* target, int mode, float* lp,
-                                          void* workspace, size_t workspace_bytes,
-                                          biv_stream_t stream) {
-  BIV_REQUIRE(target && lp, "lm_head_logprob: null target or lp");
-  BIV_REQUIRE(V % 4 == 0, "lm_head_logprob: V=%d must be a multiple of 4", V);
+namespace biv {
+
+// The fused head's GEMM: lse[row * ng + g] = (max, sum exp(z - max)) of columns
+// [128 g, 128 g + 128), zt[row] = the logit at target[row] (unset where the target
+// is outside [0, V)); both in the workspace.
+biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, const uint16_t* W,
+                          int64_t ldw, int M, int V, int K, const int32_t* target, int mode,
+                          void* workspace, size_t workspace_bytes, const float2** lse,
+                          const float** zt, int* ngroups, biv_stream_t stream) {
   biv_gemm_desc d;
   memset(&d, 0, sizeof(d));
   d.M = M; d.N = V; d.K = K;
   d.a_dtype = BIV_BF16; d.b_dtype = BIV_BF16; d.c_dtype = BIV_F32;
   d.A = h; d.lda = ldh; d.B = W; d.ldb = ldw;
-  d.C = lp; d.ldc = V;   // C is not written; validate() wants a non-null target
+  // (C is not written; validate() wants a non-null pointer)
+  d.C = const_cast<int32_t*>(target); d.ldc = V;
   d.mode = mode;
   biv_status st = validate(&d);
   if (st != BIV_OK) return st;
-  if (M == 0) return BIV_OK;
   int ng = 0;
   const size_t need = lse_bytes(M, V, &ng);
   if (!workspace || workspace_bytes < need)
-    return set_error(BIV_ERR_WORKSPACE, "lm_head_logprob: workspace of %zu bytes needed", need);
+    return set_error(BIV_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", what, need);
   if (!aligned16(workspace))
-    return set_error(BIV_ERR_INVALID, "lm_head_logprob: workspace must be 16-byte aligned");
+    return set_error(BIV_ERR_INVALID, "%s: workspace must be 16-byte aligned", what);
   const Plan p = plan_lse(d);
   CUtensorMap ta, tb;
   if (!make_bf16_maps(&ta, &tb, h, ldh, M, W, ldw, V, K, p))
-    return set_error(BIV_ERR_CUDA, "lm_head_logprob: tensor map encoding failed");
+    return set_error(BIV_ERR_CUDA, "%s: tensor map encoding failed", what);
   auto kern = gemm_bf16_kernel<kWideN, true, false, true>;
   static bool attr = false;
   if (!attr) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(kSmemBudget)) != cudaSuccess)
-      return set_error(BIV_ERR_CUDA, "lm_head_logprob: cannot set shared memory size");
+      return set_error(BIV_ERR_CUDA, "%s: cannot set shared memory size", what);
     attr = true;
   }
   GemmArgs a;
@@ -1738,13 +1740,41 @@ extern "C" biv_status biv_lm_head_logprob(const uint16_t* h, int64_t ldh, const 
   a.ngroups = ng;
   a.err = device_error_word();
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  cudaStream_t s = as_cuda(stream);
   launch_pdl(kern, int(std::min<int64_t>(p.tiles, sms)), kGemmThreads,
-             GemmSmem<kWideN>::bytes(p.stages, p.m_box, true, p.kpb), s, ta, tb, a);
-  st = check_launch("lm_head_logprob gemm");
+             GemmSmem<kWideN>::bytes(p.stages, p.m_box, true, p.kpb), as_cuda(stream), ta, tb, a);
+  *lse = a.lse;
+  *zt = a.zt;
+  *ngroups = ng;
+  return check_launch(what);
+}
+
+}  // namespace biv
+
+extern "C" biv_status biv_lm_head_logprob(const uint16_t* h, int64_t ldh, const uint16_t* W,
+                                          int64_t ldw, int M, int V, int K,
+                                          const int32_t* target, int mode, float* lp,
+                                          void* workspace, size_t workspace_bytes,
+                                          biv_stream_t stream) {
+  BIV_REQUIRE(target && lp, "lm_head_logprob: null target or lp");
+  BIV_REQUIRE(V % 4 == 0, "lm_head_logprob: V=%d must be a multiple of 4", V);
+  if (M == 0) {
+    // the sizes and pointers are checked without rows too
+    biv_gemm_desc d;
+    memset(&d, 0, sizeof(d));
+    d.N = V; d.K = K;
+    d.a_dtype = BIV_BF16; d.b_dtype = BIV_BF16; d.c_dtype = BIV_F32;
+    d.A = h; d.lda = ldh; d.B = W; d.ldb = ldw;
+    d.C = lp; d.ldc = V;
+    d.mode = mode;
+    return validate(&d);
+  }
+  const float2* lse;
+  const float* zt;
+  int ng;
+  biv_status st = lm_head_groups("lm_head_logprob", h, ldh, W, ldw, M, V, K, target, mode, workspace,
+                                 workspace_bytes, &lse, &zt, &ng, stream);
   if (st != BIV_OK) return st;
-  launch_pdl(lse_combine_kernel, (M + kLseWarps - 1) / kLseWarps, kLseWarps * 32, 0, s,
-             static_cast<const float2*>(a.lse), ng, static_cast<const float*>(a.zt), target, M, V,
-             lp, a.err);
+  launch_pdl(lse_combine_kernel, (M + kLseWarps - 1) / kLseWarps, kLseWarps * 32, 0, as_cuda(stream),
+             lse, ng, zt, target, M, V, lp, device_error_word());
   return check_launch("lm_head_logprob combine");
 }
