@@ -14,12 +14,11 @@
 //  - Rows whose coefficients are 0 (prompts, padding, clipped tokens) have no
 //    gradient: the rows that count are gathered first, so that what the others
 //    hold is never multiplied, and no time is spent on them.
-//  - dz is rounded to bf16, the type of the products' other operands: an error
-//    of at most 2^-8 of each term.  The term of a row's own target is usually
-//    the largest by far; what its rounding cut off is added back in FP32 (to dh
-//    by the fold, to dW by the epilogue of the tile that holds the target), so
-//    that only the p terms carry rounding errors.  For FP32 gradients dz is kept
-//    as two bf16 parts, hi + lo, and both are multiplied.
+//  - The term of a row's own target is usually the largest by far.  It stays
+//    out of the matrix products and is added in FP32, to dh by the fold and to
+//    dW by the epilogue of the tile that holds the target.  The p terms enter
+//    the products as bf16, the type of the other operands: an error of at most
+//    2^-8 of each of them; for FP32 gradients as two bf16 parts, hi + lo (2^-16).
 //  - dh is summed over the vocabulary in chunks of kChunk columns, each
 //    accumulated from zero in TMEM in ascending columns, and the chunks added
 //    in ascending order in FP32: a row's dh depends on that row, V and K only.
@@ -41,16 +40,15 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
 namespace {
 
 constexpr int kChunk = 8192;      // vocabulary columns per FP32 partial of dh
-constexpr int kTM = 128;          // tile rows (TMEM lanes)
-constexpr int kTN = 256;          // tile columns
+constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
+constexpr int kTN = 256;          // tile columns: each CTA brings half of B
 constexpr int kTK = 128;          // K elements per stage: two 128-byte panels
-constexpr int kPanel = kTM * 128; // bytes of a 128-row panel of 64 bf16
-constexpr int kABytes = 2 * kPanel;
-constexpr int kBBytes = 4 * kPanel;
-constexpr int kStages = 2;
+constexpr int kPanel = 128 * 128; // bytes of a 128-row panel of 64 bf16
+constexpr int kOperand = 2 * kPanel;   // a CTA's part of A or B in a stage
+constexpr int kStages = 3;
 constexpr int kEpi = 8;
 constexpr int kThreads = 64 + 32 * kEpi;
-constexpr int kSmem = 1024 + kStages * (kABytes + kBBytes) + 256;
+constexpr int kSmem = 1024 + kStages * 2 * kOperand + 256;
 
 // Device-side state of one call, at the head of its workspace.
 struct Rows {
@@ -62,7 +60,7 @@ struct Rows {
   float* lse;         // [cap]
   float* dlp;         // [cap]
   float* cp;          // [cap] dlse - dlp: the factor of p
-  float2* res;        // [cap] what rounding cut off dz at the target: of one part, of two
+  float* dzt;         // [cap] dz at the target
   uint16_t* h;        // [cap][kp] gathered rows, zeros behind them and behind K
   float* acc;         // [slots][cap][ka] chunk partials of dh
   uint16_t* dz;       // [parts][cap][cols]
@@ -96,7 +94,7 @@ Layout layout(int T, int V, int K, bool want_dh, bool f32) {
   l.cols = int(std::min<int64_t>(int64_t(l.per_pass) * kChunk, (int64_t(V) + kTN - 1) / kTN * kTN));
   const size_t sizes[12] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(V) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
-                            size_t(l.cap) * 4, size_t(l.cap) * 8, size_t(l.cap) * l.kp * 2,
+                            size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * l.kp * 2,
                             want_dh ? part * l.slots : 0,
                             size_t(l.parts) * l.cap * l.cols * 2};
   l.bytes = 0;
@@ -118,7 +116,7 @@ Rows rows_of(const Layout& l, void* ws) {
   r.lse = reinterpret_cast<float*>(b + l.off[5]);
   r.dlp = reinterpret_cast<float*>(b + l.off[6]);
   r.cp = reinterpret_cast<float*>(b + l.off[7]);
-  r.res = reinterpret_cast<float2*>(b + l.off[8]);
+  r.dzt = reinterpret_cast<float*>(b + l.off[8]);
   r.h = reinterpret_cast<uint16_t*>(b + l.off[9]);
   r.acc = reinterpret_cast<float*>(b + l.off[10]);
   r.dz = reinterpret_cast<uint16_t*>(b + l.off[11]);
@@ -243,11 +241,10 @@ __global__ void __launch_bounds__(256) gather_kernel(
 
 // ----------------------------------------------------------------- GEMMs --
 struct Maps {
-  CUtensorMap hk;    // gathered h, K-major A of the scores: {64, 128 rows, 2}
-  CUtensorMap hn;    // gathered h, MN-major B of dW: {64, 128 rows, 4}
-  CUtensorMap wk;    // W, K-major B of the scores: {64, 256 rows, 2} ({64, 256} when K % 64)
-  CUtensorMap wn;    // W, MN-major B of dh: {64, 128 rows, 4} ({64, 128} when K % 64)
-  CUtensorMap dz;    // dz, both products' A: {64, 128 rows, 2}
+  // boxes of {64 columns, 128 rows, 2 panels} ({64, 128} of W when K % 64)
+  CUtensorMap h;     // gathered h: K-major A of the scores, MN-major B of dW
+  CUtensorMap w;     // W: K-major B of the scores, MN-major B of dh
+  CUtensorMap dz;    // dz: K-major A of dh, MN-major A of dW
 };
 
 struct Args {
@@ -314,7 +311,7 @@ __device__ __forceinline__ Item item_at(const Args& a, int n, int i) {
     it.m0 = (j / tk) * kTM;
     it.n0 = (j % tk) * kTN;
     it.k0 = 0;
-    it.nk = tm;
+    it.nk = cdiv(n, kTK);
     it.parts = a.parts_w;
     it.slot = 0;
   }
@@ -322,19 +319,28 @@ __device__ __forceinline__ Item item_at(const Args& a, int n, int i) {
 }
 
 // PHASE 0: the scores of a piece and their dz; PHASE 1: dh and dW of it.
+// Persistent pairs of CTAs (clusters of two), 320 threads each: warp 0 = TMA
+// producer, warp 1 = TMEM owner and, in the pair's first CTA, MMA issuer, warps
+// 2..9 = epilogue (lane quarter = warp % 4, column half = (warp - 2) / 4).  A
+// tile is 256 x 256: each CTA loads its 128 rows of A and of B, the first CTA
+// issues cta_group::2 MMAs over both, and each CTA's TMEM gets its 128 rows.
+// full barriers live in the first CTA and count both CTAs' bytes; empty and
+// tfull are signalled in both by multicast commits; both epilogues arrive on
+// the first CTA's tempty.
 template <int PHASE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_grad_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (the offset is the same in both CTAs of a pair)
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kBBytes);
+  uint8_t* sB = smem + kStages * kOperand;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kOperand);
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
   const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -343,17 +349,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(tfull0 + 8 * j, 1);
-      mbar_init(tempty0 + 8 * j, kEpi);
+      mbar_init(tempty0 + 8 * j, 2 * kEpi);
     }
     fence_barrier_init();
   }
   __syncwarp();
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc2(smem_u32(tmem_slot), 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
@@ -365,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = pair; i < items && ok; i += pairs) {
         const Item it = item_at<PHASE>(a, n, i);
         for (int kb = 0; kb < it.nk * it.parts; ++kb) {
           const int s = issued % kStages;
@@ -373,40 +380,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t bar = full0 + 8 * s;
-          const uint32_t da = smem_u32(sA + s * kABytes), db = smem_u32(sB + s * kBBytes);
-          mbar_expect_tx(bar, kABytes + kBBytes);
+          const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
+          const uint32_t da = smem_u32(sA + s * kOperand), db = smem_u32(sB + s * kOperand);
+          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 4 * kOperand);
           const int part = kb / it.nk, k = kb % it.nk;
+          const int m = it.m0 + rank * 128, nn = it.n0 + rank * 128;
           if (PHASE == 0) {
-            tma_load_3d(da, &maps.hk, bar, 0, it.m0, 2 * k);
+            tma2_load_3d(da, &maps.h, bar, 0, m, 2 * k);
             if (a.w3) {
-              tma_load_3d(db, &maps.wk, bar, 0, a.v0 + it.n0, 2 * k);
+              tma2_load_3d(db, &maps.w, bar, 0, a.v0 + nn, 2 * k);
             } else {
               for (int q = 0; q < 2; ++q)
-                tma_load_2d(db + q * 2 * kPanel, &maps.wk, bar, (2 * k + q) * 64, a.v0 + it.n0);
+                tma2_load_2d(db + q * kPanel, &maps.w, bar, (2 * k + q) * 64, a.v0 + nn);
             }
           } else if (it.type == kDh) {
             const int v = it.k0 + k * kTK;
-            tma_load_3d(da, &maps.dz, bar, 0, part * a.cap + it.m0, v / 64);
+            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + m, v / 64);
             if (a.w3) {
-              tma_load_3d(db, &maps.wn, bar, 0, a.v0 + v, it.n0 / 64);
+              tma2_load_3d(db, &maps.w, bar, 0, a.v0 + v, nn / 64);
             } else {
-              for (int q = 0; q < 4; ++q)
-                tma_load_2d(db + q * kPanel, &maps.wn, bar, it.n0 + q * 64, a.v0 + v);
+              for (int q = 0; q < 2; ++q)
+                tma2_load_2d(db + q * kPanel, &maps.w, bar, nn + q * 64, a.v0 + v);
             }
           } else {
-            tma_load_3d(da, &maps.dz, bar, 0, part * a.cap + k * kTK, it.m0 / 64);
-            tma_load_3d(db, &maps.hn, bar, 0, k * kTK, it.n0 / 64);
+            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + k * kTK, m / 64);
+            tma2_load_3d(db, &maps.h, bar, 0, k * kTK, nn / 64);
           }
           ++issued;
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && rank == 0) {
       int st = 0, j = 0;
       bool ok = true;
-      for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+      for (int i = pair; i < items && ok; i += pairs) {
         const Item it = item_at<PHASE>(a, n, i);
         const int nk = it.nk * it.parts;
         if (nk == 0) continue;
@@ -423,23 +431,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * kABytes), b0 = smem_u32(sB + s * kBBytes);
+          const uint32_t a0 = smem_u32(sA + s * kOperand), b0 = smem_u32(sB + s * kOperand);
 #pragma unroll
           for (int kk = 0; kk < kTK / 16; ++kk) {
             // K-major panels hold 64 K elements of a row; MN-major panels 64
             // rows or columns of the output, one K index per 128 bytes
-            const uint32_t ak = a0 + (kk >> 2) * kPanel + (kk & 3) * 32;
-            const uint32_t bk = b0 + (kk >> 2) * 2 * kPanel + (kk & 3) * 32;
+            const uint32_t ko = (kk >> 2) * kPanel + (kk & 3) * 32;
             const uint64_t ad = PHASE == 1 && it.type == kDw
                                     ? sdesc_mn_sw128(a0 + kk * 2048, kPanel, 1024)
-                                    : sdesc_k_sw128(ak);
-            const uint64_t bd =
-                PHASE == 1 ? sdesc_mn_sw128(b0 + kk * 2048, kPanel, 1024) : sdesc_k_sw128(bk);
-            umma_f16(dt, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+                                    : sdesc_k_sw128(a0 + ko);
+            const uint64_t bd = PHASE == 1 ? sdesc_mn_sw128(b0 + kk * 2048, kPanel, 1024)
+                                           : sdesc_k_sw128(b0 + ko);
+            umma2_f16(dt, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
           }
-          umma_commit(empty0 + 8 * s);
+          umma2_commit(empty0 + 8 * s);
         }
-        if (ok) umma_commit(tfull0 + 8 * b);
+        if (ok) umma2_commit(tfull0 + 8 * b);
         ++j;
       }
     }
@@ -447,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, col0 = ((warp - 2) >> 2) * (kTN / 2);
     int j = 0;
     bool ok = true;
-    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
+    for (int i = pair; i < items && ok; i += pairs) {
       const Item it = item_at<PHASE>(a, n, i);
       const int nk = it.nk * it.parts;
       const int b = j & 1;
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t ta = tmem + b * kTN + col0 + (uint32_t(q * 32) << 16);
-      const int row = it.m0 + q * 32 + lane;
+      const int row = it.m0 + rank * 128 + q * 32 + lane;
       if (PHASE == 0) {
         const bool live = row < n;
         const float lse = live ? a.r.lse[row] : 0.f, cp = live ? a.r.cp[row] : 0.f;
@@ -475,13 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x)
             d[x] = live && c + x < a.vn ? cp * expf(__uint_as_float(v[x]) - lse) : 0.f;
           if (tc >= c && tc < c + 32) {
-            const float dlp = a.r.dlp[row];
-            float full = 0.f;
+            float full = a.r.dlp[row];
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (c + x == tc) full = d[x] = d[x] + dlp;
-            const float r1 = full - bf2f(f2bf(full));
-            a.r.res[row] = make_float2(r1, r1 - bf2f(f2bf(r1)));
+              if (c + x == tc) {
+                full += d[x];
+                d[x] = 0.f;
+              }
+            a.r.dzt[row] = full;
           }
           uint32_t w[16];
 #pragma unroll
@@ -531,10 +539,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int c = it.n0 + col0 + g * 32;
           if (!live || c >= a.K) continue;
-          // rows whose target this is: the part of dz that its rounding cut off
+          // the rows whose target this is
           for (int t = first; t >= 0; t = a.r.next[t]) {
-            const float2 rr = a.r.res[t];
-            const float res = a.parts_w == 2 ? rr.y : rr.x;
+            const float dzt = a.r.dzt[t];
             const uint4* hr = reinterpret_cast<const uint4*>(a.r.h + int64_t(t) * a.kp + c);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -543,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 v[8 * x + 2 * y] = __float_as_uint(
-                    fmaf(res, __uint_as_float(uw[y] << 16), __uint_as_float(v[8 * x + 2 * y])));
+                    fmaf(dzt, __uint_as_float(uw[y] << 16), __uint_as_float(v[8 * x + 2 * y])));
                 v[8 * x + 2 * y + 1] =
-                    __float_as_uint(fmaf(res, __uint_as_float(uw[y] & 0xFFFF0000u),
+                    __float_as_uint(fmaf(dzt, __uint_as_float(uw[y] & 0xFFFF0000u),
                                          __uint_as_float(v[8 * x + 2 * y + 1])));
               }
             }
@@ -592,34 +599,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nk > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty0 + 8 * b);
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
         ++j;
       }
     }
   }
-  // the producer's copies have landed before the CTA exits
-  if (warp == 0 && lane == 0) {
+  // the pair's copies have landed, and its last remote arrivals, before it exits
+  if (warp == 0 && lane == 0 && rank == 0) {
     for (int i = max(0, issued - kStages); i < issued; ++i)
       mbar_wait(full0 + 8 * (i % kStages), (i / kStages) & 1, a.err, 100000000ull);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  __syncwarp();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
-// dh of the counted rows: the chunk partials in ascending order, then what the
-// rounding of dz cut off at the target.  One CTA per row.
+// dh of the counted rows: the chunk partials in ascending order, then the
+// target's term.  One CTA per row.
 __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __restrict__ W,
                                                       int64_t ldw, int K, int ka, int cap,
-                                                      int slots, int parts, void* dh, int64_t lddh,
-                                                      int f32) {
+                                                      int slots, void* dh, int64_t lddh, int f32) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x;
   if (i >= *r.n) return;
   const int64_t t = r.idx[i];
-  const float2 rr = r.res[i];
-  const float res = parts == 2 ? rr.y : rr.x;
+  const float dzt = r.dzt[i];
   const uint16_t* wr = W + int64_t(r.target[i]) * ldw;
   for (int c = threadIdx.x * 4; c < K; c += 1024) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -632,7 +640,7 @@ __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __
       }
     }
     for (int x = 0; x < 4 && c + x < K; ++x) {
-      const float o = fmaf(res, bf2f(wr[c + x]), s[x]);
+      const float o = fmaf(dzt, bf2f(wr[c + x]), s[x]);
       if (f32)
         static_cast<float*>(dh)[t * lddh + c + x] = o;
       else
@@ -641,26 +649,18 @@ __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __
   }
 }
 
-// bf16 rows as {64, rows, K / 64} panels, or plain rows when panels is 0
-bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t ld, int box_rows,
-              int panels) {
+// bf16 rows in boxes of 128, as {64, rows, K / 64} panels (two per box) or as plain rows
+bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t ld, bool panels) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1};
-  if (panels) {
-    const cuuint64_t dims[3] = {64, cuuint64_t(rows), cuuint64_t(K / 64)};
-    const cuuint64_t strides[2] = {cuuint64_t(ld * 2), 128};
-    const cuuint32_t box[3] = {64, cuuint32_t(box_rows), cuuint32_t(panels)};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  }
+  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, 128, 2};
+  const cuuint64_t panel_dims[3] = {64, cuuint64_t(rows), cuuint64_t(K / 64)};
   const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-  const cuuint64_t strides[1] = {cuuint64_t(ld * 2)};
-  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint64_t strides[2] = {cuuint64_t(ld * 2), 128};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, panels ? 3 : 2, const_cast<void*>(base),
+            panels ? panel_dims : dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int PHASE>
@@ -675,8 +675,8 @@ biv_status launch_grad(const Maps& maps, const Args& a, int64_t most_items, cuda
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  launch_pdl(lm_grad_kernel<PHASE>, int(std::max<int64_t>(1, std::min<int64_t>(most_items, sms))),
-             kThreads, kSmem, s, maps, a);
+  const int pairs = int(std::max<int64_t>(1, std::min<int64_t>(most_items, sms / 2)));
+  launch_pdl(lm_grad_kernel<PHASE>, 2 * pairs, kThreads, kSmem, s, maps, a);
   return check_launch("lm_head_backward");
 }
 
@@ -897,11 +897,9 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   a.r = rows_of(l, d->workspace);
   Maps m;
   a.w3 = K % 64 == 0;
-  if (!map_rows(&m.hk, a.r.h, l.kp, l.cap, l.kp, 128, 2) ||
-      !map_rows(&m.hn, a.r.h, l.kp, l.cap, l.kp, 128, 4) ||
-      !map_rows(&m.wk, d->W, K, V, d->ldw, 256, a.w3 ? 2 : 0) ||
-      !map_rows(&m.wn, d->W, K, V, d->ldw, 128, a.w3 ? 4 : 0) ||
-      !map_rows(&m.dz, a.r.dz, l.cols, int64_t(l.cap) * l.parts, l.cols, 128, 2))
+  if (!map_rows(&m.h, a.r.h, l.kp, l.cap, l.kp, true) ||
+      !map_rows(&m.w, d->W, K, V, d->ldw, a.w3 != 0) ||
+      !map_rows(&m.dz, a.r.dz, l.cols, int64_t(l.cap) * l.parts, l.cols, true))
     return set_error(BIV_ERR_CUDA, "lm_head_backward: tensor map encoding failed");
   a.V = V; a.K = K; a.kp = l.kp; a.ka = l.ka; a.cap = l.cap; a.cols = l.cols;
   a.slots = l.slots;
@@ -929,8 +927,8 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
     if ((st = launch_grad<1>(m, a, items, s)) != BIV_OK) return st;
   }
   if (!d->dh) return BIV_OK;
-  launch_pdl(dh_fold_kernel, T, 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap, l.slots, a.parts_h,
-             d->dh, d->lddh, int(d->dh_dtype == BIV_F32));
+  launch_pdl(dh_fold_kernel, T, 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap, l.slots, d->dh,
+              d->lddh, int(d->dh_dtype == BIV_F32));
   return check_launch("lm_head_backward fold");
 }
 
