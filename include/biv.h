@@ -749,6 +749,82 @@ biv_status biv_lm_head_backward_workspace(int T, int V, int K, int dh_dtype, int
                                           size_t* bytes);
 biv_status biv_lm_head_backward(const biv_lm_grad_desc* desc, biv_stream_t stream);
 
+/* ------------------------------------------------- activations in 8 bits --
+ * What a trainer holds between its forward and its backward, in 8 bits ("No
+ * More Train-Inference Mismatch", section "方法细节": fused RMSNorm with residual
+ * and SiLU MLP, and their backward).  A row is quantised as by biv_act_quant_fp8
+ * ("Finish RL Training Faster", section "让训练前向使用推理的数值": one quantisation
+ * rule): per 128 consecutive elements s = amax / 448 (1 when amax is 0), code =
+ * e4m3_rne_satfinite(v / s); codes uint8 rows without gaps, scales float32
+ * [rows, ceil(width / 128)].  16-byte aligned rows; d and I multiples of 16.
+ *
+ * biv_add_rmsnorm_fp8: biv_add_rmsnorm with 8-bit outputs beside or in place of
+ * the bf16 one.  r' = bf16(x + residual) goes to residual_out (NULL: back to
+ * residual; without a residual r' = x and nothing is written), v = r' * inv * w,
+ *   y = bf16(v)        (r', inv and y have biv_add_rmsnorm's bits)
+ *   codes, scales of v (in FP32: one rounding; biv_add_rmsnorm and then
+ *                       biv_act_quant_fp8 round twice), an FP8 GEMM's A
+ *   keep, keep_scales of r' (what biv_act_quant_fp8 of r' writes), inv float32
+ *                      [rows]: what the backward reads
+ * y, codes, keep and inv may be NULL, but not both y and codes; codes and keep
+ * each come with their scales.  y may alias x, residual_out residual.
+ * d <= 8192.  A row's bits depend on the row only.  A row with an infinite or
+ * NaN element gives NaN in that row (its kept codes hold NaN where the element
+ * is not finite, or v / s is not). */
+typedef struct {
+  const uint16_t* x; int64_t x_stride;
+  uint16_t* residual; int64_t r_stride;       /* or NULL */
+  uint16_t* residual_out; int64_t ro_stride;  /* or NULL */
+  const uint16_t* w;
+  uint16_t* y; int64_t y_stride;
+  uint8_t* codes; float* scales;
+  uint8_t* keep; float* keep_scales;
+  float* inv;
+  int rows, d;
+  float eps;
+} biv_norm_fp8_desc;
+biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* desc, biv_stream_t stream);
+
+/* Backward of it from the kept rows: with x = code * s, inv as the forward wrote
+ * it and dy the gradient of v,
+ *   dx = inv*(w*dy) - x*(inv^3*sum(x*w*dy)/d) (+ dres),
+ *   dw float32 [d] = sum over rows of dy*x*inv (added to dw when accumulate is 1).
+ * dres: the gradient that reaches r' past the norm, of dx's type, or NULL.  dy
+ * BIV_F32 or BIV_BF16, dx likewise.  dx may be dres, or dy where types and strides
+ * agree.  dw is summed in an order fixed by rows and d.  Workspace:
+ * biv_rmsnorm_backward_fp8_workspace bytes, 16-byte aligned, no initial value. */
+typedef struct {
+  const uint8_t* keep; const float* keep_scales; const float* inv;
+  const uint16_t* w;
+  const void* dy; int64_t dy_stride; int dy_dtype;
+  const void* dres; int64_t dres_stride;
+  void* dx; int64_t dx_stride; int dx_dtype;
+  float* dw;
+  int accumulate;
+  int rows, d;
+  void* workspace;
+  size_t workspace_bytes;
+} biv_norm_bwd_fp8_desc;
+biv_status biv_rmsnorm_backward_fp8_workspace(int rows, int d, size_t* bytes);
+biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* desc, biv_stream_t stream);
+
+/* biv_silu_mul (y bf16 [rows, I], its bits; NULL: not written) that also keeps
+ * its input gate_up bf16 [rows, 2I] in 8 bits: keep uint8 [rows, 2I], keep_scales
+ * float32 [rows, 2 ceil(I / 128)]; gate and up are quantised apart, each half's
+ * groups start at its first column. */
+biv_status biv_silu_mul_keep_fp8(const uint16_t* gate_up, int64_t gu_stride, uint16_t* y,
+                                 int64_t y_stride, uint8_t* keep, float* keep_scales, int rows, int I,
+                                 biv_stream_t stream);
+
+/* Backward of it from the kept rows (gate, up = code * s): dgate_up rows of 2I as
+ * biv_silu_mul_backward writes them, BIV_F32 or BIV_BF16, from dy BIV_F32 or
+ * BIV_BF16 rows of I; y (bf16 rows of I, or NULL) gets silu(gate) * up of the kept
+ * values, which the gradient of the product behind it reads. */
+biv_status biv_silu_mul_backward_fp8(const uint8_t* keep, const float* keep_scales, const void* dy,
+                                     int64_t dy_stride, int dy_dtype, void* dgate_up,
+                                     int64_t dgate_up_stride, int dgate_up_dtype, uint16_t* y,
+                                     int64_t y_stride, int rows, int I, biv_stream_t stream);
+
 /* ------------------------------------------------------ optimizer step --
  * AdamW over many tensors at once, writing the model's own weights in
  * place (captured graphs keep their addresses; BF16 weights that the forward

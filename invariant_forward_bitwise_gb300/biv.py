@@ -35,6 +35,8 @@ EXPORTS = [
     "biv_policy_loss_workspace", "biv_policy_loss", "biv_policy_loss_logits",
     "biv_lm_head_loss_workspace", "biv_lm_head_loss",
     "biv_lm_head_backward_workspace", "biv_lm_head_backward",
+    "biv_add_rmsnorm_fp8", "biv_rmsnorm_backward_fp8_workspace", "biv_rmsnorm_backward_fp8",
+    "biv_silu_mul_keep_fp8", "biv_silu_mul_backward_fp8",
     "biv_opt_plan", "biv_grad_norm_workspace", "biv_grad_norm", "biv_adamw",
 ]
 
@@ -147,6 +149,25 @@ class LmGradDesc(C.Structure):
                 ("accumulate", C.c_int), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
 
 
+class NormFp8Desc(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_stride", C.c_int64),
+                ("residual", C.c_void_p), ("r_stride", C.c_int64),
+                ("residual_out", C.c_void_p), ("ro_stride", C.c_int64),
+                ("w", C.c_void_p), ("y", C.c_void_p), ("y_stride", C.c_int64),
+                ("codes", C.c_void_p), ("scales", C.c_void_p),
+                ("keep", C.c_void_p), ("keep_scales", C.c_void_p), ("inv", C.c_void_p),
+                ("rows", C.c_int), ("d", C.c_int), ("eps", C.c_float)]
+
+
+class NormBwdFp8Desc(C.Structure):
+    _fields_ = [("keep", C.c_void_p), ("keep_scales", C.c_void_p), ("inv", C.c_void_p), ("w", C.c_void_p),
+                ("dy", C.c_void_p), ("dy_stride", C.c_int64), ("dy_dtype", C.c_int),
+                ("dres", C.c_void_p), ("dres_stride", C.c_int64),
+                ("dx", C.c_void_p), ("dx_stride", C.c_int64), ("dx_dtype", C.c_int),
+                ("dw", C.c_void_p), ("accumulate", C.c_int), ("rows", C.c_int), ("d", C.c_int),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t)]
+
+
 class OptTensor(C.Structure):
     _fields_ = [("param", C.c_void_p), ("master", C.c_void_p), ("grad", C.c_void_p),
                 ("m", C.c_void_p), ("v", C.c_void_p),
@@ -219,6 +240,10 @@ def load(path: str = LIB_PATH) -> C.CDLL:
         "biv_policy_loss_logits": ([P, P, I64, I, P, I, F, P, P, P, I64, I, P], I),
         "biv_lm_head_loss_workspace": ([I, I, P], I), "biv_lm_head_loss": ([P, P], I),
         "biv_lm_head_backward_workspace": ([I, I, I, I, I, P], I), "biv_lm_head_backward": ([P, P], I),
+        "biv_add_rmsnorm_fp8": ([P, P], I),
+        "biv_rmsnorm_backward_fp8_workspace": ([I, I, P], I), "biv_rmsnorm_backward_fp8": ([P, P], I),
+        "biv_silu_mul_keep_fp8": ([P, I64, P, I64, P, P, I, I, P], I),
+        "biv_silu_mul_backward_fp8": ([P, P, P, I64, I, P, I64, I, P, I64, I, I, P], I),
         "biv_opt_plan": ([P, I, P, P], I), "biv_grad_norm_workspace": ([I64, P], I),
         "biv_grad_norm": ([P, I, I64, F, P, P, C.c_size_t, P], I), "biv_adamw": ([P, P], I),
     }
@@ -762,6 +787,110 @@ def biv_lm_head_backward(h, W, target, lse, dlp, dh, dW, workspace, dlse=None, a
                    None if dW is None else dW.data_ptr(), lddw, wt,
                    int(accumulate), workspace.data_ptr(), workspace.numel())
     _check(load().biv_lm_head_backward(C.byref(d), _stream(stream)), "biv_lm_head_backward")
+
+
+# -------------------------------------------------- activations in 8 bits --
+def _bf16_rows(what, t, rows, width, dev):
+    """(address, row stride) of a bf16 matrix of at least `rows` rows, or of None."""
+    if t is None:
+        return None, 0
+    ld, kind = _matrix(what, t, rows, width, dev)
+    if kind != BF16:
+        raise ValueError(f"{what} must be bf16")
+    return t.data_ptr(), ld
+
+
+def _codes_of(what, codes, scales, rows, width, groups, dev):
+    """The addresses of 8-bit rows without gaps and of their scales, or of None."""
+    if (codes is None) != (scales is None):
+        raise ValueError(f"{what} and its scales go together")
+    if codes is None:
+        return None, None
+    _rows_ok(what, codes, torch.uint8, rows * width, dev)
+    _rows_ok(what + "'s scales", scales, torch.float32, rows * groups, dev)
+    return codes.data_ptr(), scales.data_ptr()
+
+
+def biv_add_rmsnorm_fp8(x, residual, w, eps, residual_out=None, y=None, codes=None, scales=None, keep=None,
+                        keep_scales=None, inv=None, stream=None):
+    """RMSNorm of x + residual with 8-bit outputs: y bf16 and/or codes, scales of
+    the normed rows; keep, keep_scales, inv for biv_rmsnorm_backward_fp8 (see
+    include/biv.h).  residual may be None; residual_out None writes it in place."""
+    dev = _device()
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, d = x.shape
+    g = (d + 127) // 128
+    _rows_ok("w", w, torch.bfloat16, d, dev)
+    px, xs = _bf16_rows("x", x, rows, d, dev)
+    pr, rs = _bf16_rows("residual", residual, rows, d, dev)
+    po, ros = _bf16_rows("residual_out", residual_out, rows, d, dev)
+    py, ys = _bf16_rows("y", y, rows, d, dev)
+    pc, ps = _codes_of("codes", codes, scales, rows, d, g, dev)
+    pk, pks = _codes_of("keep", keep, keep_scales, rows, d, g, dev)
+    desc = NormFp8Desc(px, xs, pr, rs, po, ros, w.data_ptr(), py, ys, pc, ps, pk, pks,
+                       _vector("inv", inv, rows, dev), rows, d, eps)
+    _check(load().biv_add_rmsnorm_fp8(C.byref(desc), _stream(stream)), "biv_add_rmsnorm_fp8")
+
+
+def biv_rmsnorm_backward_fp8_workspace(rows: int, d: int) -> int:
+    n = C.c_size_t(0)
+    _check(load().biv_rmsnorm_backward_fp8_workspace(rows, d, C.byref(n)), "biv_rmsnorm_backward_fp8_workspace")
+    return n.value
+
+
+def biv_rmsnorm_backward_fp8(keep, keep_scales, inv, w, dy, dx, dw, workspace, dres=None, accumulate=False,
+                             stream=None):
+    """dx [rows, d] (float32 or bf16) and dw float32 [d] from kept 8-bit rows; dres
+    (of dx's type) is added to dx, accumulate adds to dw."""
+    dev = _device()
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    rows, d = dy.shape
+    pk, ps = _codes_of("keep", keep, keep_scales, rows, d, (d + 127) // 128, dev)
+    dys, yt = _matrix("dy", dy, rows, d, dev)
+    dxs, xt = _matrix("dx", dx, rows, d, dev)
+    pr, rs = None, 0
+    if dres is not None:
+        rs, rt = _matrix("dres", dres, rows, d, dev)
+        if rt != xt:
+            raise ValueError("dres must have dx's type")
+        pr = dres.data_ptr()
+    _rows_ok("w", w, torch.bfloat16, d, dev)
+    _rows_ok("dw", dw, torch.float32, d, dev)
+    _rows_ok("workspace", workspace, torch.uint8, 0, dev)
+    desc = NormBwdFp8Desc(pk, ps, _vector("inv", inv, rows, dev), w.data_ptr(), dy.data_ptr(), dys, yt, pr, rs,
+                          dx.data_ptr(), dxs, xt, dw.data_ptr(), int(accumulate), rows, d, workspace.data_ptr(),
+                          workspace.numel())
+    _check(load().biv_rmsnorm_backward_fp8(C.byref(desc), _stream(stream)), "biv_rmsnorm_backward_fp8")
+
+
+def biv_silu_mul_keep_fp8(gate_up, y, keep, keep_scales, stream=None):
+    """biv_silu_mul (y bf16 [rows, I] or None) that keeps gate_up in 8 bits: keep
+    uint8 [rows, 2I], keep_scales float32 [rows, 2 ceil(I / 128)]."""
+    dev = _device()
+    if gate_up.dim() != 2 or gate_up.size(1) % 2:
+        raise ValueError("gate_up must be a matrix of 2I columns")
+    rows, I = gate_up.size(0), gate_up.size(1) // 2  # noqa: E741
+    pg, gs = _bf16_rows("gate_up", gate_up, rows, 2 * I, dev)
+    py, ys = _bf16_rows("y", y, rows, I, dev)
+    pk, ps = _codes_of("keep", keep, keep_scales, rows, 2 * I, 2 * ((I + 127) // 128), dev)
+    _check(load().biv_silu_mul_keep_fp8(pg, gs, py, ys, pk, ps, rows, I, _stream(stream)), "biv_silu_mul_keep_fp8")
+
+
+def biv_silu_mul_backward_fp8(keep, keep_scales, dy, dgate_up, y=None, stream=None):
+    """dgate_up [rows, 2I] from kept 8-bit rows and dy [rows, I] (each float32 or
+    bf16); y bf16 [rows, I] gets the activation of the kept values."""
+    dev = _device()
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    rows, I = dy.shape  # noqa: E741
+    pk, ps = _codes_of("keep", keep, keep_scales, rows, 2 * I, 2 * ((I + 127) // 128), dev)
+    dys, yt = _matrix("dy", dy, rows, I, dev)
+    dgs, gt = _matrix("dgate_up", dgate_up, rows, 2 * I, dev)
+    py, ys = _bf16_rows("y", y, rows, I, dev)
+    _check(load().biv_silu_mul_backward_fp8(pk, ps, dy.data_ptr(), dys, yt, dgate_up.data_ptr(), dgs, gt, py, ys,
+                                            rows, I, _stream(stream)), "biv_silu_mul_backward_fp8")
 
 
 # ------------------------------------------------------- optimizer step --

@@ -1,0 +1,517 @@
+// Rows in 8 bits: RMSNorm with the residual's addition and 8-bit outputs, and
+// the activations that a trainer keeps in 8 bits with the backward passes that
+// read them.  All rows are quantised alike: per 128 consecutive elements s =
+// amax / 448 (1 when amax is 0), code = e4m3_rne_satfinite(v / s), as
+// biv_act_quant_fp8 does.  Memory-bound: one pass over the inputs, 16-byte
+// accesses, sums in FP32 in an order fixed by the row length.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace biv {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]),
+                    pack_bf2(f[6], f[7]));
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float half_warp_max(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+// two e4m3 codes, the first in the low byte
+__device__ __forceinline__ uint32_t codes2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// the values of four codes
+__device__ __forceinline__ void values4(uint32_t c, float s, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h =
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> (16 * i)), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * i] = v.x * s;
+    f[2 * i + 1] = v.y * s;
+  }
+}
+
+// The codes of a lane's 8 values of a group that 16 lanes share, and its scale.
+// Every lane of the warp calls this; lanes behind the row hold zeros.
+// The quotients are those of an IEEE division: with r the correctly rounded
+// 1 / s, Markstein's correction q + (v - q s) r of q = v r gives them in three
+// operations each where nothing under- or overflows; groups whose scale is far
+// from 1 divide.
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = half_warp_max(amax);
+  s = amax == 0.f ? 1.0f : amax / 448.0f;
+  float q[8];
+  if (s > 0x1p-60f && s < 0x1p60f) {
+    const float r = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q0 = v[i] * r;
+      q[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
+  }
+  return make_uint2(codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16),
+                    codes2(q[4], q[5]) | (codes2(q[6], q[7]) << 16));
+}
+
+// ---------------------------------------------------- add + RMSNorm, FP8 ----
+// A team of W warps per row (W = ceil(d / 256), at most 8), 8 / W rows per CTA.
+// Thread t of a team owns the 8-element chunks t, t + 256, ...: the sums run
+// in biv_add_rmsnorm's order (its warps without chunks add zeros), so inv and
+// y have its bits.  Half a warp holds a 128-element group.
+struct NormArgs {
+  const uint16_t* x; int64_t xs;
+  const uint16_t* res; int64_t rs;
+  uint16_t* res_out; int64_t ros;
+  const uint16_t* w;
+  uint16_t* y; int64_t ys;
+  uint8_t* codes; float* scales;
+  uint8_t* keep; float* keep_scales;
+  float* inv;
+  int rows, d, team;      // warps per row
+  float eps;
+};
+
+template <int CPT>
+__global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float warp_ss[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = 8 / a.team, mine = warp / a.team;        // rows per CTA, this warp's
+  const int64_t row = int64_t(blockIdx.x) * per + mine;
+  const bool on = mine < per && row < a.rows;
+  const int t = (warp - mine * a.team) * 32 + lane;        // thread of the team
+  const int chunks = a.d / 8, groups = (a.d + 127) / 128;
+  float v[CPT][8];
+  uint4 wq[CPT];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * 256;
+    const bool live = on && c < chunks;
+    uint4 xv = make_uint4(0u, 0u, 0u, 0u), rv = xv;
+    wq[i] = xv;
+    if (live) {
+      xv = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.xs) + c);
+      if (a.res) rv = reinterpret_cast<const uint4*>(a.res + row * a.rs)[c];
+      wq[i] = __ldg(reinterpret_cast<const uint4*>(a.w) + c);
+    }
+    unpack8(xv, v[i]);
+    if (a.res) {
+      float r[8];
+      unpack8(rv, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = bf2f(f2bf(v[i][j] + r[j]));
+      if (live) reinterpret_cast<uint4*>(a.res_out + row * a.ros)[c] = pack8(v[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  }
+  ss = warp_sum(ss);
+  float tot = ss;
+  if (a.team > 1) {
+    if (lane == 0) warp_ss[warp] = ss;
+    __syncthreads();
+    tot = 0.f;
+    if (on)
+      for (int i = 0; i < a.team; ++i) tot += warp_ss[mine * a.team + i];
+  }
+  const float inv = 1.0f / sqrtf(tot / float(a.d) + a.eps);
+  if (on && t == 0 && a.inv) a.inv[row] = inv;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = t + i * 256;
+    const bool live = on && c < chunks;
+    float s;
+    if (a.keep) {
+      const uint2 k = quant8(v[i], s);
+      if (live) {
+        reinterpret_cast<uint2*>(a.keep + row * a.d)[c] = k;
+        if ((lane & 15) == 0) a.keep_scales[row * groups + c / 16] = s;
+      }
+    }
+    float wv[8];
+    unpack8(wq[i], wv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = live ? (v[i][j] * inv) * wv[j] : 0.f;
+    if (a.y && live) reinterpret_cast<uint4*>(a.y + row * a.ys)[c] = pack8(v[i]);
+    if (a.codes) {
+      const uint2 k = quant8(v[i], s);
+      if (live) {
+        reinterpret_cast<uint2*>(a.codes + row * a.d)[c] = k;
+        if ((lane & 15) == 0) a.scales[row * groups + c / 16] = s;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------ RMSNorm backward ----
+// A CTA of W warps (W = ceil(d / 1024), at most 8) walks rows r0, r0 + grid, ...;
+// lane l of warp w owns the chunks (w * 4 + i) * 32 + l, i = 0..3, of 8 elements
+// and keeps their dw sums over the CTA's rows, which a second kernel adds up.
+template <bool F32>
+__device__ __forceinline__ void load8(const void* p, int64_t e, float (&f)[8]) {
+  if (F32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + e);
+    const float4 a = s[0], b = s[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + e), f);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, int64_t e, const float (&f)[8]) {
+  if (F32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + e);
+    d[0] = make_float4(f[0], f[1], f[2], f[3]);
+    d[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + e) = pack8(f);
+  }
+}
+
+struct NormBackArgs {
+  const uint8_t* keep; const float* scales; const float* inv;
+  const uint16_t* w;
+  const void* dy; int64_t dys;
+  const void* dres; int64_t drs;
+  void* dx; int64_t dxs;
+  float* parts;          // [grid][d]
+  int rows, d;
+};
+
+constexpr int kBackChunks = 4;
+
+template <bool DYF, bool DXF>
+__global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_constant__ NormBackArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float red[2][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int chunks = a.d / 8, groups = (a.d + 127) / 128;
+  float dw[kBackChunks][8];
+  uint4 wq[kBackChunks];
+#pragma unroll
+  for (int i = 0; i < kBackChunks; ++i) {
+    const int c = (warp * kBackChunks + i) * 32 + lane;
+    wq[i] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+    const float inv = a.inv[row];
+    float x[kBackChunks][8], g[kBackChunks][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kBackChunks; ++i) {
+      const int c = (warp * kBackChunks + i) * 32 + lane;
+      if (c < chunks) {
+        const uint2 k = reinterpret_cast<const uint2*>(a.keep + row * a.d)[c];
+        const float s = a.scales[row * groups + c / 16];
+        load8<DYF>(a.dy, row * a.dys + c * 8, g[i]);
+        values4(k.x, s, x[i]);
+        values4(k.y, s, x[i] + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = g[i][j] = 0.f;
+      }
+      float wv[8];
+      unpack8(wq[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] = fmaf(g[i][j], x[i][j] * inv, dw[i][j]);
+        g[i][j] *= wv[j];
+        sum = fmaf(g[i][j], x[i][j], sum);
+      }
+    }
+    sum = warp_sum(sum);
+    if (warps > 1) {      // (two buffers: one barrier per row)
+      if (lane == 0) red[turn][warp] = sum;
+      __syncthreads();
+      sum = 0.f;
+      for (int i = 0; i < warps; ++i) sum += red[turn][i];
+    }
+    const float corr = inv * inv * inv * (sum / float(a.d));
+#pragma unroll
+    for (int i = 0; i < kBackChunks; ++i) {
+      const int c = (warp * kBackChunks + i) * 32 + lane;
+      if (c >= chunks) continue;
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = inv * g[i][j] - x[i][j] * corr;
+      if (a.dres) {
+        float r[8];
+        load8<DXF>(a.dres, row * a.drs + c * 8, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += r[j];
+      }
+      store8<DXF>(a.dx, row * a.dxs + c * 8, o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kBackChunks; ++i) {
+    const int c = (warp * kBackChunks + i) * 32 + lane;
+    if (c < chunks) store8<true>(a.parts, int64_t(blockIdx.x) * a.d + c * 8, dw[i]);
+  }
+}
+
+// dw[c] = the CTAs' partial sums: 8 warps take partials w, w + 8, ... in order
+// of 32 columns, and their sums are added in warp order
+__global__ void __launch_bounds__(256) dw_sum_kernel(const float* __restrict__ parts, int n, int d,
+                                                     float* __restrict__ dw, int accumulate) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sums[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < d)
+    for (int i = warp; i < n; i += 8) s += parts[int64_t(i) * d + c];
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+    dw[c] = accumulate ? dw[c] + s : s;
+  }
+}
+
+int back_warps(int d) { return (d + 1023) / 1024; }
+// CTAs of the backward: fixed by the row count and length, so that dw's order is
+int back_grid(int rows, int d) { return std::min(rows, 2432 / back_warps(d)); }
+
+// --------------------------------------------------------------- SiLU-mul ----
+// Half a warp per (row, 128-wide group of gate and of up), 8 values a lane.
+__global__ void __launch_bounds__(256) silu_mul_keep_kernel(
+    const uint16_t* __restrict__ gu, int64_t gs, int64_t rows, int I, uint8_t* __restrict__ keep,
+    float* __restrict__ scales, uint16_t* __restrict__ y, int64_t ys) {
+  pdl_wait();
+  pdl_trigger();
+  const int groups = (I + 127) / 128;
+  const int64_t hw = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 4;
+  const int lane = threadIdx.x & 31;
+  const bool on = hw < rows * groups;
+  const int64_t row = on ? hw / groups : 0;
+  const int g = on ? int(hw % groups) : 0, c0 = g * 128 + (lane & 15) * 8;
+  const bool live = on && c0 < I;
+  float gv[8], uv[8];
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  if (live) {
+    a = __ldg(reinterpret_cast<const uint4*>(gu + row * gs + c0));
+    b = __ldg(reinterpret_cast<const uint4*>(gu + row * gs + I + c0));
+  }
+  unpack8(a, gv);
+  unpack8(b, uv);
+  float sg, su;
+  const uint2 kg = quant8(gv, sg), ku = quant8(uv, su);
+  if (!live) return;
+  *reinterpret_cast<uint2*>(keep + row * 2 * I + c0) = kg;
+  *reinterpret_cast<uint2*>(keep + row * 2 * I + I + c0) = ku;
+  if ((lane & 15) == 0) {
+    scales[row * 2 * groups + g] = sg;
+    scales[row * 2 * groups + groups + g] = su;
+  }
+  if (y) {
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = (gv[j] / (1.0f + expf(-gv[j]))) * uv[j];
+    *reinterpret_cast<uint4*>(y + row * ys + c0) = pack8(o);
+  }
+}
+
+template <bool DYF, bool DGF>
+__global__ void __launch_bounds__(256) silu_mul_bwd_fp8_kernel(
+    const uint8_t* __restrict__ keep, const float* __restrict__ scales, const void* __restrict__ dy,
+    int64_t dys, int64_t rows, int I, void* __restrict__ dgu, int64_t dgs, uint16_t* __restrict__ y,
+    int64_t ys) {
+  pdl_wait();
+  pdl_trigger();
+  const int cpr = I / 8, groups = (I + 127) / 128;
+  const int64_t e = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+  if (e >= rows * cpr) return;
+  const int64_t row = e / cpr;
+  const int c = int(e % cpr), c0 = c * 8;
+  const uint2 kg = __ldg(reinterpret_cast<const uint2*>(keep + row * 2 * I + c0));
+  const uint2 ku = __ldg(reinterpret_cast<const uint2*>(keep + row * 2 * I + I + c0));
+  const float sg = __ldg(scales + row * 2 * groups + c / 16);
+  const float su = __ldg(scales + row * 2 * groups + groups + c / 16);
+  float g[8], u[8], d[8], dg[8], du[8], o[8];
+  load8<DYF>(dy, row * dys + c0, d);
+  values4(kg.x, sg, g);
+  values4(kg.y, sg, g + 4);
+  values4(ku.x, su, u);
+  values4(ku.y, su, u + 4);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float s = 1.0f / (1.0f + expf(-g[j]));
+    const float a = g[j] * s;
+    dg[j] = d[j] * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
+    du[j] = d[j] * a;
+    o[j] = a * u[j];
+  }
+  store8<DGF>(dgu, row * dgs + c0, dg);
+  store8<DGF>(dgu, row * dgs + I + c0, du);
+  if (y) *reinterpret_cast<uint4*>(y + row * ys + c0) = pack8(o);
+}
+
+bool row_ok(const void* p, int64_t stride, int64_t width, int size) {
+  return p && aligned16(p) && stride >= width && stride * size % 16 == 0;
+}
+bool float_type(int t) { return t == BIV_F32 || t == BIV_BF16; }
+int size_of(int t) { return t == BIV_F32 ? 4 : 2; }
+
+}  // namespace
+}  // namespace biv
+
+using namespace biv;
+
+extern "C" {
+
+biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* d, biv_stream_t stream) {
+  BIV_REQUIRE(d, "add_rmsnorm_fp8: null descriptor");
+  BIV_REQUIRE(d->rows >= 0 && d->d > 0 && d->d % 16 == 0 && d->d <= 8192,
+              "add_rmsnorm_fp8: rows=%d d=%d (d a multiple of 16, at most 8192)", d->rows, d->d);
+  if (d->rows == 0) return BIV_OK;
+  BIV_REQUIRE(row_ok(d->x, d->x_stride, d->d, 2) && d->w && aligned16(d->w),
+              "add_rmsnorm_fp8: x or w null or misaligned");
+  uint16_t* out = d->residual_out ? d->residual_out : const_cast<uint16_t*>(d->residual);
+  const int64_t os = d->residual_out ? d->ro_stride : d->r_stride;
+  BIV_REQUIRE(!d->residual || (row_ok(d->residual, d->r_stride, d->d, 2) && row_ok(out, os, d->d, 2)),
+              "add_rmsnorm_fp8: residual misaligned");
+  BIV_REQUIRE(d->residual || !d->residual_out, "add_rmsnorm_fp8: residual_out without a residual");
+  BIV_REQUIRE(!d->y || row_ok(d->y, d->y_stride, d->d, 2), "add_rmsnorm_fp8: y misaligned");
+  BIV_REQUIRE((d->codes == nullptr) == (d->scales == nullptr) && aligned16(d->codes),
+              "add_rmsnorm_fp8: codes and scales go together, codes 16-byte aligned");
+  BIV_REQUIRE((d->keep == nullptr) == (d->keep_scales == nullptr) && aligned16(d->keep),
+              "add_rmsnorm_fp8: keep and keep_scales go together, keep 16-byte aligned");
+  BIV_REQUIRE(d->y || d->codes, "add_rmsnorm_fp8: no output");
+  NormArgs a;
+  a.x = d->x; a.xs = d->x_stride;
+  a.res = d->residual; a.rs = d->r_stride;
+  a.res_out = out; a.ros = os;
+  a.w = d->w;
+  a.y = d->y; a.ys = d->y_stride;
+  a.codes = d->codes; a.scales = d->scales;
+  a.keep = d->keep; a.keep_scales = d->keep_scales;
+  a.inv = d->inv;
+  a.rows = d->rows; a.d = d->d; a.eps = d->eps;
+  a.team = std::min(8, (d->d + 255) / 256);
+  const int per = 8 / a.team;
+  const unsigned grid = unsigned((d->rows + per - 1) / per);
+  cudaStream_t s = as_cuda(stream);
+  const int cpt = (d->d / 8 + 255) / 256;
+  launch_pdl(cpt == 1   ? add_rmsnorm_fp8_kernel<1>
+             : cpt == 2 ? add_rmsnorm_fp8_kernel<2>
+             : cpt == 3 ? add_rmsnorm_fp8_kernel<3>
+                        : add_rmsnorm_fp8_kernel<4>,
+             grid, 256, 0, s, a);
+  return check_launch("add_rmsnorm_fp8");
+}
+
+biv_status biv_rmsnorm_backward_fp8_workspace(int rows, int d, size_t* bytes) {
+  BIV_REQUIRE(bytes && rows >= 0 && d > 0 && d <= 8192, "rmsnorm_backward_fp8_workspace: bad arguments");
+  *bytes = size_t(back_grid(rows, d)) * d * 4;
+  return BIV_OK;
+}
+
+biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t stream) {
+  BIV_REQUIRE(d, "rmsnorm_backward_fp8: null descriptor");
+  BIV_REQUIRE(d->rows >= 0 && d->d > 0 && d->d % 16 == 0 && d->d <= 8192,
+              "rmsnorm_backward_fp8: rows=%d d=%d (d a multiple of 16, at most 8192)", d->rows, d->d);
+  BIV_REQUIRE(float_type(d->dy_dtype) && float_type(d->dx_dtype),
+              "rmsnorm_backward_fp8: gradients are bf16 or f32");
+  BIV_REQUIRE(d->accumulate == 0 || d->accumulate == 1, "rmsnorm_backward_fp8: accumulate is 0 or 1");
+  BIV_REQUIRE(d->dw, "rmsnorm_backward_fp8: null dw");
+  cudaStream_t s = as_cuda(stream);
+  if (d->rows > 0) {
+    BIV_REQUIRE(d->keep && aligned16(d->keep) && d->keep_scales && d->inv && d->w && aligned16(d->w),
+                "rmsnorm_backward_fp8: keep, scales, inv or w null or misaligned");
+    BIV_REQUIRE(row_ok(d->dy, d->dy_stride, d->d, size_of(d->dy_dtype)) &&
+                    row_ok(d->dx, d->dx_stride, d->d, size_of(d->dx_dtype)) &&
+                    (!d->dres || row_ok(d->dres, d->dres_stride, d->d, size_of(d->dx_dtype))),
+                "rmsnorm_backward_fp8: dy, dx and dres need 16-byte aligned rows");
+    const size_t need = size_t(back_grid(d->rows, d->d)) * d->d * 4;
+    if (!d->workspace || d->workspace_bytes < need)
+      return set_error(BIV_ERR_WORKSPACE, "rmsnorm_backward_fp8: workspace of %zu bytes needed", need);
+    BIV_REQUIRE(aligned16(d->workspace), "rmsnorm_backward_fp8: workspace must be 16-byte aligned");
+    NormBackArgs a;
+    a.keep = d->keep; a.scales = d->keep_scales; a.inv = d->inv; a.w = d->w;
+    a.dy = d->dy; a.dys = d->dy_stride;
+    a.dres = d->dres; a.drs = d->dres_stride;
+    a.dx = d->dx; a.dxs = d->dx_stride;
+    a.parts = static_cast<float*>(d->workspace);
+    a.rows = d->rows; a.d = d->d;
+    const bool yf = d->dy_dtype == BIV_F32, xf = d->dx_dtype == BIV_F32;
+    launch_pdl(yf ? (xf ? rmsnorm_bwd_fp8_kernel<true, true> : rmsnorm_bwd_fp8_kernel<true, false>)
+                  : (xf ? rmsnorm_bwd_fp8_kernel<false, true> : rmsnorm_bwd_fp8_kernel<false, false>),
+               back_grid(d->rows, d->d), 32 * back_warps(d->d), 0, s, a);
+    biv_status st = check_launch("rmsnorm_backward_fp8");
+    if (st != BIV_OK) return st;
+  }
+  launch_pdl(dw_sum_kernel, (d->d + 31) / 32, 256, 0, s, static_cast<const float*>(d->workspace),
+             d->rows > 0 ? back_grid(d->rows, d->d) : 0, d->d, d->dw, d->accumulate);
+  return check_launch("rmsnorm_backward_fp8 dw");
+}
+
+biv_status biv_silu_mul_keep_fp8(const uint16_t* gate_up, int64_t gu_stride, uint16_t* y,
+                                 int64_t y_stride, uint8_t* keep, float* keep_scales, int rows, int I,
+                                 biv_stream_t stream) {
+  BIV_REQUIRE(rows >= 0 && I > 0 && I % 16 == 0 && I <= (1 << 24), "silu_mul_keep_fp8: rows=%d I=%d (I %% 16)", rows, I);
+  if (rows == 0) return BIV_OK;
+  BIV_REQUIRE(row_ok(gate_up, gu_stride, int64_t(2) * I, 2) && (!y || row_ok(y, y_stride, I, 2)) && keep &&
+                  aligned16(keep) && keep_scales,
+              "silu_mul_keep_fp8: null or misaligned pointer");
+  const int64_t blocks = (int64_t(rows) * ((I + 127) / 128) + 15) / 16;
+  BIV_REQUIRE(blocks < (int64_t(1) << 31), "silu_mul_keep_fp8: too many rows");
+  launch_pdl(silu_mul_keep_kernel, unsigned(blocks), 256, 0, as_cuda(stream), gate_up, gu_stride,
+             int64_t(rows), I, keep, keep_scales, y, y_stride);
+  return check_launch("silu_mul_keep_fp8");
+}
+
+biv_status biv_silu_mul_backward_fp8(const uint8_t* keep, const float* keep_scales, const void* dy,
+                                     int64_t dy_stride, int dy_dtype, void* dgate_up,
+                                     int64_t dgate_up_stride, int dgate_up_dtype, uint16_t* y,
+                                     int64_t y_stride, int rows, int I, biv_stream_t stream) {
+  BIV_REQUIRE(rows >= 0 && I > 0 && I % 16 == 0 && I <= (1 << 24), "silu_mul_backward_fp8: rows=%d I=%d (I %% 16)", rows, I);
+  BIV_REQUIRE(float_type(dy_dtype) && float_type(dgate_up_dtype),
+              "silu_mul_backward_fp8: gradients are bf16 or f32");
+  if (rows == 0) return BIV_OK;
+  BIV_REQUIRE(keep && aligned16(keep) && keep_scales && row_ok(dy, dy_stride, I, size_of(dy_dtype)) &&
+                  row_ok(dgate_up, dgate_up_stride, int64_t(2) * I, size_of(dgate_up_dtype)) &&
+                  (!y || row_ok(y, y_stride, I, 2)),
+              "silu_mul_backward_fp8: null or misaligned pointer");
+  const int64_t blocks = (int64_t(rows) * (I / 8) + 255) / 256;
+  BIV_REQUIRE(blocks < (int64_t(1) << 31), "silu_mul_backward_fp8: too many rows");
+  const bool yf = dy_dtype == BIV_F32, gf = dgate_up_dtype == BIV_F32;
+  launch_pdl(yf ? (gf ? silu_mul_bwd_fp8_kernel<true, true> : silu_mul_bwd_fp8_kernel<true, false>)
+                : (gf ? silu_mul_bwd_fp8_kernel<false, true> : silu_mul_bwd_fp8_kernel<false, false>),
+             unsigned(blocks), 256, 0, as_cuda(stream), keep, keep_scales, dy, dy_stride, int64_t(rows), I,
+             dgate_up, dgate_up_stride, y, y_stride);
+  return check_launch("silu_mul_backward_fp8");
+}
+
+}  // extern "C"
