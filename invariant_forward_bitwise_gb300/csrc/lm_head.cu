@@ -811,7 +811,8 @@ biv_status biv_lm_head_loss_workspace(int T, int V, size_t* bytes) {
 biv_status biv_lm_head_loss(const biv_lm_loss_desc* d, biv_stream_t stream) {
   BIV_REQUIRE(d, "lm_head_loss: null descriptor");
   BIV_REQUIRE(d->T >= 0 && d->V > 0 && d->K > 0, "lm_head_loss: bad sizes T=%d V=%d K=%d", d->T, d->V, d->K);
-  BIV_REQUIRE(d->stats && (d->T == 0 || (d->target && d->lp && d->lse)), "lm_head_loss: null pointer");
+  BIV_REQUIRE(d->stats && (d->T == 0 || (d->h && d->W && d->target && d->lp && d->lse)),
+              "lm_head_loss: null pointer");
   BIV_REQUIRE(d->reduce == BIV_LOSS_TOKEN_MEAN || d->reduce == BIV_LOSS_SUM,
               "lm_head_loss: reduce is TOKEN_MEAN or SUM");
   BIV_REQUIRE(d->reduce != BIV_LOSS_SUM || (d->norm > 0.f && d->norm <= 3e38f), "lm_head_loss: norm must be > 0");
