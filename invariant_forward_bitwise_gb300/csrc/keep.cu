@@ -51,25 +51,28 @@ __device__ __forceinline__ void values4(uint32_t c, float s, float* f) {
 
 // The codes of a lane's 8 values of a group that 16 lanes share, and its scale.
 // Every lane of the warp calls this; lanes behind the row hold zeros.
-// The quotients are those of an IEEE division: with r the correctly rounded
-// 1 / s, Markstein's correction q + (v - q s) r of q = v r gives them in three
-// operations each where nothing under- or overflows; groups whose scale is far
-// from 1 divide.
+// Scale and quotients are those of IEEE divisions: with r the correctly rounded
+// reciprocal of the divisor, Markstein's correction q + (v - q s) r of q = v r
+// gives them in three operations where nothing under- or overflows; groups
+// whose scale is far from 1 divide.
 __device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
   amax = half_warp_max(amax);
-  s = amax == 0.f ? 1.0f : amax / 448.0f;
   float q[8];
-  if (s > 0x1p-60f && s < 0x1p60f) {
-    const float r = 1.0f / s;
+  if (amax > 0x1p-60f && amax < 0x1p60f) {
+    constexpr float r448 = 1.0f / 448.0f;
+    s = amax * r448;
+    s = fmaf(fmaf(-s, 448.0f, amax), r448, s);
+    const float r = __frcp_rn(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q0 = v[i] * r;
       q[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
     }
   } else {
+    s = amax == 0.f ? 1.0f : amax / 448.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = v[i] / s;
   }
@@ -207,47 +210,90 @@ struct NormBackArgs {
 
 constexpr int kBackChunks = 4;
 
-template <bool DYF, bool DXF>
+// 8 values of a row as they lie in memory
+template <bool F32>
+struct Raw8 {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t e) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (F32 ? 4 : 2));
+    v[0] = s[0];
+    if (F32) v[F32 ? 1 : 0] = s[1];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if (F32) {
+      const uint4 a = v[0], b = v[F32 ? 1 : 0];
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+      f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+      f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+      f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+};
+
+// What a lane reads of one row.  It stays as it lies in memory (as floats the
+// row's two passes over it took 181 to 231 registers a thread, 158 us for
+// 16384 x 2048), and the next row's is loaded before this one is reduced.
+template <bool DYF, bool DXF, bool RES>
+struct BackRow {
+  uint2 k[kBackChunks];
+  float s[kBackChunks];
+  Raw8<DYF> dy[kBackChunks];
+  Raw8<DXF> res[RES ? kBackChunks : 1];
+  float inv;
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int c0, int chunks, int groups) {
+    inv = __ldg(a.inv + row);
+#pragma unroll
+    for (int i = 0; i < kBackChunks; ++i) {
+      const int c = c0 + i * 32;
+      if (c < chunks) {
+        k[i] = __ldg(reinterpret_cast<const uint2*>(a.keep + row * a.d) + c);
+        s[i] = __ldg(a.scales + row * groups + c / 16);
+        dy[i].load(a.dy, row * a.dys + c * 8);
+        if (RES) res[RES ? i : 0].load(a.dres, row * a.drs + c * 8);
+      }
+    }
+  }
+};
+
+template <bool DYF, bool DXF, bool RES>
 __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_constant__ NormBackArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int chunks = a.d / 8, groups = (a.d + 127) / 128;
+  const int c0 = warp * kBackChunks * 32 + lane;
   float dw[kBackChunks][8];
   uint4 wq[kBackChunks];
 #pragma unroll
   for (int i = 0; i < kBackChunks; ++i) {
-    const int c = (warp * kBackChunks + i) * 32 + lane;
+    const int c = c0 + i * 32;
     wq[i] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
   }
+  BackRow<DYF, DXF, RES> next;
+  next.load(a, blockIdx.x, c0, chunks, groups);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-    const float inv = a.inv[row];
-    float x[kBackChunks][8], g[kBackChunks][8];
+    const BackRow<DYF, DXF, RES> r = next;
+    if (row + gridDim.x < a.rows) next.load(a, row + gridDim.x, c0, chunks, groups);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kBackChunks; ++i) {
-      const int c = (warp * kBackChunks + i) * 32 + lane;
-      if (c < chunks) {
-        const uint2 k = reinterpret_cast<const uint2*>(a.keep + row * a.d)[c];
-        const float s = a.scales[row * groups + c / 16];
-        load8<DYF>(a.dy, row * a.dys + c * 8, g[i]);
-        values4(k.x, s, x[i]);
-        values4(k.y, s, x[i] + 4);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = g[i][j] = 0.f;
-      }
-      float wv[8];
+      if (c0 + i * 32 >= chunks) continue;
+      float x[8], g[8], wv[8];
+      values4(r.k[i].x, r.s[i], x);
+      values4(r.k[i].y, r.s[i], x + 4);
+      r.dy[i].get(g);
       unpack8(wq[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[i][j] = fmaf(g[i][j], x[i][j] * inv, dw[i][j]);
-        g[i][j] *= wv[j];
-        sum = fmaf(g[i][j], x[i][j], sum);
+        const float gx = g[j] * x[j];
+        sum = fmaf(gx, wv[j], sum);
+        dw[i][j] = fmaf(gx, r.inv, dw[i][j]);
       }
     }
     sum = warp_sum(sum);
@@ -257,28 +303,38 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
       sum = 0.f;
       for (int i = 0; i < warps; ++i) sum += red[turn][i];
     }
-    const float corr = inv * inv * inv * (sum / float(a.d));
+    const float corr = r.inv * r.inv * r.inv * (sum / float(a.d));
 #pragma unroll
     for (int i = 0; i < kBackChunks; ++i) {
-      const int c = (warp * kBackChunks + i) * 32 + lane;
+      const int c = c0 + i * 32;
       if (c >= chunks) continue;
-      float o[8];
+      float x[8], g[8], wv[8], o[8];
+      values4(r.k[i].x, r.s[i], x);
+      values4(r.k[i].y, r.s[i], x + 4);
+      r.dy[i].get(g);
+      unpack8(wq[i], wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = inv * g[i][j] - x[i][j] * corr;
-      if (a.dres) {
-        float r[8];
-        load8<DXF>(a.dres, row * a.drs + c * 8, r);
+      for (int j = 0; j < 8; ++j) o[j] = r.inv * (g[j] * wv[j]) - x[j] * corr;
+      if (RES) {
+        float t[8];
+        r.res[RES ? i : 0].get(t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += r[j];
+        for (int j = 0; j < 8; ++j) o[j] += t[j];
       }
       store8<DXF>(a.dx, row * a.dxs + c * 8, o);
     }
   }
 #pragma unroll
   for (int i = 0; i < kBackChunks; ++i) {
-    const int c = (warp * kBackChunks + i) * 32 + lane;
+    const int c = c0 + i * 32;
     if (c < chunks) store8<true>(a.parts, int64_t(blockIdx.x) * a.d + c * 8, dw[i]);
   }
+}
+
+template <bool DYF, bool DXF>
+void launch_back(const NormBackArgs& a, int grid, int threads, cudaStream_t s) {
+  launch_pdl(a.dres ? rmsnorm_bwd_fp8_kernel<DYF, DXF, true> : rmsnorm_bwd_fp8_kernel<DYF, DXF, false>,
+             grid, threads, 0, s, a);
 }
 
 // dw[c] = the CTAs' partial sums: 8 warps take partials w, w + 8, ... in order
@@ -466,9 +522,11 @@ biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t
     a.parts = static_cast<float*>(d->workspace);
     a.rows = d->rows; a.d = d->d;
     const bool yf = d->dy_dtype == BIV_F32, xf = d->dx_dtype == BIV_F32;
-    launch_pdl(yf ? (xf ? rmsnorm_bwd_fp8_kernel<true, true> : rmsnorm_bwd_fp8_kernel<true, false>)
-                  : (xf ? rmsnorm_bwd_fp8_kernel<false, true> : rmsnorm_bwd_fp8_kernel<false, false>),
-               back_grid(d->rows, d->d), 32 * back_warps(d->d), 0, s, a);
+    const int grid = back_grid(d->rows, d->d), threads = 32 * back_warps(d->d);
+    if (yf)
+      xf ? launch_back<true, true>(a, grid, threads, s) : launch_back<true, false>(a, grid, threads, s);
+    else
+      xf ? launch_back<false, true>(a, grid, threads, s) : launch_back<false, false>(a, grid, threads, s);
     biv_status st = check_launch("rmsnorm_backward_fp8");
     if (st != BIV_OK) return st;
   }
