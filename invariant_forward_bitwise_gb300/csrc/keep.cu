@@ -19,9 +19,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
+// two bf16 in one conversion
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]),
-                    pack_bf2(f[6], f[7]));
+  return make_uint4(bf2(f[0], f[1]), bf2(f[2], f[3]), bf2(f[4], f[5]), bf2(f[6], f[7]));
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -98,8 +102,11 @@ struct NormArgs {
   float eps;
 };
 
+// r' is held as bf16 and its kept codes are written before the row's sum is
+// waited for: fewer registers, so more rows in flight.
 template <int CPT>
-__global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
+    add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ float warp_ss[8];
@@ -109,35 +116,61 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const __grid_const
   const bool on = mine < per && row < a.rows;
   const int t = (warp - mine * a.team) * 32 + lane;        // thread of the team
   const int chunks = a.d / 8, groups = (a.d + 127) / 128;
-  float v[CPT][8];
-  uint4 wq[CPT];
-  float ss = 0.f;
+  uint4 rp[CPT], wq[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * 256;
-    const bool live = on && c < chunks;
-    uint4 xv = make_uint4(0u, 0u, 0u, 0u), rv = xv;
-    wq[i] = xv;
-    if (live) {
-      xv = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.xs) + c);
-      if (a.res) rv = reinterpret_cast<const uint4*>(a.res + row * a.rs)[c];
+    rp[i] = wq[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (on && c < chunks) {
+      rp[i] = __ldg(reinterpret_cast<const uint4*>(a.x + row * a.xs) + c);
       wq[i] = __ldg(reinterpret_cast<const uint4*>(a.w) + c);
     }
-    unpack8(xv, v[i]);
-    if (a.res) {
-      float r[8];
-      unpack8(rv, r);
+  }
+  if (a.res) {
+    uint4 rv[CPT];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = bf2f(f2bf(v[i][j] + r[j]));
-      if (live) reinterpret_cast<uint4*>(a.res_out + row * a.ros)[c] = pack8(v[i]);
+    for (int i = 0; i < CPT; ++i) {
+      const int c = t + i * 256;
+      rv[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (on && c < chunks) rv[i] = reinterpret_cast<const uint4*>(a.res + row * a.rs)[c];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    for (int i = 0; i < CPT; ++i) {
+      const int c = t + i * 256;
+      float x[8], r[8];
+      unpack8(rp[i], x);
+      unpack8(rv[i], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] += r[j];
+      rp[i] = pack8(x);
+      if (on && c < chunks) reinterpret_cast<uint4*>(a.res_out + row * a.ros)[c] = rp[i];
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    float v[8];
+    unpack8(rp[i], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
   }
   ss = warp_sum(ss);
+  if (a.team > 1 && lane == 0) warp_ss[warp] = ss;
+  if (a.keep) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = t + i * 256;
+      float v[8], s;
+      unpack8(rp[i], v);
+      const uint2 k = quant8(v, s);
+      if (on && c < chunks) {
+        reinterpret_cast<uint2*>(a.keep + row * a.d)[c] = k;
+        if ((lane & 15) == 0) a.keep_scales[row * groups + c / 16] = s;
+      }
+    }
+  }
   float tot = ss;
   if (a.team > 1) {
-    if (lane == 0) warp_ss[warp] = ss;
     __syncthreads();
     tot = 0.f;
     if (on)
@@ -149,21 +182,19 @@ __global__ void __launch_bounds__(256) add_rmsnorm_fp8_kernel(const __grid_const
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * 256;
     const bool live = on && c < chunks;
-    float s;
-    if (a.keep) {
-      const uint2 k = quant8(v[i], s);
-      if (live) {
-        reinterpret_cast<uint2*>(a.keep + row * a.d)[c] = k;
-        if ((lane & 15) == 0) a.keep_scales[row * groups + c / 16] = s;
-      }
-    }
-    float wv[8];
+    float v[8], wv[8];
+    unpack8(rp[i], v);
     unpack8(wq[i], wv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = live ? (v[i][j] * inv) * wv[j] : 0.f;
-    if (a.y && live) reinterpret_cast<uint4*>(a.y + row * a.ys)[c] = pack8(v[i]);
+    for (int j = 0; j < 8; ++j) v[j] = (v[j] * inv) * wv[j];
+    if (a.y && live) reinterpret_cast<uint4*>(a.y + row * a.ys)[c] = pack8(v);
     if (a.codes) {
-      const uint2 k = quant8(v[i], s);
+      if (!live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
+      float s;
+      const uint2 k = quant8(v, s);
       if (live) {
         reinterpret_cast<uint2*>(a.codes + row * a.d)[c] = k;
         if ((lane & 15) == 0) a.scales[row * groups + c / 16] = s;
@@ -362,17 +393,36 @@ int back_grid(int rows, int d) { return std::min(rows, 2432 / back_warps(d)); }
 
 // --------------------------------------------------------------- SiLU-mul ----
 // Half a warp per (row, 128-wide group of gate and of up), 8 values a lane.
+// Issue-bound as much as memory-bound: group indexes are 32-bit, and a row is
+// found by a multiplication (with 64-bit divisions biv_silu_mul_keep_fp8 of
+// 8192 x 6144 issued 56 instructions a column and took 94 us).
+
+// n / d for n < 2^31 as (mulhi(n, m) + n) >> s (Granlund and Montgomery)
+struct Divider {
+  uint32_t m, d;
+  int s;
+};
+Divider divider(uint32_t d) {
+  int s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  return {uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1), d, s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) {
+  return (__umulhi(n, v.m) + n) >> v.s;
+}
+
 __global__ void __launch_bounds__(256) silu_mul_keep_kernel(
-    const uint16_t* __restrict__ gu, int64_t gs, int64_t rows, int I, uint8_t* __restrict__ keep,
-    float* __restrict__ scales, uint16_t* __restrict__ y, int64_t ys) {
+    const uint16_t* __restrict__ gu, int64_t gs, uint32_t items, Divider by_groups, int I,
+    uint8_t* __restrict__ keep, float* __restrict__ scales, uint16_t* __restrict__ y, int64_t ys) {
   pdl_wait();
   pdl_trigger();
-  const int groups = (I + 127) / 128;
-  const int64_t hw = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 4;
+  const int groups = int(by_groups.d);
+  const uint32_t hw = blockIdx.x * 16u + (threadIdx.x >> 4);
   const int lane = threadIdx.x & 31;
-  const bool on = hw < rows * groups;
-  const int64_t row = on ? hw / groups : 0;
-  const int g = on ? int(hw % groups) : 0, c0 = g * 128 + (lane & 15) * 8;
+  const bool on = hw < items;
+  const uint32_t r = divide(on ? hw : 0, by_groups);
+  const int64_t row = r;
+  const int g = on ? int(hw - r * by_groups.d) : 0, c0 = g * 128 + (lane & 15) * 8;
   const bool live = on && c0 < I;
   float gv[8], uv[8];
   uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
@@ -402,19 +452,21 @@ __global__ void __launch_bounds__(256) silu_mul_keep_kernel(
 template <bool DYF, bool DGF>
 __global__ void __launch_bounds__(256) silu_mul_bwd_fp8_kernel(
     const uint8_t* __restrict__ keep, const float* __restrict__ scales, const void* __restrict__ dy,
-    int64_t dys, int64_t rows, int I, void* __restrict__ dgu, int64_t dgs, uint16_t* __restrict__ y,
-    int64_t ys) {
+    int64_t dys, uint32_t items, Divider by_groups, int I, void* __restrict__ dgu, int64_t dgs,
+    uint16_t* __restrict__ y, int64_t ys) {
   pdl_wait();
   pdl_trigger();
-  const int cpr = I / 8, groups = (I + 127) / 128;
-  const int64_t e = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
-  if (e >= rows * cpr) return;
-  const int64_t row = e / cpr;
-  const int c = int(e % cpr), c0 = c * 8;
+  const int groups = int(by_groups.d);
+  const uint32_t hw = blockIdx.x * 16u + (threadIdx.x >> 4);
+  if (hw >= items) return;
+  const uint32_t r = divide(hw, by_groups);
+  const int64_t row = r;
+  const int gi = int(hw - r * by_groups.d), c0 = gi * 128 + (threadIdx.x & 15) * 8;
+  if (c0 >= I) return;
   const uint2 kg = __ldg(reinterpret_cast<const uint2*>(keep + row * 2 * I + c0));
   const uint2 ku = __ldg(reinterpret_cast<const uint2*>(keep + row * 2 * I + I + c0));
-  const float sg = __ldg(scales + row * 2 * groups + c / 16);
-  const float su = __ldg(scales + row * 2 * groups + groups + c / 16);
+  const float sg = __ldg(scales + row * 2 * groups + gi);
+  const float su = __ldg(scales + row * 2 * groups + groups + gi);
   float g[8], u[8], d[8], dg[8], du[8], o[8];
   load8<DYF>(dy, row * dys + c0, d);
   values4(kg.x, sg, g);
@@ -543,10 +595,11 @@ biv_status biv_silu_mul_keep_fp8(const uint16_t* gate_up, int64_t gu_stride, uin
   BIV_REQUIRE(row_ok(gate_up, gu_stride, int64_t(2) * I, 2) && (!y || row_ok(y, y_stride, I, 2)) && keep &&
                   aligned16(keep) && keep_scales,
               "silu_mul_keep_fp8: null or misaligned pointer");
-  const int64_t blocks = (int64_t(rows) * ((I + 127) / 128) + 15) / 16;
-  BIV_REQUIRE(blocks < (int64_t(1) << 31), "silu_mul_keep_fp8: too many rows");
-  launch_pdl(silu_mul_keep_kernel, unsigned(blocks), 256, 0, as_cuda(stream), gate_up, gu_stride,
-             int64_t(rows), I, keep, keep_scales, y, y_stride);
+  const Divider groups = divider(uint32_t((I + 127) / 128));
+  const int64_t items = int64_t(rows) * groups.d;
+  BIV_REQUIRE(items < (int64_t(1) << 31), "silu_mul_keep_fp8: 2^31 groups of 128 or more");
+  launch_pdl(silu_mul_keep_kernel, unsigned((items + 15) / 16), 256, 0, as_cuda(stream), gate_up, gu_stride,
+             uint32_t(items), groups, I, keep, keep_scales, y, y_stride);
   return check_launch("silu_mul_keep_fp8");
 }
 
@@ -562,13 +615,14 @@ biv_status biv_silu_mul_backward_fp8(const uint8_t* keep, const float* keep_scal
                   row_ok(dgate_up, dgate_up_stride, int64_t(2) * I, size_of(dgate_up_dtype)) &&
                   (!y || row_ok(y, y_stride, I, 2)),
               "silu_mul_backward_fp8: null or misaligned pointer");
-  const int64_t blocks = (int64_t(rows) * (I / 8) + 255) / 256;
-  BIV_REQUIRE(blocks < (int64_t(1) << 31), "silu_mul_backward_fp8: too many rows");
+  const Divider groups = divider(uint32_t((I + 127) / 128));
+  const int64_t items = int64_t(rows) * groups.d;
+  BIV_REQUIRE(items < (int64_t(1) << 31), "silu_mul_backward_fp8: 2^31 groups of 128 or more");
   const bool yf = dy_dtype == BIV_F32, gf = dgate_up_dtype == BIV_F32;
   launch_pdl(yf ? (gf ? silu_mul_bwd_fp8_kernel<true, true> : silu_mul_bwd_fp8_kernel<true, false>)
                 : (gf ? silu_mul_bwd_fp8_kernel<false, true> : silu_mul_bwd_fp8_kernel<false, false>),
-             unsigned(blocks), 256, 0, as_cuda(stream), keep, keep_scales, dy, dy_stride, int64_t(rows), I,
-             dgate_up, dgate_up_stride, y, y_stride);
+             unsigned((items + 15) / 16), 256, 0, as_cuda(stream), keep, keep_scales, dy, dy_stride,
+             uint32_t(items), groups, I, dgate_up, dgate_up_stride, y, y_stride);
   return check_launch("silu_mul_backward_fp8");
 }
 
