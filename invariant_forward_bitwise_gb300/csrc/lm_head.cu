@@ -7,10 +7,10 @@
 //
 // Backward (biv_lm_head_backward): with z = h.W^T and p = exp(z - lse),
 //   dz = dlp (onehot(target) - p) + dlse p,   dh = dz.W,   dW = dz^T.h.
-// The logits are formed again in pieces of the vocabulary: per piece one GEMM
-// whose epilogue turns its FP32 accumulators into bf16 dz (scores kernel),
-// then both products of that dz (grads kernel), each on tcgen05 with FP32
-// accumulators in TMEM.
+// The logits are formed again in chunks of the vocabulary: per chunk a product
+// whose epilogue turns its FP32 accumulators into bf16 dz, then both products
+// of that dz, all on tcgen05 with FP32 accumulators in TMEM, in one persistent
+// kernel.
 //  - Rows whose coefficients are 0 (prompts, padding, clipped tokens) have no
 //    gradient: the rows that count are gathered first, so that what the others
 //    hold is never multiplied, and no time is spent on them.
@@ -19,10 +19,11 @@
 //    dW by the epilogue of the tile that holds the target.  The p terms enter
 //    the products as bf16, the type of the other operands: an error of at most
 //    2^-8 of each of them; for FP32 gradients as two bf16 parts, hi + lo (2^-16).
-//  - dh is summed over the vocabulary in chunks of kChunk columns, each
-//    accumulated from zero in TMEM in ascending columns, and the chunks added
-//    in ascending order in FP32: a row's dh depends on that row, V and K only.
-//    dW is one accumulation over the counted rows in ascending order.
+//  - dh is summed over the vocabulary in chunks (at most kMaxChunk columns, a
+//    length that follows V alone), each accumulated from zero in TMEM in
+//    ascending columns, and the chunks added in ascending order in FP32: a row's
+//    dh depends on that row, V and K only.  dW is one accumulation over the
+//    counted rows in ascending order.
 #include <algorithm>
 #include <cstring>
 
@@ -39,7 +40,7 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
 
 namespace {
 
-constexpr int kChunk = 8192;      // vocabulary columns per FP32 partial of dh
+constexpr int kMaxChunk = 4096;   // vocabulary columns per FP32 partial of dh, at most
 constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
 constexpr int kTN = 256;          // tile columns: each CTA brings half of B
 constexpr int kTK = 128;          // K elements per stage: two 128-byte panels
@@ -48,57 +49,70 @@ constexpr int kOperand = 2 * kPanel;   // a CTA's part of A or B in a stage
 constexpr int kStages = 3;
 constexpr int kEpi = 8;
 constexpr int kThreads = 64 + 32 * kEpi;
-constexpr int kSmem = 1024 + kStages * 2 * kOperand + 256;
+constexpr int kTickets = 4;       // work items announced ahead
+constexpr int kSmem = 1024 + kStages * 2 * kOperand + 512;
 
-// Device-side state of one call, at the head of its workspace.
+// Device-side state of one call, in its workspace.
 struct Rows {
-  int* n;             // [1] rows that count
-  int* idx;           // [cap] their row numbers, ascending
-  int* target;        // [cap]
-  int* head;          // [V] first counted row with that target, or -1
-  int* next;          // [cap] next counted row with the same target, or -1
-  float* lse;         // [cap]
-  float* dlp;         // [cap]
-  float* cp;          // [cap] dlse - dlp: the factor of p
-  float* dzt;         // [cap] dz at the target
-  uint16_t* h;        // [cap][kp] gathered rows, zeros behind them and behind K
-  float* acc;         // [slots][cap][ka] chunk partials of dh
-  uint16_t* dz;       // [parts][cap][cols]
+  int* n;                   // [1] rows that count
+  int* idx;                 // [cap] their row numbers, ascending
+  int* target;              // [cap]
+  int* skey;                // [cap] targets in ascending order (rows ascending among equals)
+  int* srow;                // [cap] the counted row that each belongs to
+  float* lse;               // [cap]
+  float* dlp;               // [cap]
+  float* cp;                // [cap] dlse - dlp: the factor of p
+  float* dzt;               // [cap] dz at the target
+  uint16_t* h;              // [cap][kp] gathered rows, zeros behind them and behind K
+  float* acc;               // [slots][cap][ka] chunk partials of dh
+  uint16_t* dz;             // [parts][cap][ring * chunk]
+  int* ticket;              // next work item
+  int* sdone;               // [chunks] warps that have written their part of a chunk's dz
+  int* hdone;               // [chunks] warps that are done with its dh
+  int* gdone;               // [chunks] warps that are done with its dh and dW
 };
 
 struct Layout {
   int cap, kp, ka;          // rows, gathered row pitch, partial row pitch
-  int chunks, per_pass;     // chunks of V, chunks per pass
-  int slots;                // 1: the partials are added up as they come
-  int cols;                 // dz row pitch
+  int chunk, chunks;        // columns per chunk, their number
+  int slots;                // chunks: partials side by side; 1: added up as they come
+  int ahead;                // chunks whose scores are formed ahead of their products
+  int ring;                 // chunks of dz held
   int parts;                // bf16 parts of dz
-  size_t off[12], bytes;
+  size_t off[16], bytes;
 };
 
+// dh's partials lie side by side up to this size (few rows: its chunks are then
+// independent of one another, and one kernel adds them up); above, each chunk
+// is added to one array as it comes (4096 x 2048 rows: 34 MB, which L2 holds).
 constexpr size_t kSlotBytes = size_t(192) << 20;
-constexpr size_t kPieceBytes = size_t(96) << 20;
 
-Layout layout(int T, int V, int K, bool want_dh, bool f32) {
+Layout layout(int T, int V, int K, bool f32) {
   Layout l;
   l.cap = (T + kTM - 1) / kTM * kTM;
   l.kp = (K + kTK - 1) / kTK * kTK;
   l.ka = (K + kTN - 1) / kTN * kTN;
-  l.chunks = (V + kChunk - 1) / kChunk;
+  // (by V alone: dh's bits follow it.  8 chunks or more shorten the chain of
+  // stages of a small vocabulary's dh)
+  l.chunk = std::min(kMaxChunk, ((V + 7) / 8 + kTN - 1) / kTN * kTN);
+  l.chunks = (V + l.chunk - 1) / l.chunk;
   l.parts = f32 ? 2 : 1;
   const size_t part = size_t(l.cap) * l.ka * 4;
-  l.slots = want_dh && l.chunks > 1 && part * l.chunks <= kSlotBytes ? l.chunks : 1;
-  const size_t piece = size_t(l.cap) * kChunk * 2 * l.parts;
-  l.per_pass = l.slots > 1 || !want_dh
-                   ? int(std::min<size_t>(l.chunks, std::max<size_t>(1, kPieceBytes / piece)))
-                   : 1;
-  l.cols = int(std::min<int64_t>(int64_t(l.per_pass) * kChunk, (int64_t(V) + kTN - 1) / kTN * kTN));
-  const size_t sizes[12] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(V) * 4,
+  l.slots = part * l.chunks <= kSlotBytes ? l.chunks : 1;
+  // The scores of a chunk have to be done when its products start: enough
+  // chunks ahead for about 48 stages of work in each of 76 pairs of CTAs, the
+  // time of an item and a half.
+  const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = l.chunk / kTN;
+  const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * 2 * tm);
+  l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (48 * 76 + stages - 1) / stages)));
+  l.ring = std::min(l.chunks, 2 * l.ahead + 1);
+  const size_t sizes[16] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * l.kp * 2,
-                            want_dh ? part * l.slots : 0,
-                            size_t(l.parts) * l.cap * l.cols * 2};
+                            part * l.slots, size_t(l.parts) * l.cap * l.ring * l.chunk * 2, 16,
+                            size_t(l.chunks) * 4, size_t(l.chunks) * 4, size_t(l.chunks) * 4};
   l.bytes = 0;
-  for (int i = 0; i < 12; ++i) {
+  for (int i = 0; i < 16; ++i) {
     l.off[i] = l.bytes;
     l.bytes += (sizes[i] + 255) / 256 * 256;
   }
@@ -111,8 +125,8 @@ Rows rows_of(const Layout& l, void* ws) {
   r.n = reinterpret_cast<int*>(b + l.off[0]);
   r.idx = reinterpret_cast<int*>(b + l.off[1]);
   r.target = reinterpret_cast<int*>(b + l.off[2]);
-  r.head = reinterpret_cast<int*>(b + l.off[3]);
-  r.next = reinterpret_cast<int*>(b + l.off[4]);
+  r.skey = reinterpret_cast<int*>(b + l.off[3]);
+  r.srow = reinterpret_cast<int*>(b + l.off[4]);
   r.lse = reinterpret_cast<float*>(b + l.off[5]);
   r.dlp = reinterpret_cast<float*>(b + l.off[6]);
   r.cp = reinterpret_cast<float*>(b + l.off[7]);
@@ -120,118 +134,109 @@ Rows rows_of(const Layout& l, void* ws) {
   r.h = reinterpret_cast<uint16_t*>(b + l.off[9]);
   r.acc = reinterpret_cast<float*>(b + l.off[10]);
   r.dz = reinterpret_cast<uint16_t*>(b + l.off[11]);
+  r.ticket = reinterpret_cast<int*>(b + l.off[12]);
+  r.sdone = reinterpret_cast<int*>(b + l.off[13]);
+  r.hdone = reinterpret_cast<int*>(b + l.off[14]);
+  r.gdone = reinterpret_cast<int*>(b + l.off[15]);
   return r;
 }
 
 // ------------------------------------------------------------- gathering --
-// CTA 0 lists the rows that count; the others set head to -1.
-__global__ void __launch_bounds__(1024) pick_rows_kernel(const int32_t* __restrict__ target,
-                                                         const float* __restrict__ dlp,
-                                                         const float* __restrict__ dlse, int T,
-                                                         int V, Rows r, int* err) {
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x > 0) {
-    for (int v = (blockIdx.x - 1) * 1024 + threadIdx.x; v < V; v += (gridDim.x - 1) * 1024)
-      r.head[v] = -1;
-    return;
-  }
-  __shared__ int warp_n[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int base = 0;
-  for (int t0 = 0; t0 < T; t0 += 1024) {
-    const int t = t0 + threadIdx.x;
-    bool on = false;
-    int tg = 0;
-    if (t < T) {
-      tg = target[t];
-      // (a NaN is not 0: its row counts)
-      on = !(dlp[t] == 0.f) || (dlse && !(dlse[t] == 0.f));
-      if (on && (tg < 0 || tg >= V)) {
-        raise_error(err, kErrBadIndex);
-        on = false;
-      }
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, on);
-    __syncthreads();
-    if (lane == 0) warp_n[warp] = __popc(m);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += warp_n[w];
-      all += warp_n[w];
-    }
-    if (on) {
-      const int i = before + __popc(m & ((1u << lane) - 1));
-      r.idx[i] = t;
-      r.target[i] = tg;
-    }
-    base += all;
-  }
-  if (threadIdx.x == 0) *r.n = base;
+constexpr int kScan = 4096;       // targets in shared memory at a time
+
+__device__ __forceinline__ int warp_add(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-__device__ __forceinline__ void zero_row(void* base, int64_t ld, int f32, int64_t row, int K, int lane) {
-  if (f32) {
-    float* d = static_cast<float*>(base) + row * ld;
-    for (int c = lane; c < K; c += 32) d[c] = 0.f;
-  } else {
-    uint16_t* d = static_cast<uint16_t*>(base) + row * ld;
-    for (int c = lane; c < K; c += 32) d[c] = 0;
-  }
-}
-
-// A warp per row of [0, cap): counted row i is gathered with its scalars and
-// its place in the chain of rows with the same target; up to the next multiple
-// of 128 behind the last one zeros are written.  The warp also clears row i of
-// dh where that row does not count.
+// A warp per row t of [0, cap).  It counts the rows that count before t (t's
+// place i among them), all of them (n), and those that come before it in the
+// order of (target, row); writes row i's scalars, gathers its h, or clears dh
+// of a row that does not count; and writes zeros to gathered row t where t lies
+// between n and the next multiple of 256.
 __global__ void __launch_bounds__(256) gather_kernel(
-    const uint16_t* __restrict__ h, int64_t ldh, const float* __restrict__ lse,
-    const float* __restrict__ dlp, const float* __restrict__ dlse, int T, int K, int kp, int cap,
-    void* dh, int64_t lddh, int dh_f32, Rows r) {
+    const uint16_t* __restrict__ h, int64_t ldh, const int32_t* __restrict__ target,
+    const float* __restrict__ lse, const float* __restrict__ dlp, const float* __restrict__ dlse,
+    int T, int V, int K, int kp, int cap, int chunks, void* dh, int64_t lddh, int dh_f32, Rows r,
+    int* err) {
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (i >= cap) return;
-  const int n = *r.n;
-  if (dh && i < T) {
-    const float c = dlp[i], z = dlse ? dlse[i] : 0.f;
-    bool on = !(c == 0.f) || !(z == 0.f);
-    if (on) {   // a row with a bad target is not in the list
-      int lo = 0, hi = n;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (r.idx[mid] < i) lo = mid + 1; else hi = mid;
-      }
-      on = lo < n && r.idx[lo] == i;
-    }
-    if (!on) zero_row(dh, lddh, dh_f32, i, K, lane);
+  __shared__ __align__(16) int key[kScan];     // the target of a row that counts, or -1
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.x * 8 + warp;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < chunks; i += 256) r.sdone[i] = r.hdone[i] = r.gdone[i] = 0;
+    if (threadIdx.x == 0) *r.ticket = 0;
   }
-  if (i >= (n + kTM - 1) / kTM * kTM) return;
-  uint4* dst = reinterpret_cast<uint4*>(r.h + int64_t(i) * kp);
-  if (i >= n) {
-    for (int c = lane; c < kp / 8; c += 32) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+  int tg = -1;
+  if (t < T) {
+    const int x = target[t];
+    // (a NaN is not 0: its row counts)
+    if (!(dlp[t] == 0.f) || (dlse && !(dlse[t] == 0.f))) {
+      if (x >= 0 && x < V)
+        tg = x;
+      else if (lane == 0)
+        raise_error(err, kErrBadIndex);
+    }
+  }
+  int before = 0, all = 0, lower = 0;
+  for (int j0 = 0; j0 < T; j0 += kScan) {
+    __syncthreads();
+    for (int j = threadIdx.x; j < kScan; j += 256) {
+      const int x = j0 + j;
+      int k = -1;
+      if (x < T && (!(dlp[x] == 0.f) || (dlse && !(dlse[x] == 0.f)))) {
+        k = target[x];
+        if (k < 0 || k >= V) k = -1;
+      }
+      key[j] = k;
+    }
+    __syncthreads();
+    const int m = min(kScan, (T - j0 + 127) / 128 * 128);
+    for (int j = lane * 4; j < m; j += 128) {
+      const int4 k4 = *reinterpret_cast<const int4*>(key + j);
+      const int k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const bool on = k[x] >= 0, first = j0 + j + x < t;
+        all += on;
+        before += on && first;
+        lower += on && (k[x] < tg || (k[x] == tg && first));
+      }
+    }
+  }
+  all = warp_add(all);
+  before = warp_add(before);
+  lower = warp_add(lower);
+  if (t == 0 && lane == 0) *r.n = all;
+  if (t >= cap) return;
+  if (t >= all && t < (all + kTM - 1) / kTM * kTM) {
+    uint4* z = reinterpret_cast<uint4*>(r.h + int64_t(t) * kp);
+    for (int c = lane; c < kp / 8; c += 32) z[c] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (t >= T) return;
+  if (tg < 0) {
+    if (dh) {
+      if (dh_f32) {
+        float* d = static_cast<float*>(dh) + t * lddh;
+        for (int c = lane; c < K; c += 32) d[c] = 0.f;
+      } else {
+        uint16_t* d = static_cast<uint16_t*>(dh) + t * lddh;
+        for (int c = lane; c < K; c += 32) d[c] = 0;
+      }
+    }
     return;
   }
-  const int t = r.idx[i], tg = r.target[i];
-  const uint4* src = reinterpret_cast<const uint4*>(h + int64_t(t) * ldh);
+  const int i = before;
+  const uint4* src = reinterpret_cast<const uint4*>(h + t * ldh);
+  uint4* dst = reinterpret_cast<uint4*>(r.h + int64_t(i) * kp);
   for (int c = lane; c < kp / 8; c += 32)
     dst[c] = c < K / 8 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-  // the chain of rows with this target
-  int nx = -1;
-  for (int j0 = i + 1; j0 < n && nx < 0; j0 += 32) {
-    const int j = j0 + lane;
-    const unsigned m = __ballot_sync(0xffffffffu, j < n && r.target[j] == tg);
-    if (m) nx = j0 + __ffs(m) - 1;
-  }
-  bool first = true;
-  for (int j0 = 0; j0 < i && first; j0 += 32) {
-    const int j = j0 + lane;
-    first = __ballot_sync(0xffffffffu, j < i && r.target[j] == tg) == 0;
-  }
   if (lane == 0) {
-    r.next[i] = nx;
-    if (first) r.head[tg] = i;
+    r.idx[i] = t;
+    r.target[i] = tg;
+    r.skey[lower] = tg;
+    r.srow[lower] = i;
     const float c = dlp[t];
     r.lse[i] = lse[t];
     r.dlp[i] = c;
@@ -249,85 +254,209 @@ struct Maps {
 
 struct Args {
   Rows r;
-  int V, K, kp, ka, cap, cols;
-  int w3;                  // W's maps bring several panels at once (K % 64 == 0)
-  int v0, vn;              // this pass: columns [v0, v0 + vn) of V
-  int c0, nc;              // its chunks
-  int slots;
+  int V, K, kp, ka, cap;
+  int w3;                  // W's maps bring two panels at once (K % 64 == 0)
+  int chunk, chunks, ahead, ring, slots;
   int parts, parts_h, parts_w;
+  const uint16_t* W; int64_t ldw;
+  void* dh; int64_t lddh; int dh_f32, dh_vec;
   void* dW; int64_t lddw; int dw_f32, dw_vec, accumulate;
-  int want_dh;
   int* err;
-};
-
-enum { kScores = 0, kDh = 1, kDw = 2 };
-struct Item {
-  int type, m0, n0;        // tile origin
-  int k0;                  // first K index (dh: column of the piece)
-  int nk;                  // stages of one part
-  int parts;
-  int slot;
 };
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-template <int PHASE>
-__device__ __forceinline__ int item_count(const Args& a, int n) {
-  const int tm = cdiv(n, kTM);
-  if (PHASE == 0) return tm * cdiv(a.vn, kTN);
-  const int tk = cdiv(a.K, kTN);
-  return (a.want_dh ? tm * tk * a.nc : 0) + (a.dW ? cdiv(a.vn, kTM) * tk : 0);
+enum { kScores = 0, kDh = 1, kDw = 2 };
+struct Item {
+  int type, m0, n0;        // tile origin
+  int p;                   // chunk
+  int nk;                  // stages of one part
+  int parts;
+};
+
+// The work items of a call, in the order in which they are handed out: scores
+// S(p) and products G(p) = dh and dW of chunk p as
+//   S(0) .. S(ahead), G(0), S(ahead + 1), G(1), S(ahead + 2), ..., G(chunks - 1)
+// so that a group's inputs are (all but) done when its turn comes.
+struct Plan {
+  int n, tm, tk;
+  int chunks, ahead;
+  int last;                // columns of the last chunk
+  int s, s_last;           // items of S
+  int dh;                  // dh items of G
+  int g, g_last;           // items of G
+  int head, body, total;   // S(0..ahead); those and the pairs G(p), S(p + ahead + 1)
+};
+
+__device__ __forceinline__ Plan plan_of(const Args& a) {
+  Plan p;
+  p.n = *a.r.n;
+  p.tm = cdiv(p.n, kTM);
+  p.tk = cdiv(a.K, kTN);
+  p.chunks = a.chunks;
+  p.ahead = a.ahead;
+  p.last = a.V - (a.chunks - 1) * a.chunk;
+  p.s = p.tm * (a.chunk / kTN);
+  p.s_last = p.tm * cdiv(p.last, kTN);
+  p.dh = a.dh ? p.tm * p.tk : 0;
+  p.g = p.dh + (a.dW ? p.tk * (a.chunk / kTM) : 0);
+  p.g_last = p.dh + (a.dW ? p.tk * cdiv(p.last, kTM) : 0);
+  const int first = min(p.ahead + 1, p.chunks);      // groups of scores at the head
+  p.head = first == p.chunks ? (first - 1) * p.s + p.s_last : first * p.s;
+  const int both = p.chunks - first;                 // pairs of groups
+  p.body = p.head + (both ? both * (p.g + p.s) - p.s + p.s_last : 0);
+  p.total = p.body + (p.chunks - both - 1) * p.g + p.g_last;
+  return p;
 }
 
-// dh's items come first: they are the long ones
-template <int PHASE>
-__device__ __forceinline__ Item item_at(const Args& a, int n, int i) {
-  const int tm = cdiv(n, kTM);
+__device__ __forceinline__ Item item_at(const Args& a, const Plan& p, int i) {
   Item it;
-  if (PHASE == 0) {
+  bool scores = false;
+  int j;                   // the item of its group
+  const int both = p.chunks - min(p.ahead + 1, p.chunks);
+  if (i < p.head) {
+    scores = true;
+    it.p = min(i / p.s, p.chunks - 1);
+    j = i - it.p * p.s;
+  } else if (i < p.body) {
+    const int q = min((i - p.head) / (p.g + p.s), both - 1);
+    j = i - p.head - q * (p.g + p.s);
+    scores = j >= p.g;
+    if (scores) j -= p.g;
+    it.p = scores ? q + p.ahead + 1 : q;
+  } else {
+    const int q = min((i - p.body) / p.g, p.chunks - both - 1);
+    j = i - p.body - q * p.g;
+    it.p = both + q;
+  }
+  const int cols = it.p == p.chunks - 1 ? p.last : a.chunk;
+  if (scores) {
     it.type = kScores;
-    it.m0 = (i % tm) * kTM;
-    it.n0 = (i / tm) * kTN;
-    it.k0 = 0;
+    it.m0 = j % p.tm * kTM;
+    it.n0 = j / p.tm * kTN;
     it.nk = a.kp / kTK;
     it.parts = 1;
-    it.slot = 0;
-    return it;
-  }
-  const int tk = cdiv(a.K, kTN);
-  const int ndh = a.want_dh ? tm * tk * a.nc : 0;
-  if (i < ndh) {
-    const int c = i / (tm * tk), j = i % (tm * tk);
+  } else if (j < p.dh) {       // dh's items come first: they are the long ones
     it.type = kDh;
-    it.m0 = (j / tk) * kTM;
-    it.n0 = (j % tk) * kTN;
-    it.k0 = c * kChunk;
-    it.nk = cdiv(min(kChunk, a.vn - it.k0), kTK);
+    it.m0 = j / p.tk * kTM;
+    it.n0 = j % p.tk * kTN;
+    it.nk = cdiv(cols, kTK);
     it.parts = a.parts_h;
-    it.slot = a.slots > 1 ? a.c0 + c : 0;
   } else {
-    const int j = i - ndh;
+    j -= p.dh;
     it.type = kDw;
-    it.m0 = (j / tk) * kTM;
-    it.n0 = (j % tk) * kTN;
-    it.k0 = 0;
-    it.nk = cdiv(n, kTK);
+    it.m0 = j / p.tk * kTM;
+    it.n0 = j % p.tk * kTN;
+    it.nk = cdiv(p.n, kTK);
     it.parts = a.parts_w;
-    it.slot = 0;
   }
   return it;
 }
 
-// PHASE 0: the scores of a piece and their dz; PHASE 1: dh and dW of it.
-// Persistent pairs of CTAs (clusters of two), 320 threads each: warp 0 = TMA
-// producer, warp 1 = TMEM owner and, in the pair's first CTA, MMA issuer, warps
-// 2..9 = epilogue (lane quarter = warp % 4, column half = (warp - 2) / 4).  A
-// tile is 256 x 256: each CTA loads its 128 rows of A and of B, the first CTA
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_all() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+// a counter of finished warps reaches `want` (bounded wait)
+__device__ bool wait_count(const int* p, int want, int* err) {
+  if (load_acquire(p) >= want) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (load_acquire(p) < want) {
+    __nanosleep(64);
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      raise_error(err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Everything that an item reads has been written, and nothing still reads what
+// it overwrites.  Counters count kEpi warps of two CTAs per item.
+__device__ bool item_ready(const Args& a, const Plan& p, const Item& it) {
+  constexpr int kPer = 2 * kEpi;
+  const bool end = it.p == p.chunks - 1;
+  if (it.type == kScores)      // the ring's chunk of dz is free
+    return it.p < a.ring || wait_count(a.r.gdone + it.p - a.ring, kPer * p.g, a.err);
+  if (!wait_count(a.r.sdone + it.p, kPer * (end ? p.s_last : p.s), a.err)) return false;
+  // partials that are added up as they come: the chunk before is in
+  return !(it.type == kDh && a.slots == 1 && it.p > 0) ||
+         wait_count(a.r.hdone + it.p - 1, kPer * p.dh, a.err);
+}
+
+// 32 columns of a row from registers, bf16 or FP32
+__device__ __forceinline__ void store32(void* base, int64_t off, int f32, bool vec, int left,
+                                        const float (&v)[32]) {
+  if (f32) {
+    float* d = static_cast<float*>(base) + off;
+    if (vec) {
+#pragma unroll
+      for (int x = 0; x < 32; x += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = __float_as_uint(v[x + y]);
+        st_global_v8(d + x, w);
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if (x < left) d[x] = v[x];
+    }
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(base) + off;
+    if (vec) {
+      uint32_t w[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) w[x] = bf2(v[2 * x], v[2 * x + 1]);
+      st_global_v8(d, w);
+      st_global_v8(d + 16, w + 8);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        if (x < left) d[x] = f2bf(v[x]);
+    }
+  }
+}
+
+// v += f * 32 bf16 of a row (16-byte aligned), the first `left` of them
+__device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint16_t* row, int left) {
+  const uint4* r = reinterpret_cast<const uint4*>(row);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (8 * x >= left) break;
+    const uint4 u = __ldg(r + x);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      v[8 * x + 2 * y] = fmaf(f, __uint_as_float(w[y] << 16), v[8 * x + 2 * y]);
+      v[8 * x + 2 * y + 1] = fmaf(f, __uint_as_float(w[y] & 0xFFFF0000u), v[8 * x + 2 * y + 1]);
+    }
+  }
+}
+
+// All three products of a call in one launch: persistent pairs of CTAs
+// (clusters of two), 320 threads each.  Warp 0 = TMA producer and, in the
+// pair's first CTA, the taker of work items; warp 1 = TMEM owner and, in the
+// first CTA, MMA issuer; warps 2..9 = epilogue (lane quarter = warp % 4, column
+// half = (warp - 2) / 4).
+// A tile is 256 x 256: each CTA loads its 128 rows of A and of B, the first CTA
 // issues cta_group::2 MMAs over both, and each CTA's TMEM gets its 128 rows.
 // full barriers live in the first CTA and count both CTAs' bytes; empty and
 // tfull are signalled in both by multicast commits; both epilogues arrive on
 // the first CTA's tempty.
-template <int PHASE>
+// Items are taken from a counter in their order and announced to both CTAs
+// through a ring in shared memory.  An item depends on items before it only,
+// and those are taken by pairs that run: whatever else the GPU runs, the waits
+// end.  (As two launches per chunk, whose last waves left pairs idle and whose
+// W came from HBM twice for few rows: 4.04 ms at 4096 x 151936 x 2048 with a
+// quarter of the rows masked and 0.50 ms at 200 rows.)
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_grad_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -338,9 +467,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kOperand);
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
   const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  const uint32_t kfull0 = smem_u32(bars + 2 * kStages + 4);
+  const uint32_t kempty0 = smem_u32(bars + 2 * kStages + 4 + kTickets);
+  volatile int* ticket = reinterpret_cast<int*>(bars + 2 * kStages + 4 + 2 * kTickets);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4 + 3 * kTickets);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = int(cluster_rank()), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int rank = int(cluster_rank());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -351,7 +483,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(tfull0 + 8 * j, 1);
       mbar_init(tempty0 + 8 * j, 2 * kEpi);
     }
+    for (int j = 0; j < kTickets; ++j) {
+      mbar_init(kfull0 + 8 * j, 1);
+      // readers: both epilogues, the MMA issuer, the second CTA's producer
+      mbar_init(kempty0 + 8 * j, 2 * kEpi + 2);
+    }
     fence_barrier_init();
+    tma_prefetch_desc(&maps.h);
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.dz);
   }
   __syncwarp();
   if (warp == 1) {
@@ -365,15 +505,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();
-  const int n = *a.r.n;
-  const int items = item_count<PHASE>(a, n);
+  const Plan plan = plan_of(a);
+
+  // the seq-th announced item, or -1
+  int seq = 0;
+  auto next_item = [&](bool& ok) -> int {
+    const int k = seq % kTickets;
+    if (!mbar_wait_cluster(kfull0 + 8 * k, (seq / kTickets) & 1, a.err)) {
+      ok = false;
+      return -1;
+    }
+    ++seq;
+    return ticket[k];
+  };
+  auto release_item = [&]() {
+    mbar_arrive_cluster(cluster_addr(kempty0 + 8 * ((seq - 1) % kTickets), 0));
+  };
 
   int issued = 0;
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      for (int i = pair; i < items && ok; i += pairs) {
-        const Item it = item_at<PHASE>(a, n, i);
+      int taken = rank == 0 ? atomicAdd(a.r.ticket, 1) : 0;
+      while (ok) {
+        int i;
+        Item it;
+        if (rank == 0) {
+          i = taken < plan.total ? taken : -1;
+          if (i >= 0) {
+            taken = atomicAdd(a.r.ticket, 1);   // (used after this item)
+            it = item_at(a, plan, i);
+            if (!item_ready(a, plan, it)) {
+              ok = false;
+              i = -1;
+            }
+            fence_proxy_async_all();      // what others wrote is read by TMA
+          }
+          const int k = seq % kTickets;
+          if (seq >= kTickets && !mbar_wait_cluster(kempty0 + 8 * k, ((seq / kTickets) - 1) & 1, a.err))
+            break;
+          for (int c = 0; c < 2; ++c) {
+            store_cluster(cluster_addr(smem_u32(const_cast<int*>(ticket + k)), c), i);
+            mbar_arrive_cluster(cluster_addr(kfull0 + 8 * k, c));
+          }
+          ++seq;
+        } else {
+          i = next_item(ok);
+          if (ok) release_item();
+          if (i >= 0) {
+            it = item_at(a, plan, i);
+            fence_proxy_async_all();
+          }
+        }
+        if (i < 0) break;
+        const int slot = it.p % a.ring * a.chunk, v0 = it.p * a.chunk;
         for (int kb = 0; kb < it.nk * it.parts; ++kb) {
           const int s = issued % kStages;
           if (issued >= kStages && !mbar_wait(empty0 + 8 * s, ((issued / kStages) - 1) & 1, a.err)) {
@@ -385,25 +570,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_expect_tx(full0 + 8 * s, 4 * kOperand);
           const int part = kb / it.nk, k = kb % it.nk;
           const int m = it.m0 + rank * 128, nn = it.n0 + rank * 128;
-          if (PHASE == 0) {
+          if (it.type == kScores) {
             tma2_load_3d(da, &maps.h, bar, 0, m, 2 * k);
             if (a.w3) {
-              tma2_load_3d(db, &maps.w, bar, 0, a.v0 + nn, 2 * k);
+              tma2_load_3d(db, &maps.w, bar, 0, v0 + nn, 2 * k);
             } else {
               for (int q = 0; q < 2; ++q)
-                tma2_load_2d(db + q * kPanel, &maps.w, bar, (2 * k + q) * 64, a.v0 + nn);
+                tma2_load_2d(db + q * kPanel, &maps.w, bar, (2 * k + q) * 64, v0 + nn);
             }
           } else if (it.type == kDh) {
-            const int v = it.k0 + k * kTK;
-            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + m, v / 64);
+            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + m, (slot + k * kTK) / 64);
             if (a.w3) {
-              tma2_load_3d(db, &maps.w, bar, 0, a.v0 + v, nn / 64);
+              tma2_load_3d(db, &maps.w, bar, 0, v0 + k * kTK, nn / 64);
             } else {
               for (int q = 0; q < 2; ++q)
-                tma2_load_2d(db + q * kPanel, &maps.w, bar, nn + q * 64, a.v0 + v);
+                tma2_load_2d(db + q * kPanel, &maps.w, bar, nn + q * 64, v0 + k * kTK);
             }
           } else {
-            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + k * kTK, m / 64);
+            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + k * kTK, (slot + m) / 64);
             tma2_load_3d(db, &maps.h, bar, 0, k * kTK, nn / 64);
           }
           ++issued;
@@ -414,16 +598,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0 && rank == 0) {
       int st = 0, j = 0;
       bool ok = true;
-      for (int i = pair; i < items && ok; i += pairs) {
-        const Item it = item_at<PHASE>(a, n, i);
+      while (ok) {
+        const int i = next_item(ok);
+        if (!ok) break;
+        release_item();
+        if (i < 0) break;
+        const Item it = item_at(a, plan, i);
         const int nk = it.nk * it.parts;
         if (nk == 0) continue;
         const int b = j & 1;
         if (j >= 2 && !mbar_wait(tempty0 + 8 * b, ((j >> 1) - 1) & 1, a.err)) break;
         tc_fence_after();
         const uint32_t dt = tmem + b * kTN;
-        const uint32_t idesc = idesc_mma(1u, kTM, kTN) | (it.type == kDw ? 1u << 15 : 0u) |
-                               (it.type != kScores ? 1u << 16 : 0u);
+        // K-major panels hold 64 K elements of a row; MN-major panels 64 rows or
+        // columns of the output, one K index per 128 bytes
+        const bool a_mn = it.type == kDw, b_mn = it.type != kScores;
+        const uint32_t idesc =
+            idesc_mma(1u, kTM, kTN) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         for (int kb = 0; kb < nk; ++kb, ++st) {
           const int s = st % kStages;
           if (!mbar_wait(full0 + 8 * s, (st / kStages) & 1, a.err)) {
@@ -434,14 +625,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t a0 = smem_u32(sA + s * kOperand), b0 = smem_u32(sB + s * kOperand);
 #pragma unroll
           for (int kk = 0; kk < kTK / 16; ++kk) {
-            // K-major panels hold 64 K elements of a row; MN-major panels 64
-            // rows or columns of the output, one K index per 128 bytes
-            const uint32_t ko = (kk >> 2) * kPanel + (kk & 3) * 32;
-            const uint64_t ad = PHASE == 1 && it.type == kDw
-                                    ? sdesc_mn_sw128(a0 + kk * 2048, kPanel, 1024)
-                                    : sdesc_k_sw128(a0 + ko);
-            const uint64_t bd = PHASE == 1 ? sdesc_mn_sw128(b0 + kk * 2048, kPanel, 1024)
-                                           : sdesc_k_sw128(b0 + ko);
+            const uint32_t ko = (kk >> 2) * kPanel + (kk & 3) * 32, mo = kk * 2048;
+            const uint64_t ad = a_mn ? sdesc_mn_sw128(a0 + mo, kPanel, 1024) : sdesc_k_sw128(a0 + ko);
+            const uint64_t bd = b_mn ? sdesc_mn_sw128(b0 + mo, kPanel, 1024) : sdesc_k_sw128(b0 + ko);
             umma2_f16(dt, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
           }
           umma2_commit(empty0 + 8 * s);
@@ -454,33 +640,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3, col0 = ((warp - 2) >> 2) * (kTN / 2);
     int j = 0;
     bool ok = true;
-    for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_at<PHASE>(a, n, i);
+    while (true) {
+      const int i = next_item(ok);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) release_item();
+      if (i < 0) break;
+      const Item it = item_at(a, plan, i);
       const int nk = it.nk * it.parts;
       const int b = j & 1;
       if (nk > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (j >> 1) & 1, a.err))) {
-          ok = false;
-          break;
-        }
+        if (!__all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (j >> 1) & 1, a.err))) break;
         tc_fence_after();
       }
       const uint32_t ta = tmem + b * kTN + col0 + (uint32_t(q * 32) << 16);
       const int row = it.m0 + rank * 128 + q * 32 + lane;
-      if (PHASE == 0) {
-        const bool live = row < n;
+      const int v0 = it.p * a.chunk, cols = min(a.chunk, a.V - v0);
+      if (it.type == kScores) {
+        const bool live = row < plan.n;
         const float lse = live ? a.r.lse[row] : 0.f, cp = live ? a.r.cp[row] : 0.f;
-        const int tc = live ? a.r.target[row] - a.v0 : -1;   // the target's column of the piece
-        uint16_t* dst = a.r.dz + int64_t(row) * a.cols + it.n0 + col0;
+        const int tc = live ? a.r.target[row] - v0 : -1;     // the target's column of the chunk
+        const int64_t pitch = int64_t(a.ring) * a.chunk;
+        uint16_t* dst = a.r.dz + row * pitch + it.p % a.ring * a.chunk + it.n0 + col0;
         for (int g = 0; g < kTN / 64; ++g) {
           uint32_t v[32];
           tmem_ld32(ta + g * 32, v);
           tmem_ld_wait();
-          const int c = it.n0 + col0 + g * 32;               // column of the piece
+          const int c = it.n0 + col0 + g * 32;               // column of the chunk
           float d[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            d[x] = live && c + x < a.vn ? cp * expf(__uint_as_float(v[x]) - lse) : 0.f;
+            d[x] = live && c + x < cols ? cp * expf(__uint_as_float(v[x]) - lse) : 0.f;
           if (tc >= c && tc < c + 32) {
             float full = a.r.dlp[row];
 #pragma unroll
@@ -491,44 +680,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             a.r.dzt[row] = full;
           }
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) w[x] = pack_bf2(d[2 * x], d[2 * x + 1]);
-          st_global_v8(dst + g * 32, w);
-          st_global_v8(dst + g * 32 + 16, w + 8);
+          store32(dst, g * 32, 0, true, 32, d);
           if (a.parts == 2) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              w[x] = pack_bf2(d[2 * x] - bf2f(f2bf(d[2 * x])), d[2 * x + 1] - bf2f(f2bf(d[2 * x + 1])));
-            uint16_t* lo = dst + int64_t(a.cap) * a.cols + g * 32;
-            st_global_v8(lo, w);
-            st_global_v8(lo + 16, w + 8);
+            for (int x = 0; x < 32; ++x) d[x] -= bf2f(f2bf(d[x]));
+            store32(dst, a.cap * pitch + g * 32, 0, true, 32, d);
           }
         }
       } else if (it.type == kDh) {
-        float* dst = a.r.acc + (int64_t(it.slot) * a.cap + row) * a.ka + it.n0 + col0;
-        const bool add = a.slots == 1 && a.c0 > 0;
+        const bool live = row < plan.n;
+        const bool add = a.slots == 1 && it.p > 0;
+        const bool end = a.slots == 1 && it.p == a.chunks - 1;
+        float* dst = a.r.acc + (int64_t(a.slots > 1 ? it.p : 0) * a.cap + row) * a.ka + it.n0 + col0;
+        float dzt = 0.f;
+        int64_t out = 0;
+        const uint16_t* wr = a.W;
+        if (end && live) {
+          dzt = __ldcg(a.r.dzt + row);
+          out = a.r.idx[row] * a.lddh;
+          wr += a.r.target[row] * a.ldw;
+        }
         for (int g = 0; g < kTN / 64; ++g) {
+          const int c = it.n0 + col0 + g * 32;
           uint32_t v[32];
           tmem_ld32(ta + g * 32, v);
           tmem_ld_wait();
+          if (!live) continue;
+          float f[32];
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            if (add) {
-              const float4 o0 = *reinterpret_cast<const float4*>(dst + g * 32 + x);
-              const float4 o1 = *reinterpret_cast<const float4*>(dst + g * 32 + x + 4);
-              const float o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+          if (add) {
 #pragma unroll
-              for (int y = 0; y < 8; ++y) v[x + y] = __float_as_uint(o[y] + __uint_as_float(v[x + y]));
+            for (int x = 0; x < 32; x += 4) {
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(dst + g * 32 + x));
+              f[x] = o.x + f[x];
+              f[x + 1] = o.y + f[x + 1];
+              f[x + 2] = o.z + f[x + 2];
+              f[x + 3] = o.w + f[x + 3];
             }
-            st_global_v8(dst + g * 32 + x, v + x);
+          }
+          if (!end) {
+            store32(dst, g * 32, 1, true, 32, f);
+          } else if (c < a.K) {
+            add_row32(f, dzt, wr + c, a.K - c);
+            store32(a.dh, out + c, a.dh_f32, a.dh_vec && c + 32 <= a.K, a.K - c, f);
           }
         }
       } else {
-        const int vr = a.v0 + row;                           // row of dW
-        const bool live = row < a.vn;
-        const int first = live && nk > 0 ? a.r.head[vr] : -1;
+        const int vr = v0 + row;                             // row of dW
+        const bool live = row < cols;
+        // the counted rows whose target this is
+        int first = 0;
+        if (live) {
+          int hi = plan.n;
+          while (first < hi) {
+            const int mid = (first + hi) >> 1;
+            if (a.r.skey[mid] < vr) first = mid + 1; else hi = mid;
+          }
+        }
         for (int g = 0; g < kTN / 64; ++g) {
+          const int c = it.n0 + col0 + g * 32;
           uint32_t v[32];
           if (nk > 0) {
             tmem_ld32(ta + g * 32, v);
@@ -537,71 +748,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = 0u;
           }
-          const int c = it.n0 + col0 + g * 32;
           if (!live || c >= a.K) continue;
-          // the rows whose target this is
-          for (int t = first; t >= 0; t = a.r.next[t]) {
-            const float dzt = a.r.dzt[t];
-            const uint4* hr = reinterpret_cast<const uint4*>(a.r.h + int64_t(t) * a.kp + c);
+          float f[32];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint4 u = hr[x];
-              const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                v[8 * x + 2 * y] = __float_as_uint(
-                    fmaf(dzt, __uint_as_float(uw[y] << 16), __uint_as_float(v[8 * x + 2 * y])));
-                v[8 * x + 2 * y + 1] =
-                    __float_as_uint(fmaf(dzt, __uint_as_float(uw[y] & 0xFFFF0000u),
-                                         __uint_as_float(v[8 * x + 2 * y + 1])));
-              }
-            }
+          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+          for (int t = first; t < plan.n && a.r.skey[t] == vr; ++t) {
+            const int r = a.r.srow[t];
+            add_row32(f, __ldcg(a.r.dzt + r), a.r.h + int64_t(r) * a.kp + c, 32);
           }
-          const bool vec = a.dw_vec && c + 32 <= a.K;
-          if (a.dw_f32) {
-            float* dst = static_cast<float*>(a.dW) + int64_t(vr) * a.lddw + c;
-            if (vec) {
-              if (a.accumulate) {
+          const int64_t out = int64_t(vr) * a.lddw + c;
+          if (a.accumulate) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  v[x] = __float_as_uint(dst[x] + __uint_as_float(v[x]));
-              }
-#pragma unroll
-              for (int x = 0; x < 32; x += 8) st_global_v8(dst + x, v + x);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (c + x < a.K)
-                  dst[x] = (a.accumulate ? dst[x] : 0.f) + __uint_as_float(v[x]);
-            }
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(a.dW) + int64_t(vr) * a.lddw + c;
-            if (a.accumulate) {
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (c + x < a.K) v[x] = __float_as_uint(bf2f(dst[x]) + __uint_as_float(v[x]));
-            }
-            if (vec) {
-              uint32_t w[16];
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                w[x] = pack_bf2(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-              st_global_v8(dst, w);
-              st_global_v8(dst + 16, w + 8);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (c + x < a.K) dst[x] = f2bf(__uint_as_float(v[x]));
-            }
+            for (int x = 0; x < 32; ++x)
+              if (c + x < a.K)
+                f[x] += a.dw_f32 ? static_cast<const float*>(a.dW)[out + x]
+                                 : bf2f(static_cast<const uint16_t*>(a.dW)[out + x]);
           }
+          store32(a.dW, out, a.dw_f32, a.dw_vec && c + 32 <= a.K, a.K - c, f);
         }
       }
-      if (nk > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
-        ++j;
+      if (it.type == kScores) fence_proxy_async_all();   // dz is read by TMA
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence();
+        if (it.type == kDh) add_release(a.r.hdone + it.p, 1);
+        add_release((it.type == kScores ? a.r.sdone : a.r.gdone) + it.p, 1);
+        if (nk > 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
       }
+      if (nk > 0) ++j;
     }
   }
   // the pair's copies have landed, and its last remote arrivals, before it exits
@@ -617,35 +792,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc2(tmem, 512);
 }
 
-// dh of the counted rows: the chunk partials in ascending order, then the
-// target's term.  One CTA per row.
+// dh of the counted rows from partials side by side: the chunks in ascending
+// order, then the target's term.  4 columns a thread, a CTA per row and 1024
+// columns; 8 chunks are loaded ahead of their additions.
 __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __restrict__ W,
-                                                      int64_t ldw, int K, int ka, int cap,
-                                                      int slots, void* dh, int64_t lddh, int f32) {
+                                                      int64_t ldw, int K, int ka, int cap, int slots,
+                                                      void* dh, int64_t lddh, int f32) {
   pdl_wait();
   pdl_trigger();
-  const int i = blockIdx.x;
-  if (i >= *r.n) return;
-  const int64_t t = r.idx[i];
+  const int i = blockIdx.x, c = blockIdx.y * 1024 + threadIdx.x * 4;
+  if (i >= *r.n || c >= K) return;
+  const int64_t out = r.idx[i] * lddh + c;
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(W + r.target[i] * ldw + c));
   const float dzt = r.dzt[i];
-  const uint16_t* wr = W + int64_t(r.target[i]) * ldw;
-  for (int c = threadIdx.x * 4; c < K; c += 1024) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < slots; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(r.acc + (int64_t(k) * cap + i) * ka + c);
-      if (k == 0) {
-        s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
-      } else {
-        s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+  const float* src = r.acc + int64_t(i) * ka + c;
+  const int64_t pitch = int64_t(cap) * ka;
+  float4 s = __ldcg(reinterpret_cast<const float4*>(src));
+  for (int k0 = 1; k0 < slots; k0 += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 + k < slots) v[k] = __ldcg(reinterpret_cast<const float4*>(src + (k0 + k) * pitch));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k0 + k < slots) {
+        s.x += v[k].x; s.y += v[k].y; s.z += v[k].z; s.w += v[k].w;
       }
-    }
-    for (int x = 0; x < 4 && c + x < K; ++x) {
-      const float o = fmaf(dzt, bf2f(wr[c + x]), s[x]);
-      if (f32)
-        static_cast<float*>(dh)[t * lddh + c + x] = o;
-      else
-        static_cast<uint16_t*>(dh)[t * lddh + c + x] = f2bf(o);
-    }
+  }
+  const float o[4] = {fmaf(dzt, __uint_as_float(w.x << 16), s.x), fmaf(dzt, __uint_as_float(w.x & 0xFFFF0000u), s.y),
+                      fmaf(dzt, __uint_as_float(w.y << 16), s.z), fmaf(dzt, __uint_as_float(w.y & 0xFFFF0000u), s.w)};
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (f32)
+      static_cast<float*>(dh)[out + x] = o[x];
+    else
+      static_cast<uint16_t*>(dh)[out + x] = f2bf(o[x]);
   }
 }
 
@@ -663,20 +844,22 @@ bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int PHASE>
-biv_status launch_grad(const Maps& maps, const Args& a, int64_t most_items, cudaStream_t s) {
+biv_status launch_grad(const Maps& maps, const Args& a, cudaStream_t s) {
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(lm_grad_kernel<PHASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(lm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+        cudaSuccess)
       return set_error(BIV_ERR_CUDA, "lm_head_backward: cannot set shared memory size");
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
+  // no more pairs than a chunk's items can be, and one per two SMs
+  const int64_t tm = a.cap / kTM, tn = a.chunk / kTN, tk = a.ka / kTN;
+  const int64_t most = std::max(tm * tn, tk * (tm + tn)) * a.chunks;
   const int sms = sm_count() > 0 ? sm_count() : 148;
-  const int pairs = int(std::max<int64_t>(1, std::min<int64_t>(most_items, sms / 2)));
-  launch_pdl(lm_grad_kernel<PHASE>, 2 * pairs, kThreads, kSmem, s, maps, a);
+  const int pairs = int(std::max<int64_t>(1, std::min<int64_t>(most, sms / 2)));
+  launch_pdl(lm_grad_kernel, 2 * pairs, kThreads, kSmem, s, maps, a);
   return check_launch("lm_head_backward");
 }
 
@@ -860,7 +1043,7 @@ biv_status biv_lm_head_backward_workspace(int T, int V, int K, int dh_dtype, int
   biv_status st = lm_grad_sizes("lm_head_backward_workspace", T, V, K, dh_dtype, dw_dtype);
   if (st != BIV_OK) return st;
   BIV_REQUIRE(bytes, "lm_head_backward_workspace: null output");
-  *bytes = T == 0 ? 0 : layout(T, V, K, true, dh_dtype == BIV_F32 || dw_dtype == BIV_F32).bytes;
+  *bytes = T == 0 ? 0 : layout(T, V, K, dh_dtype == BIV_F32 || dw_dtype == BIV_F32).bytes;
   return BIV_OK;
 }
 
@@ -887,7 +1070,7 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
                   d->ldw % 8 == 0,
               "lm_head_backward: h and W need 16-byte aligned rows");
   BIV_REQUIRE(!d->dh || d->lddh >= K, "lm_head_backward: dh's rows overlap");
-  const Layout l = layout(T, V, K, true, d->dh_dtype == BIV_F32 || d->dw_dtype == BIV_F32);
+  const Layout l = layout(T, V, K, d->dh_dtype == BIV_F32 || d->dw_dtype == BIV_F32);
   if (!d->workspace || d->workspace_bytes < l.bytes)
     return set_error(BIV_ERR_WORKSPACE, "lm_head_backward: workspace of %zu bytes needed", l.bytes);
   BIV_REQUIRE((reinterpret_cast<uintptr_t>(d->workspace) & 255) == 0,
@@ -898,38 +1081,32 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   a.r = rows_of(l, d->workspace);
   Maps m;
   a.w3 = K % 64 == 0;
+  const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = (int64_t(V) + kTN - 1) / kTN + l.chunks;
+  BIV_REQUIRE(tm * tn + tk * (tm * l.chunks + tn) < (int64_t(1) << 30), "lm_head_backward: too many tiles");
   if (!map_rows(&m.h, a.r.h, l.kp, l.cap, l.kp, true) ||
       !map_rows(&m.w, d->W, K, V, d->ldw, a.w3 != 0) ||
-      !map_rows(&m.dz, a.r.dz, l.cols, int64_t(l.cap) * l.parts, l.cols, true))
+      !map_rows(&m.dz, a.r.dz, int64_t(l.ring) * l.chunk, int64_t(l.cap) * l.parts,
+                int64_t(l.ring) * l.chunk, true))
     return set_error(BIV_ERR_CUDA, "lm_head_backward: tensor map encoding failed");
-  a.V = V; a.K = K; a.kp = l.kp; a.ka = l.ka; a.cap = l.cap; a.cols = l.cols;
-  a.slots = l.slots;
+  a.V = V; a.K = K; a.kp = l.kp; a.ka = l.ka; a.cap = l.cap;
+  a.chunk = l.chunk; a.chunks = l.chunks; a.ahead = l.ahead; a.ring = l.ring; a.slots = l.slots;
   a.parts = l.parts;
   a.parts_h = d->dh_dtype == BIV_F32 ? 2 : 1;
   a.parts_w = d->dw_dtype == BIV_F32 ? 2 : 1;
+  a.W = d->W; a.ldw = d->ldw;
+  a.dh = d->dh; a.lddh = d->lddh; a.dh_f32 = d->dh_dtype == BIV_F32;
+  a.dh_vec = (reinterpret_cast<uintptr_t>(d->dh) & 31) == 0 && (d->lddh * hb) % 32 == 0;
   a.dW = d->dW; a.lddw = d->lddw; a.dw_f32 = d->dw_dtype == BIV_F32;
   a.dw_vec = (reinterpret_cast<uintptr_t>(d->dW) & 31) == 0 && (d->lddw * wb) % 32 == 0;
   a.accumulate = d->accumulate;
-  a.want_dh = d->dh != nullptr;
   a.err = device_error_word();
-  launch_pdl(pick_rows_kernel, 1 + std::min((V + 1023) / 1024, 128), 1024, 0, s, d->target, d->dlp, d->dlse,
-             T, V, a.r, a.err);
+  launch_pdl(gather_kernel, (l.cap + 7) / 8, 256, 0, s, d->h, d->ldh, d->target, d->lse, d->dlp, d->dlse, T, V,
+             K, l.kp, l.cap, l.chunks, d->dh, d->lddh, a.dh_f32, a.r, a.err);
   if ((st = check_launch("lm_head_backward rows")) != BIV_OK) return st;
-  launch_pdl(gather_kernel, (l.cap + 7) / 8, 256, 0, s, d->h, d->ldh, d->lse, d->dlp, d->dlse, T, K, l.kp,
-             l.cap, d->dh, d->lddh, int(d->dh_dtype == BIV_F32), a.r);
-  if ((st = check_launch("lm_head_backward gather")) != BIV_OK) return st;
-  const int64_t tm = l.cap / kTM, tk = (K + kTN - 1) / kTN;
-  for (a.c0 = 0; a.c0 < l.chunks; a.c0 += l.per_pass) {
-    a.nc = std::min(l.per_pass, l.chunks - a.c0);
-    a.v0 = a.c0 * kChunk;
-    a.vn = std::min(V - a.v0, a.nc * kChunk);
-    if ((st = launch_grad<0>(m, a, tm * ((a.vn + kTN - 1) / kTN), s)) != BIV_OK) return st;
-    const int64_t items = (a.want_dh ? tm * tk * a.nc : 0) + (a.dW ? tk * ((a.vn + kTM - 1) / kTM) : 0);
-    if ((st = launch_grad<1>(m, a, items, s)) != BIV_OK) return st;
-  }
-  if (!d->dh) return BIV_OK;
-  launch_pdl(dh_fold_kernel, T, 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap, l.slots, d->dh,
-              d->lddh, int(d->dh_dtype == BIV_F32));
+  if ((st = launch_grad(m, a, s)) != BIV_OK) return st;
+  if (!d->dh || l.slots == 1) return BIV_OK;
+  launch_pdl(dh_fold_kernel, dim3(T, (K + 1023) / 1024), 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap,
+             l.slots, d->dh, d->lddh, a.dh_f32);
   return check_launch("lm_head_backward fold");
 }
 
