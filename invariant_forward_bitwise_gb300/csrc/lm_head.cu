@@ -43,10 +43,9 @@ namespace {
 constexpr int kMaxChunk = 4096;   // vocabulary columns per FP32 partial of dh, at most
 constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
 constexpr int kTN = 256;          // tile columns: each CTA brings half of B
-constexpr int kTK = 128;          // K elements per stage: two 128-byte panels
-constexpr int kPanel = 128 * 128; // bytes of a 128-row panel of 64 bf16
-constexpr int kOperand = 2 * kPanel;   // a CTA's part of A or B in a stage
-constexpr int kStages = 3;
+constexpr int kTK = 64;           // K elements per stage
+constexpr int kOperand = 128 * kTK * 2;   // bytes of a CTA's part of A or B in a stage
+constexpr int kStages = 7;
 constexpr int kEpi = 8;
 constexpr int kThreads = 64 + 32 * kEpi;
 constexpr int kTickets = 4;       // work items announced ahead
@@ -68,8 +67,8 @@ struct Rows {
   uint16_t* dz;             // [parts][cap][ring * chunk]
   int* ticket;              // next work item
   int* sdone;               // [chunks] warps that have written their part of a chunk's dz
-  int* hdone;               // [chunks] warps that are done with its dh
-  int* gdone;               // [chunks] warps that are done with its dh and dW
+  int* hdone;               // [chunks] warps that have added their part of its dh
+  int* gdone;               // [chunks] products that have read it
 };
 
 struct Layout {
@@ -103,7 +102,7 @@ Layout layout(int T, int V, int K, bool f32) {
   // chunks ahead for about 48 stages of work in each of 76 pairs of CTAs, the
   // time of an item and a half.
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = l.chunk / kTN;
-  const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * 2 * tm);
+  const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * (l.cap / kTK));
   l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (48 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
   const size_t sizes[16] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
@@ -246,16 +245,17 @@ __global__ void __launch_bounds__(256) gather_kernel(
 
 // ----------------------------------------------------------------- GEMMs --
 struct Maps {
-  // boxes of {64 columns, 128 rows, 2 panels} ({64, 128} of W when K % 64)
-  CUtensorMap h;     // gathered h: K-major A of the scores, MN-major B of dW
-  CUtensorMap w;     // W: K-major B of the scores, MN-major B of dh
-  CUtensorMap dz;    // dz: K-major A of dh, MN-major A of dW
+  // K-major operands: boxes of 64 K elements of 128 rows; MN-major ones: boxes of
+  // 64 K indices (rows) by two panels of 64 columns (W when K % 64: one panel)
+  CUtensorMap hk, hn;   // gathered h: A of the scores, B of dW
+  CUtensorMap wk, wn;   // W: B of the scores, B of dh
+  CUtensorMap dk, dn;   // dz: A of dh, A of dW
 };
 
 struct Args {
   Rows r;
   int V, K, kp, ka, cap;
-  int w3;                  // W's maps bring two panels at once (K % 64 == 0)
+  int w2;                  // W's map brings two panels at once (K % 64 == 0)
   int chunk, chunks, ahead, ring, slots;
   int parts, parts_h, parts_w;
   const uint16_t* W; int64_t ldw;
@@ -267,11 +267,9 @@ struct Args {
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 enum { kScores = 0, kDh = 1, kDw = 2 };
-struct Item {
-  int type, m0, n0;        // tile origin
-  int p;                   // chunk
-  int nk;                  // stages of one part
-  int parts;
+// a work item as it is announced: type, origin of the tile, chunk
+struct __align__(16) Item {
+  int type, m0, n0, p;
 };
 
 // The work items of a call, in the order in which they are handed out: scores
@@ -329,28 +327,24 @@ __device__ __forceinline__ Item item_at(const Args& a, const Plan& p, int i) {
     j = i - p.body - q * p.g;
     it.p = both + q;
   }
-  const int cols = it.p == p.chunks - 1 ? p.last : a.chunk;
   if (scores) {
     it.type = kScores;
     it.m0 = j % p.tm * kTM;
     it.n0 = j / p.tm * kTN;
-    it.nk = a.kp / kTK;
-    it.parts = 1;
-  } else if (j < p.dh) {       // dh's items come first: they are the long ones
-    it.type = kDh;
-    it.m0 = j / p.tk * kTM;
-    it.n0 = j % p.tk * kTN;
-    it.nk = cdiv(cols, kTK);
-    it.parts = a.parts_h;
   } else {
-    j -= p.dh;
-    it.type = kDw;
+    it.type = j < p.dh ? kDh : kDw;       // dh's items come first: they are the long ones
+    if (j >= p.dh) j -= p.dh;
     it.m0 = j / p.tk * kTM;
     it.n0 = j % p.tk * kTN;
-    it.nk = cdiv(p.n, kTK);
-    it.parts = a.parts_w;
   }
   return it;
+}
+
+// stages of one part of an item, and its parts
+__device__ __forceinline__ int item_stages(const Args& a, const Plan& p, const Item& it, int& parts) {
+  parts = it.type == kScores ? 1 : it.type == kDh ? a.parts_h : a.parts_w;
+  if (it.type == kScores) return a.kp / kTK;
+  return cdiv(it.type == kDw ? p.n : it.p == p.chunks - 1 ? p.last : a.chunk, kTK);
 }
 
 __device__ __forceinline__ int load_acquire(const int* p) {
@@ -379,12 +373,12 @@ __device__ bool wait_count(const int* p, int want, int* err) {
 }
 
 // Everything that an item reads has been written, and nothing still reads what
-// it overwrites.  Counters count kEpi warps of two CTAs per item.
+// it overwrites.  sdone and hdone count kEpi warps of two CTAs per item, gdone items.
 __device__ bool item_ready(const Args& a, const Plan& p, const Item& it) {
   constexpr int kPer = 2 * kEpi;
   const bool end = it.p == p.chunks - 1;
   if (it.type == kScores)      // the ring's chunk of dz is free
-    return it.p < a.ring || wait_count(a.r.gdone + it.p - a.ring, kPer * p.g, a.err);
+    return it.p < a.ring || wait_count(a.r.gdone + it.p - a.ring, p.g, a.err);
   if (!wait_count(a.r.sdone + it.p, kPer * (end ? p.s_last : p.s), a.err)) return false;
   // partials that are added up as they come: the chunk before is in
   return !(it.type == kDh && a.slots == 1 && it.p > 0) ||
@@ -444,19 +438,19 @@ __device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint16_
 // All three products of a call in one launch: persistent pairs of CTAs
 // (clusters of two), 320 threads each.  Warp 0 = TMA producer and, in the
 // pair's first CTA, the taker of work items; warp 1 = TMEM owner and, in the
-// first CTA, MMA issuer; warps 2..9 = epilogue (lane quarter = warp % 4, column
-// half = (warp - 2) / 4).
+// first CTA, MMA issuer, in the second the one that counts finished products;
+// warps 2..9 = epilogue (lane quarter = warp % 4, column half = (warp - 2) / 4).
 // A tile is 256 x 256: each CTA loads its 128 rows of A and of B, the first CTA
 // issues cta_group::2 MMAs over both, and each CTA's TMEM gets its 128 rows.
 // full barriers live in the first CTA and count both CTAs' bytes; empty and
 // tfull are signalled in both by multicast commits; both epilogues arrive on
-// the first CTA's tempty.
+// the first CTA's tempty.  A stage is 64 K elements, 512 cycles of MMA: seven of
+// them leave six for the round trip of a stage's bytes (three stages of 128
+// left two of 1024 cycles, which L2's latency and 64 KB did not always fit in).
 // Items are taken from a counter in their order and announced to both CTAs
 // through a ring in shared memory.  An item depends on items before it only,
 // and those are taken by pairs that run: whatever else the GPU runs, the waits
-// end.  (As two launches per chunk, whose last waves left pairs idle and whose
-// W came from HBM twice for few rows: 4.04 ms at 4096 x 151936 x 2048 with a
-// quarter of the rows masked and 0.50 ms at 200 rows.)
+// end.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_grad_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -465,12 +459,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kOperand;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kOperand);
+  Item* ring = reinterpret_cast<Item*>(bars);                        // [kTickets]
+  bars += 2 * kTickets;
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
   const uint32_t tfull0 = smem_u32(bars + 2 * kStages), tempty0 = smem_u32(bars + 2 * kStages + 2);
   const uint32_t kfull0 = smem_u32(bars + 2 * kStages + 4);
   const uint32_t kempty0 = smem_u32(bars + 2 * kStages + 4 + kTickets);
-  volatile int* ticket = reinterpret_cast<int*>(bars + 2 * kStages + 4 + 2 * kTickets);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4 + 3 * kTickets);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4 + 2 * kTickets);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = int(cluster_rank());
 
@@ -481,17 +476,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(tfull0 + 8 * j, 1);
-      mbar_init(tempty0 + 8 * j, 2 * kEpi);
+      mbar_init(tempty0 + 8 * j, 2 * kEpi + 1);     // (and the counter of finished products)
     }
     for (int j = 0; j < kTickets; ++j) {
       mbar_init(kfull0 + 8 * j, 1);
-      // readers: both epilogues, the MMA issuer, the second CTA's producer
-      mbar_init(kempty0 + 8 * j, 2 * kEpi + 2);
+      // readers: both epilogues and both warps 1, the second CTA's producer
+      mbar_init(kempty0 + 8 * j, 2 * kEpi + 3);
     }
     fence_barrier_init();
-    tma_prefetch_desc(&maps.h);
-    tma_prefetch_desc(&maps.w);
-    tma_prefetch_desc(&maps.dz);
+    tma_prefetch_desc(&maps.hk);
+    tma_prefetch_desc(&maps.wk);
+    tma_prefetch_desc(&maps.dk);
+    tma_prefetch_desc(&maps.hn);
+    tma_prefetch_desc(&maps.wn);
+    tma_prefetch_desc(&maps.dn);
   }
   __syncwarp();
   if (warp == 1) {
@@ -507,16 +505,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_trigger();
   const Plan plan = plan_of(a);
 
-  // the seq-th announced item, or -1
+  // the next announced item (type < 0: no more); false: the wait ran out
   int seq = 0;
-  auto next_item = [&](bool& ok) -> int {
+  auto next_item = [&](Item& it) {
     const int k = seq % kTickets;
-    if (!mbar_wait_cluster(kfull0 + 8 * k, (seq / kTickets) & 1, a.err)) {
-      ok = false;
-      return -1;
-    }
+    if (!mbar_wait_cluster(kfull0 + 8 * k, (seq / kTickets) & 1, a.err)) return false;
+    const int4 v = load_shared4(smem_u32(ring + k));
+    it.type = v.x; it.m0 = v.y; it.n0 = v.z; it.p = v.w;
     ++seq;
-    return ticket[k];
+    return true;
   };
   auto release_item = [&]() {
     mbar_arrive_cluster(cluster_addr(kempty0 + 8 * ((seq - 1) % kTickets), 0));
@@ -527,126 +524,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int taken = rank == 0 ? atomicAdd(a.r.ticket, 1) : 0;
+      int s = 0, turn = 0;      // stage, its use
       while (ok) {
-        int i;
         Item it;
         if (rank == 0) {
-          i = taken < plan.total ? taken : -1;
-          if (i >= 0) {
+          it.type = -1;
+          if (taken < plan.total) {
+            it = item_at(a, plan, taken);
             taken = atomicAdd(a.r.ticket, 1);   // (used after this item)
-            it = item_at(a, plan, i);
-            if (!item_ready(a, plan, it)) {
-              ok = false;
-              i = -1;
-            }
-            fence_proxy_async_all();      // what others wrote is read by TMA
+            if (!item_ready(a, plan, it)) it.type = -1;
           }
           const int k = seq % kTickets;
           if (seq >= kTickets && !mbar_wait_cluster(kempty0 + 8 * k, ((seq / kTickets) - 1) & 1, a.err))
             break;
           for (int c = 0; c < 2; ++c) {
-            store_cluster(cluster_addr(smem_u32(const_cast<int*>(ticket + k)), c), i);
+            store_cluster(cluster_addr(smem_u32(ring + k), c), make_int4(it.type, it.m0, it.n0, it.p));
             mbar_arrive_cluster(cluster_addr(kfull0 + 8 * k, c));
           }
           ++seq;
         } else {
-          i = next_item(ok);
-          if (ok) release_item();
-          if (i >= 0) {
-            it = item_at(a, plan, i);
-            fence_proxy_async_all();
-          }
+          if (!next_item(it)) break;
+          release_item();
         }
-        if (i < 0) break;
-        const int slot = it.p % a.ring * a.chunk, v0 = it.p * a.chunk;
-        for (int kb = 0; kb < it.nk * it.parts; ++kb) {
-          const int s = issued % kStages;
-          if (issued >= kStages && !mbar_wait(empty0 + 8 * s, ((issued / kStages) - 1) & 1, a.err)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
-          const uint32_t da = smem_u32(sA + s * kOperand), db = smem_u32(sB + s * kOperand);
-          if (rank == 0) mbar_expect_tx(full0 + 8 * s, 4 * kOperand);
-          const int part = kb / it.nk, k = kb % it.nk;
-          const int m = it.m0 + rank * 128, nn = it.n0 + rank * 128;
-          if (it.type == kScores) {
-            tma2_load_3d(da, &maps.h, bar, 0, m, 2 * k);
-            if (a.w3) {
-              tma2_load_3d(db, &maps.w, bar, 0, v0 + nn, 2 * k);
-            } else {
-              for (int q = 0; q < 2; ++q)
-                tma2_load_2d(db + q * kPanel, &maps.w, bar, (2 * k + q) * 64, v0 + nn);
+        if (it.type < 0) break;
+        fence_proxy_async_all();      // what others wrote is read by TMA
+        int parts;
+        const int nk = item_stages(a, plan, it, parts);
+        const int dz0 = it.p % a.ring * a.chunk, v0 = it.p * a.chunk;
+        const int m = it.m0 + rank * 128, nn = it.n0 + rank * 128;
+        for (int part = 0; part < parts && ok; ++part) {
+          const int dzr = part * a.cap;
+          for (int k = 0; k < nk; ++k) {
+            if (turn > 0 && !mbar_wait(empty0 + 8 * s, (turn - 1) & 1, a.err)) {
+              ok = false;
+              break;
             }
-          } else if (it.type == kDh) {
-            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + m, (slot + k * kTK) / 64);
-            if (a.w3) {
-              tma2_load_3d(db, &maps.w, bar, 0, v0 + k * kTK, nn / 64);
+            const uint32_t bar = cluster_addr(full0 + 8 * s, 0);
+            const uint32_t da = smem_u32(sA + s * kOperand), db = smem_u32(sB + s * kOperand);
+            if (rank == 0) mbar_expect_tx(full0 + 8 * s, 4 * kOperand);
+            if (it.type == kScores) {
+              tma2_load_2d(da, &maps.hk, bar, k * kTK, m);
+              tma2_load_2d(db, &maps.wk, bar, k * kTK, v0 + nn);
+            } else if (it.type == kDh) {
+              tma2_load_2d(da, &maps.dk, bar, dz0 + k * kTK, dzr + m);
+              if (a.w2) {
+                tma2_load_3d(db, &maps.wn, bar, 0, v0 + k * kTK, nn / 64);
+              } else {
+                tma2_load_2d(db, &maps.wn, bar, nn, v0 + k * kTK);
+                tma2_load_2d(db + kOperand / 2, &maps.wn, bar, nn + 64, v0 + k * kTK);
+              }
             } else {
-              for (int q = 0; q < 2; ++q)
-                tma2_load_2d(db + q * kPanel, &maps.w, bar, nn + q * 64, v0 + k * kTK);
+              tma2_load_3d(da, &maps.dn, bar, 0, dzr + k * kTK, (dz0 + m) / 64);
+              tma2_load_3d(db, &maps.hn, bar, 0, k * kTK, nn / 64);
             }
-          } else {
-            tma2_load_3d(da, &maps.dz, bar, 0, part * a.cap + k * kTK, (slot + m) / 64);
-            tma2_load_3d(db, &maps.h, bar, 0, k * kTK, nn / 64);
+            ++issued;
+            if (++s == kStages) {
+              s = 0;
+              ++turn;
+            }
           }
-          ++issued;
         }
       }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      int st = 0, j = 0;
+      int s = 0, turn = 0, j = 0;
       bool ok = true;
-      while (ok) {
-        const int i = next_item(ok);
-        if (!ok) break;
+      Item it;
+      while (ok && next_item(it)) {
         release_item();
-        if (i < 0) break;
-        const Item it = item_at(a, plan, i);
-        const int nk = it.nk * it.parts;
+        if (it.type < 0) break;
+        int parts;
+        const int nk = item_stages(a, plan, it, parts) * parts;
         if (nk == 0) continue;
         const int b = j & 1;
-        if (j >= 2 && !mbar_wait(tempty0 + 8 * b, ((j >> 1) - 1) & 1, a.err)) break;
+        if (j >= 2 && !mbar_wait_cluster(tempty0 + 8 * b, ((j >> 1) - 1) & 1, a.err)) break;
         tc_fence_after();
         const uint32_t dt = tmem + b * kTN;
-        // K-major panels hold 64 K elements of a row; MN-major panels 64 rows or
-        // columns of the output, one K index per 128 bytes
+        // K-major: 64 K elements of a row in 128 bytes; MN-major: 64 rows or
+        // columns of the output of one K index
         const bool a_mn = it.type == kDw, b_mn = it.type != kScores;
         const uint32_t idesc =
             idesc_mma(1u, kTM, kTN) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-        for (int kb = 0; kb < nk; ++kb, ++st) {
-          const int s = st % kStages;
-          if (!mbar_wait(full0 + 8 * s, (st / kStages) & 1, a.err)) {
+        const uint32_t astep = a_mn ? 2048 : 32, bstep = b_mn ? 2048 : 32;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!mbar_wait(full0 + 8 * s, turn & 1, a.err)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t a0 = smem_u32(sA + s * kOperand), b0 = smem_u32(sB + s * kOperand);
+          const uint64_t ad = a_mn ? sdesc_mn_sw128(a0, kOperand / 2, 1024) : sdesc_k_sw128(a0);
+          const uint64_t bd = b_mn ? sdesc_mn_sw128(b0, kOperand / 2, 1024) : sdesc_k_sw128(b0);
 #pragma unroll
-          for (int kk = 0; kk < kTK / 16; ++kk) {
-            const uint32_t ko = (kk >> 2) * kPanel + (kk & 3) * 32, mo = kk * 2048;
-            const uint64_t ad = a_mn ? sdesc_mn_sw128(a0 + mo, kPanel, 1024) : sdesc_k_sw128(a0 + ko);
-            const uint64_t bd = b_mn ? sdesc_mn_sw128(b0 + mo, kPanel, 1024) : sdesc_k_sw128(b0 + ko);
-            umma2_f16(dt, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (int kk = 0; kk < kTK / 16; ++kk)     // (addresses count 16 bytes)
+            umma2_f16(dt, ad + kk * (astep >> 4), bd + kk * (bstep >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
           umma2_commit(empty0 + 8 * s);
+          if (++s == kStages) {
+            s = 0;
+            ++turn;
+          }
         }
         if (ok) umma2_commit(tfull0 + 8 * b);
         ++j;
+      }
+    } else if (lane == 0) {
+      // A product is finished: its reads of dz are done.  (The epilogue's own
+      // threads would wait for their stores first.)
+      int j = 0;
+      Item it;
+      while (next_item(it)) {
+        release_item();
+        if (it.type < 0) break;
+        int parts;
+        if (item_stages(a, plan, it, parts) > 0) {
+          if (!mbar_wait(tfull0 + 8 * (j & 1), (j >> 1) & 1, a.err)) break;
+          mbar_arrive_cluster(cluster_addr(tempty0 + 8 * (j & 1), 0));
+          ++j;
+        }
+        if (it.type != kScores) add_release(a.r.gdone + it.p, 1);
       }
     }
   } else {
     const int q = warp & 3, col0 = ((warp - 2) >> 2) * (kTN / 2);
     int j = 0;
-    bool ok = true;
-    while (true) {
-      const int i = next_item(ok);
-      if (!__all_sync(0xffffffffu, ok)) break;
+    Item it;
+    while (__all_sync(0xffffffffu, next_item(it))) {
       if (lane == 0) release_item();
-      if (i < 0) break;
-      const Item it = item_at(a, plan, i);
-      const int nk = it.nk * it.parts;
+      if (it.type < 0) break;
+      int parts;
+      const int nk = item_stages(a, plan, it, parts);
       const int b = j & 1;
       if (nk > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (j >> 1) & 1, a.err))) break;
@@ -767,16 +774,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           store32(a.dW, out, a.dw_f32, a.dw_vec && c + 32 <= a.K, a.K - c, f);
         }
       }
-      if (it.type == kScores) fence_proxy_async_all();   // dz is read by TMA
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence();
-        if (it.type == kDh) add_release(a.r.hdone + it.p, 1);
-        add_release((it.type == kScores ? a.r.sdone : a.r.gdone) + it.p, 1);
-        if (nk > 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+      if (nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+        ++j;
       }
-      if (nk > 0) ++j;
+      if (it.type == kScores || (it.type == kDh && a.slots == 1)) {
+        if (it.type == kScores) fence_proxy_async_all();   // dz is read by TMA
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence();
+          add_release((it.type == kScores ? a.r.sdone : a.r.hdone) + it.p, 1);
+        }
+      }
     }
   }
   // the pair's copies have landed, and its last remote arrivals, before it exits
@@ -830,11 +841,13 @@ __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __
   }
 }
 
-// bf16 rows in boxes of 128, as {64, rows, K / 64} panels (two per box) or as plain rows
-bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t ld, bool panels) {
+// bf16 rows: boxes of 64 columns and box_rows rows, or (panels) of two such
+// panels of {64, rows, K / 64}
+bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t ld, int box_rows,
+              bool panels) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, 128, 2};
+  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, cuuint32_t(box_rows), 2};
   const cuuint64_t panel_dims[3] = {64, cuuint64_t(rows), cuuint64_t(K / 64)};
   const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
   const cuuint64_t strides[2] = {cuuint64_t(ld * 2), 128};
@@ -1080,13 +1093,15 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   memset(&a, 0, sizeof(a));
   a.r = rows_of(l, d->workspace);
   Maps m;
-  a.w3 = K % 64 == 0;
+  a.w2 = K % 64 == 0;
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = (int64_t(V) + kTN - 1) / kTN + l.chunks;
   BIV_REQUIRE(tm * tn + tk * (tm * l.chunks + tn) < (int64_t(1) << 30), "lm_head_backward: too many tiles");
-  if (!map_rows(&m.h, a.r.h, l.kp, l.cap, l.kp, true) ||
-      !map_rows(&m.w, d->W, K, V, d->ldw, a.w3 != 0) ||
-      !map_rows(&m.dz, a.r.dz, int64_t(l.ring) * l.chunk, int64_t(l.cap) * l.parts,
-                int64_t(l.ring) * l.chunk, true))
+  const int64_t dzc = int64_t(l.ring) * l.chunk, dzr = int64_t(l.cap) * l.parts;
+  if (!map_rows(&m.hk, a.r.h, l.kp, l.cap, l.kp, 128, false) ||
+      !map_rows(&m.hn, a.r.h, l.kp, l.cap, l.kp, 64, true) ||
+      !map_rows(&m.wk, d->W, K, V, d->ldw, 128, false) ||
+      !map_rows(&m.wn, d->W, K, V, d->ldw, 64, K % 64 == 0) ||
+      !map_rows(&m.dk, a.r.dz, dzc, dzr, dzc, 128, false) || !map_rows(&m.dn, a.r.dz, dzc, dzr, dzc, 64, true))
     return set_error(BIV_ERR_CUDA, "lm_head_backward: tensor map encoding failed");
   a.V = V; a.K = K; a.kp = l.kp; a.ka = l.ka; a.cap = l.cap;
   a.chunk = l.chunk; a.chunks = l.chunks; a.ahead = l.ahead; a.ring = l.ring; a.slots = l.slots;
