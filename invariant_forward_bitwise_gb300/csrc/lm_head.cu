@@ -22,8 +22,8 @@
 //  - dh is summed over the vocabulary in chunks (at most kMaxChunk columns, a
 //    length that follows V alone), each accumulated from zero in TMEM in
 //    ascending columns, and the chunks added in ascending order in FP32: a row's
-//    dh depends on that row, V and K only.  dW is one accumulation over the
-//    counted rows in ascending order.
+//    dh depends on that row, V, K and the gradients' types only.  dW is one
+//    accumulation over the counted rows in ascending order.
 #include <algorithm>
 #include <cstring>
 
@@ -40,16 +40,20 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
 
 namespace {
 
-constexpr int kMaxChunk = 4096;   // vocabulary columns per FP32 partial of dh, at most
+constexpr int kMaxChunk = 8192;   // vocabulary columns per FP32 partial of dh, at most
 constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
 constexpr int kTN = 256;          // tile columns: each CTA brings half of B
 constexpr int kTK = 64;           // K elements per stage
 constexpr int kOperand = 128 * kTK * 2;   // bytes of a CTA's part of A or B in a stage
-constexpr int kStages = 7;
+constexpr int kStages = 6;
 constexpr int kEpi = 8;
-constexpr int kThreads = 64 + 32 * kEpi;
-constexpr int kTickets = 4;       // work items announced ahead
-constexpr int kSmem = 1024 + kStages * 2 * kOperand + 512;
+constexpr int kThreads = 96 + 32 * kEpi;
+constexpr int kTickets = 2;       // work items announced ahead
+constexpr int kTile = 32 * 128;   // bytes of an epilogue warp's staging: 32 rows of 128 bytes
+constexpr int kKeys = 256;        // targets kept in shared memory, when no more rows count
+constexpr int kSmem = 1024 + kStages * 2 * kOperand + kEpi * kTile + 512 + kKeys * 4;
+// Stages of a FP32 gradient's products that are added up in TMEM (see lm_grad_kernel).
+constexpr int kPiece = 8;
 
 // Device-side state of one call, in its workspace.
 struct Rows {
@@ -99,11 +103,11 @@ Layout layout(int T, int V, int K, bool f32) {
   const size_t part = size_t(l.cap) * l.ka * 4;
   l.slots = part * l.chunks <= kSlotBytes ? l.chunks : 1;
   // The scores of a chunk have to be done when its products start: enough
-  // chunks ahead for about 48 stages of work in each of 76 pairs of CTAs, the
-  // time of an item and a half.
+  // chunks ahead for about 144 stages of work in each of 76 pairs of CTAs, the
+  // time of a dh item (200 x 151936: 48 stages 508 us, 144 430, 256 427).
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = l.chunk / kTN;
   const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * (l.cap / kTK));
-  l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (48 * 76 + stages - 1) / stages)));
+  l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (144 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
   const size_t sizes[16] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
@@ -250,6 +254,8 @@ struct Maps {
   CUtensorMap hk, hn;   // gathered h: A of the scores, B of dW
   CUtensorMap wk, wn;   // W: B of the scores, B of dh
   CUtensorMap dk, dn;   // dz: A of dh, A of dW
+  // stores of 32 rows by 128 bytes (dz in two parts: by 64 bytes)
+  CUtensorMap ds, ws;   // dz, dW
 };
 
 struct Args {
@@ -260,7 +266,7 @@ struct Args {
   int parts, parts_h, parts_w;
   const uint16_t* W; int64_t ldw;
   void* dh; int64_t lddh; int dh_f32, dh_vec;
-  void* dW; int64_t lddw; int dw_f32, dw_vec, accumulate;
+  void* dW; int64_t lddw; int dw_f32, dw_tma, accumulate;
   int* err;
 };
 
@@ -374,15 +380,63 @@ __device__ bool wait_count(const int* p, int want, int* err) {
 
 // Everything that an item reads has been written, and nothing still reads what
 // it overwrites.  sdone and hdone count kEpi warps of two CTAs per item, gdone items.
-__device__ bool item_ready(const Args& a, const Plan& p, const Item& it) {
+// A chunk that a pair has found ready is not asked for again.
+struct Ready {
+  int free = -1, scores = -1, sums = -1;
+};
+__device__ bool item_ready(const Args& a, const Plan& p, const Item& it, Ready& known) {
   constexpr int kPer = 2 * kEpi;
   const bool end = it.p == p.chunks - 1;
-  if (it.type == kScores)      // the ring's chunk of dz is free
-    return it.p < a.ring || wait_count(a.r.gdone + it.p - a.ring, p.g, a.err);
-  if (!wait_count(a.r.sdone + it.p, kPer * (end ? p.s_last : p.s), a.err)) return false;
+  if (it.type == kScores) {      // the ring's chunk of dz is free
+    if (it.p < a.ring || known.free == it.p) return true;
+    known.free = it.p;
+    return wait_count(a.r.gdone + it.p - a.ring, p.g, a.err);
+  }
+  if (known.scores != it.p) {
+    known.scores = it.p;
+    if (!wait_count(a.r.sdone + it.p, kPer * (end ? p.s_last : p.s), a.err)) return false;
+  }
   // partials that are added up as they come: the chunk before is in
-  return !(it.type == kDh && a.slots == 1 && it.p > 0) ||
-         wait_count(a.r.hdone + it.p - 1, kPer * p.dh, a.err);
+  if (it.type != kDh || a.slots > 1 || it.p == 0 || known.sums == it.p) return true;
+  known.sums = it.p;
+  return wait_count(a.r.hdone + it.p - 1, kPer * p.dh, a.err);
+}
+
+// The first of n ascending keys that is v or more, by a warp: 32 probes a round
+// (two rounds for 1024 keys, where a lane alone takes ten loads in a chain).
+__device__ __forceinline__ int warp_lower_bound(const int* key, int n, int v, int lane) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int span = hi - lo, step = (span + 31) / 32;
+    const int below = __popc(__ballot_sync(0xffffffffu, key[lo + min((lane + 1) * step, span) - 1] < v));
+    hi = below == 32 ? hi : lo + min((below + 1) * step, span) - 1;
+    lo += min(below * step, span);
+  }
+  return lo;
+}
+
+// The keys in [first, end) that are v0 + lane, of n ascending ones.
+__device__ __forceinline__ void warp_keys(const int* key, int n, int v0, int lane, int& first, int& end) {
+  const int base = warp_lower_bound(key, n, v0, lane);
+  const int k = base + lane < n ? key[base + lane] - v0 : 32;
+  const int some = __popc(__ballot_sync(0xffffffffu, k < 32));
+  first = end = base;
+  if (some < 32) {
+    for (int i = 0; i < some; ++i) {
+      const int o = __shfl_sync(0xffffffffu, k, i);
+      first += o < lane;
+      end += o <= lane;
+    }
+  } else {
+    for (int up = 0; up < 2; ++up) {
+      int lo = base, hi = n;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (key[mid] < v0 + lane + up) lo = mid + 1; else hi = mid;
+      }
+      (up ? end : first) = lo;
+    }
+  }
 }
 
 // 32 columns of a row from registers, bf16 or FP32
@@ -419,6 +473,58 @@ __device__ __forceinline__ void store32(void* base, int64_t off, int f32, bool v
   }
 }
 
+// 32 columns of a lane's row into its warp's staging, as TMA reads them: 16-byte
+// pieces, those of 128-byte rows exchanged by (row % 8), those of 64-byte rows by
+// (row / 2 % 4), so that neither side meets bank conflicts.
+__device__ __forceinline__ void stage_f32(uint32_t base, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    store_shared4(base + lane * 128 + ((x ^ (lane & 7)) << 4), __float_as_uint(v[4 * x]), __float_as_uint(v[4 * x + 1]),
+                  __float_as_uint(v[4 * x + 2]), __float_as_uint(v[4 * x + 3]));
+}
+// the first (half 0) or second half of a 128-byte row
+__device__ __forceinline__ void stage_bf16(uint32_t base, int lane, int half, const float (&v)[32]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    store_shared4(base + lane * 128 + (((half * 4 + x) ^ (lane & 7)) << 4), bf2(v[8 * x], v[8 * x + 1]),
+                  bf2(v[8 * x + 2], v[8 * x + 3]), bf2(v[8 * x + 4], v[8 * x + 5]), bf2(v[8 * x + 6], v[8 * x + 7]));
+}
+// a 64-byte row
+__device__ __forceinline__ void stage_part(uint32_t base, int lane, const float (&v)[32]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    store_shared4(base + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4), bf2(v[8 * x], v[8 * x + 1]),
+                  bf2(v[8 * x + 2], v[8 * x + 3]), bf2(v[8 * x + 4], v[8 * x + 5]), bf2(v[8 * x + 6], v[8 * x + 7]));
+}
+
+// v += 32 columns of a row, bf16 or FP32
+__device__ __forceinline__ void add32(const void* base, int64_t off, int f32, bool vec, int left, float (&v)[32]) {
+  if (vec && f32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 o = s[x];
+      v[4 * x] += o.x; v[4 * x + 1] += o.y; v[4 * x + 2] += o.z; v[4 * x + 3] += o.w;
+    }
+  } else if (vec) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint4 u = s[x];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        v[8 * x + 2 * y] += __uint_as_float(w[y] << 16);
+        v[8 * x + 2 * y + 1] += __uint_as_float(w[y] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 32; ++x)
+      if (x < left) v[x] += f32 ? static_cast<const float*>(base)[off + x] : bf2f(static_cast<const uint16_t*>(base)[off + x]);
+  }
+}
+
 // v += f * 32 bf16 of a row (16-byte aligned), the first `left` of them
 __device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint16_t* row, int left) {
   const uint4* r = reinterpret_cast<const uint4*>(row);
@@ -436,21 +542,38 @@ __device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint16_
 }
 
 // All three products of a call in one launch: persistent pairs of CTAs
-// (clusters of two), 320 threads each.  Warp 0 = TMA producer and, in the
-// pair's first CTA, the taker of work items; warp 1 = TMEM owner and, in the
-// first CTA, MMA issuer, in the second the one that counts finished products;
-// warps 2..9 = epilogue (lane quarter = warp % 4, column half = (warp - 2) / 4).
+// (clusters of two), 352 threads each.  Warp 0 = TMA producer; warp 1 = TMEM
+// owner and, in the pair's first CTA, MMA issuer, in the second the one that
+// counts finished products; warps 2..9 = epilogue (lane quarter = warp % 4,
+// column half = (warp - 2) / 4); warp 10 of the first CTA takes work items.
 // A tile is 256 x 256: each CTA loads its 128 rows of A and of B, the first CTA
 // issues cta_group::2 MMAs over both, and each CTA's TMEM gets its 128 rows.
 // full barriers live in the first CTA and count both CTAs' bytes; empty and
 // tfull are signalled in both by multicast commits; both epilogues arrive on
-// the first CTA's tempty.  A stage is 64 K elements, 512 cycles of MMA: seven of
-// them leave six for the round trip of a stage's bytes (three stages of 128
-// left two of 1024 cycles, which L2's latency and 64 KB did not always fit in).
+// the first CTA's tempty.
+//
 // Items are taken from a counter in their order and announced to both CTAs
 // through a ring in shared memory.  An item depends on items before it only,
 // and those are taken by pairs that run: whatever else the GPU runs, the waits
-// end.
+// end.  Taking an item, finding its inputs ready and announcing it is a chain of
+// round trips to L2, thousands of cycles long, which is why a warp of its own
+// does it (by the producer, 13 rows x 4096: 25.4 us, now 22.1; 4096 x 151936:
+// 3815 -> 3700 us), but only two ahead: items held by a pair that is busy are
+// late for those that wait for them (200 x 151936, four ahead 524 us, two 430).
+// Barrier arrivals that hand nothing over are relaxed, since a release waits
+// for the warp's stores; an epilogue warp stores through shared memory and TMA,
+// 32 rows of 128 bytes at a time (stores by lanes, a row each: 541 us, now 504).
+//
+// F32: the MMAs' FP32 accumulators truncate, so that a sum's error grows with
+// its number of steps.  For FP32 gradients an accumulator takes kPiece stages
+// (512 K elements); the epilogue adds the pieces up in registers, rounding to
+// nearest.  1000 x 32003 x 2048, 2-norm against 64 bits: dh 3.3e-6 -> 5.8e-7, dW
+// 2.2e-6 -> 5.5e-7, 397 (pieces of 16: 1.1e-6) -> 425 us.
+//
+// What bounds it: at 4096 x 151936 a stage of 64 K elements (512 cycles at the
+// MMA's rate) takes 670 under the card's power limit, as cuBLAS's products do;
+// small calls the chain of scores, products and fold.
+template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     lm_grad_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a) {
   extern __shared__ uint8_t smem_raw[];
@@ -458,7 +581,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kOperand;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sB + kStages * kOperand);
+  uint8_t* staging = sB + kStages * kOperand;
+  int* keys = reinterpret_cast<int*>(staging + kEpi * kTile);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(keys + kKeys);
   Item* ring = reinterpret_cast<Item*>(bars);                        // [kTickets]
   bars += 2 * kTickets;
   const uint32_t full0 = smem_u32(bars), empty0 = smem_u32(bars + kStages);
@@ -480,8 +605,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int j = 0; j < kTickets; ++j) {
       mbar_init(kfull0 + 8 * j, 1);
-      // readers: both epilogues and both warps 1, the second CTA's producer
-      mbar_init(kempty0 + 8 * j, 2 * kEpi + 3);
+      mbar_init(kempty0 + 8 * j, 2 * kEpi + 4);     // readers: the warps of both CTAs but the taker
     }
     fence_barrier_init();
     tma_prefetch_desc(&maps.hk);
@@ -490,6 +614,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.hn);
     tma_prefetch_desc(&maps.wn);
     tma_prefetch_desc(&maps.dn);
+    tma_prefetch_desc(&maps.ds);
+    if (a.dw_tma) tma_prefetch_desc(&maps.ws);
   }
   __syncwarp();
   if (warp == 1) {
@@ -515,39 +641,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ++seq;
     return true;
   };
+  // (behind a branch on what was read: the slot may be written from then on)
   auto release_item = [&]() {
-    mbar_arrive_cluster(cluster_addr(kempty0 + 8 * ((seq - 1) % kTickets), 0));
+    mbar_arrive_relaxed(cluster_addr(kempty0 + 8 * ((seq - 1) % kTickets), 0));
+  };
+
+  // accumulators that an item's products go through
+  auto pieces = [&](const Item& it) {
+    int parts;
+    const int nk = item_stages(a, plan, it, parts) * parts;
+    return F32 ? cdiv(nk, kPiece) : int(nk > 0);
   };
 
   int issued = 0;
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      int taken = rank == 0 ? atomicAdd(a.r.ticket, 1) : 0;
       int s = 0, turn = 0;      // stage, its use
-      while (ok) {
-        Item it;
-        if (rank == 0) {
-          it.type = -1;
-          if (taken < plan.total) {
-            it = item_at(a, plan, taken);
-            taken = atomicAdd(a.r.ticket, 1);   // (used after this item)
-            if (!item_ready(a, plan, it)) it.type = -1;
-          }
-          const int k = seq % kTickets;
-          if (seq >= kTickets && !mbar_wait_cluster(kempty0 + 8 * k, ((seq / kTickets) - 1) & 1, a.err))
-            break;
-          for (int c = 0; c < 2; ++c) {
-            store_cluster(cluster_addr(smem_u32(ring + k), c), make_int4(it.type, it.m0, it.n0, it.p));
-            mbar_arrive_cluster(cluster_addr(kfull0 + 8 * k, c));
-          }
-          ++seq;
-        } else {
-          if (!next_item(it)) break;
-          release_item();
-        }
+      Item it, before;
+      before.type = before.p = -1;
+      while (ok && next_item(it)) {
         if (it.type < 0) break;
-        fence_proxy_async_all();      // what others wrote is read by TMA
+        release_item();
+        if (it.type != before.type || it.p != before.p)
+          fence_proxy_async_all();    // what others wrote is read by TMA
+        before = it;
         int parts;
         const int nk = item_stages(a, plan, it, parts);
         const int dz0 = it.p % a.ring * a.chunk, v0 = it.p * a.chunk;
@@ -586,21 +704,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (warp == 2 + kEpi) {
+    // takes work items, waits for what they read and announces them
+    if (lane == 0 && rank == 0) {
+      Ready known;
+      bool ok = true;
+      while (ok) {
+        Item it;
+        it.type = -1;
+        const int taken = atomicAdd(a.r.ticket, 1);
+        if (taken < plan.total) {
+          it = item_at(a, plan, taken);
+          if (!item_ready(a, plan, it, known)) it.type = -1;
+        }
+        const int k = seq % kTickets;
+        if (seq >= kTickets && !mbar_wait_cluster(kempty0 + 8 * k, ((seq / kTickets) - 1) & 1, a.err)) break;
+        for (int c = 0; c < 2; ++c) {
+          store_cluster(cluster_addr(smem_u32(ring + k), c), make_int4(it.type, it.m0, it.n0, it.p));
+          mbar_arrive_cluster(cluster_addr(kfull0 + 8 * k, c));
+        }
+        ++seq;
+        ok = it.type >= 0;
+      }
+    }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       int s = 0, turn = 0, j = 0;
       bool ok = true;
       Item it;
       while (ok && next_item(it)) {
-        release_item();
         if (it.type < 0) break;
+        release_item();
         int parts;
         const int nk = item_stages(a, plan, it, parts) * parts;
-        if (nk == 0) continue;
-        const int b = j & 1;
-        if (j >= 2 && !mbar_wait_cluster(tempty0 + 8 * b, ((j >> 1) - 1) & 1, a.err)) break;
-        tc_fence_after();
-        const uint32_t dt = tmem + b * kTN;
+        uint32_t dt = 0;
         // K-major: 64 K elements of a row in 128 bytes; MN-major: 64 rows or
         // columns of the output of one K index
         const bool a_mn = it.type == kDw, b_mn = it.type != kScores;
@@ -608,6 +745,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             idesc_mma(1u, kTM, kTN) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
         const uint32_t astep = a_mn ? 2048 : 32, bstep = b_mn ? 2048 : 32;
         for (int kb = 0; kb < nk; ++kb) {
+          const bool begin = F32 ? kb % kPiece == 0 : kb == 0;
+          if (begin) {
+            if (j >= 2 && !mbar_wait_cluster(tempty0 + 8 * (j & 1), ((j >> 1) - 1) & 1, a.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            dt = tmem + (j & 1) * kTN;
+          }
           if (!mbar_wait(full0 + 8 * s, turn & 1, a.err)) {
             ok = false;
             break;
@@ -618,15 +764,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t bd = b_mn ? sdesc_mn_sw128(b0, kOperand / 2, 1024) : sdesc_k_sw128(b0);
 #pragma unroll
           for (int kk = 0; kk < kTK / 16; ++kk)     // (addresses count 16 bytes)
-            umma2_f16(dt, ad + kk * (astep >> 4), bd + kk * (bstep >> 4), idesc, (kb | kk) != 0 ? 1u : 0u);
+            umma2_f16(dt, ad + kk * (astep >> 4), bd + kk * (bstep >> 4), idesc, begin && kk == 0 ? 0u : 1u);
           umma2_commit(empty0 + 8 * s);
+          if (kb == nk - 1 || (F32 && kb % kPiece == kPiece - 1)) {
+            umma2_commit(tfull0 + 8 * (j & 1));
+            ++j;
+          }
           if (++s == kStages) {
             s = 0;
             ++turn;
           }
         }
-        if (ok) umma2_commit(tfull0 + 8 * b);
-        ++j;
       }
     } else if (lane == 0) {
       // A product is finished: its reads of dz are done.  (The epilogue's own
@@ -634,49 +782,132 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int j = 0;
       Item it;
       while (next_item(it)) {
-        release_item();
         if (it.type < 0) break;
-        int parts;
-        if (item_stages(a, plan, it, parts) > 0) {
-          if (!mbar_wait(tfull0 + 8 * (j & 1), (j >> 1) & 1, a.err)) break;
-          mbar_arrive_cluster(cluster_addr(tempty0 + 8 * (j & 1), 0));
-          ++j;
+        release_item();
+        bool ok = true;
+        for (int left = pieces(it); ok && left > 0; --left, ++j) {
+          ok = mbar_wait(tfull0 + 8 * (j & 1), (j >> 1) & 1, a.err);
+          if (ok) mbar_arrive_relaxed(cluster_addr(tempty0 + 8 * (j & 1), 0));
         }
+        if (!ok) break;
         if (it.type != kScores) add_release(a.r.gdone + it.p, 1);
       }
     }
   } else {
     const int q = warp & 3, col0 = ((warp - 2) >> 2) * (kTN / 2);
+    const uint32_t tile = smem_u32(staging) + (warp - 2) * kTile;
+    const int* skey = a.r.skey;
+    if (plan.n <= kKeys) {
+      for (int i = threadIdx.x - 64; i < plan.n; i += 32 * kEpi) keys[i] = a.r.skey[i];
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpi) : "memory");
+      skey = keys;
+    }
+    // the staging may be written again; it has been written and is stored
+    auto stage_begin = [&]() {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    };
+    auto stage_end = [&](const CUtensorMap* map, int x, int y, int y2) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(map, tile, x, y);
+        if (y2 >= 0) tma_store_2d(map, tile + kTile / 2, x, y2);
+        bulk_commit();
+      }
+    };
     int j = 0;
     Item it;
     while (__all_sync(0xffffffffu, next_item(it))) {
-      if (lane == 0) release_item();
       if (it.type < 0) break;
-      int parts;
-      const int nk = item_stages(a, plan, it, parts);
-      const int b = j & 1;
-      if (nk > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * b, (j >> 1) & 1, a.err))) break;
-        tc_fence_after();
-      }
-      const uint32_t ta = tmem + b * kTN + col0 + (uint32_t(q * 32) << 16);
+      if (lane == 0) release_item();
+      const int np = pieces(it);
+      const uint32_t ta = tmem + col0 + (uint32_t(q * 32) << 16);
       const int row = it.m0 + rank * 128 + q * 32 + lane;
       const int v0 = it.p * a.chunk, cols = min(a.chunk, a.V - v0);
-      if (it.type == kScores) {
-        const bool live = row < plan.n;
-        const float lse = live ? a.r.lse[row] : 0.f, cp = live ? a.r.cp[row] : 0.f;
-        const int tc = live ? a.r.target[row] - v0 : -1;     // the target's column of the chunk
-        const int64_t pitch = int64_t(a.ring) * a.chunk;
-        uint16_t* dst = a.r.dz + row * pitch + it.p % a.ring * a.chunk + it.n0 + col0;
-        for (int g = 0; g < kTN / 64; ++g) {
-          uint32_t v[32];
-          tmem_ld32(ta + g * 32, v);
-          tmem_ld_wait();
-          const int c = it.n0 + col0 + g * 32;               // column of the chunk
-          float d[32];
+      // What the row needs is loaded before its products are waited for (after
+      // them, these chains of loads were most of the epilogue of a call of few
+      // rows, whose dW tiles are four stages long).
+      const bool live = it.type == kDw ? row < cols : row < plan.n;
+      const bool end = it.type == kDh && a.slots == 1 && it.p == a.chunks - 1;
+      float lse = 0.f, cp = 0.f, dzt = 0.f;
+      int tgt = -1, first = 0, last = 0, r0 = 0;
+      int64_t out = 0;
+      if (it.type == kDw) {
+        // the counted rows whose target this row of dW is
+        warp_keys(skey, plan.n, v0 + row - lane, lane, first, last);
+        if (first < last) {
+          r0 = a.r.srow[first];
+          dzt = __ldcg(a.r.dzt + r0);
+        }
+      } else if (live && it.type == kScores) {
+        lse = a.r.lse[row];
+        cp = a.r.cp[row];
+        tgt = a.r.target[row];
+      } else if (live && end) {
+        dzt = __ldcg(a.r.dzt + row);
+        out = a.r.idx[row] * a.lddh;
+        tgt = a.r.target[row];
+      }
+      bool ok = true;
+      float acc[F32 ? kTN / 64 : 1][32];
+      if (F32) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            d[x] = live && c + x < cols ? cp * expf(__uint_as_float(v[x]) - lse) : 0.f;
+        for (int g = 0; g < kTN / 64; ++g)
+#pragma unroll
+          for (int x = 0; x < 32; ++x) acc[F32 ? g : 0][x] = 0.f;
+        for (int i = 0; i < np; ++i, ++j) {
+          ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (j & 1), (j >> 1) & 1, a.err));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < kTN / 64; ++g) {
+            uint32_t v[32];
+            tmem_ld32(ta + (j & 1) * kTN + g * 32, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) acc[F32 ? g : 0][x] += __uint_as_float(v[x]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_relaxed(cluster_addr(tempty0 + 8 * (j & 1), 0));
+        }
+      } else if (np > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(tfull0 + 8 * (j & 1), (j >> 1) & 1, a.err));
+        tc_fence_after();
+      }
+      if (!ok) break;
+      // the products of 32 columns
+      auto product = [&](int g, float (&f)[32]) {
+        if (F32) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) f[x] = acc[F32 ? g : 0][x];
+        } else if (np > 0) {
+          uint32_t v[32];
+          tmem_ld32(ta + (j & 1) * kTN + g * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) f[x] = 0.f;
+        }
+      };
+      if (it.type == kScores) {
+        const int tc = live ? tgt - v0 : -1;                 // the target's column of the chunk
+        const int x0 = it.p % a.ring * a.chunk + it.n0 + col0, y0 = row - lane;
+#pragma unroll
+        for (int g = 0; g < kTN / 64; ++g) {
+          float d[32];
+          product(g, d);
+          const int c = it.n0 + col0 + g * 32;               // column of the chunk
+          // (rows behind the counted ones have h = 0 and cp = 0)
+#pragma unroll
+          for (int x = 0; x < 32; ++x) d[x] = cp * expf(d[x] - lse);
+          if (c + 32 > cols) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) d[x] = c + x < cols ? d[x] : 0.f;
+          }
           if (tc >= c && tc < c + 32) {
             float full = a.r.dlp[row];
 #pragma unroll
@@ -687,35 +918,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             a.r.dzt[row] = full;
           }
-          store32(dst, g * 32, 0, true, 32, d);
-          if (a.parts == 2) {
+          if (F32) {
+            stage_begin();
+            stage_part(tile, lane, d);
 #pragma unroll
             for (int x = 0; x < 32; ++x) d[x] -= bf2f(f2bf(d[x]));
-            store32(dst, a.cap * pitch + g * 32, 0, true, 32, d);
+            stage_part(tile + kTile / 2, lane, d);
+            stage_end(&maps.ds, x0 + g * 32, y0, a.cap + y0);
+          } else {
+            if (g % 2 == 0) stage_begin();
+            stage_bf16(tile, lane, g % 2, d);
+            if (g % 2) stage_end(&maps.ds, x0 + (g - 1) * 32, y0, -1);
           }
         }
       } else if (it.type == kDh) {
-        const bool live = row < plan.n;
         const bool add = a.slots == 1 && it.p > 0;
-        const bool end = a.slots == 1 && it.p == a.chunks - 1;
         float* dst = a.r.acc + (int64_t(a.slots > 1 ? it.p : 0) * a.cap + row) * a.ka + it.n0 + col0;
-        float dzt = 0.f;
-        int64_t out = 0;
-        const uint16_t* wr = a.W;
-        if (end && live) {
-          dzt = __ldcg(a.r.dzt + row);
-          out = a.r.idx[row] * a.lddh;
-          wr += a.r.target[row] * a.ldw;
-        }
+        const uint16_t* wr = a.W + (end && live ? tgt * a.ldw : 0);
+#pragma unroll
         for (int g = 0; g < kTN / 64; ++g) {
           const int c = it.n0 + col0 + g * 32;
-          uint32_t v[32];
-          tmem_ld32(ta + g * 32, v);
-          tmem_ld_wait();
-          if (!live) continue;
           float f[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
+          product(g, f);
+          if (!live) continue;
           if (add) {
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
@@ -735,60 +960,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         const int vr = v0 + row;                             // row of dW
-        const bool live = row < cols;
-        // the counted rows whose target this is
-        int first = 0;
-        if (live) {
-          int hi = plan.n;
-          while (first < hi) {
-            const int mid = (first + hi) >> 1;
-            if (a.r.skey[mid] < vr) first = mid + 1; else hi = mid;
-          }
-        }
+        const bool targets = __any_sync(0xffffffffu, first < last);
+#pragma unroll
         for (int g = 0; g < kTN / 64; ++g) {
           const int c = it.n0 + col0 + g * 32;
-          uint32_t v[32];
-          if (nk > 0) {
-            tmem_ld32(ta + g * 32, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = 0u;
-          }
-          if (!live || c >= a.K) continue;
           float f[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) f[x] = __uint_as_float(v[x]);
-          for (int t = first; t < plan.n && a.r.skey[t] == vr; ++t) {
-            const int r = a.r.srow[t];
-            add_row32(f, __ldcg(a.r.dzt + r), a.r.h + int64_t(r) * a.kp + c, 32);
+          product(g, f);
+          const bool on = live && c < a.K;
+          if (targets && on && first < last) {
+            add_row32(f, dzt, a.r.h + int64_t(r0) * a.kp + c, 32);
+            for (int t = first + 1; t < last; ++t) {
+              const int r = a.r.srow[t];
+              add_row32(f, __ldcg(a.r.dzt + r), a.r.h + int64_t(r) * a.kp + c, 32);
+            }
           }
-          const int64_t out = int64_t(vr) * a.lddw + c;
-          if (a.accumulate) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (c + x < a.K)
-                f[x] += a.dw_f32 ? static_cast<const float*>(a.dW)[out + x]
-                                 : bf2f(static_cast<const uint16_t*>(a.dW)[out + x]);
+          if (a.accumulate && on)
+            add32(a.dW, int64_t(vr) * a.lddw + c, a.dw_f32, a.dw_tma && c + 32 <= a.K, a.K - c, f);
+          // (a tile's store leaves out what lies behind V and K, but none starts there)
+          if (!a.dw_tma) {
+            if (on) store32(a.dW, int64_t(vr) * a.lddw + c, a.dw_f32, false, a.K - c, f);
+          } else if (a.dw_f32) {
+            stage_begin();
+            stage_f32(tile, lane, f);
+            if (c < a.K && vr - lane < a.V) stage_end(&maps.ws, c, vr - lane, -1);
+          } else {
+            if (g % 2 == 0) stage_begin();
+            stage_bf16(tile, lane, g % 2, f);
+            if (g % 2 && c - 32 < a.K && vr - lane < a.V) stage_end(&maps.ws, c - 32, vr - lane, -1);
           }
-          store32(a.dW, out, a.dw_f32, a.dw_vec && c + 32 <= a.K, a.K - c, f);
         }
       }
-      if (nk > 0) {
+      if (!F32 && np > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+        if (lane == 0) mbar_arrive_relaxed(cluster_addr(tempty0 + 8 * (j & 1), 0));
         ++j;
       }
       if (it.type == kScores || (it.type == kDh && a.slots == 1)) {
-        if (it.type == kScores) fence_proxy_async_all();   // dz is read by TMA
         __syncwarp();
         if (lane == 0) {
+          if (it.type == kScores) {      // dz was written by TMA and is read by TMA
+            bulk_wait();
+            fence_proxy_async_all();
+          }
           __threadfence();
           add_release((it.type == kScores ? a.r.sdone : a.r.hdone) + it.p, 1);
         }
       }
     }
+    if (lane == 0) bulk_wait();
   }
   // the pair's copies have landed, and its last remote arrivals, before it exits
   if (warp == 0 && lane == 0 && rank == 0) {
@@ -843,26 +1063,29 @@ __global__ void __launch_bounds__(256) dh_fold_kernel(Rows r, const uint16_t* __
 
 // bf16 rows: boxes of 64 columns and box_rows rows, or (panels) of two such
 // panels of {64, rows, K / 64}
+// (stores) of `cols` columns
 bool map_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t ld, int box_rows,
-              bool panels) {
+              bool panels, int cols = 64, bool f32 = false) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {64, cuuint32_t(box_rows), 2};
+  const cuuint32_t es[3] = {1, 1, 1}, box[3] = {cuuint32_t(cols), cuuint32_t(box_rows), 2};
   const cuuint64_t panel_dims[3] = {64, cuuint64_t(rows), cuuint64_t(K / 64)};
   const cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
-  const cuuint64_t strides[2] = {cuuint64_t(ld * 2), 128};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, panels ? 3 : 2, const_cast<void*>(base),
+  const int size = f32 ? 4 : 2;
+  const cuuint64_t strides[2] = {cuuint64_t(ld * size), 128};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, panels ? 3 : 2, const_cast<void*>(base),
             panels ? panel_dims : dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool F32>
 biv_status launch_grad(const Maps& maps, const Args& a, cudaStream_t s) {
   static bool set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(lm_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
+    if (cudaFuncSetAttribute(lm_grad_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) !=
         cudaSuccess)
       return set_error(BIV_ERR_CUDA, "lm_head_backward: cannot set shared memory size");
     if (dev >= 0 && dev < 64) set[dev] = true;
@@ -872,7 +1095,7 @@ biv_status launch_grad(const Maps& maps, const Args& a, cudaStream_t s) {
   const int64_t most = std::max(tm * tn, tk * (tm + tn)) * a.chunks;
   const int sms = sm_count() > 0 ? sm_count() : 148;
   const int pairs = int(std::max<int64_t>(1, std::min<int64_t>(most, sms / 2)));
-  launch_pdl(lm_grad_kernel, 2 * pairs, kThreads, kSmem, s, maps, a);
+  launch_pdl(lm_grad_kernel<F32>, 2 * pairs, kThreads, kSmem, s, maps, a);
   return check_launch("lm_head_backward");
 }
 
@@ -1093,6 +1316,8 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   memset(&a, 0, sizeof(a));
   a.r = rows_of(l, d->workspace);
   Maps m;
+  memset(&m, 0, sizeof(m));
+  a.dw_tma = d->dW && aligned16(d->dW) && (d->lddw * wb) % 16 == 0;
   a.w2 = K % 64 == 0;
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = (int64_t(V) + kTN - 1) / kTN + l.chunks;
   BIV_REQUIRE(tm * tn + tk * (tm * l.chunks + tn) < (int64_t(1) << 30), "lm_head_backward: too many tiles");
@@ -1101,7 +1326,10 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
       !map_rows(&m.hn, a.r.h, l.kp, l.cap, l.kp, 64, true) ||
       !map_rows(&m.wk, d->W, K, V, d->ldw, 128, false) ||
       !map_rows(&m.wn, d->W, K, V, d->ldw, 64, K % 64 == 0) ||
-      !map_rows(&m.dk, a.r.dz, dzc, dzr, dzc, 128, false) || !map_rows(&m.dn, a.r.dz, dzc, dzr, dzc, 64, true))
+      !map_rows(&m.dk, a.r.dz, dzc, dzr, dzc, 128, false) || !map_rows(&m.dn, a.r.dz, dzc, dzr, dzc, 64, true) ||
+      !map_rows(&m.ds, a.r.dz, dzc, dzr, dzc, 32, false, l.parts == 2 ? 32 : 64) ||
+      (a.dw_tma && !map_rows(&m.ws, d->dW, K, V, d->lddw, 32, false, d->dw_dtype == BIV_F32 ? 32 : 64,
+                             d->dw_dtype == BIV_F32)))
     return set_error(BIV_ERR_CUDA, "lm_head_backward: tensor map encoding failed");
   a.V = V; a.K = K; a.kp = l.kp; a.ka = l.ka; a.cap = l.cap;
   a.chunk = l.chunk; a.chunks = l.chunks; a.ahead = l.ahead; a.ring = l.ring; a.slots = l.slots;
@@ -1112,13 +1340,12 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   a.dh = d->dh; a.lddh = d->lddh; a.dh_f32 = d->dh_dtype == BIV_F32;
   a.dh_vec = (reinterpret_cast<uintptr_t>(d->dh) & 31) == 0 && (d->lddh * hb) % 32 == 0;
   a.dW = d->dW; a.lddw = d->lddw; a.dw_f32 = d->dw_dtype == BIV_F32;
-  a.dw_vec = (reinterpret_cast<uintptr_t>(d->dW) & 31) == 0 && (d->lddw * wb) % 32 == 0;
   a.accumulate = d->accumulate;
   a.err = device_error_word();
   launch_pdl(gather_kernel, (l.cap + 7) / 8, 256, 0, s, d->h, d->ldh, d->target, d->lse, d->dlp, d->dlse, T, V,
              K, l.kp, l.cap, l.chunks, d->dh, d->lddh, a.dh_f32, a.r, a.err);
   if ((st = check_launch("lm_head_backward rows")) != BIV_OK) return st;
-  if ((st = launch_grad(m, a, s)) != BIV_OK) return st;
+  if ((st = l.parts == 2 ? launch_grad<true>(m, a, s) : launch_grad<false>(m, a, s)) != BIV_OK) return st;
   if (!d->dh || l.slots == 1) return BIV_OK;
   launch_pdl(dh_fold_kernel, dim3(T, (K + 1023) / 1024), 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap,
              l.slots, d->dh, d->lddh, a.dh_f32);
