@@ -170,6 +170,7 @@ struct GemmArgs {
   float2* lse;
   float* zt;
   int ngroups;
+  const int* m_tiles;          // LSE: number of 128-row tiles that count, then their indexes (or null: all)
   int ws_v8;                   // partial mode: the workspace is 32-byte aligned
   int* err;
 };
@@ -236,16 +237,19 @@ __global__ void __launch_bounds__(kGemmThreads, PARTIAL ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int KB = (p.K + 63) / 64;
   const int chunks = (KB + p.kc_blocks - 1) / p.kc_blocks;
-  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
-  const int tiles = tiles_m * tiles_n;
+  int tiles_m = (p.M + BM - 1) / BM;
+  const int tiles_n = (p.N + BN - 1) / BN;
   static_assert(!PARTIAL || kPartialOk, "partial mode needs tiles of at most 128 columns");
   constexpr bool partial = PARTIAL;
-  const int items = partial ? tiles * chunks : tiles;
+  int items = partial ? tiles_m * tiles_n * chunks : tiles_m * tiles_n;
   // item -> tile and chunk range
   auto item_tile = [&](int i) { return partial ? i / chunks : i; };
   auto item_c0 = [&](int i) { return partial ? i % chunks : 0; };
   auto item_c1 = [&](int i) { return partial ? i % chunks + 1 : chunks; };
-  auto tile_m0 = [&](int t) { return (p.n_fastest ? t / tiles_n : t % tiles_m) * BM; };
+  auto tile_m0 = [&](int t) {
+    const int i = p.n_fastest ? t / tiles_n : t % tiles_m;
+    return (LSE && p.m_tiles ? p.m_tiles[1 + i] : i) * BM;
+  };
   auto tile_n0 = [&](int t) { return (p.n_fastest ? t % tiles_n : t / tiles_m) * BN; };
 
   if (threadIdx.x == 0) {
@@ -269,6 +273,11 @@ __global__ void __launch_bounds__(kGemmThreads, PARTIAL ? 2 : 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();  // TMEM is held: the next kernel in the stream may be scheduled
+  if (LSE && p.m_tiles) {      // the kernel before wrote the list
+    pdl_wait();
+    tiles_m = p.m_tiles[0];
+    items = tiles_m * tiles_n;
+  }
 
   int issued = 0;
   if (warp == 0) {
@@ -470,16 +479,20 @@ __global__ void __launch_bounds__(kGemmThreads, PARTIAL ? 2 : 1)
         // the row's logits z[nb .. nb+nv) of this half tile: their max, then
         // sum exp(z - max) over four interleaved chains (x = e mod 4, x
         // ascending) added as (c0 + c1) + (c2 + c3)
+        // (columns behind the last one are -inf and add 0: a condition per column
+        // compiled to 256 branches, 5 us of a tile)
         const int nb = n0 + col0, nv = min(HALF, p.N - nb);
+        if (nv < HALF) {
+#pragma unroll
+          for (int x = 0; x < HALF; ++x) r[x] = x < nv ? r[x] : -INFINITY;
+        }
+        float gm = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < HALF; ++x) gm = fmaxf(gm, r[x]);
+        float cs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < HALF; ++x) cs[x & 3] += expf(r[x] - gm);
         if (live && nv > 0) {
-          float gm = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < HALF; ++x)
-            if (x < nv) gm = fmaxf(gm, r[x]);
-          float cs[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < HALF; ++x)
-            if (x < nv) cs[x & 3] += expf(r[x] - gm);
           p.lse[int64_t(row) * p.ngroups + nb / kLseGroup] =
               make_float2(gm, (cs[0] + cs[1]) + (cs[2] + cs[3]));
           const int tg = p.target[row];
@@ -1699,8 +1712,8 @@ namespace biv {
 // is outside [0, V)); both in the workspace.
 biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, const uint16_t* W,
                           int64_t ldw, int M, int V, int K, const int32_t* target, int mode,
-                          void* workspace, size_t workspace_bytes, const float2** lse,
-                          const float** zt, int* ngroups, biv_stream_t stream) {
+                          const int* m_tiles, void* workspace, size_t workspace_bytes,
+                          const float2** lse, const float** zt, int* ngroups, biv_stream_t stream) {
   biv_gemm_desc d;
   memset(&d, 0, sizeof(d));
   d.M = M; d.N = V; d.K = K;
@@ -1738,6 +1751,7 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
   a.lse = static_cast<float2*>(workspace);
   a.zt = reinterpret_cast<float*>(static_cast<float2*>(workspace) + size_t(M) * ng);
   a.ngroups = ng;
+  a.m_tiles = m_tiles;
   a.err = device_error_word();
   const int sms = sm_count() > 0 ? sm_count() : 148;
   launch_pdl(kern, int(std::min<int64_t>(p.tiles, sms)), kGemmThreads,
@@ -1771,8 +1785,8 @@ extern "C" biv_status biv_lm_head_logprob(const uint16_t* h, int64_t ldh, const 
   const float2* lse;
   const float* zt;
   int ng;
-  biv_status st = lm_head_groups("lm_head_logprob", h, ldh, W, ldw, M, V, K, target, mode, workspace,
-                                 workspace_bytes, &lse, &zt, &ng, stream);
+  biv_status st = lm_head_groups("lm_head_logprob", h, ldh, W, ldw, M, V, K, target, mode, nullptr,
+                                 workspace, workspace_bytes, &lse, &zt, &ng, stream);
   if (st != BIV_OK) return st;
   launch_pdl(lse_combine_kernel, (M + kLseWarps - 1) / kLseWarps, kLseWarps * 32, 0, as_cuda(stream),
              lse, ng, zt, target, M, V, lp, device_error_word());

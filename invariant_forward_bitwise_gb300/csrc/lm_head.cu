@@ -32,10 +32,11 @@
 namespace biv {
 // gemm.cu: the fused head's GEMM.  lse[row * ng + g] = (max, sum exp(z - max)) of
 // columns [128 g, 128 g + 128), zt[row] = the logit at target[row] (unset where
-// the target is outside [0, V)).
+// the target is outside [0, V)).  m_tiles (or null: all rows): on the device, the
+// number of 128-row tiles to compute and their indexes.
 biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, const uint16_t* W,
                           int64_t ldw, int M, int V, int K, const int32_t* target, int mode,
-                          void* ws, size_t ws_bytes, const float2** lse, const float** zt, int* ng,
+                          const int* m_tiles, void* ws, size_t ws_bytes, const float2** lse, const float** zt, int* ng,
                           biv_stream_t stream);
 
 namespace {
@@ -1105,8 +1106,98 @@ constexpr int kMaxParts = 1024;   // blocks whose sums the last kernel adds up
 
 struct LossSums { double w, nll, sq; };
 
-// lp and lse as biv_lm_head_logprob merges the groups (lane l takes groups l,
-// l + 32, ... in order, then a xor tree); sums of the counted rows of each CTA.
+// whether a row counts
+__device__ __forceinline__ bool row_on(int target, float weight, int ignore) {
+  return target != ignore && weight != 0.f;
+}
+
+// The 128-row tiles with a counted row, in ascending order: their number, then
+// their indexes.  One CTA, a warp per tile.
+__global__ void __launch_bounds__(1024) row_tiles_kernel(const int32_t* __restrict__ target,
+                                                         const float* __restrict__ weight, int T, int ignore,
+                                                         int* __restrict__ list) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int some[32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int t0 = 0; t0 < T; t0 += 32 * 128) {
+    bool on = false;
+    for (int t = t0 + warp * 128 + lane, i = 0; i < 4 && t < T; ++i, t += 32)
+      on |= row_on(target[t], weight ? weight[t] : 1.f, ignore);
+    on = __any_sync(0xffffffffu, on);
+    if (lane == 0) some[warp] = on;
+    __syncthreads();
+    const unsigned all = __ballot_sync(0xffffffffu, some[lane]);
+    if (on && lane == 0) list[1 + n + __popc(all & ((1u << warp) - 1))] = t0 / 128 + warp;
+    n += __popc(all);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) list[0] = n;
+}
+
+// lp and lse of a row as biv_lm_head_logprob merges the groups (lane l takes
+// groups l, l + 32, ... in order, then a xor tree), and on lane 0 its terms of the sums.
+__device__ __forceinline__ void row_loss(const float2* __restrict__ g, int ng, const float* __restrict__ zt,
+                                         int row, int tg, float wt, int V, float* lp, float* lse, int* err,
+                                         LossSums& mine, float& l) {
+  const int lane = threadIdx.x & 31;
+  g += int64_t(row) * ng;
+  float mx = -INFINITY;
+  for (int i = lane; i < ng; i += 32) mx = fmaxf(mx, g[i].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float s = 0.f;
+  for (int i = lane; i < ng; i += 32) {
+    const float2 v = g[i];
+    s = fmaf(v.y, expf(v.x - mx), s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) {
+    l = mx + logf(s);
+    float p = NAN;
+    if (tg < 0 || tg >= V)
+      raise_error(err, kErrBadIndex);
+    else
+      p = zt[row] - l;
+    lp[row] = p;
+    lse[row] = l;
+    mine.w += wt;
+    mine.nll -= double(wt) * p;
+    mine.sq += double(wt) * l * l;
+  }
+}
+
+__device__ __forceinline__ LossSums warp_sums(LossSums s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.w += __shfl_xor_sync(0xffffffffu, s.w, o);
+    s.nll += __shfl_xor_sync(0xffffffffu, s.nll, o);
+    s.sq += __shfl_xor_sync(0xffffffffu, s.sq, o);
+  }
+  return s;
+}
+
+// what the loss divides by
+__device__ __forceinline__ double loss_scale(const LossSums& s, int mean, float norm) {
+  const double over = mean ? s.w : double(norm);
+  return over != 0. ? 1. / over : 0.;
+}
+__device__ __forceinline__ void write_stats(const LossSums& s, double inv, float z_coef, float* stats) {
+  stats[0] = float((s.nll + double(z_coef) * s.sq) * inv);
+  stats[1] = float(s.nll * inv);
+  stats[2] = float(s.sq * inv);
+  stats[3] = float(s.w);
+}
+__device__ __forceinline__ void write_coefs(int t, float wt, bool on, float l, double inv, float z_coef, float* dlp,
+                                            float* dlse) {
+  const float c = on ? float(wt * inv) : 0.f;
+  if (dlp) dlp[t] = -c;
+  if (dlse) dlse[t] = c == 0.f ? 0.f : float(2. * z_coef * c * l);
+}
+
+// Rows, and sums of the counted rows of each CTA.
 __global__ void __launch_bounds__(kLossRows * 32) lse_rows_kernel(
     const float2* __restrict__ groups, int ng, const float* __restrict__ zt,
     const int32_t* __restrict__ target, const float* __restrict__ weight, int T, int V, int ignore,
@@ -1119,35 +1210,11 @@ __global__ void __launch_bounds__(kLossRows * 32) lse_rows_kernel(
   for (int row = blockIdx.x * kLossRows + warp; row < T; row += gridDim.x * kLossRows) {
     const int tg = target[row];
     const float wt = weight ? weight[row] : 1.f;
-    if (tg == ignore || wt == 0.f) {
-      if (lane == 0) lp[row] = lse[row] = 0.f;
-      continue;
-    }
-    const float2* g = groups + int64_t(row) * ng;
-    float mx = -INFINITY;
-    for (int i = lane; i < ng; i += 32) mx = fmaxf(mx, g[i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float s = 0.f;
-    for (int i = lane; i < ng; i += 32) {
-      const float2 v = g[i];
-      s = fmaf(v.y, expf(v.x - mx), s);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      const float l = mx + logf(s);
-      float p = NAN;
-      if (tg < 0 || tg >= V)
-        raise_error(err, kErrBadIndex);
-      else
-        p = zt[row] - l;
-      lp[row] = p;
-      lse[row] = l;
-      mine.w += wt;
-      mine.nll -= double(wt) * p;
-      mine.sq += double(wt) * l * l;
-    }
+    float l;
+    if (row_on(tg, wt, ignore))
+      row_loss(groups, ng, zt, row, tg, wt, V, lp, lse, err, mine, l);
+    else if (lane == 0)
+      lp[row] = lse[row] = 0.f;
   }
   if (lane == 0) sums[warp] = mine;
   __syncthreads();
@@ -1171,47 +1238,75 @@ __global__ void __launch_bounds__(256) loss_rows_kernel(
     float* __restrict__ stats) {
   pdl_wait();
   pdl_trigger();
-  __shared__ double tot[3];
+  __shared__ double scale;
   if (threadIdx.x < 32) {
-    double w = 0., nll = 0., sq = 0.;
+    LossSums s = {0., 0., 0.};
     for (int i = threadIdx.x; i < nparts; i += 32) {
-      w += parts[i].w;
-      nll += parts[i].nll;
-      sq += parts[i].sq;
+      s.w += parts[i].w;
+      s.nll += parts[i].nll;
+      s.sq += parts[i].sq;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w += __shfl_xor_sync(0xffffffffu, w, o);
-      nll += __shfl_xor_sync(0xffffffffu, nll, o);
-      sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    }
+    s = warp_sums(s);
     if (threadIdx.x == 0) {
-      tot[0] = w;
-      tot[1] = nll;
-      tot[2] = sq;
+      scale = loss_scale(s, mean, norm);
+      if (blockIdx.x == 0) write_stats(s, scale, z_coef, stats);
     }
   }
   __syncthreads();
-  const double over = mean ? tot[0] : double(norm);
-  const double inv = over != 0. ? 1. / over : 0.;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    stats[0] = float((tot[1] + double(z_coef) * tot[2]) * inv);
-    stats[1] = float(tot[1] * inv);
-    stats[2] = float(tot[2] * inv);
-    stats[3] = float(tot[0]);
-  }
+  const double inv = scale;
   for (int t = blockIdx.x * 256 + threadIdx.x; t < T; t += gridDim.x * 256) {
     const float wt = weight ? weight[t] : 1.f;
-    const float c = target[t] == ignore || wt == 0.f ? 0.f : float(wt * inv);
-    if (dlp) dlp[t] = -c;
-    if (dlse) dlse[t] = c == 0.f ? 0.f : float(2. * z_coef * c * lse[t]);
+    write_coefs(t, wt, row_on(target[t], wt, ignore), lse[t], inv, z_coef, dlp, dlse);
   }
 }
+
+// Both for at most 32 rows, a warp each, in one CTA (13 rows of 4096: one launch
+// less).
+__global__ void __launch_bounds__(1024) few_rows_kernel(
+    const float2* __restrict__ groups, int ng, const float* __restrict__ zt,
+    const int32_t* __restrict__ target, const float* __restrict__ weight, int T, int V, int ignore,
+    float z_coef, int mean, float norm, float* __restrict__ lp, float* __restrict__ lse,
+    float* __restrict__ dlp, float* __restrict__ dlse, float* __restrict__ stats, int* err) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ LossSums sums[32];
+  __shared__ double scale;
+  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  LossSums mine = {0., 0., 0.};
+  const float wt = row < T && weight ? weight[row] : 1.f;
+  bool on = false;
+  float l = 0.f;
+  if (row < T) {
+    const int tg = target[row];
+    on = row_on(tg, wt, ignore);
+    if (on)
+      row_loss(groups, ng, zt, row, tg, wt, V, lp, lse, err, mine, l);
+    else if (lane == 0)
+      lp[row] = lse[row] = 0.f;
+  }
+  if (lane == 0) sums[row] = mine;
+  __syncthreads();
+  // (one warp: FP64 is slow on this GPU, and all 32 would queue for it)
+  if (row == 0) {
+    const LossSums tot = warp_sums(sums[lane]);
+    if (lane == 0) {
+      scale = loss_scale(tot, mean, norm);
+      write_stats(tot, scale, z_coef, stats);
+    }
+  }
+  __syncthreads();
+  if (row < T && lane == 0) write_coefs(row, wt, on, l, scale, z_coef, dlp, dlse);
+}
+
+// Tiles of rows that do not count (prompts, padding) are left out of the
+// product where that can save more than finding them costs: 3 us, against 100 us
+// or more of a product of this many multiplications.
+bool skip_tiles(int T, int V, int K) { return T > 256 && double(T) * V * K >= 8e10; }
 
 size_t loss_bytes(int T, int V) {
   size_t g = 0;
   biv_lm_head_logprob_workspace(T, V, &g);
-  return (g + 255) / 256 * 256 + kMaxParts * sizeof(LossSums);
+  return (g + 255) / 256 * 256 + kMaxParts * sizeof(LossSums) + ((T + 127) / 128 + size_t(1)) * 4;
 }
 
 }  // namespace
@@ -1244,25 +1339,36 @@ biv_status biv_lm_head_loss(const biv_lm_loss_desc* d, biv_stream_t stream) {
   biv_lm_head_logprob_workspace(d->T, d->V, &gb);
   gb = (gb + 255) / 256 * 256;
   LossSums* parts = reinterpret_cast<LossSums*>(static_cast<uint8_t*>(d->workspace) + gb);
+  int* tiles = reinterpret_cast<int*>(parts + kMaxParts);
+  const int mean = d->reduce == BIV_LOSS_TOKEN_MEAN;
+  biv_status st;
   int blocks = 0;
   if (d->T > 0) {
     const float2* groups;
     const float* zt;
     int ng;
-    biv_status st = lm_head_groups("lm_head_loss", d->h, d->ldh, d->W, d->ldw, d->T, d->V, d->K,
-                                   d->target, BIV_MODE_INVARIANT, d->workspace, gb, &groups, &zt, &ng,
-                                   stream);
+    const bool skip = skip_tiles(d->T, d->V, d->K);
+    if (skip) {
+      launch_pdl(row_tiles_kernel, 1, 1024, 0, s, d->target, d->weight, d->T, d->ignore_index, tiles);
+      if ((st = check_launch("lm_head_loss tiles")) != BIV_OK) return st;
+    }
+    st = lm_head_groups("lm_head_loss", d->h, d->ldh, d->W, d->ldw, d->T, d->V, d->K, d->target,
+                        BIV_MODE_INVARIANT, skip ? tiles : nullptr, d->workspace, gb, &groups, &zt, &ng, stream);
     if (st != BIV_OK) return st;
+    if (d->T <= 32) {
+      launch_pdl(few_rows_kernel, 1, 1024, 0, s, groups, ng, zt, d->target, d->weight, d->T, d->V, d->ignore_index,
+                 d->z_coef, mean, d->norm, d->lp, d->lse, d->dlp, d->dlse, d->stats, device_error_word());
+      return check_launch("lm_head_loss");
+    }
     blocks = int(std::min<int64_t>((d->T + kLossRows - 1) / kLossRows, kMaxParts));
     launch_pdl(lse_rows_kernel, blocks, kLossRows * 32, 0, s, groups, ng, zt, d->target, d->weight, d->T,
                d->V, d->ignore_index, d->lp, d->lse, parts, device_error_word());
-    st = check_launch("lm_head_loss rows");
-    if (st != BIV_OK) return st;
+    if ((st = check_launch("lm_head_loss rows")) != BIV_OK) return st;
   }
   launch_pdl(loss_rows_kernel, std::max(1, std::min((d->T + 255) / 256, 152)), 256, 0, s,
              static_cast<const LossSums*>(parts), blocks, d->target, d->weight,
-             static_cast<const float*>(d->lse), d->T, d->ignore_index, d->z_coef,
-             int(d->reduce == BIV_LOSS_TOKEN_MEAN), d->norm, d->dlp, d->dlse, d->stats);
+             static_cast<const float*>(d->lse), d->T, d->ignore_index, d->z_coef, mean, d->norm, d->dlp, d->dlse,
+             d->stats);
   return check_launch("lm_head_loss");
 }
 

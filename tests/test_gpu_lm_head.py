@@ -399,6 +399,59 @@ def test_logprobs_are_those_of_the_fused_head(B):
 
 
 @gpu
+@pytest.mark.parametrize("which", ["prompts", "tail", "one", "none", "all", "weights"])
+def test_row_tiles_that_do_not_count(B, which):
+    """A product large enough that 128-row tiles without counted rows are left out."""
+    T, V, K = 1111, 36000, 2048
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(V, K, device="cuda", generator=g) * 0.04).bfloat16()
+    target = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    row = torch.arange(T, device="cuda")
+    on = {"prompts": row % 500 >= 300, "tail": row < 385, "one": row == 1110, "none": row < 0, "all": row >= 0,
+          "weights": (row // 128) % 2 == 1}[which]
+    weight = torch.where(on, 0.5 + torch.rand(T, device="cuda", generator=g), 0.0) if which == "weights" else None
+    if weight is None:
+        target = torch.where(on, target, -100)
+    ws = torch.empty(B.biv_lm_head_loss_workspace(T, V), dtype=torch.uint8, device="cuda")
+    ref = torch.empty(T, device="cuda")
+    B.biv_lm_head_logprob(h, W, target.clamp_min(0), ref, ws)
+    h[~on] = float("nan")
+    ws.fill_(255)
+    lp, lse, dlp, dlse = (torch.full((T,), 5.0, device="cuda") for _ in range(4))
+    stats = torch.empty(4, device="cuda")
+    B.biv_lm_head_loss(h, W, target, lp, lse, stats, ws, weight=weight, dlp=dlp, dlse=dlse, z_coef=0.5)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    assert same(lp, torch.where(on, ref, 0.0)) and bool((lse[~on] == 0).all()) and bool((lse[on] > 0).all())
+    w = (on if weight is None else weight).to(F64)
+    share = w / max(float(w.sum()), 1e-30)
+    # (each a handful of FP32 roundings of values computed in 64 bits)
+    assert torch.allclose(dlp.to(F64), -share, rtol=2.0 ** -22, atol=0)
+    assert torch.allclose(dlse.to(F64), share * lse.to(F64), rtol=2.0 ** -21, atol=0)
+    nll, sq = -(share * lp.to(F64)).sum(), (share * lse.to(F64) ** 2).sum()
+    want = torch.stack([nll + 0.5 * sq, nll, sq, w.sum()])
+    assert torch.allclose(stats.to(F64), want, rtol=2.0 ** -20, atol=0)
+
+
+@gpu
+def test_few_rows_have_the_bits_of_many(B):
+    """At most 32 rows take one kernel for all sums: lp and lse are those of a larger call."""
+    T, V, K = 70, 9001, 256
+    c = Case(T, V, K)
+    out = [torch.empty(T, device="cuda") for _ in range(2)]
+    ws = torch.empty(B.biv_lm_head_loss_workspace(T, V), dtype=torch.uint8, device="cuda")
+    stats = torch.empty(4, device="cuda")
+    B.biv_lm_head_loss(c.h, c.W, c.target, *out, stats, ws)
+    for n in (1, 31, 32, 33):
+        few = [torch.empty(n, device="cuda") for _ in range(3)]
+        B.biv_lm_head_loss(c.h[5:5 + n], c.W, c.target[5:5 + n], *few[:2], stats, ws, dlp=few[2])
+        assert all(same(a, b[5:5 + n]) for a, b in zip(few, out))
+        assert torch.allclose(few[2].to(F64), torch.full((n,), -1 / n, device="cuda", dtype=F64), rtol=2.0 ** -23)
+        assert torch.allclose(stats[1].to(F64), -few[0].to(F64).mean(), rtol=2.0 ** -22) and float(stats[3]) == n
+
+
+@gpu
 def test_loss_bad_target(B):
     c = Case(20, 300, 64)
     c.target[4] = 300
