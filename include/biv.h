@@ -791,7 +791,7 @@ biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* desc, biv_stream_t strea
  *   dw float32 [d] = sum over rows of dy*x*inv (added to dw when accumulate is 1).
  * dres: the gradient that reaches r' past the norm, of dx's type, or NULL.  dy
  * BIV_F32 or BIV_BF16, dx likewise.  dx may be dres, or dy where types and strides
- * agree.  dw is summed in an order fixed by rows and d.  Workspace:
+ * agree.  dw is summed in an order fixed by rows, d and the types.  Workspace:
  * biv_rmsnorm_backward_fp8_workspace bytes, 16-byte aligned, no initial value. */
 typedef struct {
   const uint8_t* keep; const float* keep_scales; const float* inv;

@@ -11,6 +11,33 @@
 namespace biv {
 namespace {
 
+// two FP32 values in one register pair: an instruction for both (these kernels
+// issue as much as they load)
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void split(f32x2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -43,32 +70,28 @@ __device__ __forceinline__ void values4(uint32_t c, float s, float* f) {
     const __half2_raw h =
         __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> (16 * i)), __NV_E4M3);
     const float2 v = __half22float2(__half2(h));
-    f[2 * i] = v.x * s;
-    f[2 * i + 1] = v.y * s;
+    split(mul2(pair(v.x, v.y), pair(s, s)), f[2 * i], f[2 * i + 1]);
   }
 }
 
-// The codes of a lane's 8 values of a group that 16 lanes share, and its scale.
-// Every lane of the warp calls this; lanes behind the row hold zeros.
+// The codes of a lane's 8 values of a group that 16 lanes share, and its scale
+// from the group's largest magnitude.
 // Scale and quotients are those of IEEE divisions: with r the correctly rounded
 // reciprocal of the divisor, Markstein's correction q + (v - q s) r of q = v r
 // gives them in three operations where nothing under- or overflows; groups
 // whose scale is far from 1 divide.
-__device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = half_warp_max(amax);
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, float& s) {
   float q[8];
   if (amax > 0x1p-60f && amax < 0x1p60f) {
     constexpr float r448 = 1.0f / 448.0f;
     s = amax * r448;
     s = fmaf(fmaf(-s, 448.0f, amax), r448, s);
-    const float r = __frcp_rn(s);
+    const float r1 = __frcp_rn(s);
+    const f32x2 r = pair(r1, r1), minus_s = pair(-s, -s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q0 = v[i] * r;
-      q[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+    for (int i = 0; i < 8; i += 2) {
+      const f32x2 v2 = pair(v[i], v[i + 1]), q0 = mul2(v2, r);
+      split(fma2(fma2(q0, minus_s, v2), r, q0), q[i], q[i + 1]);
     }
   } else {
     s = amax == 0.f ? 1.0f : amax / 448.0f;
@@ -77,6 +100,14 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
   }
   return make_uint2(codes2(q[0], q[1]) | (codes2(q[2], q[3]) << 16),
                     codes2(q[4], q[5]) | (codes2(q[6], q[7]) << 16));
+}
+
+// (every lane of the warp calls this; lanes behind the row hold zeros)
+__device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  return quant8(v, half_warp_max(amax), s);
 }
 
 // ---------------------------------------------------- add + RMSNorm, FP8 ----
@@ -100,7 +131,7 @@ struct NormArgs {
 // r' is held as bf16 and its kept codes are written before the row's sum is
 // waited for: fewer registers, so more rows in flight.
 template <int CPT>
-__global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
+__global__ void __launch_bounds__(256, CPT <= 2 ? 5 : 4)
     add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -136,7 +167,7 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
       unpack8(rp[i], x);
       unpack8(rv[i], r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] += r[j];
+      for (int j = 0; j < 8; j += 2) split(add2(pair(x[j], x[j + 1]), pair(r[j], r[j + 1])), x[j], x[j + 1]);
       rp[i] = pack8(x);
       if (on && c < chunks) reinterpret_cast<uint4*>(a.res_out + row * a.ros)[c] = rp[i];
     }
@@ -173,6 +204,7 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
   }
   const float inv = 1.0f / sqrtf(tot / float(a.d) + a.eps);
   if (on && t == 0 && a.inv) a.inv[row] = inv;
+  const f32x2 inv2 = pair(inv, inv);
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * 256;
@@ -181,7 +213,8 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
     unpack8(rp[i], v);
     unpack8(wq[i], wv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (v[j] * inv) * wv[j];
+    for (int j = 0; j < 8; j += 2)
+      split(mul2(mul2(pair(v[j], v[j + 1]), inv2), pair(wv[j], wv[j + 1])), v[j], v[j + 1]);
     if (a.y && live) reinterpret_cast<uint4*>(a.y + row * a.ys)[c] = pack8(v);
     if (a.codes) {
       if (!live) {
@@ -199,8 +232,8 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 6 : 4)
 }
 
 // ------------------------------------------------------ RMSNorm backward ----
-// A CTA of W warps (W = ceil(d / 1024), at most 8) walks rows r0, r0 + grid, ...;
-// lane l of warp w owns the chunks (w * 4 + i) * 32 + l, i = 0..3, of 8 elements
+// A CTA of W warps (W = ceil(d / 512), at most 16) walks rows r0, r0 + grid, ...;
+// lane l of warp w owns the chunks (w * 2 + i) * 32 + l, i = 0, 1, of 8 elements
 // and keeps their dw sums over the CTA's rows, which a second kernel adds up.
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, int64_t e, float (&f)[8]) {
@@ -234,7 +267,7 @@ struct NormBackArgs {
   int rows, d;
 };
 
-constexpr int kBackChunks = 4;
+constexpr int kBackChunks = 2;
 
 // 8 values of a row as they lie in memory
 template <bool F32>
@@ -284,21 +317,21 @@ struct BackRow {
 };
 
 template <bool DYF, bool DXF, bool RES>
-__global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_constant__ NormBackArgs a) {
+__global__ void __launch_bounds__(512) rmsnorm_bwd_fp8_kernel(const __grid_constant__ NormBackArgs a) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[2][8];
+  __shared__ float red[2][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int chunks = a.d / 8, groups = (a.d + 127) / 128;
   const int c0 = warp * kBackChunks * 32 + lane;
-  float dw[kBackChunks][8];
+  f32x2 dw[kBackChunks][4];
   uint4 wq[kBackChunks];
 #pragma unroll
   for (int i = 0; i < kBackChunks; ++i) {
     const int c = c0 + i * 32;
     wq[i] = c < chunks ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dw[i][j] = 0;
   }
   BackRow<DYF, DXF, RES> next;
   next.load(a, blockIdx.x, c0, chunks, groups);
@@ -306,7 +339,8 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
     const BackRow<DYF, DXF, RES> r = next;
     if (row + gridDim.x < a.rows) next.load(a, row + gridDim.x, c0, chunks, groups);
-    float sum = 0.f;
+    f32x2 sum2 = 0;
+    const f32x2 inv2 = pair(r.inv, r.inv);
 #pragma unroll
     for (int i = 0; i < kBackChunks; ++i) {
       if (c0 + i * 32 >= chunks) continue;
@@ -316,13 +350,15 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
       r.dy[i].get(g);
       unpack8(wq[i], wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gx = g[j] * x[j];
-        sum = fmaf(gx, wv[j], sum);
-        dw[i][j] = fmaf(gx, r.inv, dw[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 gx = mul2(pair(g[2 * j], g[2 * j + 1]), pair(x[2 * j], x[2 * j + 1]));
+        sum2 = fma2(gx, pair(wv[2 * j], wv[2 * j + 1]), sum2);
+        dw[i][j] = fma2(gx, inv2, dw[i][j]);
       }
     }
-    sum = warp_sum(sum);
+    float even, odd;
+    split(sum2, even, odd);
+    float sum = warp_sum(even + odd);
     if (warps > 1) {      // (two buffers: one barrier per row)
       if (lane == 0) red[turn][warp] = sum;
       __syncthreads();
@@ -330,6 +366,7 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
       for (int i = 0; i < warps; ++i) sum += red[turn][i];
     }
     const float corr = r.inv * r.inv * r.inv * (sum / float(a.d));
+    const f32x2 minus_corr = pair(-corr, -corr);
 #pragma unroll
     for (int i = 0; i < kBackChunks; ++i) {
       const int c = c0 + i * 32;
@@ -340,12 +377,15 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
       r.dy[i].get(g);
       unpack8(wq[i], wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = r.inv * (g[j] * wv[j]) - x[j] * corr;
+      for (int j = 0; j < 8; j += 2) {
+        const f32x2 gw = mul2(pair(g[j], g[j + 1]), pair(wv[j], wv[j + 1]));
+        split(fma2(pair(x[j], x[j + 1]), minus_corr, mul2(inv2, gw)), o[j], o[j + 1]);
+      }
       if (RES) {
         float t[8];
         r.res[RES ? i : 0].get(t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += t[j];
+        for (int j = 0; j < 8; j += 2) split(add2(pair(o[j], o[j + 1]), pair(t[j], t[j + 1])), o[j], o[j + 1]);
       }
       store8<DXF>(a.dx, row * a.dxs + c * 8, o);
     }
@@ -353,7 +393,10 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_fp8_kernel(const __grid_const
 #pragma unroll
   for (int i = 0; i < kBackChunks; ++i) {
     const int c = c0 + i * 32;
-    if (c < chunks) store8<true>(a.parts, int64_t(blockIdx.x) * a.d + c * 8, dw[i]);
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split(dw[i][j], o[2 * j], o[2 * j + 1]);
+    if (c < chunks) store8<true>(a.parts, int64_t(blockIdx.x) * a.d + c * 8, o);
   }
 }
 
@@ -363,28 +406,32 @@ void launch_back(const NormBackArgs& a, int grid, int threads, cudaStream_t s) {
              grid, threads, 0, s, a);
 }
 
-// dw[c] = the CTAs' partial sums: 8 warps take partials w, w + 8, ... in order
+// dw[c] = the CTAs' partial sums: 32 warps take partials w, w + 32, ... in order
 // of 32 columns, and their sums are added in warp order
-__global__ void __launch_bounds__(256) dw_sum_kernel(const float* __restrict__ parts, int n, int d,
+__global__ void __launch_bounds__(1024) dw_sum_kernel(const float* __restrict__ parts, int n, int d,
                                                      float* __restrict__ dw, int accumulate) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sums[8][32];
+  __shared__ float sums[32][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < d)
-    for (int i = warp; i < n; i += 8) s += parts[int64_t(i) * d + c];
+#pragma unroll 8
+    for (int i = warp; i < n; i += 32) s += parts[int64_t(i) * d + c];
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < d) {
-    for (int w = 1; w < 8; ++w) s += sums[w][lane];
+#pragma unroll
+    for (int w = 1; w < 32; ++w) s += sums[w][lane];
     dw[c] = accumulate ? dw[c] + s : s;
   }
 }
 
-int back_warps(int d) { return (d + 1023) / 1024; }
-// CTAs of the backward: fixed by the row count and length, so that dw's order is
-int back_grid(int rows, int d) { return std::min(rows, 2432 / back_warps(d)); }
+int back_warps(int d) { return (d + 511) / 512; }
+// CTAs of the backward: fixed by the row count and length and by the types, so
+// that dw's order is.  As many as run at once: with bf16 gradients 20 warps per
+// SM (16384 x 2048: 44 us, with 16 49, with 24 56), with FP32 ones 16 (20: 85 us, 16 68).
+int back_grid(int rows, int d, bool bf16) { return std::min(rows, (bf16 ? 3040 : 2432) / back_warps(d)); }
 
 // --------------------------------------------------------------- SiLU-mul ----
 // Half a warp per (row, 128-wide group of gate and of up), 8 values a lane.
@@ -406,7 +453,21 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) {
   return (__umulhi(n, v.m) + n) >> v.s;
 }
 
-__global__ void __launch_bounds__(256) silu_mul_keep_kernel(
+// magnitudes of 8 gates and 8 ups: the largest of one half of a's words below,
+// of b's above (`halves` picks the low or the high ones)
+__device__ __forceinline__ __nv_bfloat162 largest(const uint4& a, const uint4& b, uint32_t halves) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {b.x, b.y, b.z, b.w};
+  __nv_bfloat162 p[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = __byte_perm(u[i], v[i], halves);
+    p[i] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  }
+  return __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+}
+
+// (six CTAs per SM: 81 us for 8192 x 6144, five 90)
+__global__ void __launch_bounds__(256, 6) silu_mul_keep_kernel(
     const uint16_t* __restrict__ gu, int64_t gs, uint32_t items, Divider by_groups, int I,
     uint8_t* __restrict__ keep, float* __restrict__ scales, uint16_t* __restrict__ y, int64_t ys) {
   pdl_wait();
@@ -427,8 +488,13 @@ __global__ void __launch_bounds__(256) silu_mul_keep_kernel(
   }
   unpack8(a, gv);
   unpack8(b, uv);
+  // the largest magnitudes of gate and of up, bf16 as they are, in one register
+  __nv_bfloat162 m = __hmax2(largest(a, b, 0x5410u), largest(a, b, 0x7632u));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float most = __low2float(m);
   float sg, su;
-  const uint2 kg = quant8(gv, sg), ku = quant8(uv, su);
+  const uint2 kg = quant8(gv, most, sg), ku = quant8(uv, __high2float(m), su);
   if (!live) return;
   *reinterpret_cast<uint2*>(keep + row * 2 * I + c0) = kg;
   *reinterpret_cast<uint2*>(keep + row * 2 * I + I + c0) = ku;
@@ -437,15 +503,35 @@ __global__ void __launch_bounds__(256) silu_mul_keep_kernel(
     scales[row * 2 * groups + groups + g] = su;
   }
   if (y) {
+    // gate / (1 + exp(-gate)): the divisor is at most exp(80), and Newton's step
+    // for the reciprocal and Markstein's for the quotient give the division's
+    // bits (for every bf16 gate; tested); groups with larger gates divide.
     float o[8];
+    if (most < 80.0f) {
+      const f32x2 one = pair(1.0f, 1.0f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = (gv[j] / (1.0f + expf(-gv[j]))) * uv[j];
+      for (int j = 0; j < 8; j += 2) {
+        // (with -1 / d and -gate the remainder's zero leaves the quotient's sign)
+        const f32x2 g2 = pair(-gv[j], -gv[j + 1]), d = add2(one, pair(expf(-gv[j]), expf(-gv[j + 1])));
+        float d0, d1, r0, r1;
+        split(d, d0, d1);
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+        f32x2 r = pair(-r0, -r1);
+        r = fma2(fma2(d, r, one), r, r);
+        const f32x2 q = mul2(g2, r);
+        split(mul2(fma2(fma2(d, q, g2), r, q), pair(uv[j], uv[j + 1])), o[j], o[j + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = (gv[j] / (1.0f + expf(-gv[j]))) * uv[j];
+    }
     *reinterpret_cast<uint4*>(y + row * ys + c0) = pack8(o);
   }
 }
 
 template <bool DYF, bool DGF>
-__global__ void __launch_bounds__(256) silu_mul_bwd_fp8_kernel(
+__global__ void __launch_bounds__(256, 6) silu_mul_bwd_fp8_kernel(
     const uint8_t* __restrict__ keep, const float* __restrict__ scales, const void* __restrict__ dy,
     int64_t dys, uint32_t items, Divider by_groups, int I, void* __restrict__ dgu, int64_t dgs,
     uint16_t* __restrict__ y, int64_t ys) {
@@ -468,13 +554,15 @@ __global__ void __launch_bounds__(256) silu_mul_bwd_fp8_kernel(
   values4(kg.y, sg, g + 4);
   values4(ku.x, su, u);
   values4(ku.y, su, u + 4);
+  const f32x2 one = pair(1.0f, 1.0f), minus = pair(-1.0f, -1.0f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float s = 1.0f / (1.0f + expf(-g[j]));
-    const float a = g[j] * s;
-    dg[j] = d[j] * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
-    du[j] = d[j] * a;
-    o[j] = a * u[j];
+  for (int j = 0; j < 8; j += 2) {
+    const f32x2 g2 = pair(g[j], g[j + 1]), u2 = pair(u[j], u[j + 1]), d2 = pair(d[j], d[j + 1]);
+    const f32x2 s = pair(1.0f / (1.0f + expf(-g[j])), 1.0f / (1.0f + expf(-g[j + 1])));
+    const f32x2 a = mul2(g2, s);
+    split(mul2(mul2(d2, u2), mul2(s, fma2(g2, fma2(s, minus, one), one))), dg[j], dg[j + 1]);
+    split(mul2(d2, a), du[j], du[j + 1]);
+    split(mul2(a, u2), o[j], o[j + 1]);
   }
   store8<DGF>(dgu, row * dgs + c0, dg);
   store8<DGF>(dgu, row * dgs + I + c0, du);
@@ -537,7 +625,7 @@ biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* d, biv_stream_t stream) 
 
 biv_status biv_rmsnorm_backward_fp8_workspace(int rows, int d, size_t* bytes) {
   BIV_REQUIRE(bytes && rows >= 0 && d > 0 && d <= 8192, "rmsnorm_backward_fp8_workspace: bad arguments");
-  *bytes = size_t(back_grid(rows, d)) * d * 4;
+  *bytes = size_t(back_grid(rows, d, true)) * d * 4;
   return BIV_OK;
 }
 
@@ -549,6 +637,7 @@ biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t
               "rmsnorm_backward_fp8: gradients are bf16 or f32");
   BIV_REQUIRE(d->accumulate == 0 || d->accumulate == 1, "rmsnorm_backward_fp8: accumulate is 0 or 1");
   BIV_REQUIRE(d->dw, "rmsnorm_backward_fp8: null dw");
+  const int grid = back_grid(d->rows, d->d, d->dy_dtype == BIV_BF16 && d->dx_dtype == BIV_BF16);
   cudaStream_t s = as_cuda(stream);
   if (d->rows > 0) {
     BIV_REQUIRE(d->keep && aligned16(d->keep) && d->keep_scales && d->inv && d->w && aligned16(d->w),
@@ -557,7 +646,7 @@ biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t
                     row_ok(d->dx, d->dx_stride, d->d, size_of(d->dx_dtype)) &&
                     (!d->dres || row_ok(d->dres, d->dres_stride, d->d, size_of(d->dx_dtype))),
                 "rmsnorm_backward_fp8: dy, dx and dres need 16-byte aligned rows");
-    const size_t need = size_t(back_grid(d->rows, d->d)) * d->d * 4;
+    const size_t need = size_t(back_grid(d->rows, d->d, true)) * d->d * 4;
     if (!d->workspace || d->workspace_bytes < need)
       return set_error(BIV_ERR_WORKSPACE, "rmsnorm_backward_fp8: workspace of %zu bytes needed", need);
     BIV_REQUIRE(aligned16(d->workspace), "rmsnorm_backward_fp8: workspace must be 16-byte aligned");
@@ -569,7 +658,7 @@ biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t
     a.parts = static_cast<float*>(d->workspace);
     a.rows = d->rows; a.d = d->d;
     const bool yf = d->dy_dtype == BIV_F32, xf = d->dx_dtype == BIV_F32;
-    const int grid = back_grid(d->rows, d->d), threads = 32 * back_warps(d->d);
+    const int threads = 32 * back_warps(d->d);
     if (yf)
       xf ? launch_back<true, true>(a, grid, threads, s) : launch_back<true, false>(a, grid, threads, s);
     else
@@ -577,8 +666,8 @@ biv_status biv_rmsnorm_backward_fp8(const biv_norm_bwd_fp8_desc* d, biv_stream_t
     biv_status st = check_launch("rmsnorm_backward_fp8");
     if (st != BIV_OK) return st;
   }
-  launch_pdl(dw_sum_kernel, (d->d + 31) / 32, 256, 0, s, static_cast<const float*>(d->workspace),
-             d->rows > 0 ? back_grid(d->rows, d->d) : 0, d->d, d->dw, d->accumulate);
+  launch_pdl(dw_sum_kernel, (d->d + 31) / 32, 1024, 0, s, static_cast<const float*>(d->workspace),
+             d->rows > 0 ? grid : 0, d->d, d->dw, d->accumulate);
   return check_launch("rmsnorm_backward_fp8 dw");
 }
 

@@ -288,6 +288,28 @@ def test_silu_mul_backward(B, rows, I, dy_t, dg_t):  # noqa: E741
 
 
 @gpu
+def test_every_gate_divides_exactly(B):
+    """silu(gate) of all 65536 bf16 gates, alone in their groups with zeros and among
+    others, has biv_silu_mul's bits (the quotient is formed without a division)."""
+    g = torch.arange(65536, device="cuda").to(torch.int32)
+    g = g.to(torch.int16).view(torch.bfloat16)
+    rows = [g.view(512, 128)]                                  # neighbours: groups of one exponent
+    rows.append(g.view(128, 512).t().contiguous().view(512, 128))     # groups of all magnitudes
+    alone = torch.zeros(65536 // 8, 128, dtype=torch.bfloat16, device="cuda")
+    alone[:, ::16] = g.view(-1, 8)
+    rows.append(alone)
+    for gate in rows:
+        for up in (1.0, -0.7265625, 3e38, 1e-30):
+            gu = torch.cat([gate, torch.full_like(gate, up)], 1)
+            y, ref = torch.empty_like(gate), torch.empty_like(gate)
+            B.biv_silu_mul(gu, ref)
+            keep, ks = u8(gate.size(0), 256), f32(gate.size(0), 2)
+            B.biv_silu_mul_keep_fp8(gu, y, keep, ks)
+            assert bool((y.isnan() == ref.isnan()).all())
+            assert same(torch.where(ref.isnan(), 0.0, y), torch.where(ref.isnan(), 0.0, ref))
+
+
+@gpu
 def test_large_gates(B):
     """Gates where exp overflows or vanishes: the limits, no NaN."""
     g = torch.tensor([[-448.0, -200.0, -100.0, -88.0, 88.0, 100.0, 200.0, 448.0] * 2], device="cuda")
