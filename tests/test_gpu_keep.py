@@ -140,6 +140,31 @@ def test_quotients_are_those_of_a_division(B):
 
 
 @gpu
+@pytest.mark.parametrize("exponent", [-50, 0, 50])
+def test_every_pair_of_mantissas(B, exponent):
+    """Kept codes of all 128 mantissas of a group's largest value times all bf16
+    values down to 2^-13 of it: an IEEE division's.  (Scaling both by a power of
+    two changes no quotient while nothing under- or overflows.)"""
+    rows = []
+    for m in range(128):
+        top = ((127 + exponent) << 7) + m                      # bits of the largest
+        below = torch.arange(top - 127 * 14, top, device="cuda", dtype=torch.int32).view(14, 127)
+        rows.append(torch.cat([torch.full((14, 1), top, device="cuda", dtype=torch.int32), below], 1))
+    x = (torch.cat(rows) << 16).view(torch.float32).bfloat16()
+    n = x.size(0)
+    codes, scales = u8(n, 128), f32(n, 1)
+    B.biv_add_rmsnorm_fp8(x, None, torch.ones(128, device="cuda").bfloat16(), EPS,
+                          y=torch.empty_like(x), keep=codes, keep_scales=scales)
+    want, ws = quantised(x.float())
+    assert same(scales, ws) and same(codes, want)
+    both = torch.cat([x, x.flip(0)], 1)
+    keep, ks = u8(n, 256), f32(n, 2)
+    B.biv_silu_mul_keep_fp8(both, None, keep, ks)
+    assert same(keep[:, :128], want) and same(keep[:, 128:], want.flip(0))
+    assert same(ks[:, :1], ws) and same(ks[:, 1:], ws.flip(0))
+
+
+@gpu
 def test_rows_with_infinities_and_nan(B):
     x = stream(6, 272, 3, spread=False).bfloat16()
     clean = x.clone()
