@@ -273,12 +273,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream) -> C.c_void_p:
+def _stream(stream) -> int:
     if stream is not None:
-        return C.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     if _raw_stream is not None:
-        return C.c_void_p(_raw_stream(_device()))
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return _raw_stream(_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(st: int, what: str):
@@ -684,15 +684,16 @@ def biv_policy_loss(desc: PolicyDesc, lp, dlp=None, stream=None):
     _check(load().biv_policy_loss(C.byref(desc), lp.data_ptr(), dlp, _stream(stream)), "biv_policy_loss")
 
 
-_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_F32, _BF16, _U8 = torch.float32, torch.bfloat16, torch.uint8
+_FLOATS = {_F32: F32, _BF16: BF16}
 
 
 def _matrix(what, t, T, V, dev):
     """(row stride, type) of a float32 or bf16 matrix of at least T rows of V values."""
-    kind, steps = _FLOATS.get(t.dtype), t.stride()
+    kind, steps, size = _FLOATS.get(t.dtype), t.stride(), t.shape
     if t.get_device() != dev:
         raise ValueError(f"{what} must be on the current CUDA device")
-    if kind is None or len(steps) != 2 or t.size(0) < T or t.size(1) != V or (V > 1 and steps[1] != 1):
+    if kind is None or len(steps) != 2 or size[0] < T or size[1] != V or (V > 1 and steps[1] != 1):
         raise ValueError(f"{what} must be a float32 or bf16 [T, V] tensor with rows of stride 1")
     # (one row: its stride says nothing, and may be below V)
     return (steps[0] if T > 1 else max(steps[0], V)), kind
@@ -736,7 +737,8 @@ def _vector(what, t, T, dev):
     """The address of a float32 vector of at least T values, or None."""
     if t is None:
         return None
-    _rows_ok(what, t, torch.float32, T, dev)
+    if t.dtype is not _F32 or t.get_device() != dev or t.numel() < T or not t.is_contiguous():
+        _rows_ok(what, t, _F32, T, dev)
     return t.data_ptr()
 
 
@@ -794,10 +796,9 @@ def _bf16_rows(what, t, rows, width, dev):
     """(address, row stride) of a bf16 matrix of at least `rows` rows, or of None."""
     if t is None:
         return None, 0
-    ld, kind = _matrix(what, t, rows, width, dev)
-    if kind != BF16:
+    if t.dtype is not _BF16:
         raise ValueError(f"{what} must be bf16")
-    return t.data_ptr(), ld
+    return t.data_ptr(), _matrix(what, t, rows, width, dev)[0]
 
 
 def _codes_of(what, codes, scales, rows, width, groups, dev):
@@ -806,9 +807,9 @@ def _codes_of(what, codes, scales, rows, width, groups, dev):
         raise ValueError(f"{what} and its scales go together")
     if codes is None:
         return None, None
-    _rows_ok(what, codes, torch.uint8, rows * width, dev)
-    _rows_ok(what + "'s scales", scales, torch.float32, rows * groups, dev)
-    return codes.data_ptr(), scales.data_ptr()
+    if codes.dtype is not _U8 or codes.get_device() != dev or codes.numel() < rows * width or not codes.is_contiguous():
+        _rows_ok(what, codes, _U8, rows * width, dev)
+    return codes.data_ptr(), _vector(what + "'s scales", scales, rows * groups, dev)
 
 
 def biv_add_rmsnorm_fp8(x, residual, w, eps, residual_out=None, y=None, codes=None, scales=None, keep=None,
