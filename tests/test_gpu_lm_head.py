@@ -276,6 +276,39 @@ def test_many_rows_dw(B):
 
 
 @gpu
+@pytest.mark.parametrize("T", [1023, 1024, 1025, 2048, 5000])
+@pytest.mark.parametrize("which", ["all", "few", "ties", "none", "one run"])
+def test_order_of_many_rows(B, T, which):
+    """Rows sorted by target in runs: targets on every side of every run, ties across
+    runs, runs without a counted row."""
+    t = torch.arange(T, device="cuda")
+    live = {"few": t % 97 == 5, "none": t < 0, "one run": (t >= 1000) & (t < 1030)}.get(which, t >= 0)
+    c = Case(T, 600, 64, seed=T, live=live, z=1e-3)
+    if which == "ties":
+        c.target.copy_((t * 7919 % 5 * 100).int())
+    c.target[~live] = 600
+    dh, dW = c.run(B, torch.float32, torch.float32)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    c.check(dh, dW)
+    again = c.run(B, torch.float32, torch.float32)
+    assert same(again[0], dh) and same(again[1], dW)
+
+
+@gpu
+def test_bad_targets_among_many_rows(B):
+    c = Case(1500, 300, 64)
+    c.target[7], c.target[1300] = 300, -1
+    dh, dW = c.run(B)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 2
+    c.live = torch.ones(1500, dtype=torch.bool, device="cuda")
+    c.live[7] = c.live[1300] = False
+    c.dlp = c.dlp * c.live
+    c.check(dh, dW)
+
+
+@gpu
 def test_offsets_beyond_32_bits(B):
     """More than 2^31 elements of W and dW."""
     T, V, K = 3, 140000, 16384
