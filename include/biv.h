@@ -725,11 +725,12 @@ biv_status biv_lm_head_loss(const biv_lm_loss_desc* desc, biv_stream_t stream);
  * and never stored.  dz enters the products as bf16 (for a FP32 gradient as
  * two bf16 parts); the term of a row's own target is added in FP32.  dh is the
  * sum of its chunks' FP32 products in ascending order: a row's dh depends on the
- * row, V, K and the gradients' types only.  dW adds the counted rows in ascending
- * order.  Every call repeats its bits.
+ * row, V, K and the gradients' types only.  dW adds the p terms of the counted
+ * rows in ascending order, then those of the rows whose target a row of W is, in
+ * an order fixed by the targets.  Every call repeats its bits.
  * T <= 2^20, V < 2^24, K <= 65536.  Workspace: biv_lm_head_backward_workspace
- * bytes (the sizes and gradient types of the call; about T (6 K + 48 Ki) bytes for
- * large T, with a FP32 gradient T (6 K + 96 Ki)), 256-byte aligned, caller-owned, no initial value; calls that can
+ * bytes (the sizes and gradient types of the call; about T (7 K + 48 Ki) bytes for
+ * large T, with a FP32 gradient T (7 K + 96 Ki)), 256-byte aligned, caller-owned, no initial value; calls that can
  * overlap on the GPU need separate ones. */
 typedef struct {
   int T, V, K;

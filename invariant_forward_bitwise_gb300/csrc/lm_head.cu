@@ -20,7 +20,7 @@
 //    the products as bf16, the type of the other operands: an error of at most
 //    2^-8 of each of them; for FP32 gradients as two bf16 parts, hi + lo (2^-16).
 //  - dh is summed over the vocabulary in chunks (at most kMaxChunk columns, a
-//    length that follows V alone), each accumulated from zero in TMEM in
+//    length that follows V and K), each accumulated from zero in TMEM in
 //    ascending columns, and the chunks added in ascending order in FP32: a row's
 //    dh depends on that row, V, K and the gradients' types only.  dW is one
 //    accumulation over the counted rows in ascending order.
@@ -42,7 +42,12 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
 
 namespace {
 
-constexpr int kMaxChunk = 8192;   // vocabulary columns per FP32 partial of dh, at most
+// Vocabulary columns per FP32 partial of dh: a length that follows V and K.  As
+// many chunks as make two dh tiles of 256 rows for each of 76 pairs of CTAs, but
+// chunks of 4096 to 8192 columns (a dh tile of K = 256 and 8192 columns is as long
+// as all the rest of 9 rows: 250 us, now 190; shorter ones cost partials), and 8
+// chunks at least of a small vocabulary.
+constexpr int kMinChunk = 4096, kMaxChunk = 8192;
 constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
 constexpr int kTN = 256;          // tile columns: each CTA brings half of B
 constexpr int kTK = 64;           // K elements per stage
@@ -65,7 +70,6 @@ struct Rows {
   int* skey;                // [cap] targets in ascending order (rows ascending among equals)
   int* srow;                // [cap] the counted row that each belongs to
   float* lse;               // [cap]
-  float* dlp;               // [cap]
   float* cp;                // [cap] dlse - dlp: the factor of p
   float* dzt;               // [cap] dz at the target
   uint16_t* h;              // [cap][kp] gathered rows, zeros behind them and behind K
@@ -78,6 +82,9 @@ struct Rows {
   // more than kRun rows: runs of kRun of them, sorted
   int* run;                 // [runs][kRun] targets in ascending order, INT_MAX behind them
   int* run_n;               // [runs] rows that count
+  // sums of dzt * h over 8 and 64 places of that order that have one target
+  float* sum8;              // [cap / 8][kp]
+  float* sum64;             // [cap / 64][kp]
   int2* run_at;             // [T] a row's place among those of its run that count, in row and in target order
 };
 
@@ -88,10 +95,11 @@ struct Layout {
   int ahead;                // chunks whose scores are formed ahead of their products
   int ring;                 // chunks of dz held
   int parts;                // bf16 parts of dz
-  size_t off[19], bytes;
+  size_t off[21], bytes;
 };
 
 constexpr int kRun = 1024;
+constexpr int kSums = 64;         // rows above which sums over equal targets are formed
 
 // dh's partials lie side by side up to this size (few rows: its chunks are then
 // independent of one another, and one kernel adds them up); above, each chunk
@@ -103,9 +111,9 @@ Layout layout(int T, int V, int K, bool f32) {
   l.cap = (T + kTM - 1) / kTM * kTM;
   l.kp = (K + kTK - 1) / kTK * kTK;
   l.ka = (K + kTN - 1) / kTN * kTN;
-  // (by V alone: dh's bits follow it.  8 chunks or more shorten the chain of
-  // stages of a small vocabulary's dh)
-  l.chunk = std::min(kMaxChunk, ((V + 7) / 8 + kTN - 1) / kTN * kTN);
+  const int want = std::max(1, 152 / (l.ka / kTN));
+  l.chunk = std::min(std::max(kMinChunk, (V + want - 1) / want), std::min(kMaxChunk, (V + 7) / 8));
+  l.chunk = (l.chunk + kTN - 1) / kTN * kTN;
   l.chunks = (V + l.chunk - 1) / l.chunk;
   l.parts = f32 ? 2 : 1;
   const size_t part = size_t(l.cap) * l.ka * 4;
@@ -118,14 +126,15 @@ Layout layout(int T, int V, int K, bool f32) {
   l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (144 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
   const size_t runs = T > kRun ? (T + kRun - 1) / kRun : 0;
-  const size_t sizes[19] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
+  const size_t sums = T > kSums ? size_t(l.cap) * l.kp * 4 : 0;
+  const size_t sizes[21] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * l.kp * 2,
                             part * l.slots, size_t(l.parts) * l.cap * l.ring * l.chunk * 2, 16,
                             size_t(l.chunks) * 4, size_t(l.chunks) * 4, size_t(l.chunks) * 4,
-                            runs * kRun * 4, runs * 4, runs * kRun * 8};
+                            runs * kRun * 4, runs * 4, runs * kRun * 8, sums / 8, sums / 64};
   l.bytes = 0;
-  for (int i = 0; i < 19; ++i) {
+  for (int i = 0; i < 21; ++i) {
     l.off[i] = l.bytes;
     l.bytes += (sizes[i] + 255) / 256 * 256;
   }
@@ -141,7 +150,6 @@ Rows rows_of(const Layout& l, void* ws) {
   r.skey = reinterpret_cast<int*>(b + l.off[3]);
   r.srow = reinterpret_cast<int*>(b + l.off[4]);
   r.lse = reinterpret_cast<float*>(b + l.off[5]);
-  r.dlp = reinterpret_cast<float*>(b + l.off[6]);
   r.cp = reinterpret_cast<float*>(b + l.off[7]);
   r.dzt = reinterpret_cast<float*>(b + l.off[8]);
   r.h = reinterpret_cast<uint16_t*>(b + l.off[9]);
@@ -154,6 +162,8 @@ Rows rows_of(const Layout& l, void* ws) {
   r.run = reinterpret_cast<int*>(b + l.off[16]);
   r.run_n = reinterpret_cast<int*>(b + l.off[17]);
   r.run_at = reinterpret_cast<int2*>(b + l.off[18]);
+  r.sum8 = reinterpret_cast<float*>(b + l.off[19]);
+  r.sum64 = reinterpret_cast<float*>(b + l.off[20]);
   return r;
 }
 
@@ -220,7 +230,8 @@ __global__ void __launch_bounds__(kRun) sort_rows_kernel(const int32_t* __restri
 // 256: the call took 4535 us with the former).
 template <bool RUNS>
 __global__ void __launch_bounds__(256) gather_kernel(
-    const uint16_t* __restrict__ h, int64_t ldh, const int32_t* __restrict__ target,
+    const uint16_t* __restrict__ h, int64_t ldh, const uint16_t* __restrict__ W, int64_t ldw,
+    const int32_t* __restrict__ target,
     const float* __restrict__ lse, const float* __restrict__ dlp, const float* __restrict__ dlse,
     int T, int V, int K, int kp, int cap, int chunks, void* dh, int64_t lddh, int dh_f32, Rows r,
     int* err) {
@@ -311,18 +322,91 @@ __global__ void __launch_bounds__(256) gather_kernel(
   }
   const int i = before;
   const uint4* src = reinterpret_cast<const uint4*>(h + t * ldh);
+  const uint4* wt = reinterpret_cast<const uint4*>(W + tg * ldw);
   uint4* dst = reinterpret_cast<uint4*>(r.h + int64_t(i) * kp);
-  for (int c = lane; c < kp / 8; c += 32)
-    dst[c] = c < K / 8 ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+  float z = 0.f;
+  constexpr int kAhead = 8;      // pieces in flight (2048 columns)
+  for (int c0 = lane; c0 < kp / 8; c0 += 32 * kAhead) {
+    uint4 v[kAhead], w[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      v[q] = w[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (c0 + 32 * q < K / 8) {
+        v[q] = __ldg(src + c0 + 32 * q);
+        w[q] = __ldg(wt + c0 + 32 * q);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      if (c0 + 32 * q < kp / 8) dst[c0 + 32 * q] = v[q];
+      const uint32_t a[4] = {v[q].x, v[q].y, v[q].z, v[q].w}, b[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        z = fmaf(__uint_as_float(a[x] << 16), __uint_as_float(b[x] << 16), z);
+        z = fmaf(__uint_as_float(a[x] & 0xFFFF0000u), __uint_as_float(b[x] & 0xFFFF0000u), z);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   if (lane == 0) {
     r.idx[i] = t;
     r.target[i] = tg;
     r.skey[lower] = tg;
     r.srow[lower] = i;
-    const float c = dlp[t];
-    r.lse[i] = lse[t];
-    r.dlp[i] = c;
-    r.cp[i] = (dlse ? dlse[t] : 0.f) - c;
+    const float c = dlp[t], l = lse[t], cp = (dlse ? dlse[t] : 0.f) - c;
+    r.lse[i] = l;
+    r.cp[i] = cp;
+    r.dzt[i] = fmaf(cp, expf(z - l), c);
+  }
+}
+
+// v += f * 8 bf16
+__device__ __forceinline__ void add_row8(float (&v)[8], float f, const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    v[2 * y] = fmaf(f, __uint_as_float(w[y] << 16), v[2 * y]);
+    v[2 * y + 1] = fmaf(f, __uint_as_float(w[y] & 0xFFFF0000u), v[2 * y + 1]);
+  }
+}
+
+// Of every 8 places of the order by target that have one target, the sum of
+// dzt * h, and of every 64 the sum of these.  A token that many rows have as
+// their target would otherwise have as many rows added to its row of dW one
+// after another, by one lane (2458 rows of two targets: 1700 us).  A CTA per 64 places
+// and 2048 columns.
+__global__ void __launch_bounds__(256) target_sums_kernel(Rows r, int kp) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = *r.n, p0 = blockIdx.x * 64, c = blockIdx.y * 2048 + threadIdx.x * 8;
+  if (p0 + 8 > n || c >= kp) return;
+  float all[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) all[x] = 0.f;
+  for (int p = p0; p < p0 + 64 && p + 8 <= n; p += 8) {
+    if (r.skey[p] != r.skey[p + 7]) continue;
+    uint4 u[8];
+    float f[8], s[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int row = r.srow[p + x];
+      f[x] = r.dzt[row];
+      u[x] = *reinterpret_cast<const uint4*>(r.h + int64_t(row) * kp + c);
+      s[x] = 0.f;
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) add_row8(s, f[x], u[x]);
+    float4* d = reinterpret_cast<float4*>(r.sum8 + int64_t(p / 8) * kp + c);
+    d[0] = make_float4(s[0], s[1], s[2], s[3]);
+    d[1] = make_float4(s[4], s[5], s[6], s[7]);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) all[x] += s[x];
+  }
+  if (p0 + 64 <= n && r.skey[p0] == r.skey[p0 + 63]) {
+    float4* d = reinterpret_cast<float4*>(r.sum64 + int64_t(p0 / 64) * kp + c);
+    d[0] = make_float4(all[0], all[1], all[2], all[3]);
+    d[1] = make_float4(all[4], all[5], all[6], all[7]);
   }
 }
 
@@ -340,6 +424,7 @@ struct Maps {
 struct Args {
   Rows r;
   int V, K, kp, ka, cap;
+  int sums;                // sums over equal targets are there
   int w2;                  // W's map brings two panels at once (K % 64 == 0)
   int chunk, chunks, ahead, ring, slots;
   int parts, parts_h, parts_w;
@@ -917,14 +1002,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         warp_keys(skey, plan.n, v0 + row - lane, lane, first, last);
         if (first < last) {
           r0 = a.r.srow[first];
-          dzt = __ldcg(a.r.dzt + r0);
+          dzt = a.r.dzt[r0];
         }
       } else if (live && it.type == kScores) {
         lse = a.r.lse[row];
         cp = a.r.cp[row];
         tgt = a.r.target[row];
       } else if (live && end) {
-        dzt = __ldcg(a.r.dzt + row);
+        dzt = a.r.dzt[row];
         out = a.r.idx[row] * a.lddh;
         tgt = a.r.target[row];
       }
@@ -987,15 +1072,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 32; ++x) d[x] = c + x < cols ? d[x] : 0.f;
           }
-          if (tc >= c && tc < c + 32) {
-            float full = a.r.dlp[row];
+          if (tc >= c && tc < c + 32) {                      // (the target's term is added apart)
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (c + x == tc) {
-                full += d[x];
-                d[x] = 0.f;
-              }
-            a.r.dzt[row] = full;
+            for (int x = 0; x < 32; ++x) d[x] = c + x == tc ? 0.f : d[x];
           }
           if (F32) {
             stage_begin();
@@ -1046,11 +1125,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           float f[32];
           product(g, f);
           const bool on = live && c < a.K;
-          if (targets && on && first < last) {
-            add_row32(f, dzt, a.r.h + int64_t(r0) * a.kp + c, 32);
-            for (int t = first + 1; t < last; ++t) {
-              const int r = a.r.srow[t];
-              add_row32(f, __ldcg(a.r.dzt + r), a.r.h + int64_t(r) * a.kp + c, 32);
+          if (targets && on) {
+            // (sums over equal targets where they are)
+            for (int t = first; t < last;) {
+              if (a.sums && (t & 7) == 0 && t + 8 <= last) {
+                const bool more = (t & 63) == 0 && t + 64 <= last;
+                add32(more ? a.r.sum64 : a.r.sum8, int64_t(t >> (more ? 6 : 3)) * a.kp + c, 1, true, 32, f);
+                t += more ? 64 : 8;
+              } else {
+                const int r = t == first ? r0 : a.r.srow[t];
+                add_row32(f, t == first ? dzt : a.r.dzt[r], a.r.h + int64_t(r) * a.kp + c, 32);
+                ++t;
+              }
             }
           }
           if (a.accumulate && on)
@@ -1503,6 +1589,7 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
   memset(&m, 0, sizeof(m));
   a.dw_tma = d->dW && aligned16(d->dW) && (d->lddw * wb) % 16 == 0;
   a.w2 = K % 64 == 0;
+  a.sums = d->dW && T > kSums;
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = (int64_t(V) + kTN - 1) / kTN + l.chunks;
   BIV_REQUIRE(tm * tn + tk * (tm * l.chunks + tn) < (int64_t(1) << 30), "lm_head_backward: too many tiles");
   const int64_t dzc = int64_t(l.ring) * l.chunk, dzr = int64_t(l.cap) * l.parts;
@@ -1530,9 +1617,13 @@ biv_status biv_lm_head_backward(const biv_lm_grad_desc* d, biv_stream_t stream) 
     launch_pdl(sort_rows_kernel, (T + kRun - 1) / kRun, kRun, 0, s, d->target, d->dlp, d->dlse, T, V, a.r);
     if ((st = check_launch("lm_head_backward order")) != BIV_OK) return st;
   }
-  launch_pdl(T > kRun ? gather_kernel<true> : gather_kernel<false>, (l.cap + 7) / 8, 256, 0, s, d->h, d->ldh, d->target, d->lse, d->dlp, d->dlse, T, V,
+  launch_pdl(T > kRun ? gather_kernel<true> : gather_kernel<false>, (l.cap + 7) / 8, 256, 0, s, d->h, d->ldh, d->W, d->ldw, d->target, d->lse, d->dlp, d->dlse, T, V,
              K, l.kp, l.cap, l.chunks, d->dh, d->lddh, a.dh_f32, a.r, a.err);
   if ((st = check_launch("lm_head_backward rows")) != BIV_OK) return st;
+  if (a.sums) {
+    launch_pdl(target_sums_kernel, dim3(l.cap / 64, (l.kp + 2047) / 2048), 256, 0, s, a.r, l.kp);
+    if ((st = check_launch("lm_head_backward targets")) != BIV_OK) return st;
+  }
   if ((st = l.parts == 2 ? launch_grad<true>(m, a, s) : launch_grad<false>(m, a, s)) != BIV_OK) return st;
   if (!d->dh || l.slots == 1) return BIV_OK;
   launch_pdl(dh_fold_kernel, dim3(T, (K + 1023) / 1024), 256, 0, s, a.r, d->W, d->ldw, K, l.ka, l.cap,

@@ -296,6 +296,20 @@ def test_order_of_many_rows(B, T, which):
 
 
 @gpu
+@pytest.mark.parametrize("T", [64, 65, 200, 1300])
+@pytest.mark.parametrize("V", [2, 3, 40])
+def test_targets_that_many_rows_share(B, T, V):
+    """Sums over 8 and 64 rows of one target, their ends, and single rows beside them."""
+    c = Case(T, V, 136, seed=V, live=torch.arange(T, device="cuda") % 11 != 3)
+    c.target.copy_((c.target.float() / V).square().mul(V).int())      # low ones are frequent
+    for t in (torch.bfloat16, torch.float32):
+        c.check(*c.run(B, t, t))
+    _, dW = c.run(B, want=(False, True))
+    again = c.run(B, want=(False, True))[1]
+    assert same(dW, again)
+
+
+@gpu
 def test_bad_targets_among_many_rows(B):
     c = Case(1500, 300, 64)
     c.target[7], c.target[1300] = 300, -1
