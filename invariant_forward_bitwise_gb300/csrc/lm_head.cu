@@ -15,8 +15,9 @@
 //    gradient: the rows that count are gathered first, so that what the others
 //    hold is never multiplied, and no time is spent on them.
 //  - The term of a row's own target is usually the largest by far.  It stays
-//    out of the matrix products and is added in FP32, to dh by the fold and to
-//    dW by the epilogue of the tile that holds the target.  The p terms enter
+//    out of the matrix products: its coefficient is formed while the rows are
+//    gathered, and it is added in FP32, to dh by the fold and to dW by the
+//    epilogue of the tile that holds the target.  The p terms enter
 //    the products as bf16, the type of the other operands: an error of at most
 //    2^-8 of each of them; for FP32 gradients as two bf16 parts, hi + lo (2^-16).
 //  - dh is summed over the vocabulary in chunks (at most kMaxChunk columns, a

@@ -21,8 +21,10 @@ tokens, every row producing a logprob, as in the trainer recompute; one more
 step runs inside cudaProfilerStart/Stop) and hybrid_decode_step (one decode step of the
 Mamba-2 hybrid unit for 3 sequences, graph-timed, then eagerly inside
 cudaProfilerStart/Stop), policy_logits (the policy loss from 1216 x 151936 FP32,
-1216 x 131072 bf16 and 1000 x 32003 FP32 logits) and adamw_8bit (67 M bf16
-weights, 8-bit states, stochastic rounding).
+1216 x 131072 bf16 and 1000 x 32003 FP32 logits), adamw_8bit (67 M bf16
+weights, 8-bit states, stochastic rounding), lm_head_grad (loss and gradient at
+200, 4096 rows x 151936 x 2048 in bf16, 1000 x 32003 x 2048 in FP32) and
+rows_8bit (the norm, its backward and the SiLU-mul with rows kept in 8 bits).
 Each case times REPS calls with CUDA events after one warm-up call and
 prints the time and the rate against the case's algorithmic bytes or FLOPs;
 it is also the command that the ncu summaries in profiles/ capture.
@@ -423,6 +425,42 @@ elif case == "adamw_8bit":
     opt = optim.AdamW([w], [grad], bits=8, rounding="stochastic", lr=1e-6)
     ms = timeit(opt.step)
     print(f"adamw_8bit n={n}: {ms*1e3:.1f} us  {n*(10 + 16/128)/(ms/1e3)/1e9:.0f} GB/s")
+elif case == "lm_head_grad":
+    for T, V, dt in ((200, 151936, torch.bfloat16), (4096, 151936, torch.bfloat16), (1000, 32003, torch.float32)):
+        K = 2048
+        h = torch.randn(T, K, device="cuda").bfloat16()
+        w = (torch.randn(V, K, device="cuda") * 0.05).bfloat16()
+        target = torch.randint(0, V, (T,), dtype=torch.int32, device="cuda")
+        lp, lse, dlp = (torch.empty(T, device="cuda") for _ in range(3))
+        dh, dw, stats = torch.empty(T, K, dtype=dt, device="cuda"), torch.empty(V, K, dtype=dt, device="cuda"), torch.empty(4, device="cuda")
+        ws = torch.empty(biv.biv_lm_head_loss_workspace(T, V), dtype=torch.uint8, device="cuda")
+        gws = torch.empty(biv.biv_lm_head_backward_workspace(T, V, K, dt, dt), dtype=torch.uint8, device="cuda")
+        ms = timeit(lambda: biv.biv_lm_head_loss(h, w, target, lp, lse, stats, ws, dlp=dlp))
+        print(f"lm_head_loss T={T} V={V}: {ms*1e3:.1f} us  {2*T*V*K/(ms/1e3)/1e12:.0f} TFLOP/s")
+        ms = timeit(lambda: biv.biv_lm_head_backward(h, w, target, lse, dlp, dh, dw, gws))
+        print(f"lm_head_grad T={T} V={V} {dt}: {ms*1e3:.1f} us  {6*T*V*K/(ms/1e3)/1e12:.0f} TFLOP/s")
+        del h, w, dh, dw, ws, gws
+elif case == "rows_8bit":
+    u8, bf = torch.uint8, torch.bfloat16
+    e = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
+    rate = lambda what, ms, n: print(f"{what}: {ms*1e3:.1f} us  {n/(ms/1e3)/1e9:.0f} GB/s")  # noqa: E731
+    R, d = 16384, 4096
+    x, r, w = torch.randn(R, d, device="cuda").bfloat16(), torch.randn(R, d, device="cuda").bfloat16(), torch.ones(d, device="cuda").bfloat16()
+    ro, y, c, sc, k, ks, inv = e(R, d, t=bf), e(R, d, t=bf), e(R, d, t=u8), e(R, d // 128), e(R, d, t=u8), e(R, d // 128), e(R)
+    ms = timeit(lambda: biv.biv_add_rmsnorm_fp8(x, r, w, 1e-6, residual_out=ro, y=y, codes=c, scales=sc, keep=k,
+                                                keep_scales=ks, inv=inv))
+    rate(f"add_rmsnorm_fp8 {R} x {d}, all outputs", ms, R * d * (10 + 8 / 128))
+    dw, ws = e(d), e(biv.biv_rmsnorm_backward_fp8_workspace(R, d), t=u8)
+    ms = timeit(lambda: biv.biv_rmsnorm_backward_fp8(k, ks, inv, w, y, x, dw, ws, dres=ro))
+    rate(f"rmsnorm_backward_fp8 {R} x {d}, bf16 with a residual's gradient", ms, R * d * (7 + 4 / 128))
+    R, width = 8192, 6144
+    gu = torch.randn(R, 2 * width, device="cuda").bfloat16()
+    y, k, ks, dgu = e(R, width, t=bf), e(R, 2 * width, t=u8), e(R, 2 * width // 128), e(R, 2 * width, t=bf)
+    ms = timeit(lambda: biv.biv_silu_mul_keep_fp8(gu, y, k, ks))
+    rate(f"silu_mul_keep_fp8 {R} x {width}", ms, R * width * (8 + 8 / 128))
+    dy, y2 = torch.randn(R, width, device="cuda").bfloat16(), e(R, width, t=bf)
+    ms = timeit(lambda: biv.biv_silu_mul_backward_fp8(k, ks, dy, dgu, y=y2))
+    rate(f"silu_mul_backward_fp8 {R} x {width}, bf16, y again", ms, R * width * (10 + 8 / 128))
 else:
     M, N, K = {"gemm_prefill": (8192, 2048, 6144), "gemm_qkv": (16384, 4096, 2048),
                "gemm_decode": (64, 2048, 6144), "lm_head": (4096, 151936, 2048)}[case]
