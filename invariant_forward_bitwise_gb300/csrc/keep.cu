@@ -119,7 +119,8 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float& s) {
 }
 
 // ---------------------------------------------------- add + RMSNorm, FP8 ----
-// A team of W warps per row (W = ceil(d / 256), at most 8), 8 / W rows per CTA.
+// A team of W warps per row (W = ceil(d / 256), at most 8), 8 / W rows per CTA (of
+// 8 / W W warps: idle ones would cost as much as the others).
 // Thread t of a team owns the 8-element chunks t, t + 256, ...: the sums run
 // in biv_add_rmsnorm's order (its warps without chunks add zeros), so inv and
 // y have its bits.  Half a warp holds a 128-element group.
@@ -139,15 +140,15 @@ struct NormArgs {
 // r' is held as bf16 and its kept codes are written before the row's sum is
 // waited for: fewer registers, so more rows in flight.
 template <int CPT>
-__global__ void __launch_bounds__(256, CPT <= 2 ? 5 : 4)
+__global__ void __launch_bounds__(256, CPT == 1 ? 8 : CPT == 2 ? 5 : 4)
     add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ float warp_ss[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = 8 / a.team, mine = warp / a.team;        // rows per CTA, this warp's
+  const int per = (blockDim.x >> 5) / a.team, mine = warp / a.team;        // rows per CTA, this warp's
   const int64_t row = int64_t(blockIdx.x) * per + mine;
-  const bool on = mine < per && row < a.rows;
+  const bool on = row < a.rows;
   const int t = (warp - mine * a.team) * 32 + lane;        // thread of the team
   const int chunks = a.d / 8, groups = (a.d + 127) / 128;
   uint4 rp[CPT], wq[CPT];
@@ -194,6 +195,7 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 5 : 4)
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = t + i * 256;
+      if (c - lane >= chunks) break;           // (the whole warp)
       float v[8], s;
       unpack8(rp[i], v);
       const uint2 k = quant8(v, s);
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(256, CPT <= 2 ? 5 : 4)
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int c = t + i * 256;
+    if (c - lane >= chunks) break;
     const bool live = on && c < chunks;
     float v[8], wv[8];
     unpack8(rp[i], v);
@@ -628,7 +631,7 @@ biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* d, biv_stream_t stream) 
              : cpt == 2 ? add_rmsnorm_fp8_kernel<2>
              : cpt == 3 ? add_rmsnorm_fp8_kernel<3>
                         : add_rmsnorm_fp8_kernel<4>,
-             grid, 256, 0, s, a);
+             grid, 32 * a.team * per, 0, s, a);
   return check_launch("add_rmsnorm_fp8");
 }
 
