@@ -1735,12 +1735,14 @@ biv_status lm_head_groups(const char* what, const uint16_t* h, int64_t ldh, cons
   if (!make_bf16_maps(&ta, &tb, h, ldh, M, W, ldw, V, K, p))
     return set_error(BIV_ERR_CUDA, "%s: tensor map encoding failed", what);
   auto kern = gemm_bf16_kernel<kWideN, true, false, true>;
-  static bool attr = false;
-  if (!attr) {
+  static bool set[64] = {};      // by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(kSmemBudget)) != cudaSuccess)
       return set_error(BIV_ERR_CUDA, "%s: cannot set shared memory size", what);
-    attr = true;
+    if (dev >= 0 && dev < 64) set[dev] = true;
   }
   GemmArgs a;
   memset(&a, 0, sizeof(a));

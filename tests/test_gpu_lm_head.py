@@ -187,6 +187,26 @@ def test_a_row_with_nan_stays_alone_in_dh(B):
 
 
 @gpu
+@pytest.mark.parametrize("low", [-3.3e38, -float("inf")])
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float32])
+def test_weights_whose_logits_are_minus_infinity(B, low, t):
+    """A vocabulary row that no h can reach has p = 0: its gradient is zero and the
+    others' are as without it, in the rows behind the counted ones of a tile too."""
+    c = Case(70, 300, 64)
+    c.h.copy_(c.h.abs() + 1)
+    c.W[5] = low
+    c.target[c.target == 5] = 6
+    keep = torch.arange(300, device="cuda") != 5
+    c.logits = c.h.to(F64) @ torch.where(keep[:, None], c.W.to(F64), 0.0).t()
+    c.logits[:, 5] = -1e4
+    c.lse = torch.logsumexp(c.logits, 1).float()
+    dh, dW = c.run(B, t, t)
+    assert bool((dW[5] == 0).all())
+    c.W[5] = 0                                     # (check multiplies it by p = 0)
+    c.check(dh if low > -float("inf") else None, dW)
+
+
+@gpu
 def test_every_row_has_the_same_target(B):
     c = Case(600, 900, 256, targets=450)
     for t in (torch.bfloat16, torch.float32):
