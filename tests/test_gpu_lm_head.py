@@ -410,6 +410,39 @@ def test_a_graph_and_two_streams_repeat_the_bits(B):
         assert same(dh, eager[k][0]) and same(dW, eager[k][1])
 
 
+@gpu
+def test_a_captured_gradient_of_many_rows_on_other_inputs(B):
+    """Sorted runs and sums over equal targets: one graph, replayed with other targets
+    and another number of counted rows, while a second stream runs a call of its own."""
+    T, V, K = 1500, 700, 136
+    cs = [Case(T, V, K, seed=s, live=torch.arange(T, device="cuda") % 7 > 2 * s) for s in (0, 1, 2)]
+    cs[1].target.copy_(cs[1].target % 4)
+    for c in cs:
+        c.h[~c.live] = 0
+    f32 = torch.float32
+    eager = [[x.clone() for x in c.run(B, f32, f32)] for c in cs]
+    new = lambda: (torch.empty(T, K, device="cuda"), torch.empty(V, K, device="cuda"),  # noqa: E731
+                   torch.empty(B.biv_lm_head_backward_workspace(T, V, K, f32, f32), dtype=torch.uint8, device="cuda"))
+    (dh, dW, ws), other = new(), new()
+    at = [t.clone() for t in (cs[0].h, cs[0].W, cs[0].target, cs[0].lse, cs[0].dlp)]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        B.biv_lm_head_backward(*at, dh, dW, ws)
+    side = torch.cuda.Stream()
+    for k in (1, 0, 2, 1):
+        for t, v in zip(at, (cs[k].h, cs[k].W, cs[k].target, cs[k].lse, cs[k].dlp)):
+            t.copy_(v)
+        torch.cuda.synchronize()
+        g.replay()
+        c = cs[2 - k]
+        B.biv_lm_head_backward(c.h, c.W, c.target, c.lse, c.dlp, *other, stream=side)
+        torch.cuda.synchronize()
+        assert same(dh, eager[k][0]) and same(dW, eager[k][1])
+        assert same(other[0], eager[2 - k][0]) and same(other[1], eager[2 - k][1])
+    assert B.biv_poll_error() == 0
+
+
 # ---------------------------------------------------------------- forward --
 @gpu
 @pytest.mark.parametrize("T,V,K", [(1, 1, 8), (13, 4096, 256), (130, 1001, 72), (300, 20011, 688), (5, 30000, 2048)])
@@ -499,6 +532,35 @@ def test_row_tiles_that_do_not_count(B, which):
     nll, sq = -(share * lp.to(F64)).sum(), (share * lse.to(F64) ** 2).sum()
     want = torch.stack([nll + 0.5 * sq, nll, sq, w.sum()])
     assert torch.allclose(stats.to(F64), want, rtol=2.0 ** -20, atol=0)
+
+
+@gpu
+def test_a_captured_loss_on_other_masks(B):
+    """The tiles that are left out follow the targets of each replay."""
+    T, V, K = 1111, 36000, 2048
+    g = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(V, K, device="cuda", generator=g) * 0.04).bfloat16()
+    target = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    row = torch.arange(T, device="cuda")
+    masks = [row >= 0, row % 500 >= 300, row < 0, row == 1110]
+    out = lambda: [torch.empty(T, device="cuda") for _ in range(3)] + [torch.empty(4, device="cuda")]  # noqa: E731
+    ws = torch.empty(B.biv_lm_head_loss_workspace(T, V), dtype=torch.uint8, device="cuda")
+    eager, got, at = [], out(), target.clone()
+    for m in masks:
+        o = out()
+        B.biv_lm_head_loss(h, W, torch.where(m, target, -100), *o[:2], o[3], ws, dlp=o[2])
+        eager.append(o)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        B.biv_lm_head_loss(h, W, at, *got[:2], got[3], ws, dlp=got[2])
+    for k in (1, 3, 0, 2, 0):
+        at.copy_(torch.where(masks[k], target, -100))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, eager[k]))
+    assert B.biv_poll_error() == 0
 
 
 @gpu
