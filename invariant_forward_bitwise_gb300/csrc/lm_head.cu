@@ -56,12 +56,13 @@ constexpr int kOperand = 128 * kTK * 2;   // bytes of a CTA's part of A or B in 
 constexpr int kStages = 6;
 constexpr int kEpi = 8;
 constexpr int kThreads = 96 + 32 * kEpi;
+constexpr int kLong = 16;         // stages of a long item
 constexpr int kTickets = 2;       // work items announced ahead
 constexpr int kTile = 32 * 128;   // bytes of an epilogue warp's staging: 32 rows of 128 bytes
 constexpr int kKeys = 256;        // targets kept in shared memory, when no more rows count
 constexpr int kSmem = 1024 + kStages * 2 * kOperand + kEpi * kTile + 512 + kKeys * 4;
 // Stages of a FP32 gradient's products that are added up in TMEM (see lm_grad_kernel).
-constexpr int kPiece = 8;
+constexpr int kPiece = 12;
 
 // Device-side state of one call, in its workspace.
 struct Rows {
@@ -731,9 +732,10 @@ __device__ __forceinline__ void add_row32(float (&v)[32], float f, const uint16_
 //
 // F32: the MMAs' FP32 accumulators truncate, so that a sum's error grows with
 // its number of steps.  For FP32 gradients an accumulator takes kPiece stages
-// (512 K elements); the epilogue adds the pieces up in registers, rounding to
-// nearest.  1000 x 32003 x 2048, 2-norm against 64 bits: dh 3.3e-6 -> 5.8e-7, dW
-// 2.2e-6 -> 5.5e-7, 397 (pieces of 16: 1.1e-6) -> 425 us.
+// (768 K elements); the epilogue adds the pieces up in registers, rounding to
+// nearest.  1000 x 32003 x 2048, 2-norm against 64 bits: without pieces 3.3e-6 (dh)
+// and 2.2e-6 (dW), with pieces of 16 stages 1.2e-6 and 1.1e-6, of 12 7.0e-7 and
+// 6.4e-7 (391 us), of 8 5.8e-7 and 5.5e-7 (409 us).
 //
 // What bounds it: at 4096 x 151936 a stage of 64 K elements (512 cycles at the
 // MMA's rate) takes 670 under the card's power limit, as cuBLAS's products do;
@@ -890,6 +892,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ++seq;
         ok = it.type >= 0;
+        // (F32, whose long items are twice as long: the next one once all have read
+        // this one; 1000 x 32003 437 us, now 418, but 200 x 151936 in bf16 444, then 462)
+        int parts;
+        if (F32 && ok && item_stages(a, plan, it, parts) * parts >= kLong)
+          ok = mbar_wait_cluster(kempty0 + 8 * k, ((seq - 1) / kTickets) & 1, a.err);
       }
     }
   } else if (warp == 1) {
