@@ -121,11 +121,12 @@ Layout layout(int T, int V, int K, bool f32) {
   const size_t part = size_t(l.cap) * l.ka * 4;
   l.slots = part * l.chunks <= kSlotBytes ? l.chunks : 1;
   // The scores of a chunk have to be done when its products start: enough
-  // chunks ahead for about 144 stages of work in each of 76 pairs of CTAs, the
-  // time of a dh item (200 x 151936: 48 stages 508 us, 144 430, 256 427).
+  // chunks ahead for about 256 stages of work in each of 76 pairs of CTAs, the
+  // time of two dh items (200 x 151936: 48 stages 508 us, 144 430, 256 427; 284 x
+  // 151936 x 256 with a FP32 gradient: 144 246 us, 256 233).
   const int64_t tm = l.cap / kTM, tk = l.ka / kTN, tn = l.chunk / kTN;
   const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * (l.cap / kTK));
-  l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (144 * 76 + stages - 1) / stages)));
+  l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (256 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
   const size_t runs = T > kRun ? (T + kRun - 1) / kRun : 0;
   const size_t sums = T > kSums ? size_t(l.cap) * l.kp * 4 : 0;
@@ -447,13 +448,17 @@ struct __align__(16) Item {
 // The work items of a call, in the order in which they are handed out: scores
 // S(p) and products G(p) = dh and dW of chunk p as
 //   S(0) .. S(ahead), G(0), S(ahead + 1), G(1), S(ahead + 2), ..., G(chunks - 1)
-// so that a group's inputs are (all but) done when its turn comes.
+// so that a group's inputs are (all but) done when its turn comes.  Where dh's
+// partials lie side by side, the groups behind the last scores are handed out
+// together, the longer kind of item (dh where few rows count) first: one of these
+// that starts last is the call's tail (2 x 131072 x 256 FP32: 176 us, now 141; 200 x 151936 433, now 423).
 struct Plan {
   int n, tm, tk;
   int chunks, ahead;
   int last;                // columns of the last chunk
   int s, s_last;           // items of S
   int dh;                  // dh items of G
+  bool h_first;            // dh's items are longer than dW's
   int g, g_last;           // items of G
   int head, body, total;   // S(0..ahead); those and the pairs G(p), S(p + ahead + 1)
 };
@@ -469,6 +474,7 @@ __device__ __forceinline__ Plan plan_of(const Args& a) {
   p.s = p.tm * (a.chunk / kTN);
   p.s_last = p.tm * cdiv(p.last, kTN);
   p.dh = a.dh ? p.tm * p.tk : 0;
+  p.h_first = a.chunk / kTK * a.parts_h >= cdiv(p.n, kTK) * a.parts_w;
   p.g = p.dh + (a.dW ? p.tk * (a.chunk / kTM) : 0);
   p.g_last = p.dh + (a.dW ? p.tk * cdiv(p.last, kTM) : 0);
   const int first = min(p.ahead + 1, p.chunks);      // groups of scores at the head
@@ -494,10 +500,20 @@ __device__ __forceinline__ Item item_at(const Args& a, const Plan& p, int i) {
     scores = j >= p.g;
     if (scores) j -= p.g;
     it.p = scores ? q + p.ahead + 1 : q;
-  } else {
+  } else if (a.slots == 1) {
     const int q = min((i - p.body) / p.g, p.chunks - both - 1);
     j = i - p.body - q * p.g;
     it.p = both + q;
+  } else {
+    // dh's and dW's items that are left
+    const int left = p.chunks - both, per = p.g - p.dh;
+    const int all_h = p.dh * left, all_w = (left - 1) * per + p.g_last - p.dh;
+    j = i - p.body;
+    const bool h = p.h_first ? j < all_h : j >= all_w;
+    if (h != p.h_first) j -= h ? all_w : all_h;
+    const int q = h ? j / p.dh : min(j / per, left - 1);
+    it.p = both + q;
+    j = h ? j - q * p.dh : p.dh + j - q * per;
   }
   if (scores) {
     it.type = kScores;
