@@ -138,7 +138,9 @@ struct NormArgs {
 };
 
 // r' is held as bf16 and its kept codes are written before the row's sum is
-// waited for: fewer registers, so more rows in flight.
+// waited for: fewer registers, so more rows in flight (16384 x 4096 with all
+// outputs 107 us, 94% of the copy rate; six CTAs per SM spilled, 120 us; rows of
+// one chunk a thread, 32768 x 1536: eight 95 us, five 106).
 template <int CPT>
 __global__ void __launch_bounds__(256, CPT == 1 ? 8 : CPT == 2 ? 5 : 4)
     add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
@@ -304,7 +306,8 @@ struct Raw8 {
 
 // What a lane reads of one row.  It stays as it lies in memory (as floats the
 // row's two passes over it took 181 to 231 registers a thread, 158 us for
-// 16384 x 2048), and the next row's is loaded before this one is reduced.
+// 16384 x 2048, now 43, 80% of the copy rate), and the next row's is loaded
+// before this one is reduced.
 template <bool DYF, bool DXF, bool RES>
 struct BackRow {
   uint2 k[kBackChunks];
