@@ -786,10 +786,10 @@ typedef struct {
 } biv_norm_fp8_desc;
 biv_status biv_add_rmsnorm_fp8(const biv_norm_fp8_desc* desc, biv_stream_t stream);
 
-/* Backward of it from the kept rows: with x = code * s, inv as the forward wrote
- * it and dy the gradient of v,
- *   dx = inv*(w*dy) - x*(inv^3*sum(x*w*dy)/d) (+ dres),
- *   dw float32 [d] = sum over rows of dy*x*inv (added to dw when accumulate is 1).
+/* Backward of it from the kept rows: with x' = code * (s * inv), inv as the forward
+ * wrote it and dy the gradient of v,
+ *   dx = inv*(w*dy - x'*(sum(w*dy*x')/d)) (+ dres),
+ *   dw float32 [d] = sum over rows of dy*x' (added to dw when accumulate is 1).
  * dres: the gradient that reaches r' past the norm, of dx's type, or NULL.  dy
  * BIV_F32 or BIV_BF16, dx likewise.  dx may be dres, or dy where types and strides
  * agree.  dw is summed in an order fixed by rows, d and the types.  Workspace:

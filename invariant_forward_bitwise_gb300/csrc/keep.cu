@@ -248,6 +248,9 @@ __global__ void __launch_bounds__(256, CPT == 1 ? 8 : CPT == 2 ? 5 : 4)
 // A CTA of W warps (W = ceil(d / 512), at most 16) walks rows r0, r0 + grid, ...;
 // lane l of warp w owns the chunks (w * 2 + i) * 32 + l, i = 0, 1, of 8 elements
 // and keeps their dw sums over the CTA's rows, which a second kernel adds up.
+// With the normed row x' = code * (s inv): dx = inv (w dy - x' mean(w dy x')),
+// dw = sum dy x'.  No power of inv is formed: the cube of a large row's is below
+// FP32's range, and the projection would be lost.
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, int64_t e, float (&f)[8]) {
   if (F32) {
@@ -359,15 +362,15 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_fp8_kernel(const __grid_const
     for (int i = 0; i < kBackChunks; ++i) {
       if (c0 + i * 32 >= chunks) continue;
       float x[8], g[8], wv[8];
-      values4(r.k[i].x, r.s[i], x);
-      values4(r.k[i].y, r.s[i], x + 4);
+      values4(r.k[i].x, r.s[i] * r.inv, x);
+      values4(r.k[i].y, r.s[i] * r.inv, x + 4);
       r.dy[i].get(g);
       unpack8(wq[i], wv);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2 gx = mul2(pair(g[2 * j], g[2 * j + 1]), pair(x[2 * j], x[2 * j + 1]));
-        sum2 = fma2(gx, pair(wv[2 * j], wv[2 * j + 1]), sum2);
-        dw[i][j] = fma2(gx, inv2, dw[i][j]);
+        const f32x2 g2 = pair(g[2 * j], g[2 * j + 1]), x2 = pair(x[2 * j], x[2 * j + 1]);
+        sum2 = fma2(mul2(g2, pair(wv[2 * j], wv[2 * j + 1])), x2, sum2);
+        dw[i][j] = fma2(g2, x2, dw[i][j]);
       }
     }
     float even, odd;
@@ -379,21 +382,21 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_fp8_kernel(const __grid_const
       sum = 0.f;
       for (int i = 0; i < warps; ++i) sum += red[turn][i];
     }
-    const float corr = r.inv * r.inv * r.inv * (sum / float(a.d));
-    const f32x2 minus_corr = pair(-corr, -corr);
+    const float mean = sum / float(a.d);
+    const f32x2 minus_mean = pair(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < kBackChunks; ++i) {
       const int c = c0 + i * 32;
       if (c >= chunks) continue;
       float x[8], g[8], wv[8], o[8];
-      values4(r.k[i].x, r.s[i], x);
-      values4(r.k[i].y, r.s[i], x + 4);
+      values4(r.k[i].x, r.s[i] * r.inv, x);
+      values4(r.k[i].y, r.s[i] * r.inv, x + 4);
       r.dy[i].get(g);
       unpack8(wq[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const f32x2 gw = mul2(pair(g[j], g[j + 1]), pair(wv[j], wv[j + 1]));
-        split(fma2(pair(x[j], x[j + 1]), minus_corr, mul2(inv2, gw)), o[j], o[j + 1]);
+        split(mul2(inv2, fma2(pair(x[j], x[j + 1]), minus_mean, gw)), o[j], o[j + 1]);
       }
       if (RES) {
         float t[8];

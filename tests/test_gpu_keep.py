@@ -451,6 +451,33 @@ def test_a_graph_and_other_streams_repeat_the_bits(B):
                 assert same(ref[k], o[k]), k
 
 
+@gpu
+@pytest.mark.parametrize("exponent", [-50, -42, 42, 50, 56])
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_rmsnorm_backward_of_large_and_small_rows(B, exponent, t):
+    """Rows of 2^42 and more, whose inv^3 is below FP32's range, and of 2^-42 and less
+    (eps 0), whose inv^3 is above it, beside ordinary ones: the projection is there."""
+    rows, d, t = 9, 272, TYPES[t]
+    x = stream(rows, d, 5, spread=False)
+    x[::2] *= 2.0 ** exponent
+    keep, ks = quantised(x.bfloat16().float())
+    inv = (1 / x.to(F64).square().mean(1).sqrt()).float()
+    g = torch.Generator(device="cuda").manual_seed(d)
+    w = (1 + 0.2 * torch.randn(d, device="cuda", generator=g)).bfloat16()
+    xh = values(keep, ks) * inv.to(F64)[:, None]
+    # a gradient along the row, of the row's size: dx is of the order of 1
+    dy = ((xh + torch.randn(rows, d, device="cuda", generator=g)) / inv[:, None]).to(t)
+    dx, dw = torch.empty(rows, d, dtype=t, device="cuda"), f32(d)
+    ws = torch.empty(B.biv_rmsnorm_backward_fp8_workspace(rows, d), dtype=torch.uint8, device="cuda")
+    B.biv_rmsnorm_backward_fp8(keep, ks, inv, w, dy, dx, dw, ws)
+    iv, gw = inv.to(F64)[:, None], dy.to(F64) * w.to(F64)
+    want = iv * (gw - xh * (gw * xh).mean(1, keepdim=True))
+    size = iv * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True))
+    tol = (d + 16) * 2.0 ** -24 * size
+    assert bool(((dx.to(F64) - want).abs() <= tol + rounding(t) * (want.abs() + tol)).all())
+    terms = dy.to(F64) * xh
+    assert bool(((dw.to(F64) - terms.sum(0)).abs() <= (rows + 8) * 2.0 ** -24 * terms.abs().sum(0) + 1e-38).all())
+
 # ----------------------------------------------------------- on the host ----
 def test_refusals_on_the_host(B):
     lib = B.load()
