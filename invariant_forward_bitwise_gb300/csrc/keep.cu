@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(128, 12) silu_mul_keep_kernel(
   __nv_bfloat162 m = __hmax2(largest(a, b, 0x5410u), largest(a, b, 0x7632u));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  // (a group of NaN alone has no largest value: 0, so that its scale is 1)
+  m = __hmax2(m, __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)));
   const float most = __low2float(m);
   float sg, su;
   const uint2 kg = quant8(gv, most, sg), ku = quant8(uv, __high2float(m), su);

@@ -478,6 +478,32 @@ def test_rmsnorm_backward_of_large_and_small_rows(B, exponent, t):
     terms = dy.to(F64) * xh
     assert bool(((dw.to(F64) - terms.sum(0)).abs() <= (rows + 8) * 2.0 ** -24 * terms.abs().sum(0) + 1e-38).all())
 
+@gpu
+def test_silu_mul_keeps_groups_of_nan_and_infinities(B):
+    """Kept codes and scales of groups that hold NaN and infinities, alone and among
+    others, are those that biv_act_quant_fp8 writes of each half."""
+    rows, I = 8, 272  # noqa: E741
+    gu = stream(rows, 2 * I, 3, spread=False).bfloat16()
+    nan, inf = float("nan"), float("inf")
+    gu[0, :128] = nan                       # a whole group, of gate
+    gu[1, I + 128:I + 256] = nan            # of up
+    gu[2, 256:I] = nan                      # the last, short one
+    gu[3, ::3] = nan
+    gu[4, 7], gu[4, I + 9] = inf, -inf
+    gu[5, :128], gu[5, I:I + 128] = inf, -inf
+    gu[6, 0], gu[6, 1:128] = inf, nan
+    y, keep, ks = torch.empty(rows, I, dtype=torch.bfloat16, device="cuda"), u8(rows, 2 * I), f32(rows, 2 * groups(I))
+    B.biv_silu_mul_keep_fp8(gu, y, keep, ks)
+    ref = torch.empty_like(y)
+    B.biv_silu_mul(gu, ref)
+    assert bool((y.isnan() == ref.isnan()).all())
+    assert same(torch.where(ref.isnan(), 0.0, y), torch.where(ref.isnan(), 0.0, ref))
+    for half in (0, 1):
+        want, s = u8(rows, I), f32(rows, groups(I))
+        B.biv_act_quant_fp8(gu[:, half * I:half * I + I].contiguous(), want, s)
+        assert same(keep[:, half * I:half * I + I], want)
+        assert same(ks[:, half * groups(I):(half + 1) * groups(I)], s)
+
 # ----------------------------------------------------------- on the host ----
 def test_refusals_on_the_host(B):
     lib = B.load()
