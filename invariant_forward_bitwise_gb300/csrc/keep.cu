@@ -38,6 +38,14 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   return v;
 }
 
+// a * b + c where the caller wants an exact zero to be -0 (rounding down; the
+// other sums it forms are exact)
+__device__ __forceinline__ f32x2 fma2_down(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 v;
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -87,6 +95,8 @@ __device__ __forceinline__ void values4(uint32_t c, float s, float* f) {
 // gives them in three operations where nothing under- or overflows; one Newton
 // step from within 1 ulp gives that r, unless the divisor's mantissa is all ones
 // (Markstein).  Groups of such a scale, or of one far from 1, divide.
+// A remainder of zero is formed as -0: times r it leaves q's sign, that of -0 / s
+// among them (+0 would make it +0).
 __device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, float& s) {
   float q[8];
   constexpr float r448 = 1.0f / 448.0f;
@@ -99,7 +109,7 @@ __device__ __forceinline__ uint2 quant8(const float (&v)[8], float amax, float& 
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const f32x2 v2 = pair(v[i], v[i + 1]), q0 = mul2(v2, r);
-      split(fma2(fma2(q0, minus_s, v2), r, q0), q[i], q[i + 1]);
+      split(fma2(fma2_down(q0, minus_s, v2), r, q0), q[i], q[i + 1]);
     }
   } else {
     s = amax == 0.f ? 1.0f : amax / 448.0f;

@@ -504,6 +504,30 @@ def test_silu_mul_keeps_groups_of_nan_and_infinities(B):
         assert same(keep[:, half * I:half * I + I], want)
         assert same(ks[:, half * groups(I):(half + 1) * groups(I)], s)
 
+@gpu
+def test_zeros_keep_their_sign(B):
+    """The code of -0 is 0x80, as the rule's quotient -0 / s and biv_act_quant_fp8 give it:
+    of zeros of r', of the normed rows (0 times a negative weight), of gate and of up."""
+    rows, d = 6, 272
+    x = stream(rows, d, 8, spread=False).bfloat16()
+    x[:, ::5], x[:, 1::5] = 0.0, -0.0
+    x[5, :128] = -0.0                       # a group of zeros alone
+    w = torch.where(torch.arange(d, device="cuda") % 3 == 0, -1.0, 1.5).bfloat16()
+    c, s, k, ks, inv = u8(rows, d), f32(rows, groups(d)), u8(rows, d), f32(rows, groups(d)), f32(rows)
+    B.biv_add_rmsnorm_fp8(x, None, w, EPS, codes=c, scales=s, keep=k, keep_scales=ks, inv=inv)
+    want, wants = u8(rows, d), f32(rows, groups(d))
+    B.biv_act_quant_fp8(x, want, wants)
+    assert bool((want[:, 1::5] == 0x80).all()) and bool((want[:5, ::5] == 0).all())
+    assert same(k, want) and same(ks, wants)
+    v = (x.float() * inv[:, None]) * w.float()
+    want, wants = quantised(v)
+    assert bool((want[:, 1::15] == 0x80).any())
+    assert same(c, want) and same(s, wants)
+    both = torch.cat([x, x.flip(0)], 1)
+    keep, ks2 = u8(rows, 2 * d), f32(rows, 2 * groups(d))
+    B.biv_silu_mul_keep_fp8(both, None, keep, ks2)
+    assert same(keep[:, :d], k) and same(keep[:, d:], k.flip(0)) and same(ks2[:, :groups(d)], ks)
+
 # ----------------------------------------------------------- on the host ----
 def test_refusals_on_the_host(B):
     lib = B.load()
