@@ -817,10 +817,12 @@ biv_status biv_silu_mul_keep_fp8(const uint16_t* gate_up, int64_t gu_stride, uin
                                  int64_t y_stride, uint8_t* keep, float* keep_scales, int rows, int I,
                                  biv_stream_t stream);
 
-/* Backward of it from the kept rows (gate, up = code * s): dgate_up rows of 2I as
- * biv_silu_mul_backward writes them, BIV_F32 or BIV_BF16, from dy BIV_F32 or
- * BIV_BF16 rows of I; y (bf16 rows of I, or NULL) gets silu(gate) * up of the kept
- * values, which the gradient of the product behind it reads. */
+/* Backward of it from the kept rows (gate, up = code * s), dy BIV_F32 or BIV_BF16
+ * rows of I.  dgate_up rows of 2I: BIV_F32, by biv_silu_mul_backward's operations
+ * (its bits where bf16 holds gate and up); BIV_BF16, the same with a sigmoid that is
+ * off by 1 ulp of FP32 at most, or by 2^-126 where it is below that, before the
+ * rounding to bf16.  y (bf16 rows of I, or NULL) gets silu(gate) * up of the kept
+ * values, by the same sigmoid, which the gradient of the product behind it reads. */
 biv_status biv_silu_mul_backward_fp8(const uint8_t* keep, const float* keep_scales, const void* dy,
                                      int64_t dy_stride, int dy_dtype, void* dgate_up,
                                      int64_t dgate_up_stride, int dgate_up_dtype, uint16_t* y,

@@ -588,9 +588,11 @@ __global__ void __launch_bounds__(128, 12) silu_mul_bwd_fp8_kernel(
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const f32x2 g2 = pair(g[j], g[j + 1]), u2 = pair(u[j], u[j + 1]), d2 = pair(d[j], d[j + 1]);
-    // (within 1 ulp, and 0 below gates of -87: an error of less than 2^-120; with
-    // divisions 8192 x 6144 took 78 us, now 72)
-    const f32x2 s = pair(rcp_approx(1.0f + expf(-g[j])), rcp_approx(1.0f + expf(-g[j + 1])));
+    // FP32 gradients: biv_silu_mul_backward's division (at the copy rate with it).  bf16
+    // ones: a sigmoid within 1 ulp, and 0 where it is below 2^-126 (gates below -87.3);
+    // with divisions 8192 x 6144 took 78 us, now 73.
+    const float d0 = 1.0f + expf(-g[j]), d1 = 1.0f + expf(-g[j + 1]);
+    const f32x2 s = DGF ? pair(1.0f / d0, 1.0f / d1) : pair(rcp_approx(d0), rcp_approx(d1));
     const f32x2 a = mul2(g2, s);
     split(mul2(mul2(d2, u2), mul2(s, fma2(g2, fma2(s, minus, one), one))), dg[j], dg[j + 1]);
     split(mul2(d2, a), du[j], du[j + 1]);

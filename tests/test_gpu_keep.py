@@ -528,6 +528,29 @@ def test_zeros_keep_their_sign(B):
     B.biv_silu_mul_keep_fp8(both, None, keep, ks2)
     assert same(keep[:, :d], k) and same(keep[:, d:], k.flip(0)) and same(ks2[:, :groups(d)], ks)
 
+@gpu
+def test_silu_mul_backward_in_fp32_has_the_bf16_forms_bits(B):
+    """Kept values that bf16 holds (every finite gate that a code and a power of two
+    make, and many ups): FP32 gradients are biv_silu_mul_backward's, bit for bit."""
+    codes = torch.arange(256, device="cuda", dtype=torch.uint8)
+    codes = codes[(codes & 0x7F) != 0x7F]                       # no NaN
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows, I = 24, 256  # noqa: E741
+    pick = lambda: codes[torch.randint(0, codes.numel(), (rows, I), device="cuda", generator=g)]  # noqa: E731
+    kg, ku = pick(), pick()
+    kg[:, :254] = codes
+    sg = (2.0 ** torch.arange(-18, 6, device="cuda", dtype=torch.float32))[:, None].expand(rows, 2).contiguous()
+    su = 2.0 ** torch.randint(-9, 3, (rows, 2), device="cuda", generator=g).float()
+    keep, ks = torch.cat([kg, ku], 1), torch.cat([sg, su], 1)
+    gate_up = torch.cat([values(kg, sg), values(ku, su)], 1)
+    assert bool((gate_up == gate_up.bfloat16().to(F64)).all())
+    for t in ("f32", "bf16"):
+        dy = torch.randn(rows, I, device="cuda", generator=g).to(TYPES[t])
+        got, ref = torch.empty(rows, 2 * I, device="cuda"), torch.empty(rows, 2 * I, device="cuda")
+        B.biv_silu_mul_backward_fp8(keep, ks, dy, got)
+        B.biv_silu_mul_backward(gate_up.bfloat16(), dy.float(), ref)
+        assert same(got, ref)
+
 # ----------------------------------------------------------- on the host ----
 def test_refusals_on_the_host(B):
     lib = B.load()
