@@ -97,7 +97,7 @@ struct Layout {
   int ahead;                // chunks whose scores are formed ahead of their products
   int ring;                 // chunks of dz held
   int parts;                // bf16 parts of dz
-  size_t off[21], bytes;
+  size_t off[20], bytes;
 };
 
 constexpr int kRun = 1024;
@@ -130,14 +130,14 @@ Layout layout(int T, int V, int K, bool f32) {
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
   const size_t runs = T > kRun ? (T + kRun - 1) / kRun : 0;
   const size_t sums = T > kSums ? size_t(l.cap) * l.kp * 4 : 0;
-  const size_t sizes[21] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
+  const size_t sizes[20] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
                             size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,
-                            size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * l.kp * 2,
-                            part * l.slots, size_t(l.parts) * l.cap * l.ring * l.chunk * 2, 16,
+                            size_t(l.cap) * 4, size_t(l.cap) * l.kp * 2, part * l.slots,
+                            size_t(l.parts) * l.cap * l.ring * l.chunk * 2, 16,
                             size_t(l.chunks) * 4, size_t(l.chunks) * 4, size_t(l.chunks) * 4,
                             runs * kRun * 4, runs * 4, runs * kRun * 8, sums / 8, sums / 64};
   l.bytes = 0;
-  for (int i = 0; i < 21; ++i) {
+  for (int i = 0; i < 20; ++i) {
     l.off[i] = l.bytes;
     l.bytes += (sizes[i] + 255) / 256 * 256;
   }
@@ -153,20 +153,20 @@ Rows rows_of(const Layout& l, void* ws) {
   r.skey = reinterpret_cast<int*>(b + l.off[3]);
   r.srow = reinterpret_cast<int*>(b + l.off[4]);
   r.lse = reinterpret_cast<float*>(b + l.off[5]);
-  r.cp = reinterpret_cast<float*>(b + l.off[7]);
-  r.dzt = reinterpret_cast<float*>(b + l.off[8]);
-  r.h = reinterpret_cast<uint16_t*>(b + l.off[9]);
-  r.acc = reinterpret_cast<float*>(b + l.off[10]);
-  r.dz = reinterpret_cast<uint16_t*>(b + l.off[11]);
-  r.ticket = reinterpret_cast<int*>(b + l.off[12]);
-  r.sdone = reinterpret_cast<int*>(b + l.off[13]);
-  r.hdone = reinterpret_cast<int*>(b + l.off[14]);
-  r.gdone = reinterpret_cast<int*>(b + l.off[15]);
-  r.run = reinterpret_cast<int*>(b + l.off[16]);
-  r.run_n = reinterpret_cast<int*>(b + l.off[17]);
-  r.run_at = reinterpret_cast<int2*>(b + l.off[18]);
-  r.sum8 = reinterpret_cast<float*>(b + l.off[19]);
-  r.sum64 = reinterpret_cast<float*>(b + l.off[20]);
+  r.cp = reinterpret_cast<float*>(b + l.off[6]);
+  r.dzt = reinterpret_cast<float*>(b + l.off[7]);
+  r.h = reinterpret_cast<uint16_t*>(b + l.off[8]);
+  r.acc = reinterpret_cast<float*>(b + l.off[9]);
+  r.dz = reinterpret_cast<uint16_t*>(b + l.off[10]);
+  r.ticket = reinterpret_cast<int*>(b + l.off[11]);
+  r.sdone = reinterpret_cast<int*>(b + l.off[12]);
+  r.hdone = reinterpret_cast<int*>(b + l.off[13]);
+  r.gdone = reinterpret_cast<int*>(b + l.off[14]);
+  r.run = reinterpret_cast<int*>(b + l.off[15]);
+  r.run_n = reinterpret_cast<int*>(b + l.off[16]);
+  r.run_at = reinterpret_cast<int2*>(b + l.off[17]);
+  r.sum8 = reinterpret_cast<float*>(b + l.off[18]);
+  r.sum64 = reinterpret_cast<float*>(b + l.off[19]);
   return r;
 }
 
