@@ -721,16 +721,24 @@ biv_status biv_lm_head_loss(const biv_lm_loss_desc* desc, biv_stream_t stream);
  * dh [T, K] rows at lddh, dW [V, K] rows at lddw, each BIV_BF16 or BIV_F32, each
  * may be NULL; they must not overlap the inputs or each other.  accumulate = 1
  * adds to dW what it holds (in FP32, one rounding).
- * The logits are formed again in pieces of at most a few chunks of 8192 columns
- * and never stored.  dz enters the products as bf16 (for a FP32 gradient as
+ * The logits are formed again in chunks of at most 8192 columns and never stored;
+ * dz of a few chunks is, in the workspace.  dz enters the products as bf16 (for a FP32 gradient as
  * two bf16 parts); the term of a row's own target is added in FP32.  dh is the
  * sum of its chunks' FP32 products in ascending order: a row's dh depends on the
  * row, V, K and the gradients' types only.  dW adds the p terms of the counted
  * rows in ascending order, then those of the rows whose target a row of W is, in
  * an order fixed by the targets.  Every call repeats its bits.
  * T <= 2^20, V < 2^24, K <= 65536.  Workspace: biv_lm_head_backward_workspace
- * bytes (the sizes and gradient types of the call; about T (7 K + 48 Ki) bytes for
- * large T, with a FP32 gradient T (7 K + 96 Ki)), 256-byte aligned, caller-owned, no initial value; calls that can
+ * bytes (the sizes and gradient types of the call), 256-byte aligned,
+ * caller-owned, no initial value.  With T' and K' = T and K rounded up to 256 it
+ * is at most the sum of
+ *   dz: 120 MiB, or 48 KiB T' (three chunks) where that is more; with a FP32
+ *     gradient 96 KiB T' + 608 MiB / (K' / 256); never more than dz of all chunks
+ *   sums of dh: 192 MiB, or 4 T' K' where that is more
+ *   rows: T' (3 K' + 64) + 1 MiB.
+ * That is far below the T x V FP32 logits of a trainer's micro-batch (4096 x
+ * 151936 x 2048: 245 of 2,374 MiB), but may be above those of few rows (200 x
+ * 151936 x 2048: 99 of 116 MiB, 13 x 151936 x 256: 86 of 7.5).  Calls that can
  * overlap on the GPU need separate ones. */
 typedef struct {
   int T, V, K;

@@ -46,8 +46,8 @@ namespace {
 // Vocabulary columns per FP32 partial of dh: a length that follows V and K.  As
 // many chunks as make two dh tiles of 256 rows for each of 76 pairs of CTAs, but
 // chunks of 4096 to 8192 columns (a dh tile of K = 256 and 8192 columns is as long
-// as all the rest of 9 rows: 250 us, now 190; shorter ones cost partials), and 8
-// chunks at least of a small vocabulary.
+// as all the rest of 9 rows: 250 us, now 190; shorter ones cost partials); a
+// vocabulary of less than 32768 in eighths, rounded up to 256 columns.
 constexpr int kMinChunk = 4096, kMaxChunk = 8192;
 constexpr int kTM = 256;          // tile rows: 128 TMEM lanes in each CTA of a pair
 constexpr int kTN = 256;          // tile columns: each CTA brings half of B
@@ -107,6 +107,8 @@ constexpr int kSums = 64;         // rows above which sums over equal targets ar
 // independent of one another, and one kernel adds them up); above, each chunk
 // is added to one array as it comes (4096 x 2048 rows: 34 MB, which L2 holds).
 constexpr size_t kSlotBytes = size_t(192) << 20;
+// bf16 dz held, where three chunks are less (L2 has 129 MB)
+constexpr int64_t kRingBytes = int64_t(120) << 20;
 
 Layout layout(int T, int V, int K, bool f32) {
   Layout l;
@@ -128,6 +130,19 @@ Layout layout(int T, int V, int K, bool f32) {
   const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * (l.cap / kTK));
   l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (256 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
+  // bf16 dz: no more chunks than L2 holds (three at least).  It costs no time
+  // (T x V x K, with what those stages ask for and with this: 600 x 131072 x 256
+  // 209 us, 219; 2048 x 131072 x 256 474, 473; 1500 x 131072 x 256 377, 366;
+  // 4000 x 151936 x 64 941, 978; 8192 x 131072 x 256 2035 and 589 MiB of workspace,
+  // 1964 and 205).  dz in two parts has twice as long dh items, which short rings
+  // hold up (13 x 151936 x 256 165 us, 204; 2000 x 151936 x 256 960, 1472).
+  if (!f32) {
+    const int64_t most = std::max<int64_t>(3, kRingBytes / (int64_t(l.cap) * l.chunk * 2));
+    if (l.ring > most) {
+      l.ring = int(most);
+      l.ahead = (l.ring - 1) / 2;
+    }
+  }
   const size_t runs = T > kRun ? (T + kRun - 1) / kRun : 0;
   const size_t sums = T > kSums ? size_t(l.cap) * l.kp * 4 : 0;
   const size_t sizes[20] = {16, size_t(l.cap) * 4, size_t(l.cap) * 4, size_t(l.cap) * 4,

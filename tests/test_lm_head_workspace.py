@@ -1,0 +1,61 @@
+"""The workspace of the LM head's gradient over its sizes, on the host: the bound that
+include/biv.h states, and its place beside the logits that it replaces."""
+import random
+
+import pytest
+import torch
+
+MIB = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def B():
+    from invariant_forward_bitwise_gb300 import biv, build
+    build.build()
+    biv.load()
+    return biv
+
+
+def up(n, to=256):
+    return (n + to - 1) // to * to
+
+
+def bound(T, V, K, f32):
+    t, k = up(T), up(K)
+    dz = t * 96 * 1024 + 608 * MIB // (k // 256) if f32 else max(120 * MIB, t * 48 * 1024)
+    # all chunks, of at most 8192 columns: up to a chunk more than V
+    dz = min(dz, t * (up(V) + 8192) * (4 if f32 else 2))
+    return dz + max(192 * MIB, 4 * t * k) + t * (3 * k + 64) + MIB
+
+
+def sizes():
+    r = random.Random(5)
+    log = lambda lo, hi: int(round(2 ** r.uniform(lo, hi)))  # noqa: E731
+    some = [(T, V, K) for T in (1, 13, 200, 257, 1000, 2000, 8192) for V in (1, 4096, 32003, 151936)
+            for K in (8, 256, 2048)]
+    return some + [(log(0, 20), log(0, 23.9), 8 * log(0, 13)) for _ in range(4000)]
+
+
+def test_the_stated_bound(B):
+    f, b = torch.float32, torch.bfloat16
+    for T, V, K in sizes():
+        for dh, dw in ((b, b), (f, b), (f, f)):
+            n = B.biv_lm_head_backward_workspace(T, V, K, dh, dw)
+            assert 0 < n <= bound(T, V, K, dh is f), (T, V, K, dh, n)
+
+
+def test_few_rows_of_a_large_vocabulary(B):
+    """dz of bf16 gradients stays within what L2 holds, or three chunks."""
+    for T in (1, 13, 200, 256, 600, 1000, 1500):
+        for V in (131072, 151936, 1 << 23):
+            for K in (8, 256, 2048):
+                rest = max(192 * MIB, 4 * up(T) * up(K)) + up(T) * (3 * up(K) + 64) + MIB
+                assert B.biv_lm_head_backward_workspace(T, V, K) <= 120 * MIB + rest
+
+
+@pytest.mark.parametrize("K", [256, 2048])
+def test_a_micro_batch_is_far_below_its_logits(B, K):
+    for T in (2048, 4096, 8192):
+        logits = 4 * T * 151936
+        assert B.biv_lm_head_backward_workspace(T, 151936, K) < logits // 4
+        assert B.biv_lm_head_backward_workspace(T, 151936, K, torch.float32, torch.float32) < logits // 1.9
