@@ -443,6 +443,47 @@ def test_a_captured_gradient_of_many_rows_on_other_inputs(B):
     assert B.biv_poll_error() == 0
 
 
+@gpu
+@pytest.mark.parametrize("T,V,K,hot,dh,dw", [
+    (300, 32768, 256, False, True, False),      # dh's products of 64 stages and two parts
+    (16384, 600, 256, False, False, True),      # dW's of 256 stages and two parts
+    (1000, 32003, 2048, True, True, True),      # a ring shorter than the chunks, partials side by side
+    (2100, 50000, 2048, True, True, True),      # and partials added up as they come
+])
+def test_fp32_gradients_have_fp32_quality(B, T, V, K, hot, dh, dw):
+    """2-norm of the error against 64 bits, relative to the gradient's.  Its parts:
+     - hi + lo of dz: a bf16 rounding is off by at most 2^-8 of the value, 2^-8 / sqrt(3) *
+       0.735 = 1.7e-3 of it in the mean square over mantissas; the second one by as much of
+       the first one's rest: 2.7e-6, of terms of random signs, so of their sums too;
+     - an accumulator truncates at each of the 48 steps of its 12 stages: by 0.72 * 2^-24 =
+       4.3e-8 of the running sum in the mean, 48 / 2 * 4.3e-8 = 1.0e-6 where the sum grows
+       steadily, and 48 / sqrt(12) * 4.3e-8 = 0.6e-6 more for its wandering;
+     - logits of size 0.5 from such sums, their difference from lse (of up to 11: 2^-21 at
+       most, 2.7e-7 in the mean square) and expf: 1e-6.
+    Added up 5.3e-6.  One bf16 part leaves 1.7e-3 of the p terms; accumulators over all
+    stages lose 1.7e-7 a stage, 9e-6 and more in the first two cases, whose dz is of p alone."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    h = torch.randn(T, K, device="cuda", generator=g).bfloat16()
+    W = (torch.randn(V, K, device="cuda", generator=g) * (0.5 / K ** 0.5)).bfloat16()
+    target = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    a = torch.randn(T, device="cuda", generator=g) / T
+    dlp, dlse = (a if hot else torch.zeros_like(a)), torch.randn(T, device="cuda", generator=g) / T
+    h64, W64 = h.to(F64), W.to(F64)
+    dz = h64 @ W64.t()
+    lse = torch.logsumexp(dz, 1).float()
+    dz.sub_(lse.to(F64)[:, None]).exp_().mul_((dlse.to(F64) - dlp.to(F64))[:, None])
+    dz[torch.arange(T, device="cuda"), target.long()] += dlp.to(F64)
+    gh, gw = torch.empty(T, K, device="cuda"), torch.empty(V, K, device="cuda")
+    ws = torch.empty(B.biv_lm_head_backward_workspace(T, V, K, torch.float32, torch.float32), dtype=torch.uint8,
+                     device="cuda").fill_(255)
+    B.biv_lm_head_backward(h, W, target, lse, dlp, gh, gw, ws, dlse=dlse)
+    torch.cuda.synchronize()
+    assert B.biv_poll_error() == 0
+    for on, got, left, right in ((dh, gh, dz, W64), (dw, gw, dz.t(), h64)):
+        if on:
+            want = left @ right
+            assert float((got.to(F64) - want).norm() / want.norm()) <= 5.3e-6
+
 # ---------------------------------------------------------------- forward --
 @gpu
 @pytest.mark.parametrize("T,V,K", [(1, 1, 8), (13, 4096, 256), (130, 1001, 72), (300, 20011, 688), (5, 30000, 2048)])
