@@ -689,7 +689,9 @@ biv_status biv_policy_loss_logits(const biv_policy_desc* desc, const void* z, in
  * dloss/dlse = 2 z_coef c lse float32 [T] (each may be NULL), ready for
  * biv_lm_head_backward; stats float32 [4]: loss, sum c nll, sum c lse^2, N.
  * A row's bits depend on the row, W and N only; the sums run in one order fixed
- * by T.  Workspace: biv_lm_head_loss_workspace bytes, 16-byte aligned,
+ * by T.  The logits' accumulators truncate, as biv_lm_head_logprob's do: a bias that
+ * a mean over rows keeps (the loss of 4096 x 151936 x 2048 is off by 3.6e-7 of
+ * itself).  Workspace: biv_lm_head_loss_workspace bytes, 16-byte aligned,
  * caller-owned, no initial value; calls that can overlap on the GPU need
  * separate ones. */
 typedef struct {
@@ -722,18 +724,20 @@ biv_status biv_lm_head_loss(const biv_lm_loss_desc* desc, biv_stream_t stream);
  * may be NULL; they must not overlap the inputs or each other.  accumulate = 1
  * adds to dW what it holds (in FP32, one rounding).
  * The logits are formed again in chunks of at most 8192 columns and never stored;
- * dz of a few chunks is, in the workspace.  dz enters the products as bf16 (for a FP32 gradient as
- * two bf16 parts); the term of a row's own target is added in FP32.  dh is the
- * sum of its chunks' FP32 products in ascending order: a row's dh depends on the
- * row, V, K and the gradients' types only.  dW adds the p terms of the counted
- * rows in ascending order, then those of the rows whose target a row of W is, in
- * an order fixed by the targets.  Every call repeats its bits.
+ * dz of a few chunks is, in the workspace.  dz enters the products as bf16, for a
+ * FP32 gradient as two bf16 parts, which leave 2.7e-6 of the p terms in the mean
+ * square; accumulators of 768 K elements are then off by about 1e-6 of a sum.  The
+ * term of a row's own target is added in FP32.  dh is the sum of its chunks' FP32
+ * products in ascending order: a row's dh depends on the row, V, K and the
+ * gradients' types only.  dW adds the p terms of the counted rows in ascending
+ * order, then those of the rows whose target a row of W is, in an order fixed by
+ * the targets.  Every call repeats its bits.
  * T <= 2^20, V < 2^24, K <= 65536.  Workspace: biv_lm_head_backward_workspace
  * bytes (the sizes and gradient types of the call), 256-byte aligned,
  * caller-owned, no initial value.  With T' and K' = T and K rounded up to 256 it
  * is at most the sum of
- *   dz: 120 MiB, or 48 KiB T' (three chunks) where that is more; with a FP32
- *     gradient 96 KiB T' + 608 MiB / (K' / 256); never more than dz of all chunks
+ *   dz: 192 MiB, or 48 KiB T' (three chunks) where that is more, but no more than
+ *     dz of all chunks; with a FP32 gradient twice as much
  *   sums of dh: 192 MiB, or 4 T' K' where that is more
  *   rows: T' (3 K' + 64) + 1 MiB.
  * That is far below the T x V FP32 logits of a trainer's micro-batch (4096 x

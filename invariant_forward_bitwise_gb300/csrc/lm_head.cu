@@ -107,8 +107,8 @@ constexpr int kSums = 64;         // rows above which sums over equal targets ar
 // independent of one another, and one kernel adds them up); above, each chunk
 // is added to one array as it comes (4096 x 2048 rows: 34 MB, which L2 holds).
 constexpr size_t kSlotBytes = size_t(192) << 20;
-// bf16 dz held, where three chunks are less (L2 has 129 MB)
-constexpr int64_t kRingBytes = int64_t(120) << 20;
+// dz held of each of its parts, where three chunks are less
+constexpr int64_t kRingBytes = int64_t(192) << 20;
 
 Layout layout(int T, int V, int K, bool f32) {
   Layout l;
@@ -130,18 +130,16 @@ Layout layout(int T, int V, int K, bool f32) {
   const int64_t stages = tm * tn * (l.kp / kTK) + l.parts * (tm * tk * (l.chunk / kTK) + tn * tk * (l.cap / kTK));
   l.ahead = int(std::max<int64_t>(1, std::min<int64_t>(l.chunks - 1, (256 * 76 + stages - 1) / stages)));
   l.ring = std::min(l.chunks, 2 * l.ahead + 1);
-  // bf16 dz: no more chunks than L2 holds (three at least).  It costs no time
-  // (T x V x K, with what those stages ask for and with this: 600 x 131072 x 256
-  // 209 us, 219; 2048 x 131072 x 256 474, 473; 1500 x 131072 x 256 377, 366;
-  // 4000 x 151936 x 64 941, 978; 8192 x 131072 x 256 2035 and 589 MiB of workspace,
-  // 1964 and 205).  dz in two parts has twice as long dh items, which short rings
-  // hold up (13 x 151936 x 256 165 us, 204; 2000 x 151936 x 256 960, 1472).
-  if (!f32) {
-    const int64_t most = std::max<int64_t>(3, kRingBytes / (int64_t(l.cap) * l.chunk * 2));
-    if (l.ring > most) {
-      l.ring = int(most);
-      l.ahead = (l.ring - 1) / 2;
-    }
+  // No more of dz than kRingBytes of each part, or three chunks (T x V x K, bf16, with
+  // what those stages ask for and with this: 8192 x 131072 x 256 589 MiB of workspace,
+  // 2020 us, and 205, 1954; 1500 x 131072 x 256 433, 377, and 241, 357; 65536 x 4096 x
+  // 256 619, 2126, and 299, 2181.  FP32: 2000 x 151936 x 256 621, 965, and 461, 977;
+  // 8192 x 32000 x 256 709, 832, and 453, 862).  120 MiB, what L2 holds, made 16384 x
+  // 4096 x 256 378 us instead of 283, and in FP32 2000 x 151936 x 256 1472.
+  const int64_t most = std::max<int64_t>(3, kRingBytes / (int64_t(l.cap) * l.chunk * 2));
+  if (l.ring > most) {
+    l.ring = int(most);
+    l.ahead = (l.ring - 1) / 2;
   }
   const size_t runs = T > kRun ? (T + kRun - 1) / kRun : 0;
   const size_t sums = T > kSums ? size_t(l.cap) * l.kp * 4 : 0;
