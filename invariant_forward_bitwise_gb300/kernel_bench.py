@@ -22,7 +22,7 @@ step runs inside cudaProfilerStart/Stop) and hybrid_decode_step (one decode step
 Mamba-2 hybrid unit for 3 sequences, graph-timed, then eagerly inside
 cudaProfilerStart/Stop), policy_logits (the policy loss from 1216 x 151936 FP32,
 1216 x 131072 bf16 and 1000 x 32003 FP32 logits), adamw_8bit (67 M bf16
-weights, 8-bit states, stochastic rounding), lm_head_grad (loss and gradient at
+weights, 8-bit states, stochastic rounding), lm_head_grad (loss and gradient, dW written and added to, at
 200, 4096 rows x 151936 x 2048 in bf16, 1000 x 32003 x 2048 in FP32) and
 rows_8bit (the norm, its backward and the SiLU-mul with rows kept in 8 bits).
 Each case times REPS calls with CUDA events after one warm-up call and
@@ -439,6 +439,8 @@ elif case == "lm_head_grad":
         print(f"lm_head_loss T={T} V={V}: {ms*1e3:.1f} us  {2*T*V*K/(ms/1e3)/1e12:.0f} TFLOP/s")
         ms = timeit(lambda: biv.biv_lm_head_backward(h, w, target, lse, dlp, dh, dw, gws))
         print(f"lm_head_grad T={T} V={V} {dt}: {ms*1e3:.1f} us  {6*T*V*K/(ms/1e3)/1e12:.0f} TFLOP/s")
+        ms = timeit(lambda: biv.biv_lm_head_backward(h, w, target, lse, dlp, dh, dw, gws, accumulate=True))
+        print(f"lm_head_grad T={T} V={V} {dt}, added to dW: {ms*1e3:.1f} us  {6*T*V*K/(ms/1e3)/1e12:.0f} TFLOP/s")
         del h, w, dh, dw, ws, gws
 elif case == "rows_8bit":
     u8, bf = torch.uint8, torch.bfloat16
