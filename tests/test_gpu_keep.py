@@ -551,6 +551,45 @@ def test_silu_mul_backward_in_fp32_has_the_bf16_forms_bits(B):
         B.biv_silu_mul_backward(gate_up.bfloat16(), dy.float(), ref)
         assert same(got, ref)
 
+@gpu
+@pytest.mark.parametrize("rows,d", [(5, 144), (33, 688), (16, 2048), (3, 8192)])
+def test_add_rmsnorm_over_its_input(B, rows, d):
+    """y over x and r' over the residual: the bits of separate outputs."""
+    x, r = stream(rows, d, 1).bfloat16(), stream(rows, d, 2).bfloat16()
+    w = (1 + 0.2 * torch.randn(d, device="cuda")).bfloat16()
+
+    def run(x, r, y, out):
+        c, s, k, ks, inv = u8(rows, d), f32(rows, groups(d)), u8(rows, d), f32(rows, groups(d)), f32(rows)
+        B.biv_add_rmsnorm_fp8(x, r, w, EPS, residual_out=out, y=y, codes=c, scales=s, keep=k, keep_scales=ks, inv=inv)
+        return [c, s, k, ks, inv, y, r if out is None else out]
+    apart = run(x, r, torch.empty_like(x), torch.empty_like(r))
+    assert all(same(a, b) for a, b in zip(apart, run(x, r, x, r)))
+
+
+@gpu
+def test_norm_offsets_beyond_32_bits(B):
+    """More than 2^31 elements of rows, kept rows and gradients."""
+    rows, d = 263000, 8192
+    e = lambda n, t: torch.empty(n, d, dtype=t, device="cuda")  # noqa: E731
+    x, y, k, dx = e(rows, torch.bfloat16), e(rows, torch.bfloat16), e(rows, torch.uint8), e(rows, torch.bfloat16)
+    tail = stream(64, d, 3, spread=False).bfloat16()
+    x.fill_(1.0)
+    x[-64:] = tail
+    w = torch.ones(d, device="cuda").bfloat16()
+    ks, inv, dw = f32(rows, groups(d)), f32(rows), f32(d)
+    B.biv_add_rmsnorm_fp8(x, None, w, EPS, y=y, keep=k, keep_scales=ks, inv=inv)
+    y2, k2, s2, i2 = e(64, torch.bfloat16), u8(64, d), f32(64, groups(d)), f32(64)
+    B.biv_add_rmsnorm_fp8(tail, None, w, EPS, y=y2, keep=k2, keep_scales=s2, inv=i2)
+    assert same(y[-64:], y2) and same(k[-64:], k2) and same(ks[-64:], s2) and same(inv[-64:], i2)
+    assert bool((y[:-64] == 1).all())
+    ws = torch.empty(B.biv_rmsnorm_backward_fp8_workspace(rows, d), dtype=torch.uint8, device="cuda")
+    B.biv_rmsnorm_backward_fp8(k, ks, inv, w, x, dx, dw, ws)
+    small, dws = e(64, torch.bfloat16), f32(d)
+    B.biv_rmsnorm_backward_fp8(k2, s2, i2, w, tail, small, dws, ws)
+    assert same(dx[-64:], small)
+    # (rows of ones along themselves have no gradient: what is left are roundings of 1)
+    assert float(dx[:-64].abs().max()) <= (d + 16) * 2.0 ** -23
+
 # ----------------------------------------------------------- on the host ----
 def test_refusals_on_the_host(B):
     lib = B.load()
