@@ -782,8 +782,8 @@ def biv_lm_head_loss(h, W, target, lp, lse, stats, workspace, weight=None, dlp=N
 
 def biv_lm_head_backward_workspace(T: int, V: int, K: int, dh_dtype=torch.bfloat16, dw_dtype=torch.bfloat16) -> int:
     n = C.c_size_t(0)
-    _check(load().biv_lm_head_backward_workspace(T, V, K, _FLOATS[dh_dtype], _FLOATS[dw_dtype], C.byref(n)),
-           "biv_lm_head_backward_workspace")
+    _check(load().biv_lm_head_backward_workspace(T, V, K, _FLOATS.get(dh_dtype, -1), _FLOATS.get(dw_dtype, -1),
+                                                 C.byref(n)), "biv_lm_head_backward_workspace")
     return n.value
 
 

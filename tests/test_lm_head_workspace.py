@@ -60,3 +60,9 @@ def test_a_micro_batch_is_far_below_its_logits(B, K):
         logits = 4 * T * 151936
         assert B.biv_lm_head_backward_workspace(T, 151936, K) < logits // 4
         assert B.biv_lm_head_backward_workspace(T, 151936, K, torch.float32, torch.float32) < logits // 1.9
+
+
+def test_refusals(B):
+    for bad in (dict(dh_dtype=torch.float16), dict(dw_dtype=torch.float64), dict(T=-1), dict(V=0), dict(K=12)):
+        with pytest.raises(B.BivError):
+            B.biv_lm_head_backward_workspace(**{**dict(T=4, V=8, K=8), **bad})
